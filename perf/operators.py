@@ -221,19 +221,13 @@ def _plain_logprob_fwd(st):
         h = torch.log(s) - w / s
         out["entropy"] = torch.where(empty, torch.zeros_like(h), h)[:, 0]
     if st["top"]:
-        left = raw.clone()
-        taken = torch.zeros_like(raw, dtype=torch.bool)
-        ids = []
-        low = float("-inf")
-        for _ in range(st["top"]):
-            i = torch.argmax(left, dim=1, keepdim=True)
-            # nothing above -inf is left: the lowest index not taken yet
-            i = torch.where(left.gather(1, i) == low,
-                            torch.argmin(taken.to(torch.uint8), dim=1, keepdim=True), i)
-            left.scatter_(1, i, low)
-            taken.scatter_(1, i, True)
-            ids.append(i)
-        ids = torch.cat(ids, dim=1)
+        # one whole number that orders values first and, among equal ones, the
+        # lowest index first (adding zero makes -0.0 equal to 0.0)
+        bits = (raw + 0.0).view(torch.int32)
+        order = torch.where(bits < 0, bits ^ 0x7FFFFFFF, bits).long()
+        last = st["vocab"] - 1
+        key = (order << 32) + (last - torch.arange(st["vocab"], device="cuda"))
+        ids = last - (torch.topk(key, st["top"], dim=1).values & 0xFFFFFFFF)
         out["top_ids"] = ids.to(_IT[st["itype"]])
         out["top_logp"] = torch.where(empty, m, x.gather(1, ids) - lse)
     return out
