@@ -98,7 +98,9 @@ typedef enum rn_status {
     RN_ERR_VARIANT = 7, /* a forced variant cannot run this shape / alignment  */
     RN_ERR_DTYPE = 8,   /* unknown storage type, or one the entry point lacks  */
     RN_ERR_SCRATCH = 9, /* the request needs more than a static scratch holds  */
-    RN_ERR_HOSTMEM = 10 /* a forward call's parameter vectors in host memory   */
+    RN_ERR_HOSTMEM = 10, /* a forward call's parameter vectors, or embed_bwd's
+                            workspace, in host memory                          */
+    RN_ERR_SCALE = 11   /* a scale that is not finite (log probabilities: > 0) */
 } rn_status;
 
 /* Storage types of x, y and the parameter vectors (statistics are FP32). */
@@ -323,6 +325,100 @@ int rms_bwd_typed(int dtype, const void *dy, const void *x, const void *w, void 
 int ln_bwd_noalloc(const float *dy, const float *x, const float *gamma, const float *mean,
                    const float *rstd, float *dx, float *dgamma, float *dbeta, int64_t rows,
                    int64_t d, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Token operators: the rows on either side of a network's normalized rows.
+ * What is said above of memory, streams, errors, aliasing and threads holds
+ * for them (programmatic launches included). Ids are signed integers of type
+ * `itype`, aligned to their size. Row strides are in elements, as in the *_strided
+ * calls; the elements between rows are neither read nor written.
+ * ------------------------------------------------------------------------ */
+enum { RN_INDEX_I32 = 0, RN_INDEX_I64 = 1 };
+
+/*
+ * Embedding rows: out_i = scale * table_{tokens_i}.
+ *   tokens [n]         ids; one outside [0, vocab) (a padding id of -1, say, or an
+ *                      id another shard owns) gives a row of zeros
+ *   table  [vocab][d]  row stride ldt >= d, of type `dtype`
+ *   out    [n][d]      row stride ldo >= d, of type `dtype`
+ * The product is computed in FP32 and rounded once, to nearest even; scale must
+ * be finite (RN_ERR_SCALE). vocab and d up to 2^30, n * d up to 2^40.
+ * One kernel launch. Accesses are as wide (16 bytes at most) as the alignment of
+ * both bases and strides and the width allow.
+ */
+int embed_fwd(int dtype, int itype, const void *tokens, const void *table, int64_t ldt, void *out,
+              int64_t ldo, int64_t n, int64_t vocab, int64_t d, float scale, void *stream);
+
+/*
+ * Gradient of the table: dtable_v = scale * sum over i with tokens_i = v of
+ * dout_i, every row of [0, vocab) written (zeros for absent ids); with
+ * `accumulate` != 0 the sums are added to dtable instead, and rows of absent
+ * ids are neither read nor written. Ids outside [0, vocab) contribute nothing.
+ *   dout   [n][d]      row stride lddo >= d, of type `dtype`
+ *   dtable [vocab][d]  row stride ldg >= d, of type `gtype`: `dtype` or
+ *                      RN_DTYPE_F32 (else RN_ERR_DTYPE)
+ * Sums are FP32, in an order fixed by n, d and the ids alone (the ids are
+ * sorted, stably, by a radix sort; no atomics touch a sum), so results repeat
+ * bit for bit; each element is rounded once. `workspace` (device memory, 16-byte
+ * aligned, caller-owned, contents on entry ignored) must hold the bytes that
+ * embed_bwd_workspace_size gives (else RN_ERR_SIZE): about 16 bytes an id and
+ * d/4 bytes an id for the sums of ids that occur many times. Calls that
+ * may run at the same time on the GPU need workspaces of their own (two graphs
+ * captured with one workspace count as such calls if they can overlap).
+ * n up to 2^31 - 1; n == 0 zeroes dtable (accumulate: does nothing). The calls
+ * launch only on `stream` and can be captured into a CUDA graph.
+ */
+int embed_bwd_workspace_size(int64_t n, int64_t vocab, int64_t d, size_t *bytes);
+
+int embed_bwd(int dtype, int gtype, int itype, const void *dout, int64_t lddo, const void *tokens,
+              void *dtable, int64_t ldg, int64_t n, int64_t vocab, int64_t d, float scale,
+              int accumulate, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Log probabilities over rows of logits. With x_j = scale * logits_j (scale, the
+ * inverse temperature, finite and > 0, else RN_ERR_SCALE) and the row's
+ * lse = log sum_j e^{x_j}:
+ *   logp     [rows]       x_t - lse for the row's target t; 0 where t is outside
+ *                         [0, vocab) (a padded row). Needs targets.
+ *   entropy  [rows]       H = -sum_j p_j log p_j, p_j = e^{x_j - lse}
+ *   lse      [rows]
+ *   top_ids, top_logp     [rows][top]: the `top` (0 .. RN_LOGPROB_MAX_TOP, at
+ *                         most vocab) largest logits' columns (of type `itype`)
+ *                         and log probabilities, largest first, equal logits by
+ *                         the lowest column first (-0 equals +0)
+ * Any output may be NULL (not wanted; entropy and alternatives then cost
+ * nothing), but not all of them (RN_ERR_NULL). Outputs are FP32.
+ *   logits   [rows][vocab]  row stride ldl >= vocab, of type `dtype`
+ *   targets  [rows]         ids; may be NULL when logp is
+ * Logits of -inf (masked columns) have probability zero; a row of nothing else
+ * gives lse = logp = -inf and entropy 0. A row that holds a NaN or a +inf gives
+ * NaN for all its values (its top_ids count NaN as the largest). All
+ * arithmetic and sums are FP32, over one read of the logits. vocab up to 2^30.
+ * One kernel launch.
+ */
+#define RN_LOGPROB_MAX_TOP 32
+
+int logprob_fwd(int dtype, int itype, const void *logits, int64_t ldl, const void *targets,
+                float *logp, float *entropy, float *lse, void *top_ids, float *top_logp,
+                int64_t rows, int64_t vocab, int top, float scale, void *stream);
+
+/*
+ * Gradient of logp and entropy:
+ *   dlogits_j = scale * (dlogp (d_jt - p_j) - dentropy p_j (log p_j + H))
+ * with lse and (where dentropy is given) entropy from the forward call.
+ *   dlogp, dentropy [rows]  FP32; either may be NULL (zero), not both
+ *   dlogits [rows][vocab]   row stride ldd >= vocab, of type `dtype`; each element
+ *                           rounded once. May be logits itself (same pointer and
+ *                           stride): the one exception to the aliasing rule.
+ * A target outside [0, vocab) takes no part (its dlogp is ignored). A row whose
+ * dlogp and dentropy are both zero or ignored, or whose lse is -inf, gets zeros (its
+ * logits are not read). Rows with |lse| >= 4096, where an FP32 lse no longer holds
+ * log p, have their sums taken again from the logits. One kernel launch.
+ */
+int logprob_bwd(int dtype, int itype, const float *dlogp, const float *dentropy,
+                const void *logits, int64_t ldl, const void *targets, const float *lse,
+                const float *entropy, void *dlogits, int64_t ldd, int64_t rows, int64_t vocab,
+                float scale, void *stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *rn_status_str(int status);

@@ -1,4 +1,5 @@
-"""Row-wise LayerNorm / RMSNorm forward on GB300 (sm_103a).
+"""Row-wise LayerNorm / RMSNorm on GB300 (sm_103a), and the token operators on
+either side of them (embedding rows, log probabilities).
 
 A thin torch-facing binding over the C ABI of ``librownorm.so``
 (include/rownorm.h): it checks tensor shapes and dtypes, allocates outputs
@@ -12,7 +13,8 @@ from . import capi
 from .capi import RowNormError, load  # noqa: F401
 
 __all__ = ["ln_fwd", "rms_fwd", "ln_fwd_residual", "rms_fwd_residual", "ln_fwd_batched",
-           "rms_fwd_batched", "ln_bwd", "rms_bwd", "capi", "RowNormError", "load"]
+           "rms_fwd_batched", "ln_bwd", "rms_bwd", "embed_fwd", "embed_bwd", "logprob_fwd",
+           "logprob_bwd", "capi", "RowNormError", "load"]
 
 
 def _stream_handle(t, stream):
@@ -339,3 +341,244 @@ def rms_bwd(dy, x, w, eps: float = 1e-5, *, dx=None, dw=None, param_grads: bool 
                             ws.numel() * 4 if ws is not None else 0, _stream_handle(x, stream))
     capi.check(st)
     return dx, dw
+
+
+# ---------------------------------------------------------------------------
+# token operators
+# ---------------------------------------------------------------------------
+def _index_code(name, t):
+    import torch
+
+    codes = {torch.int32: capi.RN_INDEX_I32, torch.int64: capi.RN_INDEX_I64}
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in codes:
+        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+    _check_f32_cuda(name, t, t.dtype)
+    return codes[t.dtype]
+
+
+def _same_device(x, **others):
+    """Every CUDA tensor of a call on x's device (or, with x in host memory, on
+    one device)."""
+    dev = x.device if x.is_cuda else None
+    for n, t in others.items():
+        if t is None or not t.is_cuda:
+            continue
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, other tensors on {dev}")
+        dev = t.device
+    return dev
+
+
+class _On:
+    """Makes the call's device current and, where the caller gives a stream of
+    its own, that stream too, so that the memory the call allocates belongs to the
+    stream that uses it."""
+
+    def __init__(self, dev, stream):
+        import torch
+
+        self._device = torch.cuda.device(dev if dev is not None else -1)
+        if isinstance(stream, int):
+            # (handle 0: the legacy default stream, torch's default stream)
+            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                      else torch.cuda.default_stream(dev))
+        elif stream is not None and dev is not None and stream.device != dev:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+        self._stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        import torch
+
+        self._device.__enter__()
+        self._stream.__enter__()
+        return int(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        self._stream.__exit__(*exc)
+        return self._device.__exit__(*exc)
+
+
+def _matrix(name, t, d, dtype):
+    """(rows, row stride) of a typed matrix of rows of d (see _rows_of)."""
+    _check_f32_cuda(name, t, dtype, contiguous=False)
+    return _rows_of(name, t, d)
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
+    """Embedding rows ``scale * table[tokens]``.
+
+    tokens: int32 or int64 ids of any shape; an id outside ``[0, vocab)`` gives a
+    row of zeros. table: ``[vocab, d]``, float32, bfloat16 or float16, contiguous
+    or a row-strided view. Returns ``out`` of shape ``tokens.shape + (d,)`` in the
+    table's type (``out`` may also be passed as a 2-D row-strided view).
+    """
+    import torch
+
+    code = _dtype_code(table)
+    if table.dim() != 2:
+        raise ValueError("table must be 2-D")
+    vocab, d = table.shape
+    it = _index_code("tokens", tokens)
+    _, ldt = _matrix("table", table, d, table.dtype)
+    dev = _same_device(table, tokens=tokens, out=out)
+    n = tokens.numel()
+    with _On(dev, stream) as s:
+        if out is None:
+            out = (torch.empty(tuple(tokens.shape) + (d,), dtype=table.dtype, device=dev)
+                   if dev is not None
+                   else _empty_like_home(table, tuple(tokens.shape) + (d,), table.dtype))
+        if out.numel() != n * d or out.shape[-1:] != (d,):
+            raise ValueError(f"out must hold {n} rows of {d}")
+        _, ldo = _matrix("out", out, d, table.dtype)
+        capi.check(capi.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt,
+                                  out.data_ptr(), ldo, n, vocab, d, float(scale), s))
+    return out
+
+
+def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtable=None,
+              accumulate: bool = False, workspace=None, stream=None):
+    """Gradient of ``embed_fwd`` with respect to the table.
+
+    dout: the rows' gradient, shape ``tokens.shape + (d,)`` (or a 2-D row-strided
+    view). Returns ``dtable`` of shape ``[vocab, d]`` in ``dtype`` (dout's type
+    unless given; float32 is the other choice), every row written; with
+    ``accumulate`` the sums are added to the ``dtable`` passed in.
+    ``workspace``: a contiguous CUDA tensor of at least
+    ``capi.embed_bwd_workspace_size(n, vocab, d)`` bytes (allocated if not given).
+    """
+    import torch
+
+    code = _dtype_code(dout)
+    it = _index_code("tokens", tokens)
+    n = tokens.numel()
+    if dout.dim() < 1:
+        raise ValueError("dout must have a last dimension")
+    d = dout.shape[-1]
+    if dout.numel() != n * d:
+        raise ValueError(f"dout must hold {n} rows of {d}")
+    _, lddo = _matrix("dout", dout, d, dout.dtype)
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dtable to add to")
+        gdtype = dout.dtype if dtype is None else dtype
+    else:
+        gdtype = dtable.dtype
+        if dtype is not None and dtype != gdtype:
+            raise TypeError(f"dtable is {gdtype}, dtype says {dtype}")
+    if gdtype not in (dout.dtype, torch.float32):
+        raise TypeError(f"dtable must be {dout.dtype} or float32")
+    dev = _same_device(dout, tokens=tokens, dtable=dtable, workspace=workspace)
+    with _On(dev, stream) as s:
+        if dtable is None:
+            dtable = (torch.empty((vocab, d), dtype=gdtype, device=dev) if dev is not None
+                      else _empty_like_home(dout, (vocab, d), gdtype))
+        if tuple(dtable.shape) != (vocab, d):
+            raise ValueError(f"dtable must be of shape [{vocab}, {d}]")
+        _, ldg = _matrix("dtable", dtable, d, gdtype)
+        need = capi.embed_bwd_workspace_size(n, vocab, d)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8,
+                                    device=dev if dev is not None else "cuda")
+        elif not (workspace.is_cuda and workspace.is_contiguous()):
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        capi.check(capi.embed_bwd(code, _dtype_code(dtable), it, dout.data_ptr(), lddo,
+                                  tokens.data_ptr(), dtable.data_ptr(), ldg, n, vocab, d,
+                                  float(scale), 1 if accumulate else 0, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), s))
+    return dtable
+
+
+def _row_vector(name, t, rows):
+    if t is not None:
+        _check_like(name, t, rows)
+
+
+def logprob_fwd(logits, targets=None, scale: float = 1.0, *, top: int = 0,
+                want_entropy: bool = True, stream=None):
+    """Log probabilities over the last dimension of ``logits`` times ``scale`` (the
+    inverse temperature).
+
+    logits: float32, bfloat16 or float16, contiguous or a 2-D row-strided view.
+    targets: int32 or int64 columns of shape ``logits.shape[:-1]``; one outside
+    ``[0, vocab)`` gets 0. Returns ``(logp, entropy, lse, top_ids, top_logp)``:
+    the targets' log probabilities (None without targets), the entropies (None
+    without ``want_entropy``), the log-sum-exps, and the ``top`` (at most 32)
+    largest columns with their log probabilities, shape ``[..., top]``, largest
+    first and the lowest column first among equal ones (None with ``top`` 0).
+    Values are float32; top_ids has targets' type (int64 without targets).
+    """
+    import torch
+
+    code = _dtype_code(logits)
+    if logits.dim() < 1:
+        raise ValueError("logits must have a last dimension")
+    vocab = logits.shape[-1]
+    rows, ldl = _matrix("logits", logits, vocab, logits.dtype)
+    lead = tuple(logits.shape[:-1])
+    it, itype = capi.RN_INDEX_I64, torch.int64
+    if targets is not None:
+        it, itype = _index_code("targets", targets), targets.dtype
+        if targets.numel() != rows:
+            raise ValueError(f"targets must have {rows} elements")
+    dev = _same_device(logits, targets=targets)
+    with _On(dev, stream) as s:
+
+        def new(shape, dtype=torch.float32):
+            if dev is not None:
+                return torch.empty(shape, dtype=dtype, device=dev)
+            return _empty_like_home(logits, shape, dtype)
+
+        logp = new(lead) if targets is not None else None
+        entropy = new(lead) if want_entropy else None
+        lse = new(lead)
+        ids = new(lead + (top,), itype) if top > 0 else None
+        top_logp = new(lead + (top,)) if top > 0 else None
+        capi.check(capi.logprob_fwd(code, it, logits.data_ptr(), ldl, _ptr(targets), _ptr(logp),
+                                    _ptr(entropy), lse.data_ptr(), _ptr(ids), _ptr(top_logp),
+                                    rows, vocab, int(top), float(scale), s))
+    return logp, entropy, lse, ids, top_logp
+
+
+def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=None, entropy=None,
+                dlogits=None, stream=None):
+    """Gradient of ``logprob_fwd``'s log probabilities (dlogp) and, where
+    ``dentropy`` is given with the forward call's ``entropy``, of its entropies,
+    with respect to the logits. dlogp may be None (then targets too). ``dlogits``:
+    allocated in the logits' type unless given; it may be ``logits`` itself.
+    """
+    import torch
+
+    code = _dtype_code(logits)
+    if logits.dim() < 1:
+        raise ValueError("logits must have a last dimension")
+    vocab = logits.shape[-1]
+    rows, ldl = _matrix("logits", logits, vocab, logits.dtype)
+    it = capi.RN_INDEX_I64
+    if targets is not None:
+        it = _index_code("targets", targets)
+        if targets.numel() != rows:
+            raise ValueError(f"targets must have {rows} elements")
+    for n, t in (("dlogp", dlogp), ("lse", lse), ("dentropy", dentropy), ("entropy", entropy)):
+        _row_vector(n, t, rows)
+    if lse is None:
+        raise TypeError("lse must be a torch.Tensor")
+    dev = _same_device(logits, dlogp=dlogp, targets=targets, lse=lse, dentropy=dentropy,
+                       entropy=entropy, dlogits=dlogits)
+    with _On(dev, stream) as s:
+        if dlogits is None:
+            dlogits = (torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+                       if dev is not None
+                       else _empty_like_home(logits, logits.shape, logits.dtype))
+        if dlogits.numel() != logits.numel() or dlogits.shape[-1] != vocab:
+            raise ValueError("dlogits must be shaped like logits")
+        _, ldd = _matrix("dlogits", dlogits, vocab, logits.dtype)
+        capi.check(capi.logprob_bwd(code, it, _ptr(dlogp), _ptr(dentropy), logits.data_ptr(), ldl,
+                                    _ptr(targets), lse.data_ptr(), _ptr(entropy),
+                                    dlogits.data_ptr(), ldd, rows, vocab, float(scale), s))
+    return dlogits

@@ -26,6 +26,7 @@ RN_ERR_VARIANT = 7
 RN_ERR_DTYPE = 8
 RN_ERR_SCRATCH = 9
 RN_ERR_HOSTMEM = 10
+RN_ERR_SCALE = 11
 
 # device error word bits
 RN_DEVERR_STAGED_TIMEOUT = 1
@@ -39,6 +40,11 @@ RN_NOALLOC_MAX_D = 4096
 RN_DTYPE_F32 = 0
 RN_DTYPE_BF16 = 1
 RN_DTYPE_F16 = 2
+
+# type of ids (tokens, targets)
+RN_INDEX_I32 = 0
+RN_INDEX_I64 = 1
+RN_LOGPROB_MAX_TOP = 32
 
 RN_VARIANT_AUTO = 0
 RN_VARIANT_WARP = 1
@@ -107,6 +113,14 @@ SIGNATURES = {
     "rms_fwd_typed": (_INT, [_INT, _INT, _P, _P, _P, _I64, _I64, _F, _P]),
     "rn_plan_for_typed": (_INT, [_INT, _INT, _INT, _I64, _P, _P, _P, _P, ctypes.POINTER(rn_plan)]),
     "rn_device_error": (_INT, [ctypes.POINTER(ctypes.c_uint), _INT]),
+    "embed_fwd": (_INT, [_INT, _INT, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _F, _P]),
+    "embed_bwd_workspace_size": (_INT, [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "embed_bwd": (_INT, [_INT, _INT, _INT, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _F, _INT, _P,
+                         ctypes.c_size_t, _P]),
+    "logprob_fwd": (_INT, [_INT, _INT, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _INT, _F,
+                           _P]),
+    "logprob_bwd": (_INT, [_INT, _INT, _P, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _F,
+                           _P]),
     "rn_pageable_host_access": (_INT, [ctypes.POINTER(_INT)]),
 }
 
@@ -318,3 +332,31 @@ def rms_bwd_typed(dtype, dy, x, w, dx, dw, rows, d, eps, workspace, workspace_by
                   stream=0) -> int:
     return load().rms_bwd_typed(dtype, dy, x, w, dx, dw, rows, d, eps, workspace,
                                 workspace_bytes, stream)
+
+
+def embed_fwd(dtype, itype, tokens, table, ldt, out, ldo, n, vocab, d, scale, stream=0) -> int:
+    return load().embed_fwd(dtype, itype, tokens, table, ldt, out, ldo, n, vocab, d, scale, stream)
+
+
+def embed_bwd_workspace_size(n: int, vocab: int, d: int) -> int:
+    out = ctypes.c_size_t(0)
+    check(load().embed_bwd_workspace_size(n, vocab, d, ctypes.byref(out)))
+    return out.value
+
+
+def embed_bwd(dtype, gtype, itype, dout, lddo, tokens, dtable, ldg, n, vocab, d, scale,
+              accumulate, workspace, workspace_bytes, stream=0) -> int:
+    return load().embed_bwd(dtype, gtype, itype, dout, lddo, tokens, dtable, ldg, n, vocab, d,
+                            scale, accumulate, workspace, workspace_bytes, stream)
+
+
+def logprob_fwd(dtype, itype, logits, ldl, targets, logp, entropy, lse, top_ids, top_logp, rows,
+                vocab, top, scale, stream=0) -> int:
+    return load().logprob_fwd(dtype, itype, logits, ldl, targets, logp, entropy, lse, top_ids,
+                              top_logp, rows, vocab, top, scale, stream)
+
+
+def logprob_bwd(dtype, itype, dlogp, dentropy, logits, ldl, targets, lse, entropy, dlogits, ldd,
+                rows, vocab, scale, stream=0) -> int:
+    return load().logprob_bwd(dtype, itype, dlogp, dentropy, logits, ldl, targets, lse, entropy,
+                              dlogits, ldd, rows, vocab, scale, stream)

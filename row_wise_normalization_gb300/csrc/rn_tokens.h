@@ -1,0 +1,129 @@
+// rn_tokens.h -- kernel arguments of the token operators (embedding rows and
+// their gradient, log probabilities and their gradient), shared by the C-ABI
+// unit and the kernel units.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "rn_params.h"
+
+namespace rn {
+
+// Ids (tokens, targets) are 32- or 64-bit signed integers.
+enum IndexType : int { IT_I32 = 0, IT_I64 = 1 };
+constexpr int index_size(int it) { return it == IT_I64 ? 8 : 4; }
+
+// Division of a 32-bit number below 2^31 by a fixed divisor: a multiplication
+// and a shift (Granlund and Montgomery, "Division by invariant integers using
+// multiplication"). With s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1,
+// n / d = (umulhi(m, n) + n) >> s; n < 2^31 keeps the sum within 32 bits.
+struct FastDiv {
+    uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+    FastDiv f;
+    f.d = d;
+    f.s = 0;
+    while (((uint64_t)1 << f.s) < d) ++f.s;
+    f.m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.s) - d)) / d + 1);
+    return f;
+}
+
+// out[i] = scale * table[tokens[i]], zeros where the id is outside [0, vocab).
+struct EmbedParams {
+    const void* tokens;
+    const void* table;
+    void* out;
+    int64_t n, vocab;
+    int64_t ldt, ldo;     // row strides in elements
+    int64_t total;        // n * vectors per row
+    FastDiv vpr;          // vectors per row
+    float scale;
+};
+// ne: elements of one vector access (1, 2, 4 or 8).
+cudaError_t embed_fwd_launch(int dtype, int itype, int ne, const EmbedParams& p, cudaStream_t s);
+
+// Stable sort of the n ids by value, with their positions. Ids outside
+// [0, vocab) are given the key `vocab`, so that they come last.
+constexpr int kSortThreads = 512;
+constexpr int kSortPerThread = 8;
+constexpr int kSortTile = kSortThreads * kSortPerThread;
+constexpr int kSortBits = 9;                 // bits of a digit, at most
+constexpr int kSortBins = 1 << kSortBits;
+struct SortParams {
+    const void* tokens;
+    int64_t n, vocab;
+    uint32_t* key[2];     // [n] each: the passes go from one to the other
+    int32_t* pos[2];      // [n] each
+    uint32_t* hist;       // [tiles][kSortBins]
+    uint32_t* present;    // one bit for each id of the vocabulary; NULL: not wanted
+    int tiles;
+    int bits;             // bits of a digit in this sort
+};
+constexpr int sort_key_bits(int64_t vocab) {
+    int b = 0;
+    while (((int64_t)1 << b) <= vocab) ++b;   // keys 0 .. vocab
+    return b;
+}
+constexpr int sort_passes(int64_t vocab) { return (sort_key_bits(vocab) + kSortBits - 1) / kSortBits; }
+// Runs every pass; the sorted arrays end in key[passes & 1], pos[passes & 1].
+cudaError_t embed_sort_launch(int itype, SortParams p, cudaStream_t s);
+
+// dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum of dout[i] over the
+// positions i with tokens[i] == v, from the sorted ids.
+constexpr int kEmbedChunk = 32;    // sorted positions one thread group sums
+struct EmbedBwdParams {
+    const void* dout;
+    void* dtable;
+    const uint32_t* key;
+    const int32_t* pos;
+    const uint32_t* present;   // NULL when accumulating (no row is cleared)
+    float* part;               // [2 * chunks][dpad]
+    int64_t n, vocab, d, dpad;
+    int64_t lddo, ldg;
+    int64_t chunks;
+    int tx, ty;                // threads across a row, chunks of a CTA
+    int slices;                // CTAs across a row
+    int seg_ctas, zero_ctas;
+    float scale;
+    int accumulate;
+};
+cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams& p,
+                             cudaStream_t s);
+
+// Log probabilities over the rows of a matrix of logits.
+constexpr int kMaxTop = 32;
+struct LogprobParams {
+    const void* logits;
+    const void* targets;    // may be NULL
+    float* logp;            // may be NULL, as every output
+    float* entropy;
+    float* lse;
+    void* top_ids;
+    float* top_logp;
+    int64_t rows, ld;
+    int vocab, top, itype;
+    float scale;
+};
+cudaError_t logprob_fwd_launch(int dtype, const LogprobParams& p, cudaStream_t s);
+
+struct LogprobBwdParams {
+    const float* dlogp;       // may be NULL
+    const float* dentropy;    // may be NULL
+    const void* logits;
+    const void* targets;      // may be NULL (with dlogp NULL)
+    const float* lse;
+    const float* entropy;     // with dentropy
+    void* dlogits;
+    int64_t rows, ld, ldd;
+    int64_t total;            // rows * tiles
+    int64_t tiles;            // tiles of a row
+    int vocab, itype;
+    float scale;
+};
+// vec: logits and dlogits of every row share a 16-byte phase.
+cudaError_t logprob_bwd_launch(int dtype, bool vec, const LogprobBwdParams& p, cudaStream_t s);
+
+}  // namespace rn

@@ -1349,8 +1349,10 @@ const char* rn_status_str(int status) {
         case RN_ERR_VARIANT: return "the requested kernel variant cannot run this request";
         case RN_ERR_DTYPE: return "unsupported storage type for this entry point";
         case RN_ERR_HOSTMEM:
-            return "the parameter vectors (gamma, beta, w) of a forward call must be in device "
-                   "memory";
+            return "the parameter vectors (gamma, beta, w) of a forward call and the workspace "
+                   "of embed_bwd must be in device memory";
+        case RN_ERR_SCALE:
+            return "scale must be finite (log probabilities: finite and > 0)";
         case RN_ERR_SCRATCH:
             return "the request needs more than the static scratch holds (ln_bwd_noalloc: "
                    "d <= 4096)";
