@@ -393,7 +393,8 @@ int embed_bwd(int dtype, int gtype, int itype, const void *dout, int64_t lddo, c
  * Logits of -inf (masked columns) have probability zero; a row of nothing else
  * gives lse = logp = -inf and entropy 0. A row that holds a NaN or a +inf gives
  * NaN for all its values (its top_ids count NaN as the largest). All
- * arithmetic and sums are FP32, over one read of the logits. vocab up to 2^30.
+ * arithmetic and sums are FP32, over one read of the logits. vocab up to 2^30,
+ * rows up to 2^31 - 1.
  * One kernel launch.
  */
 #define RN_LOGPROB_MAX_TOP 32

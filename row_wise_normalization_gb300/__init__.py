@@ -345,69 +345,134 @@ def rms_bwd(dy, x, w, eps: float = 1e-5, *, dx=None, dw=None, param_grads: bool 
 
 # ---------------------------------------------------------------------------
 # token operators
+#
+# A decoding step waits for the host side of these calls, not for their kernels
+# (a few microseconds each), so what they check is written to be checked fast:
+# types by one dictionary, contiguous device tensors first, the current device
+# and stream left alone unless the call names others.
 # ---------------------------------------------------------------------------
-def _index_code(name, t):
+_CODES = {}
+
+
+def _codes():
     import torch
 
-    codes = {torch.int32: capi.RN_INDEX_I32, torch.int64: capi.RN_INDEX_I64}
-    if not isinstance(t, torch.Tensor):
+    if not _CODES:
+        _CODES.update({torch.float32: capi.RN_DTYPE_F32, torch.bfloat16: capi.RN_DTYPE_BF16,
+                       torch.float16: capi.RN_DTYPE_F16, torch.int32: capi.RN_INDEX_I32,
+                       torch.int64: capi.RN_INDEX_I64})
+    return _CODES
+
+
+def _values(name, t):
+    """The storage code of a floating-point tensor."""
+    try:
+        code = _codes()[t.dtype]
+        if t.dtype.is_floating_point:
+            return code
+    except (AttributeError, KeyError):
+        pass
+    if not hasattr(t, "dtype"):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in codes:
-        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
-    _check_f32_cuda(name, t, t.dtype)
-    return codes[t.dtype]
+    raise TypeError(f"unsupported dtype {t.dtype} (float32, bfloat16 or float16)")
 
 
-def _same_device(x, **others):
-    """Every CUDA tensor of a call on x's device (or, with x in host memory, on
-    one device)."""
-    dev = x.device if x.is_cuda else None
-    for n, t in others.items():
-        if t is None or not t.is_cuda:
-            continue
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{n} is on {t.device}, other tensors on {dev}")
-        dev = t.device
+def _ids(name, t):
+    """The index code of a contiguous tensor of ids."""
+    try:
+        code = _codes()[t.dtype]
+        if not t.dtype.is_floating_point:
+            if not (t.is_cuda and t.is_contiguous()):
+                _check_f32_cuda(name, t, t.dtype)
+            return code
+    except (AttributeError, KeyError):
+        pass
+    if not hasattr(t, "dtype"):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+
+
+def _row_floats(name, t, rows):
+    """Address of an FP32 vector of a value a row (0 for None)."""
+    if t is None:
+        return 0
+    import torch
+
+    if not (getattr(t, "is_cuda", False) and t.dtype is torch.float32 and t.is_contiguous()):
+        _check_f32_cuda(name, t)
+    if t.numel() != rows:
+        raise ValueError(f"{name} must have {rows} elements")
+    return t.data_ptr()
+
+
+def _matrix(name, t, d, dtype):
+    """(rows, row stride) of a typed matrix of rows of d (see _rows_of)."""
+    if t.is_cuda and t.dtype is dtype and t.is_contiguous() and d > 0:
+        return t.numel() // d, d
+    _check_f32_cuda(name, t, dtype, contiguous=False)
+    return _rows_of(name, t, d)
+
+
+def _device_of(tensors):
+    """The one device of a call's CUDA tensors (None where all are in host
+    memory)."""
+    dev = None
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on {dev} and on {t.device}")
     return dev
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 class _On:
     """Makes the call's device current and, where the caller gives a stream of
     its own, that stream too, so that the memory the call allocates belongs to the
-    stream that uses it."""
+    stream that uses it. Yields the stream's handle."""
+
+    __slots__ = ("_dev", "_stream", "_inner")
 
     def __init__(self, dev, stream):
-        import torch
-
-        self._device = torch.cuda.device(dev if dev is not None else -1)
-        if isinstance(stream, int):
-            # (handle 0: the legacy default stream, torch's default stream)
-            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
-                      else torch.cuda.default_stream(dev))
-        elif stream is not None and dev is not None and stream.device != dev:
-            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
-        self._stream = torch.cuda.stream(stream)
+        self._dev, self._stream, self._inner = dev, stream, ()
 
     def __enter__(self):
         import torch
 
-        self._device.__enter__()
-        self._stream.__enter__()
-        return int(torch.cuda.current_stream().cuda_stream)
+        dev, stream = self._dev, self._stream
+        if stream is None:
+            if dev is not None and dev.index != torch.cuda.current_device():
+                self._inner = (torch.cuda.device(dev),)
+        else:
+            if isinstance(stream, int):
+                # (handle 0: the legacy default stream, torch's default stream)
+                stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                          else torch.cuda.default_stream(dev))
+            elif dev is not None and stream.device != dev:
+                raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+            self._inner = (torch.cuda.stream(stream),)
+            if dev is not None:
+                self._inner = (torch.cuda.device(dev),) + self._inner
+        for c in self._inner:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
-        self._stream.__exit__(*exc)
-        return self._device.__exit__(*exc)
+        for c in reversed(self._inner):
+            c.__exit__(*exc)
 
 
-def _matrix(name, t, d, dtype):
-    """(rows, row stride) of a typed matrix of rows of d (see _rows_of)."""
-    _check_f32_cuda(name, t, dtype, contiguous=False)
-    return _rows_of(name, t, d)
+def _new(home, dev, shape, dtype):
+    """An output on the call's device, or in host memory like `home`."""
+    import torch
 
-
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
+    if dev is not None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _empty_like_home(home, shape, dtype)
 
 
 def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
@@ -418,24 +483,22 @@ def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
     or a row-strided view. Returns ``out`` of shape ``tokens.shape + (d,)`` in the
     table's type (``out`` may also be passed as a 2-D row-strided view).
     """
-    import torch
-
-    code = _dtype_code(table)
+    dtype = getattr(table, "dtype", None)
+    code = _values("table", table)
+    it = _ids("tokens", tokens)
     if table.dim() != 2:
         raise ValueError("table must be 2-D")
     vocab, d = table.shape
-    it = _index_code("tokens", tokens)
-    _, ldt = _matrix("table", table, d, table.dtype)
-    dev = _same_device(table, tokens=tokens, out=out)
+    _, ldt = _matrix("table", table, d, dtype)
+    dev = _device_of((table, tokens, out))
     n = tokens.numel()
     with _On(dev, stream) as s:
         if out is None:
-            out = (torch.empty(tuple(tokens.shape) + (d,), dtype=table.dtype, device=dev)
-                   if dev is not None
-                   else _empty_like_home(table, tuple(tokens.shape) + (d,), table.dtype))
-        if out.numel() != n * d or out.shape[-1:] != (d,):
-            raise ValueError(f"out must hold {n} rows of {d}")
-        _, ldo = _matrix("out", out, d, table.dtype)
+            out, ldo = _new(table, dev, (*tokens.shape, d), dtype), d
+        else:
+            if out.numel() != n * d or out.shape[-1:] != (d,):
+                raise ValueError(f"out must hold {n} rows of {d}")
+            _, ldo = _matrix("out", out, d, dtype)
         capi.check(capi.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt,
                                   out.data_ptr(), ldo, n, vocab, d, float(scale), s))
     return out
@@ -454,8 +517,8 @@ def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtabl
     """
     import torch
 
-    code = _dtype_code(dout)
-    it = _index_code("tokens", tokens)
+    code = _values("dout", dout)
+    it = _ids("tokens", tokens)
     n = tokens.numel()
     if dout.dim() < 1:
         raise ValueError("dout must have a last dimension")
@@ -473,11 +536,10 @@ def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtabl
             raise TypeError(f"dtable is {gdtype}, dtype says {dtype}")
     if gdtype not in (dout.dtype, torch.float32):
         raise TypeError(f"dtable must be {dout.dtype} or float32")
-    dev = _same_device(dout, tokens=tokens, dtable=dtable, workspace=workspace)
+    dev = _device_of((dout, tokens, dtable, workspace))
     with _On(dev, stream) as s:
         if dtable is None:
-            dtable = (torch.empty((vocab, d), dtype=gdtype, device=dev) if dev is not None
-                      else _empty_like_home(dout, (vocab, d), gdtype))
+            dtable = _new(dout, dev, (vocab, d), gdtype)
         if tuple(dtable.shape) != (vocab, d):
             raise ValueError(f"dtable must be of shape [{vocab}, {d}]")
         _, ldg = _matrix("dtable", dtable, d, gdtype)
@@ -487,16 +549,11 @@ def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtabl
                                     device=dev if dev is not None else "cuda")
         elif not (workspace.is_cuda and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous CUDA tensor")
-        capi.check(capi.embed_bwd(code, _dtype_code(dtable), it, dout.data_ptr(), lddo,
+        capi.check(capi.embed_bwd(code, _values("dtable", dtable), it, dout.data_ptr(), lddo,
                                   tokens.data_ptr(), dtable.data_ptr(), ldg, n, vocab, d,
                                   float(scale), 1 if accumulate else 0, workspace.data_ptr(),
                                   workspace.numel() * workspace.element_size(), s))
     return dtable
-
-
-def _row_vector(name, t, rows):
-    if t is not None:
-        _check_like(name, t, rows)
 
 
 def logprob_fwd(logits, targets=None, scale: float = 1.0, *, top: int = 0,
@@ -515,31 +572,30 @@ def logprob_fwd(logits, targets=None, scale: float = 1.0, *, top: int = 0,
     """
     import torch
 
-    code = _dtype_code(logits)
+    code = _values("logits", logits)
     if logits.dim() < 1:
         raise ValueError("logits must have a last dimension")
     vocab = logits.shape[-1]
     rows, ldl = _matrix("logits", logits, vocab, logits.dtype)
-    lead = tuple(logits.shape[:-1])
-    it, itype = capi.RN_INDEX_I64, torch.int64
+    lead = logits.shape[:-1]
+    it, itype, tgt = capi.RN_INDEX_I64, torch.int64, 0
     if targets is not None:
-        it, itype = _index_code("targets", targets), targets.dtype
+        it, itype, tgt = _ids("targets", targets), targets.dtype, targets.data_ptr()
         if targets.numel() != rows:
             raise ValueError(f"targets must have {rows} elements")
-    dev = _same_device(logits, targets=targets)
+    dev = _device_of((logits, targets))
+    f32 = torch.float32
+    logp = entropy = ids = top_logp = None
     with _On(dev, stream) as s:
-
-        def new(shape, dtype=torch.float32):
-            if dev is not None:
-                return torch.empty(shape, dtype=dtype, device=dev)
-            return _empty_like_home(logits, shape, dtype)
-
-        logp = new(lead) if targets is not None else None
-        entropy = new(lead) if want_entropy else None
-        lse = new(lead)
-        ids = new(lead + (top,), itype) if top > 0 else None
-        top_logp = new(lead + (top,)) if top > 0 else None
-        capi.check(capi.logprob_fwd(code, it, logits.data_ptr(), ldl, _ptr(targets), _ptr(logp),
+        if targets is not None:
+            logp = _new(logits, dev, lead, f32)
+        if want_entropy:
+            entropy = _new(logits, dev, lead, f32)
+        lse = _new(logits, dev, lead, f32)
+        if top > 0:
+            ids = _new(logits, dev, (*lead, top), itype)
+            top_logp = _new(logits, dev, (*lead, top), f32)
+        capi.check(capi.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, _ptr(logp),
                                     _ptr(entropy), lse.data_ptr(), _ptr(ids), _ptr(top_logp),
                                     rows, vocab, int(top), float(scale), s))
     return logp, entropy, lse, ids, top_logp
@@ -552,33 +608,29 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
     with respect to the logits. dlogp may be None (then targets too). ``dlogits``:
     allocated in the logits' type unless given; it may be ``logits`` itself.
     """
-    import torch
-
-    code = _dtype_code(logits)
+    code = _values("logits", logits)
     if logits.dim() < 1:
         raise ValueError("logits must have a last dimension")
     vocab = logits.shape[-1]
     rows, ldl = _matrix("logits", logits, vocab, logits.dtype)
-    it = capi.RN_INDEX_I64
+    it, tgt = capi.RN_INDEX_I64, 0
     if targets is not None:
-        it = _index_code("targets", targets)
+        it, tgt = _ids("targets", targets), targets.data_ptr()
         if targets.numel() != rows:
             raise ValueError(f"targets must have {rows} elements")
-    for n, t in (("dlogp", dlogp), ("lse", lse), ("dentropy", dentropy), ("entropy", entropy)):
-        _row_vector(n, t, rows)
     if lse is None:
         raise TypeError("lse must be a torch.Tensor")
-    dev = _same_device(logits, dlogp=dlogp, targets=targets, lse=lse, dentropy=dentropy,
-                       entropy=entropy, dlogits=dlogits)
+    rows_of = [_row_floats(n, t, rows) for n, t in (("dlogp", dlogp), ("dentropy", dentropy),
+                                                    ("lse", lse), ("entropy", entropy))]
+    dev = _device_of((logits, dlogp, targets, lse, dentropy, entropy, dlogits))
     with _On(dev, stream) as s:
         if dlogits is None:
-            dlogits = (torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-                       if dev is not None
-                       else _empty_like_home(logits, logits.shape, logits.dtype))
-        if dlogits.numel() != logits.numel() or dlogits.shape[-1] != vocab:
-            raise ValueError("dlogits must be shaped like logits")
-        _, ldd = _matrix("dlogits", dlogits, vocab, logits.dtype)
-        capi.check(capi.logprob_bwd(code, it, _ptr(dlogp), _ptr(dentropy), logits.data_ptr(), ldl,
-                                    _ptr(targets), lse.data_ptr(), _ptr(entropy),
-                                    dlogits.data_ptr(), ldd, rows, vocab, float(scale), s))
+            dlogits, ldd = _new(logits, dev, logits.shape, logits.dtype), vocab
+        else:
+            if dlogits.numel() != logits.numel() or dlogits.shape[-1] != vocab:
+                raise ValueError("dlogits must be shaped like logits")
+            _, ldd = _matrix("dlogits", dlogits, vocab, logits.dtype)
+        capi.check(capi.logprob_bwd(code, it, rows_of[0], rows_of[1], logits.data_ptr(), ldl, tgt,
+                                    rows_of[2], rows_of[3], dlogits.data_ptr(), ldd, rows, vocab,
+                                    float(scale), s))
     return dlogits

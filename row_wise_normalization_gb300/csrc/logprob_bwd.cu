@@ -49,79 +49,112 @@ __device__ float2 row_sums(const T* X, int V, float scale) {
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kLpbThreads) logprob_bwd_kernel(const LogprobBwdParams p) {
     pdl_launch_dependents();
-    pdl_wait();
     const int t = threadIdx.x, V = p.vocab;
-    for (int64_t b = blockIdx.x; b < p.total; b += gridDim.x) {
-        const int64_t row = b / p.tiles;
-        const int tile = (int)(b - row * p.tiles);
-        const T* const X = (const T*)p.logits + row * p.ld;
-        T* const D = (T*)p.dlogits + row * p.ldd;
-        const int64_t id = p.targets ? ld_id(p.targets, row, p.itype) : -1;
-        const bool there = id >= 0 && id < V;
-        const float lse = ld_p1(p.lse + row);
-        float g = p.dlogp && there ? ld_p1(p.dlogp + row) : 0.f;
-        float h = p.dentropy ? ld_p1(p.dentropy + row) : 0.f;
-        const float H = p.dentropy ? ld_p1(p.entropy + row) : 0.f;
-        // a row of -inf: no probability depends on a logit
-        if (lse == -INFINITY) g = h = 0.f;
-        const bool zero = g == 0.f && h == 0.f;
-        const float gs = g * p.scale, hs = h * p.scale;
-        const int head = VEC > 1 ? head_peel_t(X, V) : 0;
-        const int nv = (V - head) / VEC;
-        const int tail0 = head + nv * VEC;
-        auto grad = [&](float z, int64_t c) {   // z = log p_c
-            const float e = ex2(z * kLog2e);
-            const float u = fmaf(hs, fmaxf(z, -128.f) + H, gs);
-            const float d = -e * u;
-            return (c == id ? gs : 0.f) + d;
-        };
-        if (!zero && fabsf(lse) >= kLpbFar) {
-            if (tile == 0) {
-                const float2 ms = row_sums<T>(X, V, p.scale);
-                for (int c = t; c < V; c += kLpbThreads) {
-                    float v[1] = {grad((ldt_x1(X + c) - ms.x) * p.scale - ms.y, c)};
-                    st_elems<T, 1>(D + c, v);
-                }
-            }
-            continue;
-        }
-        const int64_t v0 = (int64_t)tile * (kLpbThreads * kLpbU) + t;
-        float x[kLpbU][VEC];
-        if (!zero) {
-#pragma unroll
-            for (int u = 0; u < kLpbU; ++u) {
-                const int64_t v = v0 + u * kLpbThreads;
-                if (v < nv) ld_elems<T, VEC>(x[u], X + head + v * VEC);
-            }
-        }
+    const uint32_t row = fast_quot(blockIdx.x, p.tiles);
+    const int tile = (int)(blockIdx.x - row * p.tiles.d);
+    const T* const X = (const T*)p.logits + row * p.ld;
+    T* const D = (T*)p.dlogits + row * p.ldd;
+    const int head = VEC > 1 ? head_peel_t(X, V) : 0;
+    const int nv = (V - head) / VEC;
+    const int tail0 = head + nv * VEC;
+    const int v0 = tile * (kLpbThreads * kLpbU) + t;
+    pdl_wait();
+    const int64_t id64 = p.targets ? ld_id(p.targets, row, p.itype) : -1;
+    const int id = id64 >= 0 && id64 < V ? (int)id64 : -1;
+    const float lse = ld_p1(p.lse + row);
+    float g = p.dlogp && id >= 0 ? ld_p1(p.dlogp + row) : 0.f;
+    float h = p.dentropy ? ld_p1(p.dentropy + row) : 0.f;
+    const float H = p.dentropy ? ld_p1(p.entropy + row) : 0.f;
+    // a row of -inf: no probability depends on a logit
+    if (lse == -INFINITY) g = h = 0.f;
+    if (g == 0.f && h == 0.f) {
+        const Raw<VEC * (int)sizeof(T)> z = {};
 #pragma unroll
         for (int u = 0; u < kLpbU; ++u) {
-            const int64_t v = v0 + u * kLpbThreads;
-            if (v < nv) {
-                const int64_t c = head + v * VEC;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    x[u][i] = zero ? 0.f : grad(fmaf(x[u][i], p.scale, -lse), c + i);
-                st_elems<T, VEC>(D + c, x[u]);
+            const int v = v0 + u * kLpbThreads;
+            if (v < nv) st_raw(D + head + (int64_t)v * VEC, z);
+        }
+        if (tile == 0 && t < head + (V - tail0)) {
+            const float o[1] = {0.f};
+            st_elems<T, 1>(D + (t < head ? t : tail0 + t - head), o);
+        }
+        return;
+    }
+    // dlogit = e^z (a + b z) with z = log p, and gs more for the target
+    const float gs = g * p.scale, b = -h * p.scale, a = fmaf(b, H, -gs);
+    auto grad = [&](float z, int c) {
+        return ex2(z * kLog2e) * fmaf(b, fmaxf(z, -128.f), a) + (c == id ? gs : 0.f);
+    };
+    if (fabsf(lse) >= kLpbFar) {
+        if (tile == 0) {
+            const float2 ms = row_sums<T>(X, V, p.scale);
+            for (int c = t; c < V; c += kLpbThreads) {
+                const float o[1] = {grad((ldt_x1(X + c) - ms.x) * p.scale - ms.y, c)};
+                st_elems<T, 1>(D + c, o);
             }
         }
-        // the row's head and tail, by its first tile
-        if (tile == 0 && t < head + (V - tail0)) {
-            const int c = t < head ? t : tail0 + t - head;
-            float v[1] = {zero ? 0.f : grad(fmaf(ldt_x1(X + c), p.scale, -lse), c)};
-            st_elems<T, 1>(D + c, v);
+        return;
+    }
+    Raw<VEC * (int)sizeof(T)> r[kLpbU];
+#pragma unroll
+    for (int u = 0; u < kLpbU; ++u) {
+        const int v = v0 + u * kLpbThreads;
+        if (v < nv) r[u] = ld_raw<VEC * (int)sizeof(T)>(X + head + (int64_t)v * VEC);
+    }
+#pragma unroll
+    for (int u = 0; u < kLpbU; ++u) {
+        const int v = v0 + u * kLpbThreads;
+        if (v < nv) {
+            const int c = head + v * VEC;
+            float x[VEC];
+            unpack<T, VEC>(x, r[u]);
+            if constexpr (VEC == 1) {
+                x[0] = grad(fmaf(x[0], p.scale, -lse), c);
+            } else {
+                const F2 s2 = f2s(p.scale), l2 = f2s(-lse), k2 = f2s(kLog2e);
+                const F2 a2 = f2s(a), b2 = f2s(b);
+#pragma unroll
+                for (int i = 0; i < VEC; i += 2) {
+                    F2 z = fma2(f2(x[i], x[i + 1]), s2, l2);
+                    float z0, z1;
+                    f2_get(mul2(z, k2), z0, z1);
+                    const F2 e = f2(ex2(z0), ex2(z1));
+                    F2 q = a2;
+                    if (b != 0.f) {   // the row's, so the CTA's
+                        f2_get(z, z0, z1);
+                        q = fma2(b2, f2(fmaxf(z0, -128.f), fmaxf(z1, -128.f)), a2);
+                    }
+                    f2_get(mul2(e, q), x[i], x[i + 1]);
+                }
+                if ((unsigned)(id - c) < (unsigned)VEC) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) x[i] += c + i == id ? gs : 0.f;
+                }
+            }
+            st_elems<T, VEC>(D + c, x);
         }
     }
+    // the row's head and tail, by its first tile
+    if (tile == 0 && t < head + (V - tail0)) {
+        const int c = t < head ? t : tail0 + t - head;
+        const float o[1] = {grad(fmaf(ldt_x1(X + c), p.scale, -lse), c)};
+        st_elems<T, 1>(D + c, o);
+    }
+}
+
+static int64_t logprob_bwd_tiles(int vocab, int vec) {
+    const int64_t nv = ((int64_t)vocab + vec - 1) / vec, per = kLpbThreads * kLpbU;
+    return (nv + per - 1) / per;
 }
 
 template <typename T, int VEC>
 static cudaError_t logprob_bwd_go(const LogprobBwdParams& q, cudaStream_t s) {
     LogprobBwdParams p = q;
-    const int64_t nv = ((int64_t)p.vocab + VEC - 1) / VEC, per = kLpbThreads * kLpbU;
-    p.tiles = (nv + per - 1) / per;
-    p.total = p.rows * p.tiles;
-    const int64_t grid = p.total < (1 << 30) ? p.total : (1 << 30);
-    return launch_pdl(logprob_bwd_kernel<T, VEC>, (unsigned)grid, kLpbThreads, 0, s, p);
+    const int64_t tiles = logprob_bwd_tiles(p.vocab, VEC);
+    // (a matrix of that many tiles would not fit any memory)
+    if (p.rows * tiles > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    p.tiles = fast_div((uint32_t)tiles);
+    return launch_pdl(logprob_bwd_kernel<T, VEC>, (unsigned)(p.rows * tiles), kLpbThreads, 0, s, p);
 }
 
 cudaError_t logprob_bwd_launch(int dtype, bool vec, const LogprobBwdParams& p, cudaStream_t s) {

@@ -1,27 +1,40 @@
 // rn_logprob.cuh -- log probabilities over rows of logits.
 //
-// With x_j = scale * logit_j, m = max_j x_j, z_j = x_j - m, S = sum_j e^{z_j}
-// and W = sum_j e^{z_j} z_j:
-//     lse = m + log S,   log p_t = x_t - lse,   H = log S - W / S
-// (both terms of H are >= 0: nothing cancels). One pass: every thread keeps
-// its own running (m, S, W) over the batches of 16 or 32 elements it reads. A
-// batch that raises m from m0 to m1 rescales, with r = m0 - m1 <= 0,
+// With x_j = scale * logit_j and any reference c,
+//     S = sum_j e^{x_j - c},  W = sum_j e^{x_j - c} (x_j - c):
+//     lse = c + log S,   log p_t = (x_t - c) - log S,   H = log S - W / S.
+// One pass: every thread keeps a running (c, S, W) over the batches of 16 or 32
+// elements it reads, c near the largest element it has seen (both terms of H are
+// then >= 0 and nothing cancels). A batch that raises c from c0 to c1 rescales,
+// with r = c0 - c1 <= 0,
 //     S <- S e^r,  W <- e^r (W + r S).
-// Exponents are kept in units of log 2 (one instruction an exponential), and W
-// with them. A masked element (-inf) gives e = 0 and 0 * -inf = NaN in W: a
-// batch whose W comes out NaN is summed again with that product left out, so
-// that rows without a mask do not pay for the test.
+// Exponents are kept in units of log 2: z = logit * (scale * log2 e) - c is one
+// fused multiply-add, whose constant c need not equal the largest element's product
+// exactly (it is a reference, and the same in every term), and e^z one
+// special-function instruction. Pairs of elements go through the packed FP32
+// pipe: 4 instructions a pair beside the two exponentials, so that the pass
+// stays below the time its bytes take even for 16-bit logits.
+//
+// A masked element (-inf) gives e = 0 and 0 * -inf = NaN in W: a batch whose W
+// comes out NaN is summed again with that product left out, so that rows without a
+// mask do not pay for the test. A row whose largest product is beyond 1e30
+// (every column at a mask's lowest value, say) cannot be referred to c in FP32: it is
+// summed again, from differences of logits (row_again).
+//
+// A row is split over the CTAs of a cluster where there are few rows; the
+// CTAs' results meet in the first one's shared memory.
 //
 // Alternatives: the `top` largest logits, the lowest index first among equal
 // ones, found in the same pass. A candidate is a 64-bit key: the value's bits in
 // an order-preserving form above the complement of its index, so that keys
-// differ and compare as wanted. The CTA holds up to kTopCap candidates and the
-// key `thr` that a new one has to exceed. In the first batch the threshold comes
-// from the maxima of 64 groups of threads: at least `top` elements reach the
-// top-th largest of them. When the buffer is full the `top` best of it are
-// kept, thr becomes the least of them, and the threads that still hold
-// candidates of the batch go on. Which slot a candidate takes depends on the
-// order of atomics; which keys are kept does not.
+// differ and compare as wanted. Each warp keeps up to kTopCap candidates in shared
+// memory, and a new one has to exceed the threshold `thr`, below which the row's `top`
+// best cannot lie: first the top-th largest of the maxima of 64 groups of threads
+// over the first batch (at least `top` elements reach it), then the top-th of any
+// warp that has filled its buffer and kept its `top` best. Past the first batch
+// a candidate is rare (about `top` for each doubling of the columns read), so that a
+// thread compares its batch's maximum, which it has anyway, and no more. The order
+// in which warps run changes which keys are tried, not which are kept.
 #pragma once
 
 #include <type_traits>
@@ -30,11 +43,17 @@
 
 namespace rn {
 
-constexpr int kTopCap = 512;
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpU = 4;              // vectors a thread holds of a batch (masked_w: 4)
+constexpr int kLpMaxCluster = 16;
+constexpr int kTopCap = 96;          // candidates of a warp: at least 2 * 32
 constexpr int kTopGroups = 64;
+constexpr float kFar = 1e30f;
+static_assert(kMaxTop + 32 <= kTopCap, "a kept list and one round of lanes");
 
-// Bits of x in an order that compares as unsigned integers do: -inf lowest, both zeros
-// equal, any NaN highest.
+// Bits of x in an order that compares as unsigned integers do: -inf lowest, both
+// zeros equal, any NaN highest.
 __device__ __forceinline__ uint32_t order_bits(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
     if (x != x) return 0xffffffffu;
@@ -48,292 +67,523 @@ __device__ __forceinline__ unsigned long long top_key(float x, uint32_t idx) {
     return ((unsigned long long)order_bits(x) << 32) | (uint32_t)~idx;
 }
 
-// Running (m, S, W) of one thread; k = scale * log2(e).
+// The largest of the N elements held in raw vectors of T (NaN left out). 16-bit
+// elements are compared in pairs before they are widened.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __nv_bfloat16*) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, __half*) {
+    const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a),
+                              *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+template <typename T>
+__device__ __forceinline__ float raw_max(const Raw<16>* r) {
+    if constexpr (sizeof(T) == 4) {
+        float m = __uint_as_float(r[0].w[0]);
+#pragma unroll
+        for (int u = 0; u < kLpU; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = fmaxf(m, __uint_as_float(r[u].w[i]));
+        return m;
+    } else {
+        uint32_t m = r[0].w[0];
+#pragma unroll
+        for (int u = 0; u < kLpU; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max2(m, r[u].w[i], (T*)nullptr);
+        float a, b;
+        unpack2(m, a, b, (T*)nullptr);
+        return fmaxf(a, b);
+    }
+}
+// Pair i, and element i, of the raw vectors.
+template <typename T>
+__device__ __forceinline__ F2 raw_pair(const Raw<16>* r, int i) {
+    if constexpr (sizeof(T) == 4) {
+        return f2(__uint_as_float(r[i / 2].w[i % 2 * 2]), __uint_as_float(r[i / 2].w[i % 2 * 2 + 1]));
+    } else {
+        float a, b;
+        unpack2(r[i / 4].w[i % 4], a, b, (T*)nullptr);
+        return f2(a, b);
+    }
+}
+template <typename T>
+__device__ __forceinline__ float raw_elem(const Raw<16>* r, int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i / 4].w[i % 4]);
+    else return half_to_f((uint16_t)(r[i / 8].w[i % 8 / 2] >> (i % 2 * 16)), (T*)nullptr);
+}
+template <typename T>
+constexpr uint32_t raw_low() {   // -inf in every element
+    return sizeof(T) == 4 ? 0xff800000u
+                          : (std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u);
+}
+
+// W of a batch that holds -inf: its products are left out. Not inlined, so that it
+// takes no registers of the pass.
+template <typename T>
+__device__ __noinline__ float masked_w(Raw<16> a, Raw<16> b, Raw<16> c, Raw<16> d, float k,
+                                       float ref) {
+    const Raw<16> r[kLpU] = {a, b, c, d};
+    float w = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLpU * Elem<T>::kVec; ++i) {
+        const float z = fmaf(raw_elem<T>(r, i), k, -ref), e = ex2(z);
+        if (e != 0.f) w = fmaf(e, z, w);
+    }
+    return w;
+}
+
+// Running (c, S, W) with the largest logit m; k = scale * log2(e).
 template <bool ENT>
 struct Soft {
-    float m, s, w;   // m: raw logit
+    float m, c, s, w;
     __device__ __forceinline__ void init() {
         m = -INFINITY;
+        c = -kFar;     // finite, so that -inf - c is -inf and no NaN arises
         s = 0.f;
         w = 0.f;
     }
-    // the reference of the exponents: m, or 0 while nothing above -inf was seen
-    static __device__ __forceinline__ float ref(float m) { return m == -INFINITY ? 0.f : m; }
-    __device__ __forceinline__ void raise(float m1, float k) {
-        const float r = m == -INFINITY ? 0.f : (m - m1) * k;   // S is 0 then
-        const float f = ex2(r);
-        // (r may be -inf where f is 0)
-        if constexpr (ENT) w = f == 0.f ? 0.f : f * fmaf(r, s, w);
+    __device__ __forceinline__ void rescale(float c1) {
+        const float r = c - c1, f = ex2(r);
+        if constexpr (ENT) w = f * fmaf(r, s, w);
         s *= f;
-        m = m1;
+        c = c1;
     }
-    template <int N>
-    __device__ __forceinline__ void add(const float* x, float k) {
-        float mx = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) mx = fmaxf(mx, x[i]);
-        if (mx > m) raise(mx, k);
-        const float c = ref(m);
-        float sb = 0.f, wb = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float z = (x[i] - c) * k;
-            const float e = ex2(z);
-            sb += e;
-            if constexpr (ENT) wb = fmaf(e, z, wb);
+    __device__ __forceinline__ void reach(float mx, float k) {
+        if (mx > m) {
+            m = mx;
+            rescale(fminf(fmaxf(mx * k, -kFar), kFar));
         }
-        if constexpr (ENT) {
-            if (wb != wb) {
-                wb = 0.f;
+    }
+    // one element
+    __device__ __forceinline__ void add(float x, float k) {
+        reach(x, k);
+        const float z = fmaf(x, k, -c), e = ex2(z);
+        s += e;
+        if constexpr (ENT) w += e != 0.f ? e * z : 0.f;
+    }
+    // a batch of raw vectors of T whose maximum is mx
+    template <typename T>
+    __device__ __forceinline__ void add(const Raw<16>* r, float mx, float k) {
+        constexpr int NP = kLpU * Elem<T>::kVec / 2;
+        reach(mx, k);
+        F2 s2 = f2s(0.f), w2 = f2s(0.f);
+        const F2 k2 = f2s(k), c2 = f2s(-c);
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float z = (x[i] - c) * k;
-                    const float e = ex2(z);
-                    if (e != 0.f) wb = fmaf(e, z, wb);
-                }
-            }
+        for (int i = 0; i < NP; ++i) {
+            const F2 z = fma2(raw_pair<T>(r, i), k2, c2);
+            float z0, z1;
+            f2_get(z, z0, z1);
+            const F2 e = f2(ex2(z0), ex2(z1));
+            s2 = add2(s2, e);
+            if constexpr (ENT) w2 = fma2(e, z, w2);
+        }
+        float a, b;
+        f2_get(s2, a, b);
+        s += a + b;
+        if constexpr (ENT) {
+            f2_get(w2, a, b);
+            float wb = a + b;
+            if (wb != wb) wb = masked_w<T>(r[0], r[1], r[2], r[3], k, c);
             w += wb;
         }
-        s += sb;
     }
-    __device__ __forceinline__ void merge(float m2, float s2, float w2, float k) {
-        const float m1 = fmaxf(m, m2);
-        const float r1 = m == -INFINITY ? 0.f : (m - m1) * k;
-        const float r2 = m2 == -INFINITY ? 0.f : (m2 - m1) * k;
-        const float f1 = ex2(r1), f2 = ex2(r2);
-        if constexpr (ENT) {
-            // (r is -inf only where f is 0; S is finite there)
-            const float a = f1 == 0.f ? 0.f : f1 * fmaf(r1, s, w);
-            const float b = f2 == 0.f ? 0.f : f2 * fmaf(r2, s2, w2);
-            w = a + b;
-        }
+    __device__ __forceinline__ void merge(float m2, float c2, float s2, float w2) {
+        m = fmaxf(m, m2);
+        const float c1 = fmaxf(c, c2);
+        const float r1 = c - c1, r2 = c2 - c1, f1 = ex2(r1), f2 = ex2(r2);
+        if constexpr (ENT) w = f1 * fmaf(r1, s, w) + f2 * fmaf(r2, s2, w2);
         s = f1 * s + f2 * s2;
-        m = m1;
+        c = c1;
     }
 };
 
-// Shared state of a row's candidates.
+// Candidates of a CTA.
 struct TopState {
-    unsigned long long cand[kTopCap];
-    unsigned long long best[kMaxTop];
+    unsigned long long cand[kLpWarps][kTopCap];
+    unsigned long long best[kLpWarps * kMaxTop];
+    unsigned long long merged[kMaxTop];
     unsigned long long thr;
     float group[kTopGroups];
-    int count;
+    int count[kLpWarps];
 };
 
-// The `top` largest of st.cand[0..n), largest first, into st.best (fewer if n is
-// less). A key's place is the number of larger keys. All threads; ends without a barrier.
-template <int NT>
-__device__ __forceinline__ void top_rank(TopState& st, int n, int top) {
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const unsigned long long me = st.cand[i];
-        int r = 0;
-        for (int j = 0; j < n; ++j) r += st.cand[j] > me;
-        if (r < top) st.best[r] = me;
+// This warp's `top` best of its n candidates, to the front of its buffer, largest
+// first; returns how many. A key's place is the number of larger keys.
+__device__ __forceinline__ int warp_keep(unsigned long long* cand, int n, int top, int lane) {
+    constexpr int R = kTopCap / 32;
+    unsigned long long me[R];
+    int place[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        me[r] = r * 32 + lane < n ? cand[r * 32 + lane] : 0;
+        place[r] = 0;
     }
+    for (int j = 0; j < n; ++j) {
+        const unsigned long long o = cand[j];
+#pragma unroll
+        for (int r = 0; r < R; ++r) place[r] += o > me[r];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r * 32 + lane < n && place[r] < top) cand[place[r]] = me[r];
+    __syncwarp();
+    return n < top ? n : top;
 }
 
-// A full buffer: keep the best, raise the threshold. All threads; ends with a barrier.
-template <int NT>
-__device__ __forceinline__ void top_compact(TopState& st, int top) {
-    top_rank<NT>(st, kTopCap, top);
+// The values of a row that FP32 products cannot be referred to (see above), from
+// differences of logits: (m, log S, W / S in units of log 2). All threads.
+template <typename T>
+__device__ void row_again(const T* X, int V, float k, float m, float (*red)[4], float* ls,
+                          float* ws) {
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+    float s = 0.f, q = 0.f;
+    for (int i = t; i < V; i += kLpThreads) {
+        const float z = (ldt_x1(X + i) - m) * k, e = ex2(z);
+        s += e;
+        if (e != 0.f) q = fmaf(e, z, q);
+    }
+    s = warp_sum(s);
+    q = warp_sum(q);
     __syncthreads();
-    if (threadIdx.x < (unsigned)top) st.cand[threadIdx.x] = st.best[threadIdx.x];
-    if (threadIdx.x == 0) {
-        st.count = top;
-        st.thr = st.best[top - 1];
+    if (lane == 0) {
+        red[w][0] = s;
+        red[w][1] = q;
     }
     __syncthreads();
+    s = q = 0.f;
+    for (int i = 0; i < kLpWarps; ++i) {
+        s += red[i][0];
+        q += red[i][1];
+    }
+    *ls = logf(s);
+    *ws = q / s;
 }
 
-template <typename T, int NT, int VEC, bool ENT, bool TOP>
-__global__ void __launch_bounds__(NT) logprob_fwd_kernel(const LogprobParams p) {
-    constexpr int U = 4;              // vectors a thread holds of a batch
-    constexpr int NB = U * VEC;       // elements, at most 32
-    constexpr int NW = NT / 32;
-    __shared__ float red[NW][3];
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                 ::: "memory");
+}
+// The address of this CTA's shared variable in the CTA of rank r of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t r) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(a)
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(r));
+    return a;
+}
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ unsigned long long peer_u64(uint32_t a) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a));
+    return v;
+}
+
+template <typename T, bool ENT, bool TOP>
+__global__ void __launch_bounds__(kLpThreads, 2) logprob_fwd_kernel(const LogprobParams p) {
+    constexpr int VEC = Elem<T>::kVec;
+    constexpr int NB = kLpU * VEC;    // elements of a batch, at most 32
+    __shared__ float red[kLpWarps][4];
+    __shared__ __align__(8) float part[4];
     __shared__ TopState st;
     pdl_launch_dependents();
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     const float k = p.scale * kLog2e;
     const int V = p.vocab;
+    const int64_t row = blockIdx.x / (unsigned)p.split;
+    const int rank = (int)(blockIdx.x - (unsigned)row * p.split);
+    // this CTA's share of the row: vectors [va, vb), and the first also the
+    // elements before the first 16-byte boundary and after the last vector
+    const T* const X = (const T*)p.logits + row * p.ld;
+    const int head = head_peel_t(X, V);
+    const int nv = (V - head) / VEC;
+    const int tail0 = head + nv * VEC;
+    const int share = (nv + p.split - 1) / p.split;
+    const int va = min(nv, rank * share), vb = min(nv, va + share);
+    const T* const XV = X + head;
+    const int extra = rank == 0 ? head + (V - tail0) : 0;
+    Soft<ENT> a;
+    a.init();
+    int cnt = 0;                       // this warp's candidates
+    if constexpr (TOP) {
+        if (t == 0) st.thr = 0;
+    }
+    bool first = true;
     pdl_wait();
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const T* const X = (const T*)p.logits + row * p.ld;
-        // elements before the first 16-byte boundary, and after the last vector
-        const int head = VEC > 1 ? head_peel_t(X, V) : 0;
-        const int nv = (V - head) / VEC;
-        const int tail0 = head + nv * VEC;
-        Soft<ENT> a;
-        a.init();
-        if constexpr (TOP) {
-            if (t == 0) {
-                st.thr = 0;
-                st.count = 0;
+    // Candidates among the N elements of a batch whose maximum is mx. Elements of
+    // the same value as the threshold may be wanted (the lowest index first), and
+    // a NaN always is.
+    auto look = [&](auto elem, float mx, bool odd, auto col, auto in, auto n_const) {
+        constexpr int N = decltype(n_const)::value;
+        if (first) {
+            first = false;
+            constexpr int G = kLpThreads / kTopGroups;
+            float g = mx;
+#pragma unroll
+            for (int o = 1; o < G; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+            if (t % G == 0) st.group[t / G] = g;
+            __syncthreads();
+            if (t < kTopGroups) {
+                const float me = st.group[t];
+                int r = 0;
+                for (int j = 0; j < kTopGroups; ++j)
+                    r += st.group[j] > me || (st.group[j] == me && j < t);
+                // (a key without an index: every element of this value is above it)
+                if (r == p.top - 1 && me > -INFINITY)
+                    st.thr = (unsigned long long)order_bits(me) << 32;
             }
             __syncthreads();
         }
-        bool first = true;
-        // one batch: x[i] at column col(i), `have` of them
-        auto batch = [&](const float* x, auto col, auto in, auto n_const) {
-            constexpr int N = decltype(n_const)::value;
-            a.template add<N>(x, k);
-            if constexpr (TOP) {
-                if (first) {
-                    // the top-th largest of the maxima of 64 groups of threads
-                    constexpr int G = NT / kTopGroups;
-                    float mx = x[0];
+        unsigned long long thr = *(volatile unsigned long long*)&st.thr;
+        const float lo = order_value((uint32_t)(thr >> 32));   // NaN: no threshold yet
+        uint32_t pend = 0;
+        if (!(mx < lo) || odd) {
 #pragma unroll
-                    for (int i = 1; i < N; ++i) mx = fmaxf(mx, x[i]);
-#pragma unroll
-                    for (int o = 1; o < G; o <<= 1)
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    if (t % G == 0) st.group[t / G] = mx;
-                    __syncthreads();
-                    if (t < kTopGroups) {
-                        const float me = st.group[t];
-                        int r = 0;
-                        for (int j = 0; j < kTopGroups; ++j)
-                            r += st.group[j] > me || (st.group[j] == me && j < t);
-                        // (every element at this value is above a key without an index)
-                        if (r == p.top - 1 && me > -INFINITY)
-                            st.thr = (unsigned long long)order_bits(me) << 32;
-                    }
-                    __syncthreads();
-                    first = false;
-                }
-                const float lo = order_value((uint32_t)(st.thr >> 32));
-                const bool any = st.thr == 0;
-                uint32_t pend = 0;
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (in(i) && (any || !(x[i] < lo))) pend |= 1u << i;
-                while (true) {
-                    const unsigned long long thr = st.thr;
-                    if (pend) {
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            if ((pend >> i & 1u) && top_key(x[i], col(i)) <= thr)
-                                pend &= ~(1u << i);
-                        const int n = __popc(pend);
-                        int at = n ? atomicAdd(&st.count, n) : kTopCap;
-#pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            if (pend >> i & 1u) {
-                                if (at < kTopCap) {
-                                    st.cand[at] = top_key(x[i], col(i));
-                                    pend &= ~(1u << i);
-                                }
-                                ++at;
-                            }
-                    }
-                    if (!__syncthreads_or(pend != 0)) break;
-                    top_compact<NT>(st, p.top);
+            for (int i = 0; i < N; ++i)
+                if (in(i) && !(elem(i) < lo)) pend |= 1u << i;
+        }
+        unsigned lanes = __ballot_sync(0xffffffffu, pend != 0);
+        while (lanes) {
+            // one candidate of every lane that has any
+            if (cnt + 32 > kTopCap) {
+                cnt = warp_keep(st.cand[w], cnt, p.top, lane);
+                if (cnt == p.top) {
+                    thr = st.cand[w][p.top - 1];
+                    if (lane == 0) atomicMax(&st.thr, thr);
                 }
             }
-        };
-        using One = std::integral_constant<int, 1>;
-        using All = std::integral_constant<int, NB>;
-        const int step = NT * U;
-        for (int v0 = 0; v0 < nv; v0 += step) {
-            float x[NB];
+            unsigned long long key = 0;
+            if (pend) {
+                const int i = __ffs(pend) - 1;
+                pend &= pend - 1;
+                float v = elem(0);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int v = v0 + u * NT + t;
-                if (v < nv) {
-                    ld_elems<T, VEC>(x + u * VEC, X + head + (int64_t)v * VEC);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) x[u * VEC + i] = -INFINITY;
-                }
+                for (int q = 1; q < N; ++q) v = q == i ? elem(q) : v;
+                key = top_key(v, col(i));
             }
-            batch(
-                x, [&](int i) { return (uint32_t)(head + (v0 + i / VEC * NT + t) * VEC + i % VEC); },
-                [&](int i) { return v0 + i / VEC * NT + t < nv; }, All{});
+            const bool put = key > thr;
+            const unsigned who = __ballot_sync(0xffffffffu, put);
+            if (put) st.cand[w][cnt + __popc(who & ((1u << lane) - 1))] = key;
+            cnt += __popc(who);
+            __syncwarp();
+            lanes = __ballot_sync(0xffffffffu, pend != 0);
         }
-        // head and tail: fewer than 2 * VEC elements, one a thread
-        if (head + (V - tail0) > 0) {
-            const bool in = t < head + (V - tail0);
-            const int c = t < head ? t : tail0 + t - head;
-            float x = -INFINITY;
-            if (in) x = ldt_x1(X + c);
-            batch(&x, [&](int) { return (uint32_t)c; }, [&](int) { return in; }, One{});
-        }
-        // meet
+    };
+    using One = std::integral_constant<int, 1>;
+    using All = std::integral_constant<int, NB>;
+    if constexpr (TOP) __syncthreads();   // thr is set
+    for (int v0 = va; v0 < vb; v0 += kLpThreads * kLpU) {
+        Raw<16> r[kLpU];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, a.m, o);
-            const float s2 = __shfl_xor_sync(0xffffffffu, a.s, o);
-            const float w2 = __shfl_xor_sync(0xffffffffu, a.w, o);
-            a.merge(m2, s2, w2, k);
+        for (int u = 0; u < kLpU; ++u) {
+            const int v = v0 + u * kLpThreads + t;
+            if (v < vb) {
+                r[u] = ld_raw<16>(XV + (int64_t)v * VEC);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[u].w[i] = raw_low<T>();
+            }
         }
-        if (lane == 0) {
-            red[w][0] = a.m;
-            red[w][1] = a.s;
-            red[w][2] = a.w;
+        const float mx = raw_max<T>(r);
+        a.template add<T>(r, mx, k);
+        if constexpr (TOP)
+            look(
+                [&](int i) { return raw_elem<T>(r, i); }, mx, a.s != a.s,
+                [&](int i) {
+                    return (uint32_t)(head + (v0 + i / VEC * kLpThreads + t) * VEC + i % VEC);
+                },
+                [&](int i) { return v0 + i / VEC * kLpThreads + t < vb; }, All{});
+    }
+    // head and tail: fewer than 2 * VEC elements, one a thread
+    if (extra > 0) {
+        const bool in = t < extra;
+        const int c = t < head ? t : tail0 + t - head;
+        float x = -INFINITY;
+        if (in) x = ldt_x1(X + c);
+        a.add(x, k);
+        if constexpr (TOP)
+            look(
+                [&](int) { return x; }, x, a.s != a.s, [&](int) { return (uint32_t)c; }, [&](int) { return in; },
+                One{});
+    }
+    // meet: lanes, warps, the CTAs of the cluster
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, a.m, o);
+        const float c2 = __shfl_xor_sync(0xffffffffu, a.c, o);
+        const float s2 = __shfl_xor_sync(0xffffffffu, a.s, o);
+        const float w2 = __shfl_xor_sync(0xffffffffu, a.w, o);
+        a.merge(m2, c2, s2, w2);
+    }
+    if (lane == 0) {
+        red[w][0] = a.m;
+        red[w][1] = a.c;
+        red[w][2] = a.s;
+        red[w][3] = a.w;
+    }
+    if constexpr (TOP) {
+        cnt = warp_keep(st.cand[w], cnt, p.top, lane);
+        if (lane == 0) st.count[w] = cnt;
+    }
+    __syncthreads();
+    a.init();
+#pragma unroll
+    for (int i = 0; i < kLpWarps; ++i) a.merge(red[i][0], red[i][1], red[i][2], red[i][3]);
+    int total = 0;                        // the CTA's kept candidates, after each other in best
+    if constexpr (TOP) {
+        int before = 0;
+        for (int i = 0; i < kLpWarps; ++i) {
+            before += i < w ? st.count[i] : 0;
+            total += st.count[i];
         }
+        if (lane < cnt) st.best[before + lane] = st.cand[w][lane];
+    }
+    // the CTA's `top` best of `total`, into merged
+    auto merge_top = [&]() {
+        for (int i = t; i < total; i += kLpThreads) {
+            const unsigned long long me = st.best[i];
+            int r = 0;
+            for (int j = 0; j < total; ++j) r += st.best[j] > me;
+            if (r < p.top) st.merged[r] = me;
+        }
+        if (t >= total && t < p.top) st.merged[t] = 0;
+    };
+    if constexpr (TOP) {
         __syncthreads();
-        a.init();
-        for (int i = 0; i < NW; ++i) a.merge(red[i][0], red[i][1], red[i][2], k);
-        const bool none = a.m == -INFINITY && a.s == 0.f;   // every logit is -inf
-        const float ls = logf(a.s);
-        const float mx = a.m * p.scale;
-        // a row with a NaN or a +inf has none of its values
-        const float lse = a.s != a.s ? a.s : none ? -INFINITY : mx + ls;
+        merge_top();
+        __syncthreads();
+    }
+    if (p.split > 1) {
         if (t == 0) {
-            if (p.lse) p.lse[row] = lse;
-            if (ENT && p.entropy)
-                p.entropy[row] = a.s != a.s ? a.s : none ? 0.f : ls - a.w / a.s * kLn2;
-            if (p.logp) {
-                const int64_t id = ld_id(p.targets, row, p.itype);
-                float lp = 0.f;
-                if (id >= 0 && id < V) {
-                    const float x = ldt_x1(X + id);
-                    lp = lse != lse ? lse : none ? -INFINITY : (x - a.m) * p.scale - ls;
+            part[0] = a.m;
+            part[1] = a.c;
+            part[2] = a.s;
+            part[3] = a.w;
+        }
+        cluster_sync();
+        if (rank == 0) {
+            for (int q = 1; q < p.split; ++q) {
+                const uint32_t at = peer_addr(part, q);
+                a.merge(peer_f32(at), peer_f32(at + 4), peer_f32(at + 8), peer_f32(at + 12));
+            }
+            if constexpr (TOP) {
+                // (a CTA with fewer than `top` columns leaves keys of 0)
+                total = p.split * p.top;
+                for (int i = t; i < total; i += kLpThreads) {
+                    const int q = i / p.top, j = i - q * p.top;
+                    st.best[i] = q == 0 ? st.merged[j] : peer_u64(peer_addr(&st.merged[j], q));
                 }
-                p.logp[row] = lp;
             }
         }
+        cluster_sync();   // the peers' shared memory has been read
+        if (rank != 0) return;
         if constexpr (TOP) {
-            const int n = min(st.count, kTopCap);
-            top_rank<NT>(st, n, p.top);
             __syncthreads();
-            if (t < p.top) {
-                const unsigned long long key = st.best[t];
-                const uint32_t idx = ~(uint32_t)key;
-                if (p.top_ids) {
-                    if (p.itype == IT_I64)
-                        ((int64_t*)p.top_ids)[row * p.top + t] = idx;
-                    else
-                        ((int32_t*)p.top_ids)[row * p.top + t] = (int32_t)idx;
-                }
-                if (p.top_logp) {
-                    const float x = order_value((uint32_t)(key >> 32));
-                    p.top_logp[row * p.top + t] =
-                        lse != lse ? lse : x == -INFINITY ? x : (x - a.m) * p.scale - ls;
-                }
-            }
+            merge_top();
+            __syncthreads();
         }
-        __syncthreads();   // the next row reuses the shared state
+    }
+    const bool nan = a.s != a.s;
+    const bool none = a.m == -INFINITY && !nan;     // every logit is -inf
+    float ref = a.c * kLn2, ls = logf(a.s), ws = a.w / a.s;
+    const bool far = !nan && !none && !(fabsf(a.m * k) < kFar) && fabsf(a.m) < INFINITY;
+    if (far) {
+        row_again<T>(X, V, k, a.m, red, &ls, &ws);
+        ref = a.m * p.scale;
+    }
+    // log p of a logit
+    auto logp = [&](float x) {
+        if (nan || a.m == INFINITY) return __uint_as_float(0x7fffffffu);
+        if (none || x == -INFINITY) return -INFINITY;
+        if (far) return (x - a.m) * p.scale - ls;
+        // (a mask's lowest value, times k, may be beyond FP32's range)
+        return (fabsf(x * k) < kFar ? fmaf(x, k, -a.c) * kLn2 : x * p.scale - ref) - ls;
+    };
+    if (t == 0) {
+        const float bad = __uint_as_float(0x7fffffffu);
+        const bool spoilt = nan || a.m == INFINITY;
+        if (p.lse) p.lse[row] = spoilt ? bad : none ? -INFINITY : ref + ls;
+        if (ENT) p.entropy[row] = spoilt ? bad : none ? 0.f : ls - ws * kLn2;
+        if (p.logp) {
+            const int64_t id = ld_id(p.targets, row, p.itype);
+            p.logp[row] = id >= 0 && id < V ? logp(ldt_x1(X + id)) : 0.f;
+        }
+    }
+    if constexpr (TOP) {
+        if (t < p.top) {
+            const unsigned long long key = st.merged[t];
+            const uint32_t idx = ~(uint32_t)key;
+            if (p.top_ids) {
+                if (p.itype == IT_I64)
+                    ((int64_t*)p.top_ids)[row * p.top + t] = idx;
+                else
+                    ((int32_t*)p.top_ids)[row * p.top + t] = (int32_t)idx;
+            }
+            if (p.top_logp) p.top_logp[row * p.top + t] = logp(order_value((uint32_t)(key >> 32)));
+        }
     }
 }
 
-template <typename T, int VEC, bool ENT, bool TOP>
-static cudaError_t logprob_fwd_go(const LogprobParams& p, cudaStream_t s) {
-    constexpr int NT = 512;
-    const int64_t grid = p.rows < (1 << 30) ? p.rows : (1 << 30);
-    return launch_pdl(logprob_fwd_kernel<T, NT, VEC, ENT, TOP>, (unsigned)grid, NT, 0, s, p);
+// CTAs a row is split over: as many as keep every SM at its two resident CTAs, while
+// each still has a whole batch of its threads to read.
+inline int logprob_split(int64_t rows, int vocab, int vec, int sms) {
+    const int64_t batches = (vocab / vec + kLpThreads * kLpU - 1) / (kLpThreads * kLpU);
+    int c = 1;
+    while (c < kLpMaxCluster && rows * c * 2 <= 2 * (int64_t)sms && c * 2 <= batches) c *= 2;
+    return c;
+}
+
+template <typename T, bool ENT, bool TOP>
+static cudaError_t logprob_fwd_go(const LogprobParams& q, cudaStream_t s) {
+    LogprobParams p = q;
+    auto* kernel = logprob_fwd_kernel<T, ENT, TOP>;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    p.split = logprob_split(p.rows, p.vocab, Elem<T>::kVec, sms);
+    if (p.split > 8) {
+        // clusters of more than 8 CTAs have to be asked for (a setting of the function, and
+        // of the context that is current: made every time)
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess) return err;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.rows * p.split), 1, 1);
+    cfg.blockDim = dim3(kLpThreads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <typename T>
 cudaError_t logprob_fwd_t(const LogprobParams& p, cudaStream_t s) {
-    constexpr int VEC = Elem<T>::kVec;
     const bool ent = p.entropy != nullptr;
     if (p.top > 0)
-        return ent ? logprob_fwd_go<T, VEC, true, true>(p, s)
-                   : logprob_fwd_go<T, VEC, false, true>(p, s);
-    return ent ? logprob_fwd_go<T, VEC, true, false>(p, s)
-               : logprob_fwd_go<T, VEC, false, false>(p, s);
+        return ent ? logprob_fwd_go<T, true, true>(p, s) : logprob_fwd_go<T, false, true>(p, s);
+    return ent ? logprob_fwd_go<T, true, false>(p, s) : logprob_fwd_go<T, false, false>(p, s);
 }
 
 }  // namespace rn

@@ -105,6 +105,7 @@ struct LogprobParams {
     float* top_logp;
     int64_t rows, ld;
     int vocab, top, itype;
+    int split;              // CTAs of a row
     float scale;
 };
 cudaError_t logprob_fwd_launch(int dtype, const LogprobParams& p, cudaStream_t s);
@@ -118,8 +119,7 @@ struct LogprobBwdParams {
     const float* entropy;     // with dentropy
     void* dlogits;
     int64_t rows, ld, ldd;
-    int64_t total;            // rows * tiles
-    int64_t tiles;            // tiles of a row
+    FastDiv tiles;            // tiles of a row
     int vocab, itype;
     float scale;
 };

@@ -232,8 +232,8 @@ int logprob_fwd(int dtype, int itype, const void* logits, int64_t ldl, const voi
                 float* logp, float* entropy, float* lse, void* top_ids, float* top_logp,
                 int64_t rows, int64_t vocab, int top, float scale, void* stream) {
     if (!known_dtype(dtype) || !known_index(itype)) return RN_ERR_DTYPE;
-    if (rows < 0 || vocab <= 0 || vocab > kMaxVocab || ldl < vocab || !fits(rows, vocab, ldl) ||
-        top < 0 || top > RN_LOGPROB_MAX_TOP || top > vocab)
+    if (rows < 0 || rows > kMaxCount || vocab <= 0 || vocab > kMaxVocab || ldl < vocab ||
+        !fits(rows, vocab, ldl) || top < 0 || top > RN_LOGPROB_MAX_TOP || top > vocab)
         return RN_ERR_SIZE;
     if (!std::isfinite(scale) || scale <= 0.f) return RN_ERR_SCALE;
     if (rows == 0) return RN_OK;
@@ -279,8 +279,8 @@ int logprob_bwd(int dtype, int itype, const float* dlogp, const float* dentropy,
                 const float* entropy, void* dlogits, int64_t ldd, int64_t rows, int64_t vocab,
                 float scale, void* stream) {
     if (!known_dtype(dtype) || !known_index(itype)) return RN_ERR_DTYPE;
-    if (rows < 0 || vocab <= 0 || vocab > kMaxVocab || ldl < vocab || ldd < vocab ||
-        !fits(rows, vocab, ldl) || !fits(rows, vocab, ldd))
+    if (rows < 0 || rows > kMaxCount || vocab <= 0 || vocab > kMaxVocab || ldl < vocab ||
+        ldd < vocab || !fits(rows, vocab, ldl) || !fits(rows, vocab, ldd))
         return RN_ERR_SIZE;
     if (!std::isfinite(scale) || scale <= 0.f) return RN_ERR_SCALE;
     if (rows == 0) return RN_OK;
