@@ -430,40 +430,48 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _elsewhere(dev, stream):
+    """Whether a call needs another device or stream made current first."""
+    import torch
+
+    return stream is not None or (dev is not None and dev.index != torch.cuda.current_device())
+
+
 class _On:
     """Makes the call's device current and, where the caller gives a stream of
     its own, that stream too, so that the memory the call allocates belongs to the
-    stream that uses it. Yields the stream's handle."""
-
-    __slots__ = ("_dev", "_stream", "_inner")
+    stream that uses it."""
 
     def __init__(self, dev, stream):
-        self._dev, self._stream, self._inner = dev, stream, ()
-
-    def __enter__(self):
         import torch
 
-        dev, stream = self._dev, self._stream
-        if stream is None:
-            if dev is not None and dev.index != torch.cuda.current_device():
-                self._inner = (torch.cuda.device(dev),)
-        else:
-            if isinstance(stream, int):
-                # (handle 0: the legacy default stream, torch's default stream)
-                stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
-                          else torch.cuda.default_stream(dev))
-            elif dev is not None and stream.device != dev:
-                raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
-            self._inner = (torch.cuda.stream(stream),)
-            if dev is not None:
-                self._inner = (torch.cuda.device(dev),) + self._inner
+        if isinstance(stream, int):
+            # (handle 0: the legacy default stream, torch's default stream)
+            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
+                      else torch.cuda.default_stream(dev))
+        elif stream is not None and dev is not None and stream.device != dev:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
+        self._inner = [torch.cuda.stream(stream)]
+        if dev is not None:
+            self._inner.insert(0, torch.cuda.device(dev))
+
+    def __enter__(self):
         for c in self._inner:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self._inner):
             c.__exit__(*exc)
+
+
+def _current_stream(dev):
+    """Handle of the current stream of the call's device (of the current device,
+    where every tensor is in host memory)."""
+    import torch
+
+    if dev is None:
+        return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _new(home, dev, shape, dtype):
@@ -491,16 +499,18 @@ def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
     vocab, d = table.shape
     _, ldt = _matrix("table", table, d, dtype)
     dev = _device_of((table, tokens, out))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return embed_fwd(tokens, table, scale, out=out)
     n = tokens.numel()
-    with _On(dev, stream) as s:
-        if out is None:
-            out, ldo = _new(table, dev, (*tokens.shape, d), dtype), d
-        else:
-            if out.numel() != n * d or out.shape[-1:] != (d,):
-                raise ValueError(f"out must hold {n} rows of {d}")
-            _, ldo = _matrix("out", out, d, dtype)
-        capi.check(capi.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt,
-                                  out.data_ptr(), ldo, n, vocab, d, float(scale), s))
+    if out is None:
+        out, ldo = _new(table, dev, (*tokens.shape, d), dtype), d
+    else:
+        if out.numel() != n * d or out.shape[-1:] != (d,):
+            raise ValueError(f"out must hold {n} rows of {d}")
+        _, ldo = _matrix("out", out, d, dtype)
+    capi.check(capi.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt, out.data_ptr(),
+                              ldo, n, vocab, d, float(scale), _current_stream(dev)))
     return out
 
 
@@ -537,22 +547,28 @@ def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtabl
     if gdtype not in (dout.dtype, torch.float32):
         raise TypeError(f"dtable must be {dout.dtype} or float32")
     dev = _device_of((dout, tokens, dtable, workspace))
-    with _On(dev, stream) as s:
-        if dtable is None:
-            dtable = _new(dout, dev, (vocab, d), gdtype)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return embed_bwd(dout, tokens, vocab, scale, dtype=dtype, dtable=dtable,
+                             accumulate=accumulate, workspace=workspace)
+    if dtable is None:
+        dtable, ldg = _new(dout, dev, (vocab, d), gdtype), d
+    else:
         if tuple(dtable.shape) != (vocab, d):
             raise ValueError(f"dtable must be of shape [{vocab}, {d}]")
         _, ldg = _matrix("dtable", dtable, d, gdtype)
-        need = capi.embed_bwd_workspace_size(n, vocab, d)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8,
-                                    device=dev if dev is not None else "cuda")
-        elif not (workspace.is_cuda and workspace.is_contiguous()):
+    if workspace is None:
+        nbytes = capi.embed_bwd_workspace_size(n, vocab, d)
+        workspace = torch.empty(nbytes, dtype=torch.uint8,
+                                device=dev if dev is not None else "cuda")
+    else:
+        if not (workspace.is_cuda and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous CUDA tensor")
-        capi.check(capi.embed_bwd(code, _values("dtable", dtable), it, dout.data_ptr(), lddo,
-                                  tokens.data_ptr(), dtable.data_ptr(), ldg, n, vocab, d,
-                                  float(scale), 1 if accumulate else 0, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), s))
+        nbytes = workspace.numel() * workspace.element_size()
+    capi.check(capi.embed_bwd(code, _values("dtable", dtable), it, dout.data_ptr(), lddo,
+                              tokens.data_ptr(), dtable.data_ptr(), ldg, n, vocab, d,
+                              float(scale), 1 if accumulate else 0, workspace.data_ptr(), nbytes,
+                              _current_stream(dev)))
     return dtable
 
 
@@ -584,20 +600,22 @@ def logprob_fwd(logits, targets=None, scale: float = 1.0, *, top: int = 0,
         if targets.numel() != rows:
             raise ValueError(f"targets must have {rows} elements")
     dev = _device_of((logits, targets))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return logprob_fwd(logits, targets, scale, top=top, want_entropy=want_entropy)
     f32 = torch.float32
     logp = entropy = ids = top_logp = None
-    with _On(dev, stream) as s:
-        if targets is not None:
-            logp = _new(logits, dev, lead, f32)
-        if want_entropy:
-            entropy = _new(logits, dev, lead, f32)
-        lse = _new(logits, dev, lead, f32)
-        if top > 0:
-            ids = _new(logits, dev, (*lead, top), itype)
-            top_logp = _new(logits, dev, (*lead, top), f32)
-        capi.check(capi.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, _ptr(logp),
-                                    _ptr(entropy), lse.data_ptr(), _ptr(ids), _ptr(top_logp),
-                                    rows, vocab, int(top), float(scale), s))
+    if targets is not None:
+        logp = _new(logits, dev, lead, f32)
+    if want_entropy:
+        entropy = _new(logits, dev, lead, f32)
+    lse = _new(logits, dev, lead, f32)
+    if top > 0:
+        ids = _new(logits, dev, (*lead, top), itype)
+        top_logp = _new(logits, dev, (*lead, top), f32)
+    capi.check(capi.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, _ptr(logp), _ptr(entropy),
+                                lse.data_ptr(), _ptr(ids), _ptr(top_logp), rows, vocab, int(top),
+                                float(scale), _current_stream(dev)))
     return logp, entropy, lse, ids, top_logp
 
 
@@ -623,14 +641,17 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
     rows_of = [_row_floats(n, t, rows) for n, t in (("dlogp", dlogp), ("dentropy", dentropy),
                                                     ("lse", lse), ("entropy", entropy))]
     dev = _device_of((logits, dlogp, targets, lse, dentropy, entropy, dlogits))
-    with _On(dev, stream) as s:
-        if dlogits is None:
-            dlogits, ldd = _new(logits, dev, logits.shape, logits.dtype), vocab
-        else:
-            if dlogits.numel() != logits.numel() or dlogits.shape[-1] != vocab:
-                raise ValueError("dlogits must be shaped like logits")
-            _, ldd = _matrix("dlogits", dlogits, vocab, logits.dtype)
-        capi.check(capi.logprob_bwd(code, it, rows_of[0], rows_of[1], logits.data_ptr(), ldl, tgt,
-                                    rows_of[2], rows_of[3], dlogits.data_ptr(), ldd, rows, vocab,
-                                    float(scale), s))
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return logprob_bwd(dlogp, logits, targets, lse, scale, dentropy=dentropy,
+                               entropy=entropy, dlogits=dlogits)
+    if dlogits is None:
+        dlogits, ldd = _new(logits, dev, logits.shape, logits.dtype), vocab
+    else:
+        if dlogits.numel() != logits.numel() or dlogits.shape[-1] != vocab:
+            raise ValueError("dlogits must be shaped like logits")
+        _, ldd = _matrix("dlogits", dlogits, vocab, logits.dtype)
+    capi.check(capi.logprob_bwd(code, it, rows_of[0], rows_of[1], logits.data_ptr(), ldl, tgt,
+                                rows_of[2], rows_of[3], dlogits.data_ptr(), ldd, rows, vocab,
+                                float(scale), _current_stream(dev)))
     return dlogits

@@ -1,63 +1,56 @@
 // embed_bwd.cu -- gradient of embedding rows from the sorted ids:
-//   dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum_{i: id_i = v} dout[i].
+//   dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum_{i: id_i = v} dout[i]
+// for the ids that occur (embed_sort.cu clears the rows of the others).
 //
-// Bytes bound it: dout read once, every row of the gradient written once (most
-// ids of a vocabulary are absent from a batch, so most of the time goes into
-// rows of zeros). The sorted positions are cut into chunks of kEmbedChunk. A
-// group of threads takes one chunk and a slice of the columns, adds the chunk's
-// rows in registers (FP32) and, where the id changes, writes the id's row. An
-// id whose positions run over a chunk's edge leaves its sum of each chunk in
-// the workspace, and a second kernel adds those in chunk order, so that an id
-// which fills half of a batch is summed by as many groups as its rows fill.
-// CTAs beside them clear the rows of the ids that the sort did not mark
-// present. Every sum has a fixed order: results repeat bit for bit.
+// Bytes bound it: dout read once, every row of the gradient written once. The
+// sorted positions are cut into chunks of 32, a lane for each of a chunk's ids.
+// A group of threads takes one chunk and a slice of the columns, has 8 of the chunk's
+// rows in flight at a time, adds them in registers (FP32) and, where the id changes,
+// writes the id's row. An id whose positions run over a chunk's edge leaves its sum of
+// each chunk in the workspace, and a second kernel adds those in chunk order, so that an
+// id which fills half of a batch is summed by as many groups as its rows fill.
+// Every sum has a fixed order: results repeat bit for bit.
 #include "rn_tokens.cuh"
 
 namespace rn {
 
 constexpr int kSegThreads = 256;
-constexpr int kZeroRowsPerCta = 64;
+constexpr int kSegU = 8;            // rows in flight
 
 template <typename T, typename G, int NE>
 __global__ void __launch_bounds__(kSegThreads) embed_bwd_kernel(const EmbedBwdParams p) {
+    static_assert(kEmbedChunk == 32 && kEmbedChunk % kSegU == 0, "a lane for each position");
+    constexpr int B = NE * (int)sizeof(T);
     pdl_launch_dependents();
-    pdl_wait();
     G* const DG = (G*)p.dtable;
-    if ((int)blockIdx.x >= p.seg_ctas) {
-        // rows of absent ids: a warp for each row
-        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        float z[NE];
-#pragma unroll
-        for (int k = 0; k < NE; ++k) z[k] = 0.f;
-        const int64_t r0 = (int64_t)((int)blockIdx.x - p.seg_ctas) * kZeroRowsPerCta;
-        for (int k = w; k < kZeroRowsPerCta; k += kSegThreads / 32) {
-            const int64_t v = r0 + k;
-            if (v >= p.vocab) return;
-            if ((ld_u32(p.present + (v >> 5)) >> (v & 31)) & 1u) continue;
-            G* row = DG + v * p.ldg;
-            for (int64_t j = (int64_t)lane * NE; j < p.d; j += 32 * NE) st_elems<G, NE>(row + j, z);
-        }
-        return;
-    }
-    const int tx = (int)threadIdx.x % p.tx, ty = (int)threadIdx.x / p.tx;
+    const int tx = (int)threadIdx.x % p.tx, ty = (int)threadIdx.x / p.tx, lane = tx & 31;
     const int slice = (int)blockIdx.x % p.slices;
     const int64_t c = (int64_t)((int)blockIdx.x / p.slices) * p.ty + ty;
     const int64_t j = ((int64_t)slice * p.tx + tx) * NE;
-    if (c >= p.chunks || j >= p.d) return;
-    const T* const X = (const T*)p.dout + j;
+    if (c >= p.chunks) return;          // whole warps: tx is a multiple of 32
+    const bool on_row = j < p.d;
+    const T* const X = (const T*)p.dout + (on_row ? j : 0);
     const int64_t i0 = c * kEmbedChunk;
-    const int64_t i1 = i0 + kEmbedChunk < p.n ? i0 + kEmbedChunk : p.n;
-    uint32_t cur = ld_u32(p.key + i0);
-    bool open = i0 > 0 && ld_u32(p.key + i0 - 1) == cur;   // cur began in an earlier chunk
-    const bool on = i1 < p.n && ld_u32(p.key + i1) == ld_u32(p.key + i1 - 1);
+    const int cnt = (int)min((int64_t)kEmbedChunk, p.n - i0);
+    pdl_wait();
+    uint32_t my_key = 0xffffffffu;
+    int32_t my_pos = 0;
+    if (lane < cnt) {
+        my_key = ld_u32(p.key + i0 + lane);
+        my_pos = (int32_t)ld_u32((const uint32_t*)p.pos + i0 + lane);
+    }
+    const uint32_t prev = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
+    const uint32_t next = i0 + cnt < p.n ? ld_u32(p.key + i0 + cnt) : 0xffffffffu;
+    uint32_t cur = __shfl_sync(0xffffffffu, my_key, 0);
+    bool open = prev == cur;            // cur began in an earlier chunk
     float acc[NE];
 #pragma unroll
     for (int k = 0; k < NE; ++k) acc[k] = 0.f;
-    auto put = [&](bool last) {
-        if (cur >= (uint32_t)p.vocab) return;   // ids outside the vocabulary
-        if (open || (last && on)) {
-            float* w = p.part + (2 * c + (open ? 0 : 1)) * p.dpad + j;
-            st_elems<float, NE>(w, acc);
+    // cur's sum is complete as far as this chunk goes; `on`: it goes on in the next
+    auto put = [&](bool on) {
+        if (cur >= (uint32_t)p.vocab || !on_row) return;   // (ids outside the vocabulary)
+        if (open || on) {
+            st_elems<float, NE>(p.part + (2 * c + (open ? 0 : 1)) * p.dpad + j, acc);
         } else {
             G* g = DG + (int64_t)cur * p.ldg + j;
             float o[NE];
@@ -72,20 +65,18 @@ __global__ void __launch_bounds__(kSegThreads) embed_bwd_kernel(const EmbedBwdPa
             st_elems<G, NE>(g, o);
         }
     };
-    for (int64_t i = i0; i < i1; i += 4) {
-        uint32_t key[4];
-        float v[4][NE];
+    for (int i = 0; i < cnt; i += kSegU) {
+        uint32_t key[kSegU];
+        Raw<B> r[kSegU];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (i + u < i1) {
-                key[u] = ld_u32(p.key + i + u);
-                const int64_t r = (int64_t)ld_u32((const uint32_t*)p.pos + i + u);
-                if (key[u] < (uint32_t)p.vocab) ld_elems<T, NE>(v[u], X + r * p.lddo);
-            }
+        for (int u = 0; u < kSegU; ++u) {
+            key[u] = __shfl_sync(0xffffffffu, my_key, i + u);
+            const int64_t at = __shfl_sync(0xffffffffu, my_pos, i + u);
+            if (key[u] < (uint32_t)p.vocab) r[u] = ld_raw<B>(X + at * p.lddo);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (i + u < i1) {
+        for (int u = 0; u < kSegU; ++u) {
+            if (i + u < cnt) {
                 if (key[u] != cur) {
                     put(false);
                     cur = key[u];
@@ -94,81 +85,142 @@ __global__ void __launch_bounds__(kSegThreads) embed_bwd_kernel(const EmbedBwdPa
                     for (int k = 0; k < NE; ++k) acc[k] = 0.f;
                 }
                 if (cur < (uint32_t)p.vocab) {
+                    float v[NE];
+                    unpack<T, NE>(v, r[u]);
 #pragma unroll
-                    for (int k = 0; k < NE; ++k) acc[k] += v[u][k];
+                    for (int k = 0; k < NE; ++k) acc[k] += v[k];
                 }
             }
         }
     }
-    put(true);
+    put(next == cur);
 }
 
-// The ids whose positions run over a chunk's edge: the CTA of the chunk that
-// such an id begins in adds its sums, 8 warps taking every 8th chunk, then the
-// 8 sums in order.
+// The ids whose positions run over a chunk's edge. Each warp of a CTA looks at one
+// chunk and, if such an id begins in it, adds the id's sums of the chunks in order. An id
+// of more than kJoinMany chunks is left to the whole CTA: each warp takes every
+// kJoinWarps-th chunk, and the warps' sums are added in order. blockIdx.y takes blocks
+// of 32 * NE columns in turn.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinMany = 16;
+
+template <typename G, int NE>
+__device__ __forceinline__ void join_put(const EmbedBwdParams& p, uint32_t id, int64_t j,
+                                         const float* acc) {
+    float o[NE];
+    G* g = (G*)p.dtable + (int64_t)id * p.ldg + j;
+    if (p.accumulate) ld_elems<G, NE>(o, g);
+#pragma unroll
+    for (int k = 0; k < NE; ++k)
+        o[k] = p.accumulate ? fmaf(p.scale, acc[k], o[k]) : p.scale * acc[k];
+    st_elems<G, NE>(g, o);
+}
+
+// acc = the sums that chunks first, first + step, ... to last hold of the id that begins
+// in chunk c, at columns j ..
+template <int NE>
+__device__ __forceinline__ void join_sum(const EmbedBwdParams& p, float* acc, int64_t c,
+                                         int64_t first, int64_t last, int step, int64_t j) {
+#pragma unroll
+    for (int k = 0; k < NE; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int64_t q = first; q <= last; q += step) {
+        float v[NE];
+        ld_elems<float, NE>(v, p.part + (2 * q + (q == c ? 1 : 0)) * p.dpad + j);
+#pragma unroll
+        for (int k = 0; k < NE; ++k) acc[k] += v[k];
+    }
+}
 
 template <typename G, int NE>
 __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const EmbedBwdParams p) {
     __shared__ float sum[kJoinWarps][32 * NE];
+    __shared__ int64_t ends[kJoinWarps];      // last chunk of a long id (or -1)
+    __shared__ uint32_t ids[kJoinWarps];
     pdl_launch_dependents();
-    pdl_wait();
-    const int64_t c = blockIdx.x;
-    const int64_t i0 = c * kEmbedChunk, i1 = i0 + kEmbedChunk;
-    if (i1 >= p.n) return;
-    const uint32_t cur = ld_u32(p.key + i1 - 1);
-    if (cur >= (uint32_t)p.vocab || ld_u32(p.key + i1) != cur) return;
-    if (ld_u32(p.key + i0) == cur && i0 > 0 && ld_u32(p.key + i0 - 1) == cur) return;
-    // the first position after the id's
-    int64_t lo = i1, hi = p.n;
-    while (lo < hi) {
-        const int64_t m = (lo + hi) >> 1;
-        if (ld_u32(p.key + m) == cur)
-            lo = m + 1;
-        else
-            hi = m;
-    }
-    const int64_t last = (lo - 1) / kEmbedChunk;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int64_t jb = (int64_t)blockIdx.y * 32 * NE; jb < p.d; jb += (int64_t)gridDim.y * 32 * NE) {
-        const int64_t j = jb + lane * NE;
-        float acc[NE];
-#pragma unroll
-        for (int k = 0; k < NE; ++k) acc[k] = 0.f;
-        if (j < p.d) {
-            for (int64_t q = c + w; q <= last; q += kJoinWarps) {
-                float v[NE];
-                ld_elems<float, NE>(v, p.part + (2 * q + (q == c ? 1 : 0)) * p.dpad + j);
-#pragma unroll
-                for (int k = 0; k < NE; ++k) acc[k] += v[k];
+    const int64_t c0 = (int64_t)blockIdx.x * kJoinWarps, c = c0 + w;
+    const int64_t i0 = c * kEmbedChunk, i1 = i0 + kEmbedChunk;
+    pdl_wait();
+    int64_t last = -1;
+    uint32_t cur = 0xffffffffu;
+    if (i1 < p.n) {
+        // (loads together: most chunks need no more)
+        const uint32_t before = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
+        const uint32_t begin = ld_u32(p.key + i0), after = ld_u32(p.key + i1);
+        const int64_t e = min(i1 + kEmbedChunk, p.n) - 1;
+        const uint32_t far = ld_u32(p.key + e);
+        cur = ld_u32(p.key + i1 - 1);
+        if (cur < (uint32_t)p.vocab && after == cur && !(begin == cur && before == cur)) {
+            last = c + 1;
+            if (far == cur && e + 1 < p.n) {
+                // the first position after the id's
+                int64_t lo = e + 1, hi = p.n;
+                while (lo < hi) {
+                    const int64_t m = (lo + hi) >> 1;
+                    if (ld_u32(p.key + m) == cur)
+                        lo = m + 1;
+                    else
+                        hi = m;
+                }
+                last = (lo - 1) / kEmbedChunk;
             }
         }
-#pragma unroll
-        for (int k = 0; k < NE; ++k) sum[w][lane * NE + k] = acc[k];
-        __syncthreads();
-        if (w == 0 && j < p.d) {
-            float o[NE];
-            G* g = (G*)p.dtable + (int64_t)cur * p.ldg + j;
-            if (p.accumulate) ld_elems<G, NE>(o, g);
-#pragma unroll
-            for (int k = 0; k < NE; ++k) {
-                float s = sum[0][lane * NE + k];
-#pragma unroll
-                for (int q = 1; q < kJoinWarps; ++q) s += sum[q][lane * NE + k];
-                o[k] = p.accumulate ? fmaf(p.scale, s, o[k]) : p.scale * s;
-            }
-            st_elems<G, NE>(g, o);
+    }
+    const bool many = last - c > kJoinMany;
+    if (lane == 0) {
+        ends[w] = many ? last : -1;
+        ids[w] = cur;
+    }
+    const int64_t col0 = (int64_t)blockIdx.y * 32 * NE + lane * NE;
+    const int64_t step = (int64_t)gridDim.y * 32 * NE;
+    float acc[NE];
+    if (last >= 0 && !many) {
+        for (int64_t j = col0; j < p.d; j += step) {
+            join_sum<NE>(p, acc, c, c, last, 1, j);
+            join_put<G, NE>(p, cur, j, acc);
         }
-        __syncthreads();
+    }
+    __syncthreads();
+    for (int k = 0; k < kJoinWarps; ++k) {
+        if (ends[k] < 0) continue;
+        for (int64_t j = col0; j - lane * NE < p.d; j += step) {
+            if (j < p.d) join_sum<NE>(p, acc, c0 + k, c0 + k + w, ends[k], kJoinWarps, j);
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < NE; ++q) sum[w][lane * NE + q] = acc[q];
+            __syncthreads();
+            if (w == 0 && j < p.d) {
+#pragma unroll
+                for (int q = 0; q < NE; ++q) {
+                    acc[q] = sum[0][lane * NE + q];
+#pragma unroll
+                    for (int r = 1; r < kJoinWarps; ++r) acc[q] += sum[r][lane * NE + q];
+                }
+                join_put<G, NE>(p, ids[k], j, acc);
+            }
+        }
     }
 }
 
 template <typename T, typename G, int NE>
 static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
-    cudaError_t err = launch_pdl(embed_bwd_kernel<T, G, NE>, (unsigned)(p.seg_ctas + p.zero_ctas),
-                                 kSegThreads, 0, s, p);
+    const int64_t ctas = (p.chunks + p.ty - 1) / p.ty * p.slices;
+    cudaError_t err =
+        launch_pdl(embed_bwd_kernel<T, G, NE>, (unsigned)ctas, kSegThreads, 0, s, p);
     if (err != cudaSuccess || p.chunks < 2) return err;
-    return launch_pdl(embed_join_kernel<G, NE>, (unsigned)p.chunks, kJoinWarps * 32, 0, s, p);
+    const int64_t blocks = (p.d + 32 * NE - 1) / (32 * NE);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.chunks - 1 + kJoinWarps - 1) / kJoinWarps),
+                       (unsigned)(blocks < 16 ? blocks : 16), 1);
+    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, embed_join_kernel<G, NE>, p);
 }
 
 cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams& q,
@@ -179,10 +231,6 @@ cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams&
     while (p.tx < kSegThreads && p.tx < vpr) p.tx *= 2;
     p.ty = kSegThreads / p.tx;
     p.slices = (int)((vpr + p.tx - 1) / p.tx);
-    p.chunks = (p.n + kEmbedChunk - 1) / kEmbedChunk;
-    p.seg_ctas = (int)((p.chunks + p.ty - 1) / p.ty * p.slices);
-    p.zero_ctas =
-        p.accumulate ? 0 : (int)((p.vocab + kZeroRowsPerCta - 1) / kZeroRowsPerCta);
 #define RN_GO(T, G)                                           \
     {                                                         \
         if (ne == 8) return embed_bwd_go<T, G, 8>(p, s);      \

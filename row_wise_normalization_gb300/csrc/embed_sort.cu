@@ -1,36 +1,205 @@
 // embed_sort.cu -- the ids of an embedding gradient in order, with their
-// positions: a stable radix sort, lowest digit first.
+// positions (a stable radix sort, lowest digit first), and, beside it, the
+// gradient's rows of zeros.
 //
-// A vocabulary needs 10 to 18 bits, so two digits of at most 9 bits sort it.
-// A CTA takes a tile of 4096 ids. Each pass counts the tile's digits
-// (hist kernel), then every scatter CTA finds its own bases from the counts of
-// all tiles (there are few: 16 for 65536 ids, so that reading them again costs
-// less than a scan kernel of its own), ranks its ids and writes them out.
-// Ranks are stable: a warp owns 256 consecutive ids and takes 32 at a time;
-// equal digits among the 32 are found by a warp match and numbered by lane,
-// and a table of counts for each warp carries the number from one 32 to the
-// next. Nothing depends on the order in which CTAs or atomics run.
+// A vocabulary needs 10 to 18 bits, so two digits of at most 9 bits sort it. Ranks
+// are stable: a warp owns consecutive ids and takes 32 at a time; equal digits
+// among the 32 are found by a warp match and numbered by lane, and a table of counts
+// for each warp carries the number from one 32 to the next. Nothing depends on the
+// order in which CTAs or atomics run.
+//
+// Up to kSortClusterMax ids are sorted by one thread-block cluster of 1 to 16 CTAs
+// that keeps them in its CTAs' shared memory: a pass counts its digits, the CTAs
+// read each other's counts, and every id goes straight to its place in the shared
+// memory of the CTA that owns it (the last pass writes to global memory). One launch, whose
+// other clusters meanwhile clear the rows of the ids that do not occur. Those rows are
+// most of a gradient's bytes, so the sort costs no time of its own: 65536
+// ids took 39 us in four launches of their own before.
+// More ids are sorted in global memory, two launches a digit; the first of them
+// clears the rows.
+//
+// A CTA that clears owns a range of the vocabulary. It reads all ids (from L2) and
+// marks those of its range in shared memory, so that it depends on no other CTA.
 #include "rn_tokens.cuh"
 
 namespace rn {
 
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kZeroRange = 65536;   // ids a CTA marks at a time (8 KB of bits)
 
 // The sort key of the id at position i.
-__device__ __forceinline__ uint32_t id_key(const SortParams& p, int64_t i, int itype) {
-    const int64_t id = ld_id(p.tokens, i, itype);
+__device__ __forceinline__ uint32_t id_key(const SortParams& p, int64_t i) {
+    const int64_t id = ld_id(p.tokens, i, p.itype);
     return (uint32_t)((id >= 0 && id < p.vocab) ? id : p.vocab);
 }
 
-// Counts of the tile's digits. The first pass reads the ids themselves and
-// clears the bits of the ids present.
+// Clears `bytes` (a multiple of 2) at p by `lanes` threads, of which this is number l.
+__device__ __forceinline__ void clear_row(char* p, int64_t bytes, int l, int lanes) {
+    const int64_t head = min((int64_t)((0u - (unsigned)(uintptr_t)p) & 15u), bytes);
+    const int64_t nv = (bytes - head) / 16, tail = head + nv * 16;
+    const Raw<16> z = {};
+    for (int64_t v = l; v < nv; v += lanes) st_raw(p + head + v * 16, z);
+    const Raw<2> h = {};
+    for (int64_t b = 2 * l; b < head; b += 2 * lanes) st_raw(p + b, h);
+    for (int64_t b = tail + 2 * l; b < bytes; b += 2 * lanes) st_raw(p + b, h);
+}
+
+// Clears the absent rows of part z of p.zero_ctas of the vocabulary.
+__device__ void clear_absent(const SortParams& p, int z, uint32_t* bits) {
+    const int t = threadIdx.x;
+    const int64_t share = ((p.vocab + p.zero_ctas - 1) / p.zero_ctas + 31) / 32 * 32;
+    const int64_t end = min(p.vocab, (z + 1) * share);
+    // threads of a row: as many 16-byte stores as it has, up to a warp's
+    int lanes = 32;
+    while (lanes > 1 && (lanes / 2) * 16 >= p.zero_bytes) lanes /= 2;
+    for (int64_t lo = z * share; lo < end; lo += kZeroRange) {
+        const int cnt = (int)min((int64_t)kZeroRange, end - lo);
+        __syncthreads();
+        for (int w = t; w < (cnt + 31) / 32; w += kSortThreads) bits[w] = 0;
+        __syncthreads();
+        constexpr int U = 8;
+        for (int64_t i = t; i < p.n; i += kSortThreads * U) {
+            int64_t id[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                id[u] = i + u * kSortThreads < p.n ? ld_id(p.tokens, i + u * kSortThreads, p.itype)
+                                                   : -1;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint64_t k = (uint64_t)id[u] - (uint64_t)lo;
+                if (k < (uint64_t)cnt) atomicOr(&bits[k >> 5], 1u << (k & 31));
+            }
+        }
+        __syncthreads();
+        for (int r = t / lanes; r < cnt; r += kSortThreads / lanes)
+            if (!((bits[r >> 5] >> (r & 31)) & 1u))
+                clear_row(p.zero + (lo + r) * p.zero_pitch, p.zero_bytes, t % lanes, lanes);
+    }
+}
+
+// Sum of v over the threads before this one (all kSortThreads of them call it).
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* wsum) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t q = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += q;
+    }
+    if (lane == 31) wsum[w] = incl;
+    __syncthreads();
+    uint32_t run = incl - v;
+    for (int k = 0; k < w; ++k) run += wsum[k];
+    return run;
+}
+
+// The number of this lane's digit among the warp's ids so far (cnt: the warp's table,
+// advanced). All lanes; `in` false: no id.
+__device__ __forceinline__ uint32_t warp_rank(uint32_t* cnt, uint32_t dg, bool in, int lane) {
+    const unsigned same = __match_any_sync(0xffffffffu, in ? dg : (uint32_t)kSortBins);
+    const int lead = __ffs(same) - 1;
+    uint32_t r = 0;
+    if (in && lane == lead) {
+        r = cnt[dg];
+        cnt[dg] = r + __popc(same);
+    }
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, r, lead) + __popc(same & ((1u << lane) - 1));
+}
+
+// ---- up to kSortClusterMax ids: in the shared memory of a cluster ---------------
+constexpr int front_fixed_bytes() { return kSortWarps * kSortBins * 4 + kSortBins * 4; }
+constexpr int front_bytes(int share, int passes) {
+    return front_fixed_bytes() + (passes > 1 ? 2 : 1) * share * 8;
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_front_kernel(const SortParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ uint32_t wsum[kSortWarps];
+    static_assert(kSortThreads == kSortBins, "one thread for each digit");
+    static_assert(kZeroRange / 8 <= front_fixed_bytes(), "the marks of a range");
+    pdl_launch_dependents();
+    if ((int)blockIdx.x >= p.cluster) {
+        pdl_wait();
+        clear_absent(p, (int)blockIdx.x - p.cluster, (uint32_t*)smem);
+        return;
+    }
+    uint32_t(*cnt)[kSortBins] = (uint32_t(*)[kSortBins])smem;
+    uint32_t* const tots = (uint32_t*)smem + kSortWarps * kSortBins;
+    unsigned long long* const buf = (unsigned long long*)(smem + front_fixed_bytes());
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31, me = (int)blockIdx.x;
+    const uint32_t mask = (1u << p.bits) - 1;
+    const int64_t base = (int64_t)me * p.share;
+    // this CTA's ids, and this warp's of them: [w0, w1)
+    const int mine = (int)max((int64_t)0, min((int64_t)p.share, p.n - base));
+    const int per = p.share / kSortWarps;
+    const int w0 = min(mine, w * per), w1 = min(mine, w0 + per);
+    pdl_wait();
+    for (int i = w0 + lane; i < w1; i += 32)
+        buf[i] = ((unsigned long long)id_key(p, base + i) << 32) | (uint32_t)(base + i);
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        unsigned long long* const src = buf + (pass & 1) * p.share;
+        unsigned long long* const dst = buf + ((pass & 1) ^ 1) * p.share;
+        for (int k = 0; k < kSortWarps; ++k) cnt[k][t] = 0;
+        __syncthreads();
+        for (int i = w0; i < w1; i += 32) {
+            const bool in = i + lane < w1;
+            const uint32_t dg = in ? (uint32_t)(src[i + lane] >> (32 + shift)) & mask : 0;
+            warp_rank(cnt[w], dg, in, lane);
+        }
+        __syncthreads();
+        uint32_t sum = 0;
+        for (int k = 0; k < kSortWarps; ++k) sum += cnt[k][t];
+        tots[t] = sum;
+        cluster_sync();
+        uint32_t before = 0, total = 0;
+        for (int q = 0; q < p.cluster; ++q) {
+            const uint32_t c = peer_u32(peer_addr(tots + t, q));
+            if (q < me) before += c;
+            total += c;
+        }
+        uint32_t run = before + sum_before(total, wsum);
+        for (int k = 0; k < kSortWarps; ++k) {
+            const uint32_t c = cnt[k][t];
+            cnt[k][t] = run;
+            run += c;
+        }
+        __syncthreads();
+        const bool last = pass == p.passes - 1;
+        for (int i = w0; i < w1; i += 32) {
+            const bool in = i + lane < w1;
+            const unsigned long long v = in ? src[i + lane] : 0;
+            const uint32_t at = warp_rank(cnt[w], (uint32_t)(v >> (32 + shift)) & mask, in, lane);
+            if (in) {
+                if (last) {
+                    p.key[0][at] = (uint32_t)(v >> 32);
+                    p.pos[0][at] = (int32_t)v;
+                } else {
+                    const uint32_t q = at / (uint32_t)p.share;
+                    peer_store(peer_addr(dst + (at - q * (uint32_t)p.share), q), v);
+                }
+            }
+        }
+        // the peers' ids have arrived, and they are past their reads of tots
+        cluster_sync();
+    }
+}
+
+// ---- more ids: in global memory -------------------------------------------------
+// Counts of the tile's digits. The first pass reads the ids themselves, and its
+// CTAs beyond the tiles clear rows.
 template <bool FIRST>
 __global__ void __launch_bounds__(kSortThreads)
-    sort_hist_kernel(const SortParams p, int itype, int src, int shift) {
-    __shared__ uint32_t h[kSortBins];
+    sort_hist_kernel(const SortParams p, int src, int shift) {
+    __shared__ uint32_t h[FIRST ? kZeroRange / 32 : kSortBins];
     pdl_launch_dependents();
     const int t = threadIdx.x;
-    for (int b = t; b < kSortBins; b += kSortThreads) h[b] = 0;
+    if (FIRST && (int)blockIdx.x >= p.tiles) {
+        pdl_wait();
+        clear_absent(p, (int)blockIdx.x - p.tiles, h);
+        return;
+    }
+    h[t] = 0;
     __syncthreads();
     pdl_wait();
     const uint32_t mask = (1u << p.bits) - 1;
@@ -39,28 +208,43 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
     for (int j = 0; j < kSortPerThread; ++j) {
         const int64_t i = base + j * kSortThreads + t;
-        k[j] = i < p.n ? (FIRST ? id_key(p, i, itype) : ld_u32(p.key[src] + i)) : ~0u;
+        k[j] = i < p.n ? (FIRST ? id_key(p, i) : ld_u32(p.key[src] + i)) : ~0u;
     }
 #pragma unroll
     for (int j = 0; j < kSortPerThread; ++j)
         if (base + j * kSortThreads + t < p.n) atomicAdd(&h[(k[j] >> shift) & mask], 1u);
-    if (FIRST && p.present) {
-        const int64_t words = (p.vocab + 31) / 32;
-        for (int64_t w = (int64_t)blockIdx.x * kSortThreads + t; w < words;
-             w += (int64_t)gridDim.x * kSortThreads)
-            p.present[w] = 0;
-    }
     __syncthreads();
-    for (int b = t; b < kSortBins; b += kSortThreads)
-        p.hist[(int64_t)blockIdx.x * kSortBins + b] = h[b];
+    p.hist[(int64_t)blockIdx.x * kSortBins + t] = h[t];
+}
+
+// Exclusive sums of the counts, over the digits and within a digit over the tiles, in
+// place: one CTA, a thread for each digit.
+__global__ void __launch_bounds__(kSortThreads) sort_scan_kernel(const SortParams p) {
+    __shared__ uint32_t wsum[kSortWarps];
+    pdl_launch_dependents();
+    const int t = threadIdx.x;
+    pdl_wait();
+    uint32_t total = 0;
+#pragma unroll 8
+    for (int k = 0; k < p.tiles; ++k) total += ld_u32(p.hist + (int64_t)k * kSortBins + t);
+    uint32_t run = sum_before(total, wsum);
+    for (int k0 = 0; k0 < p.tiles; k0 += 8) {   // loads of a step together
+        uint32_t c[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            c[u] = k0 + u < p.tiles ? ld_u32(p.hist + (int64_t)(k0 + u) * kSortBins + t) : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (k0 + u < p.tiles) p.hist[(int64_t)(k0 + u) * kSortBins + t] = run;
+            run += c[u];
+        }
+    }
 }
 
 template <bool FIRST>
 __global__ void __launch_bounds__(kSortThreads)
-    sort_scatter_kernel(const SortParams p, int itype, int src, int shift) {
-    static_assert(kSortThreads == kSortBins, "one thread for each digit");
+    sort_scatter_kernel(const SortParams p, int src, int shift) {
     __shared__ uint32_t cnt[kSortWarps][kSortBins];
-    __shared__ uint32_t wsum[kSortWarps];
     pdl_launch_dependents();
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     for (int k = 0; k < kSortWarps; ++k) cnt[k][t] = 0;
@@ -74,47 +258,18 @@ __global__ void __launch_bounds__(kSortThreads)
     for (int j = 0; j < kSortPerThread; ++j) {
         const int64_t i = base + j * 32 + lane;
         if (i < p.n) {
-            key[j] = FIRST ? id_key(p, i, itype) : ld_u32(p.key[src] + i);
+            key[j] = FIRST ? id_key(p, i) : ld_u32(p.key[src] + i);
             pos[j] = FIRST ? (int32_t)i : (int32_t)ld_u32((const uint32_t*)p.pos[src] + i);
         } else {
             key[j] = 0;
             pos[j] = -1;
         }
     }
-    // this thread's digit: its count before this tile, and in all tiles
-    uint32_t before = 0, total = 0;
-    for (int k = 0; k < p.tiles; ++k) {
-        const uint32_t c = ld_u32(p.hist + (int64_t)k * kSortBins + t);
-        if (k < (int)blockIdx.x) before += c;
-        total += c;
-    }
-    // exclusive sum of the totals over the digits
-    uint32_t incl = total;
+    uint32_t run = ld_u32(p.hist + (int64_t)blockIdx.x * kSortBins + t);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) wsum[w] = incl;
-    // ranks within the warp's ids
-#pragma unroll
-    for (int j = 0; j < kSortPerThread; ++j) {
-        const bool in = pos[j] >= 0;
-        const uint32_t dg = in ? (key[j] >> shift) & mask : (uint32_t)kSortBins;
-        const unsigned same = __match_any_sync(0xffffffffu, dg);
-        const int lead = __ffs(same) - 1;
-        uint32_t r = 0;
-        if (in && lane == lead) {
-            r = cnt[w][dg];
-            cnt[w][dg] = r + __popc(same);
-        }
-        r = __shfl_sync(0xffffffffu, r, lead);
-        rank[j] = r + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-    }
+    for (int j = 0; j < kSortPerThread; ++j)
+        rank[j] = warp_rank(cnt[w], (key[j] >> shift) & mask, pos[j] >= 0, lane);
     __syncthreads();
-    uint32_t run = before + incl - total;
-    for (int k = 0; k < w; ++k) run += wsum[k];
     for (int k = 0; k < kSortWarps; ++k) {
         const uint32_t c = cnt[k][t];
         cnt[k][t] = run;
@@ -127,28 +282,77 @@ __global__ void __launch_bounds__(kSortThreads)
             const uint32_t at = cnt[w][(key[j] >> shift) & mask] + rank[j];
             p.key[src ^ 1][at] = key[j];
             p.pos[src ^ 1][at] = pos[j];
-            if (FIRST && p.present && key[j] < (uint32_t)p.vocab)
-                atomicOr(&p.present[key[j] >> 5], 1u << (key[j] & 31));
         }
     }
 }
 
-cudaError_t embed_sort_launch(int itype, SortParams p, cudaStream_t s) {
-    const int passes = sort_passes(p.vocab);
-    p.bits = (sort_key_bits(p.vocab) + passes - 1) / passes;
-    const unsigned grid = (unsigned)p.tiles;
-    for (int k = 0; k < passes; ++k) {
-        const int shift = k * p.bits, src = k & 1;
-        cudaError_t err =
-            k == 0 ? launch_pdl(sort_hist_kernel<true>, grid, kSortThreads, 0, s, p, itype, src,
-                                shift)
-                   : launch_pdl(sort_hist_kernel<false>, grid, kSortThreads, 0, s, p, itype, src,
-                                shift);
+static cudaError_t front_launch(SortParams& p, int sms, cudaStream_t s) {
+    // 2048 ids a CTA, until there are 16 CTAs
+    p.cluster = 1;
+    while (p.cluster < kSortMaxCluster && p.n > (int64_t)p.cluster * 2048) p.cluster *= 2;
+    const int64_t per = (p.n + p.cluster - 1) / p.cluster;
+    p.share = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
+    // clearing CTAs: one for each SM the sort leaves, in whole clusters
+    p.zero_ctas = 0;
+    if (p.zero) {
+        const int left = sms > 2 * p.cluster ? sms - p.cluster : p.cluster;
+        p.zero_ctas = left / p.cluster * p.cluster;
+    }
+    const int smem = front_bytes(p.share, p.passes);
+    // the function's limits belong to a context: raised once in each, by each thread
+    static thread_local unsigned long long prepared = 0;
+    unsigned long long ctx = 0;
+    cudaError_t err = current_context_id(&ctx);
+    if (err != cudaSuccess) return err;
+    if (ctx == 0 || prepared != ctx) {
+        err = cudaFuncSetAttribute(embed_front_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   front_bytes(kSortMaxShare, 2));
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(embed_front_kernel,
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess) return err;
-        err = k == 0 ? launch_pdl(sort_scatter_kernel<true>, grid, kSortThreads, 0, s, p, itype,
-                                  src, shift)
-                     : launch_pdl(sort_scatter_kernel<false>, grid, kSortThreads, 0, s, p, itype,
-                                  src, shift);
+        prepared = ctx;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.cluster + p.zero_ctas), 1, 1);
+    cfg.blockDim = dim3(kSortThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, embed_front_kernel, p);
+}
+
+cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    p.passes = sort_passes(p.vocab);
+    p.bits = (sort_key_bits(p.vocab) + p.passes - 1) / p.passes;
+    if (p.n <= kSortClusterMax) return front_launch(p, sms, s);
+    p.zero_ctas = p.zero ? sms : 0;
+    const unsigned grid = (unsigned)p.tiles;
+    for (int k = 0; k < p.passes; ++k) {
+        // from one pair of arrays to the other, so that the last pass ends in [0]
+        const int shift = k * p.bits, src = (p.passes - k) & 1;
+        err = k == 0 ? launch_pdl(sort_hist_kernel<true>, grid + (unsigned)p.zero_ctas,
+                                  kSortThreads, 0, s, p, src, shift)
+                     : launch_pdl(sort_hist_kernel<false>, grid, kSortThreads, 0, s, p, src, shift);
+        if (err == cudaSuccess) err = launch_pdl(sort_scan_kernel, 1, kSortThreads, 0, s, p);
+        if (err == cudaSuccess)
+            err = k == 0 ? launch_pdl(sort_scatter_kernel<true>, grid, kSortThreads, 0, s, p, src,
+                                      shift)
+                         : launch_pdl(sort_scatter_kernel<false>, grid, kSortThreads, 0, s, p, src,
+                                      shift);
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;

@@ -264,34 +264,6 @@ __device__ void row_again(const T* X, int V, float k, float m, float (*red)[4], 
     *ws = q / s;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
-                 ::: "memory");
-}
-// The address of this CTA's shared variable in the CTA of rank r of the cluster.
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t r) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(a)
-                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(r));
-    return a;
-}
-__device__ __forceinline__ float peer_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ unsigned long long peer_u64(uint32_t a) {
-    unsigned long long v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a));
-    return v;
-}
-
 template <typename T, bool ENT, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 2) logprob_fwd_kernel(const LogprobParams p) {
     constexpr int VEC = Elem<T>::kVec;

@@ -48,19 +48,28 @@ cudaError_t embed_fwd_launch(int dtype, int itype, int ne, const EmbedParams& p,
 // Stable sort of the n ids by value, with their positions. Ids outside
 // [0, vocab) are given the key `vocab`, so that they come last.
 constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortPerThread = 8;
-constexpr int kSortTile = kSortThreads * kSortPerThread;
-constexpr int kSortBits = 9;                 // bits of a digit, at most
+constexpr int kSortTile = kSortThreads * kSortPerThread;   // ids of a CTA, sorting in global memory
+constexpr int kSortBits = 9;                               // bits of a digit, at most
 constexpr int kSortBins = 1 << kSortBits;
+constexpr int kSortMaxCluster = 16;
+constexpr int kSortMaxShare = 10240;   // ids of a CTA, sorting in shared memory (160 KB)
+constexpr int64_t kSortClusterMax = (int64_t)kSortMaxCluster * kSortMaxShare;
 struct SortParams {
     const void* tokens;
     int64_t n, vocab;
-    uint32_t* key[2];     // [n] each: the passes go from one to the other
-    int32_t* pos[2];      // [n] each
-    uint32_t* hist;       // [tiles][kSortBins]
-    uint32_t* present;    // one bit for each id of the vocabulary; NULL: not wanted
+    uint32_t* key[2];     // [n] each: the result in [0]; [1] beyond kSortClusterMax only
+    int32_t* pos[2];
+    uint32_t* hist;       // [tiles][kSortBins], beyond kSortClusterMax
     int tiles;
-    int bits;             // bits of a digit in this sort
+    int bits, passes;     // bits of a digit, digits
+    int itype;
+    int cluster, share;   // CTAs that sort in shared memory, ids of each
+    // Rows of ids that do not occur, cleared beside the sort (zero_ctas > 0)
+    char* zero;
+    int64_t zero_pitch, zero_bytes;   // bytes from row to row, and of a row
+    int zero_ctas;
 };
 constexpr int sort_key_bits(int64_t vocab) {
     int b = 0;
@@ -68,25 +77,24 @@ constexpr int sort_key_bits(int64_t vocab) {
     return b;
 }
 constexpr int sort_passes(int64_t vocab) { return (sort_key_bits(vocab) + kSortBits - 1) / kSortBits; }
-// Runs every pass; the sorted arrays end in key[passes & 1], pos[passes & 1].
-cudaError_t embed_sort_launch(int itype, SortParams p, cudaStream_t s);
+// Sorts into key[0], pos[0] and, where p.zero is given, clears the rows of the ids
+// in [0, vocab) that are not among the tokens.
+cudaError_t embed_sort_launch(SortParams p, cudaStream_t s);
 
 // dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum of dout[i] over the
-// positions i with tokens[i] == v, from the sorted ids.
-constexpr int kEmbedChunk = 32;    // sorted positions one thread group sums
+// positions i with tokens[i] == v, for the ids v that occur, from the sorted ids.
+constexpr int kEmbedChunk = 32;    // sorted positions one thread group sums: a lane each
 struct EmbedBwdParams {
     const void* dout;
     void* dtable;
     const uint32_t* key;
     const int32_t* pos;
-    const uint32_t* present;   // NULL when accumulating (no row is cleared)
     float* part;               // [2 * chunks][dpad]
     int64_t n, vocab, d, dpad;
     int64_t lddo, ldg;
     int64_t chunks;
     int tx, ty;                // threads across a row, chunks of a CTA
     int slices;                // CTAs across a row
-    int seg_ctas, zero_ctas;
     float scale;
     int accumulate;
 };

@@ -78,10 +78,10 @@ int access_elems(int64_t d, const void* a, int es_a, int64_t lda, const void* b,
 
 // ---- workspace of embed_bwd -------------------------------------------------
 struct EmbedWorkspace {
-    int64_t key[2], pos[2], hist, present, part, total;   // byte offsets
+    int64_t key[2], pos[2], hist, part, total;   // byte offsets
     int64_t tiles, chunks, dpad;
 };
-EmbedWorkspace embed_workspace(int64_t n, int64_t vocab, int64_t d) {
+EmbedWorkspace embed_workspace(int64_t n, int64_t d) {
     EmbedWorkspace w;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -92,12 +92,12 @@ EmbedWorkspace embed_workspace(int64_t n, int64_t vocab, int64_t d) {
     w.tiles = (n + kSortTile - 1) / kSortTile;
     w.chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
     w.dpad = (d + 7) / 8 * 8;
+    const bool global = n > kSortClusterMax;   // the sort's second arrays and its counts
     for (int k = 0; k < 2; ++k) {
-        w.key[k] = take(n * 4);
-        w.pos[k] = take(n * 4);
+        w.key[k] = take(k == 0 || global ? n * 4 : 0);
+        w.pos[k] = take(k == 0 || global ? n * 4 : 0);
     }
-    w.hist = take(w.tiles * kSortBins * 4);
-    w.present = take((vocab + 31) / 32 * 4);
+    w.hist = take(global ? w.tiles * kSortBins * 4 : 0);
     w.part = take(2 * w.chunks * w.dpad * 4);
     w.total = at;
     return w;
@@ -107,7 +107,7 @@ bool embed_bwd_sizes_ok(int64_t n, int64_t vocab, int64_t d) {
     if (n < 0 || n > kMaxCount || vocab <= 0 || vocab > kMaxVocab || d <= 0 || d > kMaxWidth)
         return false;
     // (chunks x slices of the widest grid: 32 scalars a slice)
-    return (n / kEmbedChunk + 1) * (d / 32 + 1) + vocab / 64 + 1 < kMaxCount;
+    return (n / kEmbedChunk + 1) * (d / 32 + 1) < kMaxCount;
 }
 
 bool host_resident(const void* p) {
@@ -158,7 +158,7 @@ int embed_bwd_workspace_size(int64_t n, int64_t vocab, int64_t d, size_t* bytes)
     if (!bytes) return RN_ERR_NULL;
     *bytes = 0;
     if (!embed_bwd_sizes_ok(n, vocab, d)) return RN_ERR_SIZE;
-    if (n > 0) *bytes = (size_t)embed_workspace(n, vocab, d).total;
+    if (n > 0) *bytes = (size_t)embed_workspace(n, d).total;
     return RN_OK;
 }
 
@@ -186,14 +186,14 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
     if (misaligned(dout, es) || misaligned(tokens, is) || misaligned(dtable, gs) ||
         misaligned(workspace, 16))
         return RN_ERR_ALIGN;
-    const EmbedWorkspace w = embed_workspace(n, vocab, d);
+    const EmbedWorkspace w = embed_workspace(n, d);
     if (workspace_bytes < (size_t)w.total) return RN_ERR_SIZE;
     const Range outs[] = {{dtable, span(vocab, d, ldg) * gs}, {workspace, w.total}};
     const Range ins[] = {{dout, span(n, d, lddo) * es}, {tokens, n * is}};
     if (aliased(outs, ins)) return RN_ERR_ALIAS;
     if (host_resident(workspace)) return RN_ERR_HOSTMEM;
     char* const base = (char*)workspace;
-    SortParams sp;
+    SortParams sp = {};
     sp.tokens = tokens;
     sp.n = n;
     sp.vocab = vocab;
@@ -202,18 +202,20 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
         sp.pos[k] = (int32_t*)(base + w.pos[k]);
     }
     sp.hist = (uint32_t*)(base + w.hist);
-    sp.present = accumulate ? nullptr : (uint32_t*)(base + w.present);
     sp.tiles = (int)w.tiles;
-    sp.bits = 0;
-    cudaError_t err = embed_sort_launch(itype, sp, s);
+    sp.itype = itype;
+    if (!accumulate) {
+        sp.zero = (char*)dtable;
+        sp.zero_pitch = ldg * gs;
+        sp.zero_bytes = d * gs;
+    }
+    cudaError_t err = embed_sort_launch(sp, s);
     if (err != cudaSuccess) return done(err);
-    const int last = sort_passes(vocab) & 1;
     EmbedBwdParams p = {};
     p.dout = dout;
     p.dtable = dtable;
-    p.key = sp.key[last];
-    p.pos = sp.pos[last];
-    p.present = sp.present;
+    p.key = sp.key[0];
+    p.pos = sp.pos[0];
     p.part = (float*)(base + w.part);
     p.n = n;
     p.vocab = vocab;

@@ -125,6 +125,30 @@ def test_gradient(dtype, grad, n, vocab, d, kind):
     assert _bits_equal(rn.embed_bwd(dout, t, vocab, 1.5, dtype=DT[grad], workspace=ws), g.view)
 
 
+@pytest.mark.parametrize("n,vocab,d,kind", [
+    (2048, 400, 8, "heavy"), (2049, 400, 8, "heavy"), (30000, 131072, 3, "uniform"),
+    (33000, 511, 2, "uniform"), (33000, 512, 2, "heavy"), (100000, 50001, 4, "heavy"),
+    (163840, 1000, 2, "uniform"), (163841, 1000, 2, "uniform"), (200000, 300000, 1, "heavy"),
+    (300001, 200, 2, "one"), (170000, 1 << 20, 8, "descending"),
+])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_of_many_ids(n, vocab, d, kind, accumulate):
+    """Every size of the sort: one CTA, clusters, global memory; one digit to three."""
+    rng = np.random.default_rng([n, vocab])
+    tok = _tokens(rng, kind, n, vocab)
+    # small whole numbers: sums are exact, so the order of terms does not matter
+    vals = rng.integers(-8, 9, (n, d)).astype(np.float32)
+    dout = torch.from_numpy(vals).cuda()
+    old = torch.full((vocab, d), 3.0, device="cuda")
+    g = Framed(vocab, d, torch.float32, fill=old)
+    rn.embed_bwd(dout, torch.from_numpy(tok).cuda(), vocab, dtable=g.view, accumulate=accumulate)
+    g.check()
+    want = np.zeros((vocab, d))
+    ok = (tok >= 0) & (tok < vocab)
+    np.add.at(want, tok[ok], vals[ok])
+    assert np.array_equal(g.f64(), want + (3.0 if accumulate else 0.0))
+
+
 @pytest.mark.parametrize("dtype,grad", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
 @pytest.mark.parametrize("n,vocab,d", [(65, 200, 24), (700, 90, 129)])
 def test_gradient_accumulates(dtype, grad, n, vocab, d):
