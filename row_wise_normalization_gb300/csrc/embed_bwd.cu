@@ -3,7 +3,8 @@
 // for the ids that occur (embed_sort.cu clears the rows of the others).
 //
 // Bytes bound it: dout read once, every row of the gradient written once. The
-// sorted positions are cut into chunks of 32, a lane for each of a chunk's ids.
+// sorted positions are cut into chunks of 32 (8 in short batches), a lane for each of a
+// chunk's ids.
 // A group of threads takes one chunk and a slice of the columns, has 8 of the chunk's
 // rows in flight at a time, adds them in registers (FP32) and, where the id changes,
 // writes the id's row. An id whose positions run over a chunk's edge leaves its sum of
@@ -18,8 +19,8 @@ constexpr int kSegThreads = 256;
 constexpr int kSegU = 8;            // rows in flight
 
 template <typename T, typename G, int NE>
-__global__ void __launch_bounds__(kSegThreads) embed_bwd_kernel(const EmbedBwdParams p) {
-    static_assert(kEmbedChunk == 32 && kEmbedChunk % kSegU == 0, "a lane for each position");
+__global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBwdParams p) {
+    static_assert(kEmbedChunkMax <= 32, "a lane for each position");
     constexpr int B = NE * (int)sizeof(T);
     pdl_launch_dependents();
     G* const DG = (G*)p.dtable;
@@ -30,8 +31,8 @@ __global__ void __launch_bounds__(kSegThreads) embed_bwd_kernel(const EmbedBwdPa
     if (c >= p.chunks) return;          // whole warps: tx is a multiple of 32
     const bool on_row = j < p.d;
     const T* const X = (const T*)p.dout + (on_row ? j : 0);
-    const int64_t i0 = c * kEmbedChunk;
-    const int cnt = (int)min((int64_t)kEmbedChunk, p.n - i0);
+    const int64_t i0 = c * p.chunk;
+    const int cnt = (int)min((int64_t)p.chunk, p.n - i0);
     pdl_wait();
     uint32_t my_key = 0xffffffffu;
     int32_t my_pos = 0;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
     pdl_launch_dependents();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c0 = (int64_t)blockIdx.x * kJoinWarps, c = c0 + w;
-    const int64_t i0 = c * kEmbedChunk, i1 = i0 + kEmbedChunk;
+    const int64_t i0 = c * p.chunk, i1 = i0 + p.chunk;
     pdl_wait();
     int64_t last = -1;
     uint32_t cur = 0xffffffffu;
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
         // (loads together: most chunks need no more)
         const uint32_t before = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
         const uint32_t begin = ld_u32(p.key + i0), after = ld_u32(p.key + i1);
-        const int64_t e = min(i1 + kEmbedChunk, p.n) - 1;
+        const int64_t e = min(i1 + p.chunk, p.n) - 1;
         const uint32_t far = ld_u32(p.key + e);
         cur = ld_u32(p.key + i1 - 1);
         if (cur < (uint32_t)p.vocab && after == cur && !(begin == cur && before == cur)) {
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
                     else
                         hi = m;
                 }
-                last = (lo - 1) / kEmbedChunk;
+                last = (lo - 1) / p.chunk;
             }
         }
     }
@@ -212,7 +213,7 @@ static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
     const int64_t blocks = (p.d + 32 * NE - 1) / (32 * NE);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.chunks - 1 + kJoinWarps - 1) / kJoinWarps),
-                       (unsigned)(blocks < 16 ? blocks : 16), 1);
+                       (unsigned)(blocks < 8 ? blocks : 8), 1);
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

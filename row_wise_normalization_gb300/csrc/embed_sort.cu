@@ -11,15 +11,17 @@
 // Up to kSortClusterMax ids are sorted by one thread-block cluster of 1 to 16 CTAs
 // that keeps them in its CTAs' shared memory: a pass counts its digits, the CTAs
 // read each other's counts, and every id goes straight to its place in the shared
-// memory of the CTA that owns it (the last pass writes to global memory). One launch, whose
-// other clusters meanwhile clear the rows of the ids that do not occur. Those rows are
-// most of a gradient's bytes, so the sort costs no time of its own: 65536
-// ids took 39 us in four launches of their own before.
-// More ids are sorted in global memory, two launches a digit; the first of them
-// clears the rows.
+// memory of the CTA that owns it (the last pass writes to global memory). One launch;
+// 65536 ids took 39 us in the four launches of a sort in global memory. More ids are
+// sorted there, three launches a digit.
 //
-// A CTA that clears owns a range of the vocabulary. It reads all ids (from L2) and
-// marks those of its range in shared memory, so that it depends on no other CTA.
+// The rows of the ids that do not occur are most of a gradient's bytes, and which
+// they are the ids alone say: a CTA that clears owns a range of the vocabulary, reads all
+// ids (from L2) and marks those of its range in shared memory. So the kernel that
+// clears runs beside the sort. It is launched as the sort's programmatic dependent, and the
+// sort lets it start only after its own wait, when all work ahead of the call has
+// completed; and it waits for the sort only at its end, so that what follows it
+// follows both.
 #include "rn_tokens.cuh"
 
 namespace rn {
@@ -43,26 +45,31 @@ __device__ __forceinline__ void clear_row(char* p, int64_t bytes, int l, int lan
     for (int64_t b = tail + 2 * l; b < bytes; b += 2 * lanes) st_raw(p + b, h);
 }
 
-// Clears the absent rows of part z of p.zero_ctas of the vocabulary.
-__device__ void clear_absent(const SortParams& p, int z, uint32_t* bits) {
+// Clears the rows of the absent ids of a part of the vocabulary. What it touches no
+// kernel of the call before it does, and the one ahead has waited for all others before
+// it let this one start: it waits at its end.
+constexpr int kClearThreads = 1024;
+
+__global__ void __launch_bounds__(kClearThreads) embed_clear_kernel(const SortParams p) {
+    __shared__ uint32_t bits[kZeroRange / 32];
     const int t = threadIdx.x;
-    const int64_t share = ((p.vocab + p.zero_ctas - 1) / p.zero_ctas + 31) / 32 * 32;
-    const int64_t end = min(p.vocab, (z + 1) * share);
+    const int64_t share = ((p.vocab + gridDim.x - 1) / gridDim.x + 31) / 32 * 32;
+    const int64_t end = min(p.vocab, (int64_t)(blockIdx.x + 1) * share);
     // threads of a row: as many 16-byte stores as it has, up to a warp's
     int lanes = 32;
     while (lanes > 1 && (lanes / 2) * 16 >= p.zero_bytes) lanes /= 2;
-    for (int64_t lo = z * share; lo < end; lo += kZeroRange) {
+    for (int64_t lo = blockIdx.x * share; lo < end; lo += kZeroRange) {
         const int cnt = (int)min((int64_t)kZeroRange, end - lo);
         __syncthreads();
-        for (int w = t; w < (cnt + 31) / 32; w += kSortThreads) bits[w] = 0;
+        for (int w = t; w < (cnt + 31) / 32; w += kClearThreads) bits[w] = 0;
         __syncthreads();
         constexpr int U = 8;
-        for (int64_t i = t; i < p.n; i += kSortThreads * U) {
+        for (int64_t i = t; i < p.n; i += kClearThreads * U) {
             int64_t id[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                id[u] = i + u * kSortThreads < p.n ? ld_id(p.tokens, i + u * kSortThreads, p.itype)
-                                                   : -1;
+                id[u] = i + u * kClearThreads < p.n
+                            ? ld_id(p.tokens, i + u * kClearThreads, p.itype) : -1;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const uint64_t k = (uint64_t)id[u] - (uint64_t)lo;
@@ -70,10 +77,12 @@ __device__ void clear_absent(const SortParams& p, int z, uint32_t* bits) {
             }
         }
         __syncthreads();
-        for (int r = t / lanes; r < cnt; r += kSortThreads / lanes)
+        for (int r = t / lanes; r < cnt; r += kClearThreads / lanes)
             if (!((bits[r >> 5] >> (r & 31)) & 1u))
                 clear_row(p.zero + (lo + r) * p.zero_pitch, p.zero_bytes, t % lanes, lanes);
     }
+    pdl_launch_dependents();
+    pdl_wait();
 }
 
 // Sum of v over the threads before this one (all kSortThreads of them call it).
@@ -107,25 +116,18 @@ __device__ __forceinline__ uint32_t warp_rank(uint32_t* cnt, uint32_t dg, bool i
 }
 
 // ---- up to kSortClusterMax ids: in the shared memory of a cluster ---------------
-constexpr int front_fixed_bytes() { return kSortWarps * kSortBins * 4 + kSortBins * 4; }
-constexpr int front_bytes(int share, int passes) {
-    return front_fixed_bytes() + (passes > 1 ? 2 : 1) * share * 8;
+constexpr int cluster_fixed_bytes() { return kSortWarps * kSortBins * 4 + kSortBins * 4; }
+constexpr int cluster_bytes(int share, int passes) {
+    return cluster_fixed_bytes() + (passes > 1 ? 2 : 1) * share * 8;
 }
 
-__global__ void __launch_bounds__(kSortThreads) embed_front_kernel(const SortParams p) {
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint32_t wsum[kSortWarps];
     static_assert(kSortThreads == kSortBins, "one thread for each digit");
-    static_assert(kZeroRange / 8 <= front_fixed_bytes(), "the marks of a range");
-    pdl_launch_dependents();
-    if ((int)blockIdx.x >= p.cluster) {
-        pdl_wait();
-        clear_absent(p, (int)blockIdx.x - p.cluster, (uint32_t*)smem);
-        return;
-    }
     uint32_t(*cnt)[kSortBins] = (uint32_t(*)[kSortBins])smem;
     uint32_t* const tots = (uint32_t*)smem + kSortWarps * kSortBins;
-    unsigned long long* const buf = (unsigned long long*)(smem + front_fixed_bytes());
+    unsigned long long* const buf = (unsigned long long*)(smem + cluster_fixed_bytes());
     const int t = threadIdx.x, w = t >> 5, lane = t & 31, me = (int)blockIdx.x;
     const uint32_t mask = (1u << p.bits) - 1;
     const int64_t base = (int64_t)me * p.share;
@@ -134,6 +136,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_front_kernel(const SortPar
     const int per = p.share / kSortWarps;
     const int w0 = min(mine, w * per), w1 = min(mine, w0 + per);
     pdl_wait();
+    pdl_launch_dependents();   // in this order: see embed_clear_kernel
     for (int i = w0 + lane; i < w1; i += 32)
         buf[i] = ((unsigned long long)id_key(p, base + i) << 32) | (uint32_t)(base + i);
     for (int pass = 0; pass < p.passes; ++pass) {
@@ -186,19 +189,13 @@ __global__ void __launch_bounds__(kSortThreads) embed_front_kernel(const SortPar
 }
 
 // ---- more ids: in global memory -------------------------------------------------
-// Counts of the tile's digits. The first pass reads the ids themselves, and its
-// CTAs beyond the tiles clear rows.
+// Counts of the tile's digits. The first pass reads the ids themselves.
 template <bool FIRST>
 __global__ void __launch_bounds__(kSortThreads)
     sort_hist_kernel(const SortParams p, int src, int shift) {
-    __shared__ uint32_t h[FIRST ? kZeroRange / 32 : kSortBins];
+    __shared__ uint32_t h[kSortBins];
     pdl_launch_dependents();
     const int t = threadIdx.x;
-    if (FIRST && (int)blockIdx.x >= p.tiles) {
-        pdl_wait();
-        clear_absent(p, (int)blockIdx.x - p.tiles, h);
-        return;
-    }
     h[t] = 0;
     __syncthreads();
     pdl_wait();
@@ -245,11 +242,11 @@ template <bool FIRST>
 __global__ void __launch_bounds__(kSortThreads)
     sort_scatter_kernel(const SortParams p, int src, int shift) {
     __shared__ uint32_t cnt[kSortWarps][kSortBins];
-    pdl_launch_dependents();
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     for (int k = 0; k < kSortWarps; ++k) cnt[k][t] = 0;
     __syncthreads();
     pdl_wait();
+    pdl_launch_dependents();   // in this order: see embed_clear_kernel
     const uint32_t mask = (1u << p.bits) - 1;
     const int64_t base = (int64_t)blockIdx.x * kSortTile + w * (kSortPerThread * 32);
     uint32_t key[kSortPerThread], rank[kSortPerThread];
@@ -286,35 +283,29 @@ __global__ void __launch_bounds__(kSortThreads)
     }
 }
 
-static cudaError_t front_launch(SortParams& p, int sms, cudaStream_t s) {
+static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
     // 2048 ids a CTA, until there are 16 CTAs
     p.cluster = 1;
     while (p.cluster < kSortMaxCluster && p.n > (int64_t)p.cluster * 2048) p.cluster *= 2;
     const int64_t per = (p.n + p.cluster - 1) / p.cluster;
     p.share = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
-    // clearing CTAs: one for each SM the sort leaves, in whole clusters
-    p.zero_ctas = 0;
-    if (p.zero) {
-        const int left = sms > 2 * p.cluster ? sms - p.cluster : p.cluster;
-        p.zero_ctas = left / p.cluster * p.cluster;
-    }
-    const int smem = front_bytes(p.share, p.passes);
+    const int smem = cluster_bytes(p.share, p.passes);
     // the function's limits belong to a context: raised once in each, by each thread
     static thread_local unsigned long long prepared = 0;
     unsigned long long ctx = 0;
     cudaError_t err = current_context_id(&ctx);
     if (err != cudaSuccess) return err;
     if (ctx == 0 || prepared != ctx) {
-        err = cudaFuncSetAttribute(embed_front_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   front_bytes(kSortMaxShare, 2));
+        err = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   cluster_bytes(kSortMaxShare, 2));
         if (err == cudaSuccess)
-            err = cudaFuncSetAttribute(embed_front_kernel,
+            err = cudaFuncSetAttribute(embed_sort_kernel,
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess) return err;
         prepared = ctx;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.cluster + p.zero_ctas), 1, 1);
+    cfg.gridDim = dim3((unsigned)p.cluster, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
@@ -327,26 +318,17 @@ static cudaError_t front_launch(SortParams& p, int sms, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, embed_front_kernel, p);
+    return cudaLaunchKernelEx(&cfg, embed_sort_kernel, p);
 }
 
-cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess)
-        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return err;
-    p.passes = sort_passes(p.vocab);
-    p.bits = (sort_key_bits(p.vocab) + p.passes - 1) / p.passes;
-    if (p.n <= kSortClusterMax) return front_launch(p, sms, s);
-    p.zero_ctas = p.zero ? sms : 0;
+static cudaError_t sort_in_memory(const SortParams& p, cudaStream_t s) {
     const unsigned grid = (unsigned)p.tiles;
     for (int k = 0; k < p.passes; ++k) {
         // from one pair of arrays to the other, so that the last pass ends in [0]
         const int shift = k * p.bits, src = (p.passes - k) & 1;
-        err = k == 0 ? launch_pdl(sort_hist_kernel<true>, grid + (unsigned)p.zero_ctas,
-                                  kSortThreads, 0, s, p, src, shift)
-                     : launch_pdl(sort_hist_kernel<false>, grid, kSortThreads, 0, s, p, src, shift);
+        cudaError_t err =
+            k == 0 ? launch_pdl(sort_hist_kernel<true>, grid, kSortThreads, 0, s, p, src, shift)
+                   : launch_pdl(sort_hist_kernel<false>, grid, kSortThreads, 0, s, p, src, shift);
         if (err == cudaSuccess) err = launch_pdl(sort_scan_kernel, 1, kSortThreads, 0, s, p);
         if (err == cudaSuccess)
             err = k == 0 ? launch_pdl(sort_scatter_kernel<true>, grid, kSortThreads, 0, s, p, src,
@@ -356,6 +338,19 @@ cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;
+}
+
+cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
+    p.passes = sort_passes(p.vocab);
+    p.bits = (sort_key_bits(p.vocab) + p.passes - 1) / p.passes;
+    cudaError_t err = p.n <= kSortClusterMax ? sort_in_cluster(p, s) : sort_in_memory(p, s);
+    if (err != cudaSuccess || !p.zero) return err;
+    int dev = 0, sms = 0;
+    err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(embed_clear_kernel, (unsigned)sms, kClearThreads, 0, s, p);
 }
 
 }  // namespace rn

@@ -43,7 +43,7 @@
 
 namespace rn {
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpU = 4;              // vectors a thread holds of a batch (masked_w: 4)
 constexpr int kLpMaxCluster = 16;
@@ -204,7 +204,7 @@ struct Soft {
 // Candidates of a CTA.
 struct TopState {
     unsigned long long cand[kLpWarps][kTopCap];
-    unsigned long long best[kLpWarps * kMaxTop];
+    unsigned long long best[(kLpWarps > kLpMaxCluster ? kLpWarps : kLpMaxCluster) * kMaxTop];
     unsigned long long merged[kMaxTop];
     unsigned long long thr;
     float group[kTopGroups];
@@ -265,13 +265,15 @@ __device__ void row_again(const T* X, int V, float k, float m, float (*red)[4], 
 }
 
 template <typename T, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 2) logprob_fwd_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const LogprobParams p) {
     constexpr int VEC = Elem<T>::kVec;
     constexpr int NB = kLpU * VEC;    // elements of a batch, at most 32
     __shared__ float red[kLpWarps][4];
-    __shared__ __align__(8) float part[4];
+    __shared__ float parts[kLpMaxCluster][4];     // in a row's first CTA: every CTA's sums
+    __shared__ unsigned long long tops[TOP ? kLpMaxCluster : 1][kMaxTop];   // and candidates
     __shared__ TopState st;
     pdl_launch_dependents();
+    if (p.split > 1) cluster_arrive();            // (the peers write here: see below)
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     const float k = p.scale * kLog2e;
     const int V = p.vocab;
@@ -392,14 +394,22 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_fwd_kernel(const Logpro
                 One{});
     }
     // meet: lanes, warps, the CTAs of the cluster
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, a.m, o);
-        const float c2 = __shfl_xor_sync(0xffffffffu, a.c, o);
-        const float s2 = __shfl_xor_sync(0xffffffffu, a.s, o);
-        const float w2 = __shfl_xor_sync(0xffffffffu, a.w, o);
-        a.merge(m2, c2, s2, w2);
-    }
+    auto meet = [&](int lanes) {
+        for (int o = lanes / 2; o > 0; o >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, a.m, o);
+            const float c2 = __shfl_xor_sync(0xffffffffu, a.c, o);
+            const float s2 = __shfl_xor_sync(0xffffffffu, a.s, o);
+            const float w2 = __shfl_xor_sync(0xffffffffu, a.w, o);
+            a.merge(m2, c2, s2, w2);
+        }
+    };
+    auto take = [&](const float* v) {
+        a.m = v[0];
+        a.c = v[1];
+        a.s = v[2];
+        a.w = v[3];
+    };
+    meet(32);
     if (lane == 0) {
         red[w][0] = a.m;
         red[w][1] = a.c;
@@ -411,9 +421,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_fwd_kernel(const Logpro
         if (lane == 0) st.count[w] = cnt;
     }
     __syncthreads();
-    a.init();
-#pragma unroll
-    for (int i = 0; i < kLpWarps; ++i) a.merge(red[i][0], red[i][1], red[i][2], red[i][3]);
+    take(red[lane % kLpWarps]);
+    meet(kLpWarps);
     int total = 0;                        // the CTA's kept candidates, after each other in best
     if constexpr (TOP) {
         int before = 0;
@@ -439,30 +448,24 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_fwd_kernel(const Logpro
         __syncthreads();
     }
     if (p.split > 1) {
-        if (t == 0) {
-            part[0] = a.m;
-            part[1] = a.c;
-            part[2] = a.s;
-            part[3] = a.w;
-        }
-        cluster_sync();
-        if (rank == 0) {
-            for (int q = 1; q < p.split; ++q) {
-                const uint32_t at = peer_addr(part, q);
-                a.merge(peer_f32(at), peer_f32(at + 4), peer_f32(at + 8), peer_f32(at + 12));
-            }
-            if constexpr (TOP) {
-                // (a CTA with fewer than `top` columns leaves keys of 0)
-                total = p.split * p.top;
-                for (int i = t; i < total; i += kLpThreads) {
-                    const int q = i / p.top, j = i - q * p.top;
-                    st.best[i] = q == 0 ? st.merged[j] : peer_u64(peer_addr(&st.merged[j], q));
-                }
-            }
-        }
-        cluster_sync();   // the peers' shared memory has been read
-        if (rank != 0) return;
+        // every CTA leaves its results in the first one's shared memory, once that has started
+        cluster_wait();
+        if (t < 4) peer_store(peer_addr(&parts[rank][t], 0), t == 0   ? a.m
+                                                             : t == 1 ? a.c
+                                                             : t == 2 ? a.s
+                                                                      : a.w);
         if constexpr (TOP) {
+            // (a CTA with fewer than `top` columns leaves keys of 0)
+            if (t < p.top) peer_store(peer_addr(&tops[rank][t], 0), st.merged[t]);
+        }
+        cluster_arrive();
+        if (rank != 0) return;
+        cluster_wait();
+        take(parts[lane % p.split]);
+        meet(p.split);
+        if constexpr (TOP) {
+            total = p.split * p.top;
+            for (int i = t; i < total; i += kLpThreads) st.best[i] = tops[i / p.top][i % p.top];
             __syncthreads();
             merge_top();
             __syncthreads();
@@ -509,12 +512,12 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprob_fwd_kernel(const Logpro
     }
 }
 
-// CTAs a row is split over: as many as keep every SM at its two resident CTAs, while
-// each still has a whole batch of its threads to read.
+// CTAs a row is split over: as many as keep every SM at its four resident CTAs, while
+// each still has a whole batch of its threads to read. A power of two.
 inline int logprob_split(int64_t rows, int vocab, int vec, int sms) {
     const int64_t batches = (vocab / vec + kLpThreads * kLpU - 1) / (kLpThreads * kLpU);
     int c = 1;
-    while (c < kLpMaxCluster && rows * c * 2 <= 2 * (int64_t)sms && c * 2 <= batches) c *= 2;
+    while (c < kLpMaxCluster && rows * c * 2 <= 4 * (int64_t)sms && c * 2 <= batches) c *= 2;
     return c;
 }
 

@@ -126,8 +126,17 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ---- thread-block clusters --------------------------------------------------
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                  ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The address of this CTA's shared variable in the CTA of rank r of the cluster.
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t r) {
@@ -137,20 +146,13 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t r) {
                  : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(r));
     return a;
 }
-__device__ __forceinline__ float peer_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ uint32_t peer_u32(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ unsigned long long peer_u64(uint32_t a) {
-    unsigned long long v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-    return v;
+__device__ __forceinline__ void peer_store(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 __device__ __forceinline__ void peer_store(uint32_t a, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");

@@ -66,10 +66,9 @@ struct SortParams {
     int bits, passes;     // bits of a digit, digits
     int itype;
     int cluster, share;   // CTAs that sort in shared memory, ids of each
-    // Rows of ids that do not occur, cleared beside the sort (zero_ctas > 0)
+    // Rows of ids that do not occur, cleared beside the sort (NULL: left as they are)
     char* zero;
     int64_t zero_pitch, zero_bytes;   // bytes from row to row, and of a row
-    int zero_ctas;
 };
 constexpr int sort_key_bits(int64_t vocab) {
     int b = 0;
@@ -83,7 +82,10 @@ cudaError_t embed_sort_launch(SortParams p, cudaStream_t s);
 
 // dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum of dout[i] over the
 // positions i with tokens[i] == v, for the ids v that occur, from the sorted ids.
-constexpr int kEmbedChunk = 32;    // sorted positions one thread group sums: a lane each
+// Sorted positions one thread group sums, a lane each. Short batches get short chunks, so
+// that the GPU fills.
+constexpr int kEmbedChunkMax = 32;
+constexpr int embed_chunk(int64_t n, int64_t d) { return n <= ((int64_t)4 << 20) / d ? 8 : 32; }
 struct EmbedBwdParams {
     const void* dout;
     void* dtable;
@@ -93,6 +95,7 @@ struct EmbedBwdParams {
     int64_t n, vocab, d, dpad;
     int64_t lddo, ldg;
     int64_t chunks;
+    int chunk;                 // positions of a chunk
     int tx, ty;                // threads across a row, chunks of a CTA
     int slices;                // CTAs across a row
     float scale;

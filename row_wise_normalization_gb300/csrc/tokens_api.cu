@@ -90,7 +90,7 @@ EmbedWorkspace embed_workspace(int64_t n, int64_t d) {
         return o;
     };
     w.tiles = (n + kSortTile - 1) / kSortTile;
-    w.chunks = (n + kEmbedChunk - 1) / kEmbedChunk;
+    w.chunks = (n + embed_chunk(n, d) - 1) / embed_chunk(n, d);
     w.dpad = (d + 7) / 8 * 8;
     const bool global = n > kSortClusterMax;   // the sort's second arrays and its counts
     for (int k = 0; k < 2; ++k) {
@@ -107,7 +107,7 @@ bool embed_bwd_sizes_ok(int64_t n, int64_t vocab, int64_t d) {
     if (n < 0 || n > kMaxCount || vocab <= 0 || vocab > kMaxVocab || d <= 0 || d > kMaxWidth)
         return false;
     // (chunks x slices of the widest grid: 32 scalars a slice)
-    return (n / kEmbedChunk + 1) * (d / 32 + 1) < kMaxCount;
+    return (n / embed_chunk(n, d) + 1) * (d / 32 + 1) < kMaxCount;
 }
 
 bool host_resident(const void* p) {
@@ -224,6 +224,7 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
     p.lddo = lddo;
     p.ldg = ldg;
     p.chunks = w.chunks;
+    p.chunk = embed_chunk(n, d);
     p.scale = scale;
     p.accumulate = accumulate != 0;
     const int ne = access_elems(d, dout, es, lddo, dtable, gs, ldg);
