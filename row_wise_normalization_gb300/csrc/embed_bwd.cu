@@ -98,44 +98,45 @@ __global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBw
 }
 
 // The ids whose positions run over a chunk's edge. Each warp of a CTA looks at one
-// chunk and, if such an id begins in it, adds the id's sums of the chunks in order. An id
+// chunk and, if such an id begins in it, adds the id's sums of the chunks in order, kJoinCols
+// blocks of 128 columns at a time so that enough loads are in flight. An id
 // of more than kJoinMany chunks is left to the whole CTA: each warp takes every
-// kJoinWarps-th chunk, and the warps' sums are added in order. blockIdx.y takes blocks
-// of 32 * NE columns in turn.
+// kJoinWarps-th chunk, and the warps' sums are added in order. blockIdx.y takes the
+// blocks of columns in turn. (The sums lie in rows of their own, 16-byte aligned whatever
+// the gradient's rows are; `vec` says whether those are.)
 constexpr int kJoinWarps = 8;
 constexpr int kJoinMany = 16;
+constexpr int kJoinCols = 4;
+constexpr int kJoinBlock = 128;
 
-template <typename G, int NE>
-__device__ __forceinline__ void join_put(const EmbedBwdParams& p, uint32_t id, int64_t j,
+template <typename G>
+__device__ __forceinline__ void join_put(const EmbedBwdParams& p, bool vec, uint32_t id, int64_t j,
                                          const float* acc) {
-    float o[NE];
-    G* g = (G*)p.dtable + (int64_t)id * p.ldg + j;
-    if (p.accumulate) ld_elems<G, NE>(o, g);
+    G* const g = (G*)p.dtable + (int64_t)id * p.ldg + j;
+    auto value = [&](float old, float s) {
+        return p.accumulate ? fmaf(p.scale, s, old) : p.scale * s;
+    };
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec) {
+        if (p.accumulate) ld_elems<G, 4>(o, g);
 #pragma unroll
-    for (int k = 0; k < NE; ++k)
-        o[k] = p.accumulate ? fmaf(p.scale, acc[k], o[k]) : p.scale * acc[k];
-    st_elems<G, NE>(g, o);
-}
-
-// acc = the sums that chunks first, first + step, ... to last hold of the id that begins
-// in chunk c, at columns j ..
-template <int NE>
-__device__ __forceinline__ void join_sum(const EmbedBwdParams& p, float* acc, int64_t c,
-                                         int64_t first, int64_t last, int step, int64_t j) {
+        for (int k = 0; k < 4; ++k) o[k] = value(o[k], acc[k]);
+        st_elems<G, 4>(g, o);
+    } else {
 #pragma unroll
-    for (int k = 0; k < NE; ++k) acc[k] = 0.f;
-#pragma unroll 4
-    for (int64_t q = first; q <= last; q += step) {
-        float v[NE];
-        ld_elems<float, NE>(v, p.part + (2 * q + (q == c ? 1 : 0)) * p.dpad + j);
-#pragma unroll
-        for (int k = 0; k < NE; ++k) acc[k] += v[k];
+        for (int k = 0; k < 4; ++k)
+            if (j + k < p.d) {
+                if (p.accumulate) ld_elems<G, 1>(o + k, g + k);
+                o[k] = value(o[k], acc[k]);
+                st_elems<G, 1>(g + k, o + k);
+            }
     }
 }
 
-template <typename G, int NE>
-__global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const EmbedBwdParams p) {
-    __shared__ float sum[kJoinWarps][32 * NE];
+template <typename G>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    embed_join_kernel(const EmbedBwdParams p, bool vec) {
+    __shared__ float sum[kJoinWarps][kJoinBlock];
     __shared__ int64_t ends[kJoinWarps];      // last chunk of a long id (or -1)
     __shared__ uint32_t ids[kJoinWarps];
     pdl_launch_dependents();
@@ -173,32 +174,76 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const Embed
         ends[w] = many ? last : -1;
         ids[w] = cur;
     }
-    const int64_t col0 = (int64_t)blockIdx.y * 32 * NE + lane * NE;
-    const int64_t step = (int64_t)gridDim.y * 32 * NE;
-    float acc[NE];
+    const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
+    // chunk q's sum of the id that begins in chunk o, at block b
+    auto load = [&](float* v, int64_t q, int64_t o, int64_t b) {
+        const int64_t j = b * kJoinBlock + lane * 4;
+        if (j < p.d) {
+            ld_elems<float, 4>(v, p.part + (2 * q + (q == o ? 1 : 0)) * p.dpad + j);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = 0.f;
+        }
+    };
     if (last >= 0 && !many) {
-        for (int64_t j = col0; j < p.d; j += step) {
-            join_sum<NE>(p, acc, c, c, last, 1, j);
-            join_put<G, NE>(p, cur, j, acc);
+        for (int64_t b0 = blockIdx.y; b0 < blocks; b0 += (int64_t)gridDim.y * kJoinCols) {
+            float acc[kJoinCols][4];
+            // (the first two chunks, which every such id has, in one go)
+            float two[kJoinCols][4];
+#pragma unroll
+            for (int u = 0; u < kJoinCols; ++u) load(acc[u], c, c, b0 + u * gridDim.y);
+#pragma unroll
+            for (int u = 0; u < kJoinCols; ++u) load(two[u], c + 1, c, b0 + u * gridDim.y);
+            for (int64_t q = c + 2;; ++q) {
+#pragma unroll
+                for (int u = 0; u < kJoinCols; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[u][k] += two[u][k];
+                if (q > last) break;
+#pragma unroll
+                for (int u = 0; u < kJoinCols; ++u) load(two[u], q, c, b0 + u * gridDim.y);
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinCols; ++u) {
+                const int64_t j = (b0 + u * gridDim.y) * kJoinBlock + lane * 4;
+                if (j < p.d) join_put<G>(p, vec, cur, j, acc[u]);
+            }
         }
     }
     __syncthreads();
-    for (int k = 0; k < kJoinWarps; ++k) {
-        if (ends[k] < 0) continue;
-        for (int64_t j = col0; j - lane * NE < p.d; j += step) {
-            if (j < p.d) join_sum<NE>(p, acc, c0 + k, c0 + k + w, ends[k], kJoinWarps, j);
+    for (int m = 0; m < kJoinWarps; ++m) {
+        if (ends[m] < 0) continue;
+        for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int64_t q = c0 + m + w; q <= ends[m]; q += 8 * kJoinWarps) {
+                float v[8][4];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    if (q + u * kJoinWarps <= ends[m]) {
+                        load(v[u], q + u * kJoinWarps, c0 + m, b);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[k] += v[u][k];
+            }
             __syncthreads();
 #pragma unroll
-            for (int q = 0; q < NE; ++q) sum[w][lane * NE + q] = acc[q];
+            for (int k = 0; k < 4; ++k) sum[w][lane * 4 + k] = acc[k];
             __syncthreads();
+            const int64_t j = b * kJoinBlock + lane * 4;
             if (w == 0 && j < p.d) {
 #pragma unroll
-                for (int q = 0; q < NE; ++q) {
-                    acc[q] = sum[0][lane * NE + q];
+                for (int k = 0; k < 4; ++k) {
+                    acc[k] = sum[0][lane * 4 + k];
 #pragma unroll
-                    for (int r = 1; r < kJoinWarps; ++r) acc[q] += sum[r][lane * NE + q];
+                    for (int r = 1; r < kJoinWarps; ++r) acc[k] += sum[r][lane * 4 + k];
                 }
-                join_put<G, NE>(p, ids[k], j, acc);
+                join_put<G>(p, vec, ids[m], j, acc);
             }
         }
     }
@@ -210,7 +255,7 @@ static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
     cudaError_t err =
         launch_pdl(embed_bwd_kernel<T, G, NE>, (unsigned)ctas, kSegThreads, 0, s, p);
     if (err != cudaSuccess || p.chunks < 2) return err;
-    const int64_t blocks = (p.d + 32 * NE - 1) / (32 * NE);
+    const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.chunks - 1 + kJoinWarps - 1) / kJoinWarps),
                        (unsigned)(blocks < 8 ? blocks : 8), 1);
@@ -221,7 +266,7 @@ static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, embed_join_kernel<G, NE>, p);
+    return cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, NE % 4 == 0);
 }
 
 cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams& q,

@@ -27,14 +27,18 @@
 // Alternatives: the `top` largest logits, the lowest index first among equal
 // ones, found in the same pass. A candidate is a 64-bit key: the value's bits in
 // an order-preserving form above the complement of its index, so that keys
-// differ and compare as wanted. Each warp keeps up to kTopCap candidates in shared
-// memory, and a new one has to exceed the threshold `thr`, below which the row's `top`
-// best cannot lie: first the top-th largest of the maxima of 64 groups of threads
-// over the first batch (at least `top` elements reach it), then the top-th of any
-// warp that has filled its buffer and kept its `top` best. Past the first batch
-// a candidate is rare (about `top` for each doubling of the columns read), so that a
-// thread compares its batch's maximum, which it has anyway, and no more. The order
-// in which warps run changes which keys are tried, not which are kept.
+// differ and compare as wanted. Each warp keeps its newest candidates in shared
+// memory and its 32 best, sorted, in its lanes, and a new one has to exceed the
+// threshold `thr`, below which the row's `top` best cannot lie. It comes from groups of
+// threads: the top-th largest of the groups' maxima so far, since at least `top` elements
+// reach it. It is taken after the first batch, then each time the columns read have doubled, so
+// that about `top` candidates are met between two of them (2048 x 128000 BF16 with 8
+// alternatives: 139 us with the first threshold alone, 101 us with this). Past the first, no barrier is
+// needed: maxima only grow, and a stale one is a lower bound too. So is the top-th of what
+// a warp keeps. A batch without a candidate
+// costs a comparison of its maximum, which is there anyway; in one with a candidate, the warp
+// looks at the elements of the lane that has it, an element a lane. The order in which
+// warps run changes which keys are tried, not which are kept.
 #pragma once
 
 #include <type_traits>
@@ -47,10 +51,10 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpU = 4;              // vectors a thread holds of a batch (masked_w: 4)
 constexpr int kLpMaxCluster = 16;
-constexpr int kTopCap = 96;          // candidates of a warp: at least 2 * 32
+constexpr int kTopCap = 64;          // candidates a warp holds unsorted: 31 and 32 more
 constexpr int kTopGroups = 64;
 constexpr float kFar = 1e30f;
-static_assert(kMaxTop + 32 <= kTopCap, "a kept list and one round of lanes");
+static_assert(kMaxTop == 32, "a lane for each alternative");
 
 // Bits of x in an order that compares as unsigned integers do: -inf lowest, both
 // zeros equal, any NaN highest.
@@ -204,35 +208,45 @@ struct Soft {
 // Candidates of a CTA.
 struct TopState {
     unsigned long long cand[kLpWarps][kTopCap];
-    unsigned long long best[(kLpWarps > kLpMaxCluster ? kLpWarps : kLpMaxCluster) * kMaxTop];
-    unsigned long long merged[kMaxTop];
+    unsigned long long list[kLpMaxCluster][32];   // sorted lists of 32: the warps', the CTAs'
     unsigned long long thr;
     float group[kTopGroups];
-    int count[kLpWarps];
+    Raw<16> batch[kLpWarps][kLpU];   // the batch of the lane a warp looks at
 };
+static_assert(kLpWarps <= kLpMaxCluster, "TopState::list");
 
-// This warp's `top` best of its n candidates, to the front of its buffer, largest
-// first; returns how many. A key's place is the number of larger keys.
-__device__ __forceinline__ int warp_keep(unsigned long long* cand, int n, int top, int lane) {
-    constexpr int R = kTopCap / 32;
-    unsigned long long me[R];
-    int place[R];
+// Sorting networks over a warp's lanes, largest first, a value a lane: the last stage
+// orders a bitonic sequence, and all of them any sequence. Two sorted lists a and b
+// become the sorted 32 best of both by max(a[i], b[31 - i]) and a last stage.
+template <typename K>
+__device__ __forceinline__ K sort_stage(K v, int n, int lane) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        me[r] = r * 32 + lane < n ? cand[r * 32 + lane] : 0;
-        place[r] = 0;
+    for (int o = n / 2; o > 0; o >>= 1) {
+        const K h = __shfl_xor_sync(0xffffffffu, v, o);
+        const bool larger = ((lane & o) == 0) == ((lane & n) == 0);
+        v = (h > v) == larger ? h : v;
     }
-    for (int j = 0; j < n; ++j) {
-        const unsigned long long o = cand[j];
+    return v;
+}
+template <typename K>
+__device__ __forceinline__ K warp_sort(K v, int lane) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) place[r] += o > me[r];
+    for (int n = 2; n <= 32; n <<= 1) v = sort_stage(v, n, lane);
+    return v;
+}
+template <typename K>
+__device__ __forceinline__ K warp_merge(K a, K b, int lane) {
+    const K r = __shfl_sync(0xffffffffu, b, 31 - lane);
+    return sort_stage(r > a ? r : a, 32, lane);
+}
+
+// The n (a power of two, at most twice the warps) lists of st.list, merged into the first.
+// All threads; the lists are written and a barrier passed before.
+__device__ __forceinline__ void merge_lists(TopState& st, int n, int w, int lane) {
+    for (int h = n / 2; h > 0; h /= 2) {
+        if (w < h) st.list[w][lane] = warp_merge(st.list[w][lane], st.list[w + h][lane], lane);
+        __syncthreads();
     }
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (r * 32 + lane < n && place[r] < top) cand[place[r]] = me[r];
-    __syncwarp();
-    return n < top ? n : top;
 }
 
 // The values of a row that FP32 products cannot be referred to (see above), from
@@ -295,72 +309,58 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     if constexpr (TOP) {
         if (t == 0) st.thr = 0;
     }
-    bool first = true;
     pdl_wait();
-    // Candidates among the N elements of a batch whose maximum is mx. Elements of
-    // the same value as the threshold may be wanted (the lowest index first), and
-    // a NaN always is.
-    auto look = [&](auto elem, float mx, bool odd, auto col, auto in, auto n_const) {
-        constexpr int N = decltype(n_const)::value;
-        if (first) {
-            first = false;
-            constexpr int G = kLpThreads / kTopGroups;
-            float g = mx;
-#pragma unroll
-            for (int o = 1; o < G; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-            if (t % G == 0) st.group[t / G] = g;
-            __syncthreads();
-            if (t < kTopGroups) {
-                const float me = st.group[t];
-                int r = 0;
-                for (int j = 0; j < kTopGroups; ++j)
-                    r += st.group[j] > me || (st.group[j] == me && j < t);
-                // (a key without an index: every element of this value is above it)
-                if (r == p.top - 1 && me > -INFINITY)
-                    st.thr = (unsigned long long)order_bits(me) << 32;
-            }
-            __syncthreads();
-        }
-        unsigned long long thr = *(volatile unsigned long long*)&st.thr;
-        const float lo = order_value((uint32_t)(thr >> 32));   // NaN: no threshold yet
-        uint32_t pend = 0;
-        if (!(mx < lo) || odd) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (in(i) && !(elem(i) < lo)) pend |= 1u << i;
-        }
-        unsigned lanes = __ballot_sync(0xffffffffu, pend != 0);
-        while (lanes) {
-            // one candidate of every lane that has any
-            if (cnt + 32 > kTopCap) {
-                cnt = warp_keep(st.cand[w], cnt, p.top, lane);
-                if (cnt == p.top) {
-                    thr = st.cand[w][p.top - 1];
-                    if (lane == 0) atomicMax(&st.thr, thr);
-                }
-            }
-            unsigned long long key = 0;
-            if (pend) {
-                const int i = __ffs(pend) - 1;
-                pend &= pend - 1;
-                float v = elem(0);
-#pragma unroll
-                for (int q = 1; q < N; ++q) v = q == i ? elem(q) : v;
-                key = top_key(v, col(i));
-            }
-            const bool put = key > thr;
-            const unsigned who = __ballot_sync(0xffffffffu, put);
-            if (put) st.cand[w][cnt + __popc(who & ((1u << lane) - 1))] = key;
-            cnt += __popc(who);
-            __syncwarp();
-            lanes = __ballot_sync(0xffffffffu, pend != 0);
+    unsigned long long thr = 0;
+    unsigned long long kept = 0;          // this warp's 32 best so far, a lane each
+    // The first 32 of the warp's candidates (fewer: the rest are 0) into `kept`.
+    auto keep = [&]() {
+        __syncwarp();
+        const unsigned long long v = lane < cnt ? st.cand[w][lane] : 0;
+        kept = warp_merge(kept, warp_sort(v, lane), lane);
+        // (0 while there are fewer than `top`)
+        thr = max(thr, __shfl_sync(0xffffffffu, kept, p.top - 1));
+        const unsigned long long rest = 32 + lane < cnt ? st.cand[w][32 + lane] : 0;
+        __syncwarp();
+        st.cand[w][lane] = rest;
+        cnt = cnt > 32 ? cnt - 32 : 0;
+    };
+    // Keys of this warp's lanes, where they exceed the threshold.
+    auto append = [&](bool ok, float x, uint32_t col) {
+        const unsigned long long key = ok ? top_key(x, col) : 0;
+        const bool put = key > thr;
+        const unsigned who = __ballot_sync(0xffffffffu, put);
+        if (put) st.cand[w][cnt + __popc(who & ((1u << lane) - 1))] = key;
+        cnt += __popc(who);
+        if (cnt >= 32) {
+            keep();
+            if (lane == 0) atomicMax(&st.thr, thr);
         }
     };
-    using One = std::integral_constant<int, 1>;
-    using All = std::integral_constant<int, NB>;
-    if constexpr (TOP) __syncthreads();   // thr is set
-    for (int v0 = va; v0 < vb; v0 += kLpThreads * kLpU) {
-        Raw<16> r[kLpU];
+    // This thread's maximum so far, to its group's.
+    constexpr int kGroup = kLpThreads / kTopGroups;
+    volatile float* const groups = st.group;
+    auto tell = [&]() {
+        float g = a.m;
+#pragma unroll
+        for (int o = 1; o < kGroup; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+        if (t % kGroup == 0) groups[t / kGroup] = g;
+    };
+    // The threshold from the groups' maxima: a warp sorts them. (32 groups twice the size do
+    // for few alternatives; for 32 the least of 32 maxima would let 130 elements a
+    // doubling pass, that of 64 lets 44.) A key without an index: every element of this
+    // value is above it.
+    auto raise = [&]() {
+        float g = groups[lane];
+        const float h = groups[32 + lane];
+        if (p.top > 16)
+            g = warp_merge(warp_sort(g, lane), warp_sort(h, lane), lane);
+        else
+            g = warp_sort(fmaxf(g, h), lane);
+        g = __shfl_sync(0xffffffffu, g, p.top - 1);
+        if (g > -INFINITY) thr = max(thr, (unsigned long long)order_bits(g) << 32);
+    };
+    int turn = 0;                         // batches read
+    auto load = [&](Raw<16>* r, int v0) {
 #pragma unroll
         for (int u = 0; u < kLpU; ++u) {
             const int v = v0 + u * kLpThreads + t;
@@ -371,27 +371,56 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
                 for (int i = 0; i < 4; ++i) r[u].w[i] = raw_low<T>();
             }
         }
+    };
+    auto batch = [&](const Raw<16>* r, int v0) {
         const float mx = raw_max<T>(r);
         a.template add<T>(r, mx, k);
-        if constexpr (TOP)
-            look(
-                [&](int i) { return raw_elem<T>(r, i); }, mx, a.s != a.s,
-                [&](int i) {
-                    return (uint32_t)(head + (v0 + i / VEC * kLpThreads + t) * VEC + i % VEC);
-                },
-                [&](int i) { return v0 + i / VEC * kLpThreads + t < vb; }, All{});
+        if constexpr (TOP) {
+            if ((turn & (turn + 1)) == 0) {       // 1, 2, 4, ... batches read
+                tell();
+                if (turn == 0) {
+                    __syncthreads();              // (and st.thr is set)
+                    raise();
+                } else if (w == (turn & (kLpWarps - 1))) {
+                    raise();
+                    if (lane == 0) atomicMax(&st.thr, thr);
+                }
+            }
+            ++turn;
+            thr = max(thr, *(volatile unsigned long long*)&st.thr);
+            // (equal values may be wanted, a NaN always is; a threshold of 0 is a NaN)
+            const float lo = order_value((uint32_t)(thr >> 32));
+            unsigned lanes = __ballot_sync(0xffffffffu, !(mx < lo) || a.s != a.s);
+            while (lanes) {
+                const int from = __ffs(lanes) - 1;
+                lanes &= lanes - 1;
+                if (lane == from) {
+#pragma unroll
+                    for (int u = 0; u < kLpU; ++u) st.batch[w][u] = r[u];
+                }
+                __syncwarp();
+                const T* const e = reinterpret_cast<const T*>(st.batch[w]);
+                const int v = v0 + lane / VEC * kLpThreads + (w * 32 + from);
+                const bool in = lane < NB && v < vb;
+                const float x = in ? lds_f(e + lane) : 0.f;
+                append(in, x, (uint32_t)(head + v * VEC + lane % VEC));
+            }
+        }
+    };
+    constexpr int kStep = kLpThreads * kLpU;
+    Raw<16> r[kLpU];
+    for (int v0 = va; v0 < vb; v0 += kStep) {
+        load(r, v0);
+        batch(r, v0);
     }
     // head and tail: fewer than 2 * VEC elements, one a thread
-    if (extra > 0) {
+    if (t / 32 * 32 < extra) {
         const bool in = t < extra;
         const int c = t < head ? t : tail0 + t - head;
         float x = -INFINITY;
         if (in) x = ldt_x1(X + c);
         a.add(x, k);
-        if constexpr (TOP)
-            look(
-                [&](int) { return x; }, x, a.s != a.s, [&](int) { return (uint32_t)c; }, [&](int) { return in; },
-                One{});
+        if constexpr (TOP) append(in, x, (uint32_t)c);
     }
     // meet: lanes, warps, the CTAs of the cluster
     auto meet = [&](int lanes) {
@@ -417,36 +446,13 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
         red[w][3] = a.w;
     }
     if constexpr (TOP) {
-        cnt = warp_keep(st.cand[w], cnt, p.top, lane);
-        if (lane == 0) st.count[w] = cnt;
+        if (cnt > 0) keep();
+        st.list[w][lane] = kept;
     }
     __syncthreads();
     take(red[lane % kLpWarps]);
     meet(kLpWarps);
-    int total = 0;                        // the CTA's kept candidates, after each other in best
-    if constexpr (TOP) {
-        int before = 0;
-        for (int i = 0; i < kLpWarps; ++i) {
-            before += i < w ? st.count[i] : 0;
-            total += st.count[i];
-        }
-        if (lane < cnt) st.best[before + lane] = st.cand[w][lane];
-    }
-    // the CTA's `top` best of `total`, into merged
-    auto merge_top = [&]() {
-        for (int i = t; i < total; i += kLpThreads) {
-            const unsigned long long me = st.best[i];
-            int r = 0;
-            for (int j = 0; j < total; ++j) r += st.best[j] > me;
-            if (r < p.top) st.merged[r] = me;
-        }
-        if (t >= total && t < p.top) st.merged[t] = 0;
-    };
-    if constexpr (TOP) {
-        __syncthreads();
-        merge_top();
-        __syncthreads();
-    }
+    if constexpr (TOP) merge_lists(st, kLpWarps, w, lane);
     if (p.split > 1) {
         // every CTA leaves its results in the first one's shared memory, once that has started
         cluster_wait();
@@ -455,8 +461,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
                                                              : t == 2 ? a.s
                                                                       : a.w);
         if constexpr (TOP) {
-            // (a CTA with fewer than `top` columns leaves keys of 0)
-            if (t < p.top) peer_store(peer_addr(&tops[rank][t], 0), st.merged[t]);
+            // (a CTA with fewer columns leaves keys of 0)
+            if (t < 32) peer_store(peer_addr(&tops[rank][t], 0), st.list[0][t]);
         }
         cluster_arrive();
         if (rank != 0) return;
@@ -464,11 +470,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
         take(parts[lane % p.split]);
         meet(p.split);
         if constexpr (TOP) {
-            total = p.split * p.top;
-            for (int i = t; i < total; i += kLpThreads) st.best[i] = tops[i / p.top][i % p.top];
+            for (int q = w; q < p.split; q += kLpWarps) st.list[q][lane] = tops[q][lane];
             __syncthreads();
-            merge_top();
-            __syncthreads();
+            merge_lists(st, p.split, w, lane);
         }
     }
     const bool nan = a.s != a.s;
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     }
     if constexpr (TOP) {
         if (t < p.top) {
-            const unsigned long long key = st.merged[t];
+            const unsigned long long key = st.list[0][t];
             const uint32_t idx = ~(uint32_t)key;
             if (p.top_ids) {
                 if (p.itype == IT_I64)
