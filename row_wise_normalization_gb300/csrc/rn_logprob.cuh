@@ -15,9 +15,9 @@
 // pipe: 4 instructions a pair beside the two exponentials, so that the pass
 // stays below the time its bytes take even for 16-bit logits.
 //
-// A masked element (-inf) gives e = 0 and 0 * -inf = NaN in W: a batch whose W
-// comes out NaN is summed again with that product left out, so that rows without a
-// mask do not pay for the test. A row whose largest product is beyond 1e30
+// A masked element (-inf) gives e = 0, and 0 * -inf would be NaN in W: where entropies are
+// wanted, elements are held at -1e30 or above (NaN passes), where e is 0 as well: one packed
+// instruction a pair of BF16. A row whose largest product is beyond 2^24
 // (every column at a mask's lowest value, say) cannot be referred to c in FP32: it is
 // summed again, from differences of logits (row_again).
 //
@@ -49,11 +49,12 @@ namespace rn {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpU = 4;              // vectors a thread holds of a batch (masked_w: 4)
+constexpr int kLpU = 4;              // vectors a thread holds of a batch
 constexpr int kLpMaxCluster = 16;
 constexpr int kTopCap = 64;          // candidates a warp holds unsorted: 31 and 32 more
 constexpr int kTopGroups = 64;
-constexpr float kFar = 1e30f;
+constexpr float kRef = 16777216.f;  // references stay within 2^24: their rounding is below 1
+constexpr float kHeld = -1e30f;      // logits are held at this or above where entropies are wanted
 static_assert(kMaxTop == 32, "a lane for each alternative");
 
 // Bits of x in an order that compares as unsigned integers do: -inf lowest, both
@@ -103,41 +104,42 @@ __device__ __forceinline__ float raw_max(const Raw<16>* r) {
         return fmaxf(a, b);
     }
 }
-// Pair i, and element i, of the raw vectors.
-template <typename T>
-__device__ __forceinline__ F2 raw_pair(const Raw<16>* r, int i) {
-    if constexpr (sizeof(T) == 4) {
-        return f2(__uint_as_float(r[i / 2].w[i % 2 * 2]), __uint_as_float(r[i / 2].w[i % 2 * 2 + 1]));
-    } else {
-        float a, b;
-        unpack2(r[i / 4].w[i % 4], a, b, (T*)nullptr);
-        return f2(a, b);
-    }
-}
-template <typename T>
-__device__ __forceinline__ float raw_elem(const Raw<16>* r, int i) {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(r[i / 4].w[i % 4]);
-    else return half_to_f((uint16_t)(r[i / 8].w[i % 8 / 2] >> (i % 2 * 16)), (T*)nullptr);
-}
 template <typename T>
 constexpr uint32_t raw_low() {   // -inf in every element
     return sizeof(T) == 4 ? 0xff800000u
                           : (std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u);
 }
 
-// W of a batch that holds -inf: its products are left out. Not inlined, so that it
-// takes no registers of the pass.
-template <typename T>
-__device__ __noinline__ float masked_w(Raw<16> a, Raw<16> b, Raw<16> c, Raw<16> d, float k,
-                                       float ref) {
-    const Raw<16> r[kLpU] = {a, b, c, d};
-    float w = 0.f;
-#pragma unroll
-    for (int i = 0; i < kLpU * Elem<T>::kVec; ++i) {
-        const float z = fmaf(raw_elem<T>(r, i), k, -ref), e = ex2(z);
-        if (e != 0.f) w = fmaf(e, z, w);
+// Logits held at -1e30 or above, NaN kept: a pair of BF16, or an FP32 value.
+__device__ __forceinline__ uint32_t hold2(uint32_t w) {
+    uint32_t o;   // 0xf14a is BF16's -1e30
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(w), "r"(0xf14af14au));
+    return o;
+}
+__device__ __forceinline__ float hold1(float x) {
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(x), "f"(kHeld));
+    return o;
+}
+
+// Pair i of the raw vectors.
+template <typename T, bool HOLD>
+__device__ __forceinline__ F2 raw_pair(const Raw<16>* r, int i) {
+    float a, b;
+    if constexpr (sizeof(T) == 4) {
+        a = __uint_as_float(r[i / 2].w[i % 2 * 2]);
+        b = __uint_as_float(r[i / 2].w[i % 2 * 2 + 1]);
+    } else {
+        uint32_t w = r[i / 4].w[i % 4];
+        if constexpr (HOLD && std::is_same<T, __nv_bfloat16>::value) w = hold2(w);
+        unpack2(w, a, b, (T*)nullptr);
     }
-    return w;
+    // (FP16's own lowest value is an ordinary logit: held as FP32)
+    if constexpr (HOLD && !std::is_same<T, __nv_bfloat16>::value) {
+        a = hold1(a);
+        b = hold1(b);
+    }
+    return f2(a, b);
 }
 
 // Running (c, S, W) with the largest logit m; k = scale * log2(e).
@@ -146,7 +148,7 @@ struct Soft {
     float m, c, s, w;
     __device__ __forceinline__ void init() {
         m = -INFINITY;
-        c = -kFar;     // finite, so that -inf - c is -inf and no NaN arises
+        c = -kRef;
         s = 0.f;
         w = 0.f;
     }
@@ -159,7 +161,7 @@ struct Soft {
     __device__ __forceinline__ void reach(float mx, float k) {
         if (mx > m) {
             m = mx;
-            rescale(fminf(fmaxf(mx * k, -kFar), kFar));
+            rescale(fminf(fmaxf(mx * k, -kRef), kRef));
         }
     }
     // one element
@@ -175,10 +177,12 @@ struct Soft {
         constexpr int NP = kLpU * Elem<T>::kVec / 2;
         reach(mx, k);
         F2 s2 = f2s(0.f), w2 = f2s(0.f);
-        const F2 k2 = f2s(k), c2 = f2s(-c);
+        // (nothing above -inf yet: any reference but -kRef, above which a tiny scale might
+        // lift held values)
+        const F2 k2 = f2s(k), c2 = f2s(m == -INFINITY ? 0.f : -c);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            const F2 z = fma2(raw_pair<T>(r, i), k2, c2);
+            const F2 z = fma2(raw_pair<T, ENT>(r, i), k2, c2);
             float z0, z1;
             f2_get(z, z0, z1);
             const F2 e = f2(ex2(z0), ex2(z1));
@@ -190,9 +194,7 @@ struct Soft {
         s += a + b;
         if constexpr (ENT) {
             f2_get(w2, a, b);
-            float wb = a + b;
-            if (wb != wb) wb = masked_w<T>(r[0], r[1], r[2], r[3], k, c);
-            w += wb;
+            w += a + b;
         }
     }
     __device__ __forceinline__ void merge(float m2, float c2, float s2, float w2) {
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     }
     pdl_wait();
     unsigned long long thr = 0;
+    float lo = order_value(0);            // thr's value when last looked at
     unsigned long long kept = 0;          // this warp's 32 best so far, a lane each
     // The first 32 of the warp's candidates (fewer: the rest are 0) into `kept`.
     auto keep = [&]() {
@@ -387,10 +390,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
                 }
             }
             ++turn;
-            thr = max(thr, *(volatile unsigned long long*)&st.thr);
             // (equal values may be wanted, a NaN always is; a threshold of 0 is a NaN)
-            const float lo = order_value((uint32_t)(thr >> 32));
-            unsigned lanes = __ballot_sync(0xffffffffu, !(mx < lo) || a.s != a.s);
+            const bool odd = a.s != a.s;
+            unsigned lanes = __ballot_sync(0xffffffffu, !(mx < lo) || odd);
+            if (lanes) {   // with the other warps' threshold?
+                thr = max(thr, *(volatile unsigned long long*)&st.thr);
+                lo = order_value((uint32_t)(thr >> 32));
+                lanes = __ballot_sync(0xffffffffu, !(mx < lo) || odd);
+            }
             while (lanes) {
                 const int from = __ffs(lanes) - 1;
                 lanes &= lanes - 1;
@@ -475,10 +482,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
             merge_lists(st, p.split, w, lane);
         }
     }
-    const bool nan = a.s != a.s;
+    // (a scale with which kHeld is not far below every other product, or beyond FP32's
+    // range: the sums say nothing, and the row is summed again)
+    const bool odd = !(k > 1e-20f && k < 1e8f) && a.m > -INFINITY;
+    const bool nan = a.s != a.s && !odd;
     const bool none = a.m == -INFINITY && !nan;     // every logit is -inf
     float ref = a.c * kLn2, ls = logf(a.s), ws = a.w / a.s;
-    const bool far = !nan && !none && !(fabsf(a.m * k) < kFar) && fabsf(a.m) < INFINITY;
+    const bool far = !nan && !none && fabsf(a.m) < INFINITY &&
+                     (odd || !(fabsf(a.m * k) < kRef && fabsf(a.m) < -0.1f * kHeld));
     if (far) {
         row_again<T>(X, V, k, a.m, red, &ls, &ws);
         ref = a.m * p.scale;
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
         if (none || x == -INFINITY) return -INFINITY;
         if (far) return (x - a.m) * p.scale - ls;
         // (a mask's lowest value, times k, may be beyond FP32's range)
-        return (fabsf(x * k) < kFar ? fmaf(x, k, -a.c) * kLn2 : x * p.scale - ref) - ls;
+        return (fabsf(x * k) < kRef ? fmaf(x, k, -a.c) * kLn2 : x * p.scale - ref) - ls;
     };
     if (t == 0) {
         const float bad = __uint_as_float(0x7fffffffu);

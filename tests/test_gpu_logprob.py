@@ -114,6 +114,19 @@ def test_patterns(dtype, kind, vocab, top):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -60, 2.0 ** -13, 64.0, 2.0 ** 40])
+def test_extreme_scales_with_masks(dtype, scale):
+    rng = np.random.default_rng(21)
+    x = rounded(rng, (5, 2100), dtype, 3.0)
+    x[:, ::3] = float("-inf")
+    x[1] = torch.where(torch.isinf(x[1]), x[1], torch.finfo(DT[dtype]).min)
+    x[2, 1] = torch.finfo(DT[dtype]).max
+    x[3, 7:900] = torch.finfo(DT[dtype]).min
+    t = torch.tensor([1, 2, 4, 8, 3], device="cuda")
+    _check(x, t, scale, 4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_nan_and_infinity_poison_their_row_alone(dtype):
     rng = np.random.default_rng(8)
     x = rounded(rng, (6, 3001), dtype, 2.0)
