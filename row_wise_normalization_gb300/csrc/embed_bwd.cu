@@ -3,8 +3,7 @@
 // for the ids that occur (embed_sort.cu clears the rows of the others).
 //
 // Bytes bound it: dout read once, every row of the gradient written once. The
-// sorted positions are cut into chunks of 32 (8 in short batches), a lane for each of a
-// chunk's ids.
+// sorted positions are cut into chunks of 8 to 32, a lane for each position.
 // A group of threads takes one chunk and a slice of the columns, has 8 of the chunk's
 // rows in flight at a time, adds them in registers (FP32) and, where the id changes,
 // writes the id's row. An id whose positions run over a chunk's edge leaves its sum of
@@ -18,96 +17,129 @@ namespace rn {
 constexpr int kSegThreads = 256;
 constexpr int kSegU = 8;            // rows in flight
 
+// Vectors of NE elements a thread has of a row: 16 bytes, at most 4.
+template <typename T, int NE>
+constexpr int seg_vectors() {
+    return 16 / (NE * (int)sizeof(T)) < 4 ? 16 / (NE * (int)sizeof(T)) : 4;
+}
+
 template <typename T, typename G, int NE>
 __global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBwdParams p) {
-    static_assert(kEmbedChunkMax <= 32, "a lane for each position");
+    constexpr int M = seg_vectors<T, NE>();
     constexpr int B = NE * (int)sizeof(T);
     pdl_launch_dependents();
     G* const DG = (G*)p.dtable;
     const int tx = (int)threadIdx.x % p.tx, ty = (int)threadIdx.x / p.tx, lane = tx & 31;
     const int slice = (int)blockIdx.x % p.slices;
     const int64_t c = (int64_t)((int)blockIdx.x / p.slices) * p.ty + ty;
-    const int64_t j = ((int64_t)slice * p.tx + tx) * NE;
     if (c >= p.chunks) return;          // whole warps: tx is a multiple of 32
-    const bool on_row = j < p.d;
-    const T* const X = (const T*)p.dout + (on_row ? j : 0);
+    // this thread's vectors: every p.tx-th of the slice's
+    const int64_t j0 = ((int64_t)slice * M * p.tx + tx) * NE;
+    const int64_t step = (int64_t)p.tx * NE;
+    const T* const X = (const T*)p.dout + j0;
     const int64_t i0 = c * p.chunk;
-    const int cnt = (int)min((int64_t)p.chunk, p.n - i0);
+    const int len = (int)min((int64_t)p.chunk, p.n - i0);
     pdl_wait();
+    const uint32_t prev = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
+    const uint32_t next = i0 + len < p.n ? ld_u32(p.key + i0 + len) : 0xffffffffu;
     uint32_t my_key = 0xffffffffu;
     int32_t my_pos = 0;
-    if (lane < cnt) {
+    if (lane < len) {
         my_key = ld_u32(p.key + i0 + lane);
         my_pos = (int32_t)ld_u32((const uint32_t*)p.pos + i0 + lane);
     }
-    const uint32_t prev = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
-    const uint32_t next = i0 + cnt < p.n ? ld_u32(p.key + i0 + cnt) : 0xffffffffu;
-    uint32_t cur = __shfl_sync(0xffffffffu, my_key, 0);
-    bool open = prev == cur;            // cur began in an earlier chunk
-    float acc[NE];
+    // positions of ids outside the vocabulary come last: cnt without them
+    const int cnt = __popc(__ballot_sync(0xffffffffu, my_key < (uint32_t)p.vocab));
+    if (cnt == 0) return;
+    // bit i: position i begins an id; `open`: the chunk's first began in an earlier chunk
+    const uint32_t left = __shfl_up_sync(0xffffffffu, my_key, 1);
+    const unsigned heads = __ballot_sync(0xffffffffu, lane > 0 && my_key != left);
+    bool open = prev == __shfl_sync(0xffffffffu, my_key, 0);
+    F2 acc[M][(NE + 1) / 2];
+    auto clear = [&]() {
 #pragma unroll
-    for (int k = 0; k < NE; ++k) acc[k] = 0.f;
-    // cur's sum is complete as far as this chunk goes; `on`: it goes on in the next
-    auto put = [&](bool on) {
-        if (cur >= (uint32_t)p.vocab || !on_row) return;   // (ids outside the vocabulary)
-        if (open || on) {
-            st_elems<float, NE>(p.part + (2 * c + (open ? 0 : 1)) * p.dpad + j, acc);
-        } else {
-            G* g = DG + (int64_t)cur * p.ldg + j;
-            float o[NE];
-            if (p.accumulate) {
-                ld_elems<G, NE>(o, g);
+        for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int k = 0; k < NE; ++k) o[k] = fmaf(p.scale, acc[k], o[k]);
-            } else {
+            for (int k = 0; k < (NE + 1) / 2; ++k) acc[m][k] = f2s(0.f);
+    };
+    clear();
+    // The sum of the id of position i, complete as far as this chunk goes; `on`: it goes on in
+    // the next.
+    auto put = [&](int i, bool on) {
+        const uint32_t id = __shfl_sync(0xffffffffu, my_key, i);
+        float* const w = p.part + (2 * c + (open ? 0 : 1)) * p.dpad + j0;
+        G* const g = DG + (int64_t)id * p.ldg + j0;
 #pragma unroll
-                for (int k = 0; k < NE; ++k) o[k] = p.scale * acc[k];
+        for (int m = 0; m < M; ++m) {
+            if (j0 + m * step < p.d) {
+                float s[NE + 1], o[NE];
+#pragma unroll
+                for (int k = 0; k < (NE + 1) / 2; ++k) f2_get(acc[m][k], s[2 * k], s[2 * k + 1]);
+                if (open || on) {
+                    st_elems<float, NE>(w + m * step, s);
+                } else {
+                    if (p.accumulate) ld_elems<G, NE>(o, g + m * step);
+#pragma unroll
+                    for (int k = 0; k < NE; ++k)
+                        o[k] = p.accumulate ? fmaf(p.scale, s[k], o[k]) : p.scale * s[k];
+                    st_elems<G, NE>(g + m * step, o);
+                }
             }
-            st_elems<G, NE>(g, o);
+        }
+        open = false;
+    };
+    auto add = [&](const Raw<B>(&r)[M]) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            float v[NE + 1];
+            v[NE] = 0.f;
+            unpack<T, NE>(v, r[m]);
+#pragma unroll
+            for (int k = 0; k < (NE + 1) / 2; ++k)
+                acc[m][k] = add2(acc[m][k], f2(v[2 * k], v[2 * k + 1]));
         }
     };
     for (int i = 0; i < cnt; i += kSegU) {
-        uint32_t key[kSegU];
-        Raw<B> r[kSegU];
+        Raw<B> r[kSegU][M];
 #pragma unroll
         for (int u = 0; u < kSegU; ++u) {
-            key[u] = __shfl_sync(0xffffffffu, my_key, i + u);
-            const int64_t at = __shfl_sync(0xffffffffu, my_pos, i + u);
-            if (key[u] < (uint32_t)p.vocab) r[u] = ld_raw<B>(X + at * p.lddo);
+            const int64_t at = __shfl_sync(0xffffffffu, my_pos, (i + u) & 31);
+            if (i + u < cnt) {
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    if (j0 + m * step < p.d) r[u][m] = ld_raw<B>(X + at * p.lddo + m * step);
+            }
         }
+        const unsigned h = heads >> i;
 #pragma unroll
         for (int u = 0; u < kSegU; ++u) {
             if (i + u < cnt) {
-                if (key[u] != cur) {
-                    put(false);
-                    cur = key[u];
-                    open = false;
-#pragma unroll
-                    for (int k = 0; k < NE; ++k) acc[k] = 0.f;
+                if (h >> u & 1u) {
+                    put(i + u - 1, false);
+                    clear();
                 }
-                if (cur < (uint32_t)p.vocab) {
-                    float v[NE];
-                    unpack<T, NE>(v, r[u]);
-#pragma unroll
-                    for (int k = 0; k < NE; ++k) acc[k] += v[k];
-                }
+                add(r[u]);
             }
         }
     }
-    put(next == cur);
+    put(cnt - 1, next == __shfl_sync(0xffffffffu, my_key, cnt - 1));
 }
 
 // The ids whose positions run over a chunk's edge. Each warp of a CTA looks at one
-// chunk and, if such an id begins in it, adds the id's sums of the chunks in order, kJoinCols
-// blocks of 128 columns at a time so that enough loads are in flight. An id
-// of more than kJoinMany chunks is left to the whole CTA: each warp takes every
-// kJoinWarps-th chunk, and the warps' sums are added in order. blockIdx.y takes the
-// blocks of columns in turn. (The sums lie in rows of their own, 16-byte aligned whatever
-// the gradient's rows are; `vec` says whether those are.)
+// chunk and, if such an id begins in it and ends within kJoinWarps chunks, adds the id's sums of
+// the chunks in order, kJoinCols blocks of 128 columns at a time so that enough loads are in
+// flight. A longer id is left to the whole CTA, whose warps take its sums in turn; the
+// warps' sums are added in order. blockIdx.y takes the blocks of columns in turn.
+// In long batches an id may have thousands of sums, and it takes two launches: the
+// first also adds the kJoinWarps sums of every CTA whose chunks lie within one id, and the second
+// does the long ids with those.
+// (The sums lie in rows of their own, 16-byte aligned whatever the gradient's rows are;
+// `vec` says whether those are.)
 constexpr int kJoinWarps = 8;
-constexpr int kJoinMany = 16;
 constexpr int kJoinCols = 4;
 constexpr int kJoinBlock = 128;
+constexpr int kJoinOnce = 64;       // chunks up to which one launch does
+enum JoinStage : int { JOIN_ALL = 0, JOIN_SHORT = 1, JOIN_LONG = 2 };
 
 template <typename G>
 __device__ __forceinline__ void join_put(const EmbedBwdParams& p, bool vec, uint32_t id, int64_t j,
@@ -133,19 +165,34 @@ __device__ __forceinline__ void join_put(const EmbedBwdParams& p, bool vec, uint
     }
 }
 
+// A block's 128 columns of row q of the sums, 4 a lane.
+__device__ __forceinline__ void join_load(const EmbedBwdParams& p, float* v, int64_t q, int64_t b,
+                                          int lane) {
+    const int64_t j = b * kJoinBlock + lane * 4;
+    if (j < p.d) {
+        ld_elems<float, 4>(v, p.part + q * p.dpad + j);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = 0.f;
+    }
+}
+
 template <typename G>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    embed_join_kernel(const EmbedBwdParams p, bool vec) {
+    embed_join_kernel(const EmbedBwdParams p, bool vec, int stage) {
     __shared__ float sum[kJoinWarps][kJoinBlock];
-    __shared__ int64_t ends[kJoinWarps];      // last chunk of a long id (or -1)
-    __shared__ uint32_t ids[kJoinWarps];
+    __shared__ int64_t long_first, long_last;   // chunks of a long id that begins here (at most one)
+    __shared__ uint32_t long_id;
     pdl_launch_dependents();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c0 = (int64_t)blockIdx.x * kJoinWarps, c = c0 + w;
     const int64_t i0 = c * p.chunk, i1 = i0 + p.chunk;
+    const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
+    if (threadIdx.x == 0) long_first = -1;
     pdl_wait();
     int64_t last = -1;
     uint32_t cur = 0xffffffffu;
+    bool within = false;                 // the CTA's chunks lie within one id
     if (i1 < p.n) {
         // (loads together: most chunks need no more)
         const uint32_t before = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
@@ -153,47 +200,46 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const int64_t e = min(i1 + p.chunk, p.n) - 1;
         const uint32_t far = ld_u32(p.key + e);
         cur = ld_u32(p.key + i1 - 1);
+        if (stage == JOIN_SHORT) {
+            const int64_t g0 = c0 * p.chunk, g1 = g0 + (int64_t)kJoinWarps * p.chunk;
+            within = g0 > 0 && g1 < p.n && ld_u32(p.key + g0 - 1) == cur &&
+                     ld_u32(p.key + g1) == cur && cur < (uint32_t)p.vocab;
+        }
         if (cur < (uint32_t)p.vocab && after == cur && !(begin == cur && before == cur)) {
             last = c + 1;
             if (far == cur && e + 1 < p.n) {
-                // the first position after the id's
+                // the first position after the id's, in [lo, hi]: 32 places at a time
                 int64_t lo = e + 1, hi = p.n;
                 while (lo < hi) {
-                    const int64_t m = (lo + hi) >> 1;
-                    if (ld_u32(p.key + m) == cur)
-                        lo = m + 1;
-                    else
-                        hi = m;
+                    const int64_t w32 = (hi - lo + 31) / 32;
+                    const int64_t at = min(lo + (lane + 1) * w32, hi) - 1;
+                    const unsigned same = __ballot_sync(0xffffffffu, ld_u32(p.key + at) == cur);
+                    const int k = __popc(same);      // the first k places are the id's
+                    const int64_t from = lo + k * w32;
+                    lo = k == 32 ? hi : from;
+                    if (k < 32) hi = min(from + w32, hi) - 1;
                 }
                 last = (lo - 1) / p.chunk;
             }
         }
     }
-    const bool many = last - c > kJoinMany;
-    if (lane == 0) {
-        ends[w] = many ? last : -1;
-        ids[w] = cur;
+    const bool many = last - c >= kJoinWarps;
+    __syncthreads();
+    if (many && lane == 0) {
+        long_first = c;
+        long_last = last;
+        long_id = cur;
     }
-    const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
-    // chunk q's sum of the id that begins in chunk o, at block b
-    auto load = [&](float* v, int64_t q, int64_t o, int64_t b) {
-        const int64_t j = b * kJoinBlock + lane * 4;
-        if (j < p.d) {
-            ld_elems<float, 4>(v, p.part + (2 * q + (q == o ? 1 : 0)) * p.dpad + j);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = 0.f;
-        }
-    };
-    if (last >= 0 && !many) {
+    if (last >= 0 && !many && stage != JOIN_LONG) {
         for (int64_t b0 = blockIdx.y; b0 < blocks; b0 += (int64_t)gridDim.y * kJoinCols) {
-            float acc[kJoinCols][4];
+            float acc[kJoinCols][4], two[kJoinCols][4];
             // (the first two chunks, which every such id has, in one go)
-            float two[kJoinCols][4];
 #pragma unroll
-            for (int u = 0; u < kJoinCols; ++u) load(acc[u], c, c, b0 + u * gridDim.y);
+            for (int u = 0; u < kJoinCols; ++u)
+                join_load(p, acc[u], 2 * c + 1, b0 + u * gridDim.y, lane);
 #pragma unroll
-            for (int u = 0; u < kJoinCols; ++u) load(two[u], c + 1, c, b0 + u * gridDim.y);
+            for (int u = 0; u < kJoinCols; ++u)
+                join_load(p, two[u], 2 * (c + 1), b0 + u * gridDim.y, lane);
             for (int64_t q = c + 2;; ++q) {
 #pragma unroll
                 for (int u = 0; u < kJoinCols; ++u)
@@ -201,7 +247,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
                     for (int k = 0; k < 4; ++k) acc[u][k] += two[u][k];
                 if (q > last) break;
 #pragma unroll
-                for (int u = 0; u < kJoinCols; ++u) load(two[u], q, c, b0 + u * gridDim.y);
+                for (int u = 0; u < kJoinCols; ++u)
+                    join_load(p, two[u], 2 * q, b0 + u * gridDim.y, lane);
             }
 #pragma unroll
             for (int u = 0; u < kJoinCols; ++u) {
@@ -210,41 +257,67 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             }
         }
     }
-    __syncthreads();
-    for (int m = 0; m < kJoinWarps; ++m) {
-        if (ends[m] < 0) continue;
-        for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int64_t q = c0 + m + w; q <= ends[m]; q += 8 * kJoinWarps) {
-                float v[8][4];
+    if (within) {
+        // the sum of the CTA's chunks, in the place of the first one's
+        for (int64_t b = blockIdx.y + (int64_t)w * gridDim.y; b < blocks;
+             b += (int64_t)kJoinWarps * gridDim.y) {
+            float v[kJoinWarps][4];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    if (q + u * kJoinWarps <= ends[m]) {
-                        load(v[u], q + u * kJoinWarps, c0 + m, b);
-                    } else {
+            for (int u = 0; u < kJoinWarps; ++u) join_load(p, v[u], 2 * (c0 + u), b, lane);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
-                    }
-                }
+            for (int u = 1; u < kJoinWarps; ++u)
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[k] += v[u][k];
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sum[w][lane * 4 + k] = acc[k];
-            __syncthreads();
+                for (int k = 0; k < 4; ++k) v[0][k] += v[u][k];
             const int64_t j = b * kJoinBlock + lane * 4;
-            if (w == 0 && j < p.d) {
+            if (j < p.d) st_elems<float, 4>(p.part + 2 * c0 * p.dpad + j, v[0]);
+        }
+    }
+    __syncthreads();
+    if (long_first < 0 || stage == JOIN_SHORT) return;
+    // A long id: its sums are the first chunk's second row, the chunks up to the next CTA's,
+    // the CTAs' that lie within it (in the second of two launches), and the chunks that remain.
+    const int64_t first = long_first, end = long_last;
+    const int64_t ga = stage == JOIN_LONG ? first / kJoinWarps + 1 : 0;
+    const int64_t gb = stage == JOIN_LONG ? end / kJoinWarps : 0;   // (ga <= gb: see `many`)
+    const int64_t head = stage == JOIN_LONG ? ga * kJoinWarps - first : end + 1 - first;
+    const int64_t terms = stage == JOIN_LONG ? head + (gb - ga) + (end + 1 - gb * kJoinWarps) : head;
+    auto row = [&](int64_t t) {
+        if (t == 0) return 2 * first + 1;
+        if (t < head) return 2 * (first + t);
+        if (t < head + (gb - ga)) return 2 * (ga + t - head) * kJoinWarps;
+        return 2 * (gb * kJoinWarps + t - head - (gb - ga));
+    };
+    for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t t = w; t < terms; t += 8 * kJoinWarps) {
+            float v[8][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[k] = sum[0][lane * 4 + k];
+            for (int u = 0; u < 8; ++u) {
+                if (t + u * kJoinWarps < terms) {
+                    join_load(p, v[u], row(t + u * kJoinWarps), b, lane);
+                } else {
 #pragma unroll
-                    for (int r = 1; r < kJoinWarps; ++r) acc[k] += sum[r][lane * 4 + k];
+                    for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
                 }
-                join_put<G>(p, vec, ids[m], j, acc);
             }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] += v[u][k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[w][lane * 4 + k] = acc[k];
+        __syncthreads();
+        const int64_t j = b * kJoinBlock + lane * 4;
+        if (w == 0 && j < p.d) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[k] = sum[0][lane * 4 + k];
+#pragma unroll
+                for (int r = 1; r < kJoinWarps; ++r) acc[k] += sum[r][lane * 4 + k];
+            }
+            join_put<G>(p, vec, long_id, j, acc);
         }
     }
 }
@@ -266,17 +339,24 @@ static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, NE % 4 == 0);
+    const bool vec = NE % 4 == 0;
+    if (p.chunks <= kJoinOnce)
+        return cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, (int)JOIN_ALL);
+    err = cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, (int)JOIN_SHORT);
+    if (err != cudaSuccess) return err;
+    return cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, (int)JOIN_LONG);
 }
 
 cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams& q,
                              cudaStream_t s) {
     EmbedBwdParams p = q;
-    const int64_t vpr = p.d / ne;
+    const int bytes = ne * dtype_size(dtype);
+    const int m = 16 / bytes < 4 ? 16 / bytes : 4;      // seg_vectors
+    const int64_t vpt = (p.d / ne + m - 1) / m;         // threads a row could use
     p.tx = 32;
-    while (p.tx < kSegThreads && p.tx < vpr) p.tx *= 2;
+    while (p.tx < kSegThreads && p.tx < vpt) p.tx *= 2;
     p.ty = kSegThreads / p.tx;
-    p.slices = (int)((vpr + p.tx - 1) / p.tx);
+    p.slices = (int)((vpt + p.tx - 1) / p.tx);
 #define RN_GO(T, G)                                           \
     {                                                         \
         if (ne == 8) return embed_bwd_go<T, G, 8>(p, s);      \

@@ -55,6 +55,12 @@ __global__ void __launch_bounds__(kClearThreads) embed_clear_kernel(const SortPa
     const int t = threadIdx.x;
     const int64_t share = ((p.vocab + gridDim.x - 1) / gridDim.x + 31) / 32 * 32;
     const int64_t end = min(p.vocab, (int64_t)(blockIdx.x + 1) * share);
+    // the ids as 16-byte vectors, and fewer than two vectors' before and after
+    const int64_t per = 16 / index_size(p.itype);
+    const int64_t head = min(p.n, (int64_t)((0u - (unsigned)(uintptr_t)p.tokens) & 15u) /
+                                      index_size(p.itype));
+    const int64_t nv = (p.n - head) / per;
+    const char* const body = (const char*)p.tokens + head * index_size(p.itype);
     // threads of a row: as many 16-byte stores as it has, up to a warp's
     int lanes = 32;
     while (lanes > 1 && (lanes / 2) * 16 >= p.zero_bytes) lanes /= 2;
@@ -63,19 +69,32 @@ __global__ void __launch_bounds__(kClearThreads) embed_clear_kernel(const SortPa
         __syncthreads();
         for (int w = t; w < (cnt + 31) / 32; w += kClearThreads) bits[w] = 0;
         __syncthreads();
+        auto mark = [&](int64_t id) {
+            const uint64_t k = (uint64_t)id - (uint64_t)lo;
+            if (k < (uint64_t)cnt) atomicOr(&bits[k >> 5], 1u << (k & 31));
+        };
+        // Many loads in flight: once the first CTAs store, a load waits behind their stores
+        // (8-byte loads, twice as many rounds: some CTAs read 65536 ids for 98 us).
         constexpr int U = 8;
-        for (int64_t i = t; i < p.n; i += kClearThreads * U) {
-            int64_t id[U];
+        for (int64_t v = t; v < nv; v += kClearThreads * U) {
+            Raw<16> r[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                id[u] = i + u * kClearThreads < p.n
-                            ? ld_id(p.tokens, i + u * kClearThreads, p.itype) : -1;
+                if (v + u * kClearThreads < nv) r[u] = ld_raw<16>(body + (v + u * kClearThreads) * 16);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const uint64_t k = (uint64_t)id[u] - (uint64_t)lo;
-                if (k < (uint64_t)cnt) atomicOr(&bits[k >> 5], 1u << (k & 31));
+                if (v + u * kClearThreads < nv) {
+                    if (p.itype == IT_I64) {
+                        mark((int64_t)((uint64_t)r[u].w[1] << 32 | r[u].w[0]));
+                        mark((int64_t)((uint64_t)r[u].w[3] << 32 | r[u].w[2]));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mark((int32_t)r[u].w[k]);
+                    }
+                }
             }
         }
+        if (t < p.n - nv * per) mark(ld_id(p.tokens, t < head ? t : nv * per + t, p.itype));
         __syncthreads();
         for (int r = t / lanes; r < cnt; r += kClearThreads / lanes)
             if (!((bits[r >> 5] >> (r & 31)) & 1u))

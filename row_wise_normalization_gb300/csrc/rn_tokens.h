@@ -82,10 +82,13 @@ cudaError_t embed_sort_launch(SortParams p, cudaStream_t s);
 
 // dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum of dout[i] over the
 // positions i with tokens[i] == v, for the ids v that occur, from the sorted ids.
-// Sorted positions one thread group sums, a lane each. Short batches get short chunks, so
-// that the GPU fills.
-constexpr int kEmbedChunkMax = 32;
-constexpr int embed_chunk(int64_t n, int64_t d) { return n <= ((int64_t)4 << 20) / d ? 8 : 32; }
+// Sorted positions one thread group sums, 8 to 32 (a lane each): as many as leave 2048 groups
+// of CTA size, several rounds of what the GPU holds at once.
+constexpr int embed_chunk(int64_t n, int64_t d) {
+    int c = 8;
+    while (c < 32 && n / (2 * c) * ((d + 2047) / 2048) >= 2048) c *= 2;
+    return c;
+}
 struct EmbedBwdParams {
     const void* dout;
     void* dtable;
