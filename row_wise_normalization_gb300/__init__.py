@@ -343,315 +343,15 @@ def rms_bwd(dy, x, w, eps: float = 1e-5, *, dx=None, dw=None, param_grads: bool 
     return dx, dw
 
 
-# ---------------------------------------------------------------------------
-# token operators
-#
-# A decoding step waits for the host side of these calls, not for their kernels
-# (a few microseconds each), so what they check is written to be checked fast:
-# types by one dictionary, contiguous device tensors first, the current device
-# and stream left alone unless the call names others.
-# ---------------------------------------------------------------------------
-_CODES = {}
+
+_TOKENS = ("embed_fwd", "embed_bwd", "logprob_fwd", "logprob_bwd")
 
 
-def _codes():
-    import torch
+def __getattr__(name):
+    # the token operators, whose module imports torch
+    if name in _TOKENS:
+        from . import tokens
 
-    if not _CODES:
-        _CODES.update({torch.float32: capi.RN_DTYPE_F32, torch.bfloat16: capi.RN_DTYPE_BF16,
-                       torch.float16: capi.RN_DTYPE_F16, torch.int32: capi.RN_INDEX_I32,
-                       torch.int64: capi.RN_INDEX_I64})
-    return _CODES
-
-
-def _values(name, t):
-    """The storage code of a floating-point tensor."""
-    try:
-        code = _codes()[t.dtype]
-        if t.dtype.is_floating_point:
-            return code
-    except (AttributeError, KeyError):
-        pass
-    if not hasattr(t, "dtype"):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    raise TypeError(f"unsupported dtype {t.dtype} (float32, bfloat16 or float16)")
-
-
-def _ids(name, t):
-    """The index code of a contiguous tensor of ids."""
-    try:
-        code = _codes()[t.dtype]
-        if not t.dtype.is_floating_point:
-            if not (t.is_cuda and t.is_contiguous()):
-                _check_f32_cuda(name, t, t.dtype)
-            return code
-    except (AttributeError, KeyError):
-        pass
-    if not hasattr(t, "dtype"):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
-
-
-def _row_floats(name, t, rows):
-    """Address of an FP32 vector of a value a row (0 for None)."""
-    if t is None:
-        return 0
-    import torch
-
-    if not (getattr(t, "is_cuda", False) and t.dtype is torch.float32 and t.is_contiguous()):
-        _check_f32_cuda(name, t)
-    if t.numel() != rows:
-        raise ValueError(f"{name} must have {rows} elements")
-    return t.data_ptr()
-
-
-def _matrix(name, t, d, dtype):
-    """(rows, row stride) of a typed matrix of rows of d (see _rows_of)."""
-    if t.is_cuda and t.dtype is dtype and t.is_contiguous() and d > 0:
-        return t.numel() // d, d
-    _check_f32_cuda(name, t, dtype, contiguous=False)
-    return _rows_of(name, t, d)
-
-
-def _device_of(tensors):
-    """The one device of a call's CUDA tensors (None where all are in host
-    memory)."""
-    dev = None
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on {dev} and on {t.device}")
-    return dev
-
-
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _elsewhere(dev, stream):
-    """Whether a call needs another device or stream made current first."""
-    import torch
-
-    return stream is not None or (dev is not None and dev.index != torch.cuda.current_device())
-
-
-class _On:
-    """Makes the call's device current and, where the caller gives a stream of
-    its own, that stream too, so that the memory the call allocates belongs to the
-    stream that uses it."""
-
-    def __init__(self, dev, stream):
-        import torch
-
-        if isinstance(stream, int):
-            # (handle 0: the legacy default stream, torch's default stream)
-            stream = (torch.cuda.ExternalStream(stream, device=dev) if stream
-                      else torch.cuda.default_stream(dev))
-        elif stream is not None and dev is not None and stream.device != dev:
-            raise ValueError(f"stream belongs to {stream.device}, the tensors to {dev}")
-        self._inner = [torch.cuda.stream(stream)]
-        if dev is not None:
-            self._inner.insert(0, torch.cuda.device(dev))
-
-    def __enter__(self):
-        for c in self._inner:
-            c.__enter__()
-
-    def __exit__(self, *exc):
-        for c in reversed(self._inner):
-            c.__exit__(*exc)
-
-
-def _current_stream(dev):
-    """Handle of the current stream of the call's device (of the current device,
-    where every tensor is in host memory)."""
-    import torch
-
-    if dev is None:
-        return torch.cuda.current_stream().cuda_stream
-    return torch._C._cuda_getCurrentRawStream(dev.index)
-
-
-def _new(home, dev, shape, dtype):
-    """An output on the call's device, or in host memory like `home`."""
-    import torch
-
-    if dev is not None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    return _empty_like_home(home, shape, dtype)
-
-
-def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
-    """Embedding rows ``scale * table[tokens]``.
-
-    tokens: int32 or int64 ids of any shape; an id outside ``[0, vocab)`` gives a
-    row of zeros. table: ``[vocab, d]``, float32, bfloat16 or float16, contiguous
-    or a row-strided view. Returns ``out`` of shape ``tokens.shape + (d,)`` in the
-    table's type (``out`` may also be passed as a 2-D row-strided view).
-    """
-    dtype = getattr(table, "dtype", None)
-    code = _values("table", table)
-    it = _ids("tokens", tokens)
-    if table.dim() != 2:
-        raise ValueError("table must be 2-D")
-    vocab, d = table.shape
-    _, ldt = _matrix("table", table, d, dtype)
-    dev = _device_of((table, tokens, out))
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
-            return embed_fwd(tokens, table, scale, out=out)
-    n = tokens.numel()
-    if out is None:
-        out, ldo = _new(table, dev, (*tokens.shape, d), dtype), d
-    else:
-        if out.numel() != n * d or out.shape[-1:] != (d,):
-            raise ValueError(f"out must hold {n} rows of {d}")
-        _, ldo = _matrix("out", out, d, dtype)
-    capi.check(capi.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt, out.data_ptr(),
-                              ldo, n, vocab, d, float(scale), _current_stream(dev)))
-    return out
-
-
-def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtable=None,
-              accumulate: bool = False, workspace=None, stream=None):
-    """Gradient of ``embed_fwd`` with respect to the table.
-
-    dout: the rows' gradient, shape ``tokens.shape + (d,)`` (or a 2-D row-strided
-    view). Returns ``dtable`` of shape ``[vocab, d]`` in ``dtype`` (dout's type
-    unless given; float32 is the other choice), every row written; with
-    ``accumulate`` the sums are added to the ``dtable`` passed in.
-    ``workspace``: a contiguous CUDA tensor of at least
-    ``capi.embed_bwd_workspace_size(n, vocab, d)`` bytes (allocated if not given).
-    """
-    import torch
-
-    code = _values("dout", dout)
-    it = _ids("tokens", tokens)
-    n = tokens.numel()
-    if dout.dim() < 1:
-        raise ValueError("dout must have a last dimension")
-    d = dout.shape[-1]
-    if dout.numel() != n * d:
-        raise ValueError(f"dout must hold {n} rows of {d}")
-    _, lddo = _matrix("dout", dout, d, dout.dtype)
-    if dtable is None:
-        if accumulate:
-            raise ValueError("accumulate needs a dtable to add to")
-        gdtype = dout.dtype if dtype is None else dtype
-    else:
-        gdtype = dtable.dtype
-        if dtype is not None and dtype != gdtype:
-            raise TypeError(f"dtable is {gdtype}, dtype says {dtype}")
-    if gdtype not in (dout.dtype, torch.float32):
-        raise TypeError(f"dtable must be {dout.dtype} or float32")
-    dev = _device_of((dout, tokens, dtable, workspace))
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
-            return embed_bwd(dout, tokens, vocab, scale, dtype=dtype, dtable=dtable,
-                             accumulate=accumulate, workspace=workspace)
-    if dtable is None:
-        dtable, ldg = _new(dout, dev, (vocab, d), gdtype), d
-    else:
-        if tuple(dtable.shape) != (vocab, d):
-            raise ValueError(f"dtable must be of shape [{vocab}, {d}]")
-        _, ldg = _matrix("dtable", dtable, d, gdtype)
-    if workspace is None:
-        nbytes = capi.embed_bwd_workspace_size(n, vocab, d)
-        workspace = torch.empty(nbytes, dtype=torch.uint8,
-                                device=dev if dev is not None else "cuda")
-    else:
-        if not (workspace.is_cuda and workspace.is_contiguous()):
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        nbytes = workspace.numel() * workspace.element_size()
-    capi.check(capi.embed_bwd(code, _values("dtable", dtable), it, dout.data_ptr(), lddo,
-                              tokens.data_ptr(), dtable.data_ptr(), ldg, n, vocab, d,
-                              float(scale), 1 if accumulate else 0, workspace.data_ptr(), nbytes,
-                              _current_stream(dev)))
-    return dtable
-
-
-def logprob_fwd(logits, targets=None, scale: float = 1.0, *, top: int = 0,
-                want_entropy: bool = True, stream=None):
-    """Log probabilities over the last dimension of ``logits`` times ``scale`` (the
-    inverse temperature).
-
-    logits: float32, bfloat16 or float16, contiguous or a 2-D row-strided view.
-    targets: int32 or int64 columns of shape ``logits.shape[:-1]``; one outside
-    ``[0, vocab)`` gets 0. Returns ``(logp, entropy, lse, top_ids, top_logp)``:
-    the targets' log probabilities (None without targets), the entropies (None
-    without ``want_entropy``), the log-sum-exps, and the ``top`` (at most 32)
-    largest columns with their log probabilities, shape ``[..., top]``, largest
-    first and the lowest column first among equal ones (None with ``top`` 0).
-    Values are float32; top_ids has targets' type (int64 without targets).
-    """
-    import torch
-
-    code = _values("logits", logits)
-    if logits.dim() < 1:
-        raise ValueError("logits must have a last dimension")
-    vocab = logits.shape[-1]
-    rows, ldl = _matrix("logits", logits, vocab, logits.dtype)
-    lead = logits.shape[:-1]
-    it, itype, tgt = capi.RN_INDEX_I64, torch.int64, 0
-    if targets is not None:
-        it, itype, tgt = _ids("targets", targets), targets.dtype, targets.data_ptr()
-        if targets.numel() != rows:
-            raise ValueError(f"targets must have {rows} elements")
-    dev = _device_of((logits, targets))
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
-            return logprob_fwd(logits, targets, scale, top=top, want_entropy=want_entropy)
-    f32 = torch.float32
-    logp = entropy = ids = top_logp = None
-    if targets is not None:
-        logp = _new(logits, dev, lead, f32)
-    if want_entropy:
-        entropy = _new(logits, dev, lead, f32)
-    lse = _new(logits, dev, lead, f32)
-    if top > 0:
-        ids = _new(logits, dev, (*lead, top), itype)
-        top_logp = _new(logits, dev, (*lead, top), f32)
-    capi.check(capi.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, _ptr(logp), _ptr(entropy),
-                                lse.data_ptr(), _ptr(ids), _ptr(top_logp), rows, vocab, int(top),
-                                float(scale), _current_stream(dev)))
-    return logp, entropy, lse, ids, top_logp
-
-
-def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=None, entropy=None,
-                dlogits=None, stream=None):
-    """Gradient of ``logprob_fwd``'s log probabilities (dlogp) and, where
-    ``dentropy`` is given with the forward call's ``entropy``, of its entropies,
-    with respect to the logits. dlogp may be None (then targets too). ``dlogits``:
-    allocated in the logits' type unless given; it may be ``logits`` itself.
-    """
-    code = _values("logits", logits)
-    if logits.dim() < 1:
-        raise ValueError("logits must have a last dimension")
-    vocab = logits.shape[-1]
-    rows, ldl = _matrix("logits", logits, vocab, logits.dtype)
-    it, tgt = capi.RN_INDEX_I64, 0
-    if targets is not None:
-        it, tgt = _ids("targets", targets), targets.data_ptr()
-        if targets.numel() != rows:
-            raise ValueError(f"targets must have {rows} elements")
-    if lse is None:
-        raise TypeError("lse must be a torch.Tensor")
-    rows_of = [_row_floats(n, t, rows) for n, t in (("dlogp", dlogp), ("dentropy", dentropy),
-                                                    ("lse", lse), ("entropy", entropy))]
-    dev = _device_of((logits, dlogp, targets, lse, dentropy, entropy, dlogits))
-    if _elsewhere(dev, stream):
-        with _On(dev, stream):
-            return logprob_bwd(dlogp, logits, targets, lse, scale, dentropy=dentropy,
-                               entropy=entropy, dlogits=dlogits)
-    if dlogits is None:
-        dlogits, ldd = _new(logits, dev, logits.shape, logits.dtype), vocab
-    else:
-        if dlogits.numel() != logits.numel() or dlogits.shape[-1] != vocab:
-            raise ValueError("dlogits must be shaped like logits")
-        _, ldd = _matrix("dlogits", dlogits, vocab, logits.dtype)
-    capi.check(capi.logprob_bwd(code, it, rows_of[0], rows_of[1], logits.data_ptr(), ldl, tgt,
-                                rows_of[2], rows_of[3], dlogits.data_ptr(), ldd, rows, vocab,
-                                float(scale), _current_stream(dev)))
-    return dlogits
+        globals().update({n: getattr(tokens, n) for n in _TOKENS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -24,7 +24,7 @@ constexpr int seg_vectors() {
 }
 
 template <typename T, typename G, int NE>
-__global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBwdParams p) {
+__global__ void __launch_bounds__(kSegThreads, 4) embed_bwd_kernel(const EmbedBwdParams p) {
     constexpr int M = seg_vectors<T, NE>();
     constexpr int B = NE * (int)sizeof(T);
     pdl_launch_dependents();
@@ -55,12 +55,11 @@ __global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBw
     const uint32_t left = __shfl_up_sync(0xffffffffu, my_key, 1);
     const unsigned heads = __ballot_sync(0xffffffffu, lane > 0 && my_key != left);
     bool open = prev == __shfl_sync(0xffffffffu, my_key, 0);
-    F2 acc[M][(NE + 1) / 2];
+    constexpr int E = M * NE;           // elements of this thread, in pairs
+    F2 acc[E / 2];
     auto clear = [&]() {
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-            for (int k = 0; k < (NE + 1) / 2; ++k) acc[m][k] = f2s(0.f);
+        for (int k = 0; k < E / 2; ++k) acc[k] = f2s(0.f);
     };
     clear();
     // The sum of the id of position i, complete as far as this chunk goes; `on`: it goes on in
@@ -69,19 +68,21 @@ __global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBw
         const uint32_t id = __shfl_sync(0xffffffffu, my_key, i);
         float* const w = p.part + (2 * c + (open ? 0 : 1)) * p.dpad + j0;
         G* const g = DG + (int64_t)id * p.ldg + j0;
+        float s[E];
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) f2_get(acc[k], s[2 * k], s[2 * k + 1]);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             if (j0 + m * step < p.d) {
-                float s[NE + 1], o[NE];
-#pragma unroll
-                for (int k = 0; k < (NE + 1) / 2; ++k) f2_get(acc[m][k], s[2 * k], s[2 * k + 1]);
                 if (open || on) {
-                    st_elems<float, NE>(w + m * step, s);
+                    st_elems<float, NE>(w + m * step, s + m * NE);
                 } else {
+                    float o[NE];
                     if (p.accumulate) ld_elems<G, NE>(o, g + m * step);
 #pragma unroll
                     for (int k = 0; k < NE; ++k)
-                        o[k] = p.accumulate ? fmaf(p.scale, s[k], o[k]) : p.scale * s[k];
+                        o[k] = p.accumulate ? fmaf(p.scale, s[m * NE + k], o[k])
+                                            : p.scale * s[m * NE + k];
                     st_elems<G, NE>(g + m * step, o);
                 }
             }
@@ -89,15 +90,11 @@ __global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBw
         open = false;
     };
     auto add = [&](const Raw<B>(&r)[M]) {
+        float v[E];
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            float v[NE + 1];
-            v[NE] = 0.f;
-            unpack<T, NE>(v, r[m]);
+        for (int m = 0; m < M; ++m) unpack<T, NE>(v + m * NE, r[m]);
 #pragma unroll
-            for (int k = 0; k < (NE + 1) / 2; ++k)
-                acc[m][k] = add2(acc[m][k], f2(v[2 * k], v[2 * k + 1]));
-        }
+        for (int k = 0; k < E / 2; ++k) acc[k] = add2(acc[k], f2(v[2 * k], v[2 * k + 1]));
     };
     for (int i = 0; i < cnt; i += kSegU) {
         Raw<B> r[kSegU][M];
@@ -131,15 +128,17 @@ __global__ void __launch_bounds__(kSegThreads, 3) embed_bwd_kernel(const EmbedBw
 // flight. A longer id is left to the whole CTA, whose warps take its sums in turn; the
 // warps' sums are added in order. blockIdx.y takes the blocks of columns in turn.
 // In long batches an id may have thousands of sums, and it takes two launches: the
-// first also adds the kJoinWarps sums of every CTA whose chunks lie within one id, and the second
-// does the long ids with those.
+// first also adds the kJoinWarps sums of every CTA whose chunks lie within one id, and lists the
+// long ids; the second does those, in any order, with the CTAs' sums.
 // (The sums lie in rows of their own, 16-byte aligned whatever the gradient's rows are;
 // `vec` says whether those are.)
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCols = 4;
 constexpr int kJoinBlock = 128;
 constexpr int kJoinOnce = 64;       // chunks up to which one launch does
-enum JoinStage : int { JOIN_ALL = 0, JOIN_SHORT = 1, JOIN_LONG = 2 };
+struct alignas(16) LongId {          // its first and last chunk
+    uint32_t first, last, id, pad;
+};
 
 template <typename G>
 __device__ __forceinline__ void join_put(const EmbedBwdParams& p, bool vec, uint32_t id, int64_t j,
@@ -177,22 +176,89 @@ __device__ __forceinline__ void join_load(const EmbedBwdParams& p, float* v, int
     }
 }
 
+// The sum of a long id, by a CTA: its sums are the first chunk's second row, the chunks up to
+// the next CTA's, the CTAs' that lie within it (`grouped`), and the chunks that remain.
+template <typename G>
+__device__ __forceinline__ void join_long(const EmbedBwdParams& p, bool vec, bool grouped,
+                                          const LongId& id, float (*sum)[kJoinBlock]) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = id.first, end = id.last;
+    const int64_t ga = grouped ? first / kJoinWarps + 1 : 0;
+    const int64_t gb = grouped ? end / kJoinWarps : 0;   // (ga <= gb: it spans kJoinWarps chunks more)
+    const int64_t head = grouped ? ga * kJoinWarps - first : end + 1 - first;
+    const int64_t terms = grouped ? head + (gb - ga) + (end + 1 - gb * kJoinWarps) : head;
+    auto row = [&](int64_t t) {
+        if (t == 0) return 2 * first + 1;
+        if (t < head) return 2 * (first + t);
+        if (t < head + (gb - ga)) return 2 * (ga + t - head) * kJoinWarps;
+        return 2 * (gb * kJoinWarps + t - head - (gb - ga));
+    };
+    const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
+    for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t t = w; t < terms; t += 8 * kJoinWarps) {
+            float v[8][4];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (t + u * kJoinWarps < terms) {
+                    join_load(p, v[u], row(t + u * kJoinWarps), b, lane);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] += v[u][k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[w][lane * 4 + k] = acc[k];
+        __syncthreads();
+        const int64_t j = b * kJoinBlock + lane * 4;
+        if (w == 0 && j < p.d) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[k] = sum[0][lane * 4 + k];
+#pragma unroll
+                for (int r = 1; r < kJoinWarps; ++r) acc[k] += sum[r][lane * 4 + k];
+            }
+            join_put<G>(p, vec, id.id, j, acc);
+        }
+    }
+}
+
 template <typename G>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    embed_join_kernel(const EmbedBwdParams p, bool vec, int stage) {
+    embed_long_kernel(const EmbedBwdParams p, bool vec) {
     __shared__ float sum[kJoinWarps][kJoinBlock];
-    __shared__ int64_t long_first, long_last;   // chunks of a long id that begins here (at most one)
-    __shared__ uint32_t long_id;
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint32_t n = ld_u32(p.longs);
+    for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
+        const Raw<16> r = ld_raw<16>((const LongId*)(p.longs + 4) + i);
+        join_long<G>(p, vec, true, LongId{r.w[0], r.w[1], r.w[2], 0}, sum);
+    }
+}
+
+// `once`: the only launch, which does the long ids as well.
+template <typename G>
+__global__ void __launch_bounds__(kJoinWarps * 32, 4)
+    embed_join_kernel(const EmbedBwdParams p, bool vec, bool once) {
+    __shared__ float sum[kJoinWarps][kJoinBlock];
+    __shared__ LongId longid;           // a long id that begins here (there is one at most)
+    __shared__ bool any;
     pdl_launch_dependents();
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c0 = (int64_t)blockIdx.x * kJoinWarps, c = c0 + w;
     const int64_t i0 = c * p.chunk, i1 = i0 + p.chunk;
     const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
-    if (threadIdx.x == 0) long_first = -1;
+    if (threadIdx.x == 0) any = false;
     pdl_wait();
     int64_t last = -1;
     uint32_t cur = 0xffffffffu;
-    bool within = false;                 // the CTA's chunks lie within one id
+    bool within = false;                // the CTA's chunks lie within one id
     if (i1 < p.n) {
         // (loads together: most chunks need no more)
         const uint32_t before = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
@@ -200,7 +266,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const int64_t e = min(i1 + p.chunk, p.n) - 1;
         const uint32_t far = ld_u32(p.key + e);
         cur = ld_u32(p.key + i1 - 1);
-        if (stage == JOIN_SHORT) {
+        if (!once) {
             const int64_t g0 = c0 * p.chunk, g1 = g0 + (int64_t)kJoinWarps * p.chunk;
             within = g0 > 0 && g1 < p.n && ld_u32(p.key + g0 - 1) == cur &&
                      ld_u32(p.key + g1) == cur && cur < (uint32_t)p.vocab;
@@ -226,11 +292,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const bool many = last - c >= kJoinWarps;
     __syncthreads();
     if (many && lane == 0) {
-        long_first = c;
-        long_last = last;
-        long_id = cur;
+        any = true;
+        longid = LongId{(uint32_t)c, (uint32_t)last, cur, 0};
+        if (!once && blockIdx.y == 0)
+            ((LongId*)(p.longs + 4))[atomicAdd(p.longs, 1u)] = longid;
     }
-    if (last >= 0 && !many && stage != JOIN_LONG) {
+    if (last >= 0 && !many) {
         for (int64_t b0 = blockIdx.y; b0 < blocks; b0 += (int64_t)gridDim.y * kJoinCols) {
             float acc[kJoinCols][4], two[kJoinCols][4];
             // (the first two chunks, which every such id has, in one go)
@@ -272,66 +339,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             if (j < p.d) st_elems<float, 4>(p.part + 2 * c0 * p.dpad + j, v[0]);
         }
     }
+    if (!once) return;
     __syncthreads();
-    if (long_first < 0 || stage == JOIN_SHORT) return;
-    // A long id: its sums are the first chunk's second row, the chunks up to the next CTA's,
-    // the CTAs' that lie within it (in the second of two launches), and the chunks that remain.
-    const int64_t first = long_first, end = long_last;
-    const int64_t ga = stage == JOIN_LONG ? first / kJoinWarps + 1 : 0;
-    const int64_t gb = stage == JOIN_LONG ? end / kJoinWarps : 0;   // (ga <= gb: see `many`)
-    const int64_t head = stage == JOIN_LONG ? ga * kJoinWarps - first : end + 1 - first;
-    const int64_t terms = stage == JOIN_LONG ? head + (gb - ga) + (end + 1 - gb * kJoinWarps) : head;
-    auto row = [&](int64_t t) {
-        if (t == 0) return 2 * first + 1;
-        if (t < head) return 2 * (first + t);
-        if (t < head + (gb - ga)) return 2 * (ga + t - head) * kJoinWarps;
-        return 2 * (gb * kJoinWarps + t - head - (gb - ga));
-    };
-    for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t t = w; t < terms; t += 8 * kJoinWarps) {
-            float v[8][4];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (t + u * kJoinWarps < terms) {
-                    join_load(p, v[u], row(t + u * kJoinWarps), b, lane);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[k] += v[u][k];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) sum[w][lane * 4 + k] = acc[k];
-        __syncthreads();
-        const int64_t j = b * kJoinBlock + lane * 4;
-        if (w == 0 && j < p.d) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                acc[k] = sum[0][lane * 4 + k];
-#pragma unroll
-                for (int r = 1; r < kJoinWarps; ++r) acc[k] += sum[r][lane * 4 + k];
-            }
-            join_put<G>(p, vec, long_id, j, acc);
-        }
-    }
+    if (any) join_long<G>(p, vec, false, longid, sum);
 }
 
 template <typename T, typename G, int NE>
 static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
-    const int64_t ctas = (p.chunks + p.ty - 1) / p.ty * p.slices;
-    cudaError_t err =
-        launch_pdl(embed_bwd_kernel<T, G, NE>, (unsigned)ctas, kSegThreads, 0, s, p);
+    cudaError_t err = launch_pdl(embed_bwd_kernel<T, G, NE>,
+                                 (unsigned)((p.chunks + p.ty - 1) / p.ty * p.slices), kSegThreads,
+                                 0, s, p);
     if (err != cudaSuccess || p.chunks < 2) return err;
     const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
+    const int64_t ctas = (p.chunks - 1 + kJoinWarps - 1) / kJoinWarps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.chunks - 1 + kJoinWarps - 1) / kJoinWarps),
-                       (unsigned)(blocks < 8 ? blocks : 8), 1);
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -339,12 +360,15 @@ static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const bool vec = NE % 4 == 0;
-    if (p.chunks <= kJoinOnce)
-        return cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, (int)JOIN_ALL);
-    err = cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, (int)JOIN_SHORT);
-    if (err != cudaSuccess) return err;
-    return cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, (int)JOIN_LONG);
+    const bool vec = NE % 4 == 0, once = p.chunks <= kJoinOnce;
+    // (kJoinCols blocks a step; one launch that has long ids to do as well: a block each)
+    const int64_t wide = once ? blocks : (blocks + kJoinCols - 1) / kJoinCols;
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(wide < 8 ? wide : 8), 1);
+    err = cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, once);
+    if (err != cudaSuccess || once) return err;
+    // (an id is long if it fills a CTA's chunks: there are at most as many as CTAs)
+    cfg.gridDim = dim3((unsigned)(ctas < 32 ? ctas : 32), (unsigned)(blocks < 32 ? blocks : 32), 1);
+    return cudaLaunchKernelEx(&cfg, embed_long_kernel<G>, p, vec);
 }
 
 cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams& q,

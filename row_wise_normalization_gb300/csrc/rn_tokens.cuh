@@ -53,19 +53,21 @@ __device__ __forceinline__ Raw<B> ld_raw(const void* p) {
     }
     return r;
 }
+// (Written once and not read again by the kernel: streaming hint. It leaves the L2 to the rows that
+// are read again; embedding rows 32768 x 8192 BF16 took 137 us without it, 122 us with it.)
 template <int B>
 __device__ __forceinline__ void st_raw(void* p, const Raw<B>& r) {
     if constexpr (B == 16)
-        asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]),
+        asm volatile("st.global.cs.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]),
                      "r"(r.w[2]), "r"(r.w[3])
                      : "memory");
     else if constexpr (B == 8)
-        asm volatile("st.global.v2.b32 [%0], {%1,%2};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1])
+        asm volatile("st.global.cs.v2.b32 [%0], {%1,%2};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1])
                      : "memory");
     else if constexpr (B == 4)
-        asm volatile("st.global.b32 [%0], %1;" ::"l"(p), "r"(r.w[0]) : "memory");
+        asm volatile("st.global.cs.b32 [%0], %1;" ::"l"(p), "r"(r.w[0]) : "memory");
     else
-        asm volatile("st.global.u16 [%0], %1;" ::"l"(p), "h"((uint16_t)r.w[0]) : "memory");
+        asm volatile("st.global.cs.u16 [%0], %1;" ::"l"(p), "h"((uint16_t)r.w[0]) : "memory");
 }
 
 // NE elements of T between raw words and FP32.

@@ -42,8 +42,9 @@ struct EmbedParams {
     FastDiv vpr;          // vectors per row
     float scale;
 };
-// ne: elements of one vector access (1, 2, 4 or 8).
-cudaError_t embed_fwd_launch(int dtype, int itype, int ne, const EmbedParams& p, cudaStream_t s);
+// ne: elements of the widest access that table and out are aligned for; d: the width.
+cudaError_t embed_fwd_launch(int dtype, int itype, int ne, int64_t d, const EmbedParams& p,
+                             cudaStream_t s);
 
 // Stable sort of the n ids by value, with their positions. Ids outside
 // [0, vocab) are given the key `vocab`, so that they come last.
@@ -62,6 +63,7 @@ struct SortParams {
     uint32_t* key[2];     // [n] each: the result in [0]; [1] beyond kSortClusterMax only
     int32_t* pos[2];
     uint32_t* hist;       // [tiles][kSortBins], beyond kSortClusterMax
+    uint32_t* zeroed;     // a word that the sort clears for the kernels after it
     int tiles;
     int bits, passes;     // bits of a digit, digits
     int itype;
@@ -95,6 +97,7 @@ struct EmbedBwdParams {
     const uint32_t* key;
     const int32_t* pos;
     float* part;               // [2 * chunks][dpad]
+    uint32_t* longs;           // ids of many chunks: their number, and from [4] on 4 words each
     int64_t n, vocab, d, dpad;
     int64_t lddo, ldg;
     int64_t chunks;

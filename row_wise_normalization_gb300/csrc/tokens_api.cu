@@ -78,7 +78,7 @@ int access_elems(int64_t d, const void* a, int es_a, int64_t lda, const void* b,
 
 // ---- workspace of embed_bwd -------------------------------------------------
 struct EmbedWorkspace {
-    int64_t key[2], pos[2], hist, part, total;   // byte offsets
+    int64_t key[2], pos[2], hist, longs, part, total;   // byte offsets
     int64_t tiles, chunks, dpad;
 };
 EmbedWorkspace embed_workspace(int64_t n, int64_t d) {
@@ -98,6 +98,7 @@ EmbedWorkspace embed_workspace(int64_t n, int64_t d) {
         w.pos[k] = take(k == 0 || global ? n * 4 : 0);
     }
     w.hist = take(global ? w.tiles * kSortBins * 4 : 0);
+    w.longs = take((w.chunks / 8 + 2) * 16);   // a long id fills at least 8 chunks
     w.part = take(2 * w.chunks * w.dpad * 4);
     w.total = at;
     return w;
@@ -127,8 +128,8 @@ int embed_fwd(int dtype, int itype, const void* tokens, const void* table, int64
               int64_t ldo, int64_t n, int64_t vocab, int64_t d, float scale, void* stream) {
     if (!known_dtype(dtype) || !known_index(itype)) return RN_ERR_DTYPE;
     if (n < 0 || vocab <= 0 || vocab > kMaxVocab || d <= 0 || d > kMaxWidth || ldt < d ||
-        ldo < d || !fits(n, d, ldo) || !fits(vocab, d, ldt))
-        return RN_ERR_SIZE;
+        ldo < d || !fits(n, d, ldo) || !fits(vocab, d, ldt) || n > kMaxCount / (d / 512 + 1))
+        return RN_ERR_SIZE;   // (the last: one launch's grid, a warp for 512 elements of a row)
     if (!std::isfinite(scale)) return RN_ERR_SCALE;
     if (n == 0) return RN_OK;
     if (!tokens || !table || !out) return RN_ERR_NULL;
@@ -148,10 +149,9 @@ int embed_fwd(int dtype, int itype, const void* tokens, const void* table, int64
     p.ldt = ldt;
     p.ldo = ldo;
     p.vpr = fast_div((uint32_t)(d / ne));
-    if (n > ((int64_t)1 << 40) / (d / ne)) return RN_ERR_SIZE;   // one launch's grid
     p.total = n * (d / ne);
     p.scale = scale;
-    return done(embed_fwd_launch(dtype, itype, ne, p, (cudaStream_t)stream));
+    return done(embed_fwd_launch(dtype, itype, ne, d, p, (cudaStream_t)stream));
 }
 
 int embed_bwd_workspace_size(int64_t n, int64_t vocab, int64_t d, size_t* bytes) {
@@ -202,6 +202,7 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
         sp.pos[k] = (int32_t*)(base + w.pos[k]);
     }
     sp.hist = (uint32_t*)(base + w.hist);
+    sp.zeroed = (uint32_t*)(base + w.longs);
     sp.tiles = (int)w.tiles;
     sp.itype = itype;
     if (!accumulate) {
@@ -217,6 +218,7 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
     p.key = sp.key[0];
     p.pos = sp.pos[0];
     p.part = (float*)(base + w.part);
+    p.longs = sp.zeroed;
     p.n = n;
     p.vocab = vocab;
     p.d = d;
