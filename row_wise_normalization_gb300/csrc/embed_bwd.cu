@@ -33,9 +33,10 @@ __global__ void __launch_bounds__(kSegThreads, 4) embed_bwd_kernel(const EmbedBw
     const int slice = (int)blockIdx.x % p.slices;
     const int64_t c = (int64_t)((int)blockIdx.x / p.slices) * p.ty + ty;
     if (c >= p.chunks) return;          // whole warps: tx is a multiple of 32
-    // this thread's vectors: every p.tx-th of the slice's
-    const int64_t j0 = ((int64_t)slice * M * p.tx + tx) * NE;
-    const int64_t step = (int64_t)p.tx * NE;
+    // this thread's vectors: every 32nd of its warp's, from column j0 on
+    const int64_t j0 = (((int64_t)slice * p.tx + (tx - lane)) * M + lane) * NE;
+    constexpr int step = 32 * NE;
+    const int cols = (int)max((int64_t)-1, min((int64_t)(M * step), p.d - j0));   // of them in the row
     const T* const X = (const T*)p.dout + j0;
     const int64_t i0 = c * p.chunk;
     const int len = (int)min((int64_t)p.chunk, p.n - i0);
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kSegThreads, 4) embed_bwd_kernel(const EmbedBw
         for (int k = 0; k < E / 2; ++k) f2_get(acc[k], s[2 * k], s[2 * k + 1]);
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            if (j0 + m * step < p.d) {
+            if (m * step < cols) {
                 if (open || on) {
                     st_elems<float, NE>(w + m * step, s + m * NE);
                 } else {
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kSegThreads, 4) embed_bwd_kernel(const EmbedBw
             if (i + u < cnt) {
 #pragma unroll
                 for (int m = 0; m < M; ++m)
-                    if (j0 + m * step < p.d) r[u][m] = ld_raw<B>(X + at * p.lddo + m * step);
+                    if (m * step < cols) r[u][m] = ld_raw<B>(X + at * p.lddo + m * step);
             }
         }
         const unsigned h = heads >> i;

@@ -547,9 +547,14 @@ static cudaError_t logprob_fwd_go(const LogprobParams& q, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     p.split = logprob_split(p.rows, p.vocab, Elem<T>::kVec, sms);
     if (p.split > 8) {
-        // clusters of more than 8 CTAs have to be asked for (a setting of the function, and
-        // of the context that is current: made every time)
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        // clusters of more than 8 CTAs have to be asked for: once in each context, by each thread
+        static thread_local unsigned long long prepared = 0;
+        unsigned long long ctx = 0;
+        err = current_context_id(&ctx);
+        if (err == cudaSuccess && (ctx == 0 || prepared != ctx)) {
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            prepared = ctx;
+        }
         if (err != cudaSuccess) return err;
     }
     cudaLaunchConfig_t cfg = {};

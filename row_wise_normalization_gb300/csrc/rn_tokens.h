@@ -55,7 +55,7 @@ constexpr int kSortTile = kSortThreads * kSortPerThread;   // ids of a CTA, sort
 constexpr int kSortBits = 9;                               // bits of a digit, at most
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortMaxCluster = 16;
-constexpr int kSortMaxShare = 10240;   // ids of a CTA, sorting in shared memory (160 KB)
+constexpr int kSortMaxShare = 10240;   // ids of a CTA, sorting in shared memory
 constexpr int64_t kSortClusterMax = (int64_t)kSortMaxCluster * kSortMaxShare;
 struct SortParams {
     const void* tokens;
@@ -68,6 +68,7 @@ struct SortParams {
     int bits, passes;     // bits of a digit, digits
     int itype;
     int cluster, share;   // CTAs that sort in shared memory, ids of each
+    FastDiv owner;        // division by share
     // Rows of ids that do not occur, cleared beside the sort (NULL: left as they are)
     char* zero;
     int64_t zero_pitch, zero_bytes;   // bytes from row to row, and of a row

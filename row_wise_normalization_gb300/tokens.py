@@ -16,6 +16,7 @@ _FLOATS = {torch.float32: capi.RN_DTYPE_F32, torch.bfloat16: capi.RN_DTYPE_BF16,
            torch.float16: capi.RN_DTYPE_F16}
 _INDEX = {torch.int32: capi.RN_INDEX_I32, torch.int64: capi.RN_INDEX_I64}
 _F32 = torch.float32
+_C = capi.load()
 
 
 def _values(name, t):
@@ -149,7 +150,7 @@ def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
         if out.numel() != n * d or out.shape[-1:] != (d,):
             raise ValueError(f"out must hold {n} rows of {d}")
         ldo = _stride("out", out, d, dtype)
-    capi.check(capi.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt, out.data_ptr(),
+    capi.check(_C.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt, out.data_ptr(),
                               ldo, n, int(vocab), d, float(scale), _stream(dev)))
     return out
 
@@ -203,7 +204,7 @@ def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtabl
         if not (workspace.is_cuda and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous CUDA tensor")
         nbytes = workspace.numel() * workspace.element_size()
-    capi.check(capi.embed_bwd(code, _FLOATS[gdtype], it, dout.data_ptr(), lddo, tokens.data_ptr(),
+    capi.check(_C.embed_bwd(code, _FLOATS[gdtype], it, dout.data_ptr(), lddo, tokens.data_ptr(),
                               dtable.data_ptr(), ldg, n, int(vocab), d, float(scale), 1 if accumulate else 0,
                               workspace.data_ptr(), nbytes, _stream(dev)))
     return dtable
@@ -254,7 +255,7 @@ def logprob_fwd(logits, targets=None, scale: float = 1.0, *, top: int = 0,
         ids = _new(logits, at, lead, itype)
         top_logp = _new(logits, at, lead, _F32)
         a_ids, a_top = ids.data_ptr(), top_logp.data_ptr()
-    capi.check(capi.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, a_logp, a_entropy,
+    capi.check(_C.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, a_logp, a_entropy,
                                 lse.data_ptr(), a_ids, a_top, rows, vocab, int(top), float(scale),
                                 _stream(dev)))
     return logp, entropy, lse, ids, top_logp
@@ -296,7 +297,7 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
         if dlogits.shape != shape:
             raise ValueError("dlogits must be shaped like logits")
         ldd = _stride("dlogits", dlogits, vocab, logits.dtype)
-    capi.check(capi.logprob_bwd(code, it, a_dlogp, a_dentropy, logits.data_ptr(), ldl, tgt, a_lse,
+    capi.check(_C.logprob_bwd(code, it, a_dlogp, a_dentropy, logits.data_ptr(), ldl, tgt, a_lse,
                                 a_entropy, dlogits.data_ptr(), ldd, rows, vocab, float(scale),
                                 _stream(dev)))
     return dlogits
