@@ -1,0 +1,8 @@
+#include "embed_bwd.cuh"
+
+namespace rn {
+cudaError_t embed_bwd_bf16(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s) {
+    if (gtype != DT_F32) return embed_bwd_t<__nv_bfloat16, __nv_bfloat16>(ne, p, s);
+    return embed_bwd_t<__nv_bfloat16, float>(ne, p, s);
+}
+}  // namespace rn

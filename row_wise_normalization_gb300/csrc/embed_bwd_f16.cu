@@ -1,0 +1,8 @@
+#include "embed_bwd.cuh"
+
+namespace rn {
+cudaError_t embed_bwd_f16(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s) {
+    if (gtype != DT_F32) return embed_bwd_t<__half, __half>(ne, p, s);
+    return embed_bwd_t<__half, float>(ne, p, s);
+}
+}  // namespace rn

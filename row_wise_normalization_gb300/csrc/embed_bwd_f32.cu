@@ -1,0 +1,8 @@
+#include "embed_bwd.cuh"
+
+namespace rn {
+cudaError_t embed_bwd_f32(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s) {
+    (void)gtype;
+    return embed_bwd_t<float, float>(ne, p, s);
+}
+}  // namespace rn

@@ -18,21 +18,15 @@
 // The rows of the ids that do not occur are most of a gradient's bytes, and which
 // they are the ids alone say: a CTA that clears owns a range of the vocabulary, reads all
 // ids (from L2) and marks those of its range in shared memory. So the kernel that
-// clears runs beside the sort: in the same launch where one CTA sorts, else it is launched as the sort's programmatic dependent, and the
+// clears runs beside the sort. It is launched as the sort's programmatic dependent, and the
 // sort lets it start only after its own wait, when all work ahead of the call has
 // completed; and it waits for the sort only at its end, so that what follows it
 // follows both.
-#include "rn_tokens.cuh"
+#include "rn_embed.cuh"
 
 namespace rn {
 
 constexpr int kZeroRange = 65536;   // ids a CTA marks at a time (8 KB of bits)
-
-// The sort key of the id at position i.
-__device__ __forceinline__ uint32_t id_key(const SortParams& p, int64_t i) {
-    const int64_t id = ld_id(p.tokens, i, p.itype);
-    return (uint32_t)((id >= 0 && id < p.vocab) ? id : p.vocab);
-}
 
 // Clears `bytes` (a multiple of 2) at p by `lanes` threads, of which this is number l.
 __device__ __forceinline__ void clear_row(char* p, int64_t bytes, int l, int lanes) {
@@ -45,13 +39,15 @@ __device__ __forceinline__ void clear_row(char* p, int64_t bytes, int l, int lan
     for (int64_t b = tail + 2 * l; b < bytes; b += 2 * lanes) st_raw(p + b, h);
 }
 
-// Clears the rows of the absent ids of part `part` of the vocabulary, of `parts`.
-__device__ __forceinline__ void clear_absent(const SortParams& p, int part, int parts,
-                                             uint32_t* bits) {
+// Clears the rows of the absent ids of a part of the vocabulary. What it touches no kernel of the
+// call before it does, and the one ahead has waited for all others before it let this one
+// start: it waits at its end.
+__global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(const SortParams p) {
+    __shared__ uint32_t bits[kZeroRange / 32];
     const int t = threadIdx.x;
     // (whole groups of 32 rows: 16383 x 771 FP16 into FP32 took 69 us without, 57 us with)
-    const int64_t share = ((p.vocab + parts - 1) / parts + 31) / 32 * 32;
-    const int64_t end = min(p.vocab, (int64_t)(part + 1) * share);
+    const int64_t share = ((p.vocab + gridDim.x - 1) / gridDim.x + 31) / 32 * 32;
+    const int64_t end = min(p.vocab, (int64_t)(blockIdx.x + 1) * share);
     // the ids as 16-byte vectors, and fewer than two vectors' before and after
     const int64_t per = 16 / index_size(p.itype);
     const int64_t head = min(p.n, (int64_t)((0u - (unsigned)(uintptr_t)p.tokens) & 15u) /
@@ -61,7 +57,7 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
     // threads of a row: as many 16-byte stores as it has, up to a warp's
     int lanes = 32;
     while (lanes > 1 && (lanes / 2) * 16 >= p.zero_bytes) lanes /= 2;
-    for (int64_t lo = (int64_t)part * share; lo < end; lo += kZeroRange) {
+    for (int64_t lo = (int64_t)blockIdx.x * share; lo < end; lo += kZeroRange) {
         const int cnt = (int)min((int64_t)kZeroRange, end - lo);
         __syncthreads();
         for (int w = t; w < (cnt + 31) / 32; w += kSortThreads) bits[w] = 0;
@@ -97,154 +93,16 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
             if (!((bits[r >> 5] >> (r & 31)) & 1u))
                 clear_row(p.zero + (lo + r) * p.zero_pitch, p.zero_bytes, t % lanes, lanes);
     }
-}
-
-// The same as a kernel of its own, beside a sort in a larger cluster or in global memory. What it
-// touches no kernel of the call before it does, and the one ahead has waited for all
-// others before it let this one start: it waits at its end.
-__global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(const SortParams p) {
-    __shared__ uint32_t bits[kZeroRange / 32];
-    clear_absent(p, (int)blockIdx.x, (int)gridDim.x, bits);
     pdl_launch_dependents();
     pdl_wait();
-}
-
-// Sum of v over the threads before this one (all kSortThreads of them call it).
-__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* wsum) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t q = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += q;
-    }
-    if (lane == 31) wsum[w] = incl;
-    __syncthreads();
-    uint32_t run = incl - v;
-    for (int k = 0; k < w; ++k) run += wsum[k];
-    return run;
-}
-
-// The lanes of the warp that hold an id with this lane's digit: a ballot a bit.
-__device__ __forceinline__ unsigned same_digit(uint32_t dg, bool in) {
-    unsigned same = __ballot_sync(0xffffffffu, in);
-#pragma unroll
-    for (int b = 0; b < kSortBits; ++b) {
-        const unsigned one = __ballot_sync(0xffffffffu, dg >> b & 1u);
-        same &= dg >> b & 1u ? one : ~one;
-    }
-    return same;
-}
-// The number of this lane's digit among the warp's ids so far (cnt: the warp's table,
-// advanced). All lanes; `in` false: no id.
-__device__ __forceinline__ uint32_t warp_rank(uint32_t* cnt, uint32_t dg, unsigned same, bool in,
-                                              int lane) {
-    const uint32_t r = in ? cnt[dg] : 0;
-    const unsigned below = same & ((1u << lane) - 1);
-    __syncwarp();
-    if (in && below == 0) cnt[dg] = r + __popc(same);
-    __syncwarp();
-    return r + __popc(below);
-}
-
-// ---- up to kSortClusterMax ids: in the shared memory of a cluster ---------------
-constexpr int cluster_fixed_bytes() { return kSortWarps * kSortBins * 4 + kSortBins * 4; }
-constexpr int cluster_bytes(int share, int passes) {
-    return cluster_fixed_bytes() + (passes > 1 ? 2 : 1) * share * 8 + share * 2;
 }
 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint32_t wsum[kSortWarps];
-    static_assert(kSortThreads == kSortBins, "one thread for each digit");
-    static_assert(kZeroRange / 8 <= cluster_fixed_bytes(), "the marks of a range");
-    static_assert(kSortMaxShare <= 65536 && cluster_bytes(kSortMaxShare, 2) <= 232448 - 1024,
-                  "16-bit ranks; the shared memory of a CTA");
-    uint32_t(*cnt)[kSortBins] = (uint32_t(*)[kSortBins])smem;
-    uint32_t* const tots = (uint32_t*)smem + kSortWarps * kSortBins;
-    unsigned long long* const buf = (unsigned long long*)(smem + cluster_fixed_bytes());
-    uint16_t* const rank = (uint16_t*)(buf + (p.passes > 1 ? 2 : 1) * p.share);
-    const int t = threadIdx.x, w = t >> 5, lane = t & 31, me = (int)blockIdx.x;
-    const uint32_t mask = (1u << p.bits) - 1;
-    const int64_t base = (int64_t)me * p.share;
-    // this CTA's ids, and this warp's of them: [w0, w1)
-    const int mine = (int)max((int64_t)0, min((int64_t)p.share, p.n - base));
-    const int per = p.share / kSortWarps;
-    const int w0 = min(mine, w * per), w1 = min(mine, w0 + per);
     pdl_wait();
     pdl_launch_dependents();   // in this order: see embed_clear_kernel
-    if (me >= p.cluster) {     // beside a sort in one CTA
-        clear_absent(p, me - 1, (int)gridDim.x - 1, (uint32_t*)smem);
-        return;
-    }
-    if (me == 0 && t == 0) *p.zeroed = 0;
-    for (int i = w0 + lane; i < w1; i += 32)
-        buf[i] = ((unsigned long long)id_key(p, base + i) << 32) | (uint32_t)(base + i);
-    for (int pass = 0; pass < p.passes; ++pass) {
-        const int shift = pass * p.bits;
-        unsigned long long* const src = buf + (pass & 1) * p.share;
-        unsigned long long* const dst = buf + ((pass & 1) ^ 1) * p.share;
-        for (int k = 0; k < kSortWarps; ++k) cnt[k][t] = 0;
-        __syncthreads();
-        // (the ballots of 4 steps are independent of each other; the counts are not)
-        constexpr int U = 4;
-        for (int i0 = w0; i0 < w1; i0 += 32 * U) {
-            uint32_t dg[U];
-            unsigned same[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * 32 + lane;
-                dg[u] = i < w1 ? (uint32_t)(src[i] >> (32 + shift)) & mask : 0;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u * 32 < w1) same[u] = same_digit(dg[u], i0 + u * 32 + lane < w1);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * 32 + lane;
-                if (i0 + u * 32 >= w1) break;
-                const uint32_t r = warp_rank(cnt[w], dg[u], same[u], i < w1, lane);
-                if (i < w1) rank[i] = (uint16_t)r;
-            }
-        }
-        __syncthreads();
-        uint32_t sum = 0;
-        for (int k = 0; k < kSortWarps; ++k) sum += cnt[k][t];
-        tots[t] = sum;
-        cluster_sync();
-        // (all loads in flight: one after another they took half of the sort's time)
-        uint32_t c[kSortMaxCluster], before = 0, total = 0;
-#pragma unroll
-        for (int q = 0; q < kSortMaxCluster; ++q)
-            c[q] = q < p.cluster ? peer_u32(peer_addr(tots + t, q)) : 0;
-#pragma unroll
-        for (int q = 0; q < kSortMaxCluster; ++q) {
-            before += q < me ? c[q] : 0;
-            total += c[q];
-        }
-        uint32_t run = before + sum_before(total, wsum);
-        for (int k = 0; k < kSortWarps; ++k) {
-            const uint32_t c = cnt[k][t];
-            cnt[k][t] = run;
-            run += c;
-        }
-        __syncthreads();
-        const bool last = pass == p.passes - 1;
-#pragma unroll 4
-        for (int i = w0 + lane; i < w1; i += 32) {
-            const unsigned long long v = src[i];
-            const uint32_t at = cnt[w][(uint32_t)(v >> (32 + shift)) & mask] + rank[i];
-            if (last) {
-                p.key[0][at] = (uint32_t)(v >> 32);
-                p.pos[0][at] = (int32_t)v;
-            } else {
-                const uint32_t q = fast_quot(at, p.owner);
-                peer_store(peer_addr(dst + (at - q * (uint32_t)p.share), q), v);
-            }
-        }
-        // the peers' ids have arrived, and they are past their reads of tots
-        cluster_sync();
-    }
+    cluster_sort(p, smem, wsum, (int)blockIdx.x);
 }
 
 // ---- more ids: in global memory -------------------------------------------------
@@ -344,7 +202,7 @@ __global__ void __launch_bounds__(kSortThreads)
     }
 }
 
-static cudaError_t sort_in_cluster(SortParams& p, int sms, cudaStream_t s) {
+static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
     // 2048 ids a CTA, until there are 16 CTAs
     p.cluster = 1;
     while (p.cluster < kSortMaxCluster && p.n > (int64_t)p.cluster * 2048) p.cluster *= 2;
@@ -367,7 +225,7 @@ static cudaError_t sort_in_cluster(SortParams& p, int sms, cudaStream_t s) {
         prepared = ctx;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.cluster + (p.cluster == 1 && p.zero ? 2 * sms : 0)), 1, 1);
+    cfg.gridDim = dim3((unsigned)p.cluster, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
@@ -403,15 +261,17 @@ static cudaError_t sort_in_memory(const SortParams& p, cudaStream_t s) {
 }
 
 cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
+    p.passes = sort_passes(p.vocab);
+    p.bits = (sort_key_bits(p.vocab) + p.passes - 1) / p.passes;
+    return p.n <= kSortClusterMax ? sort_in_cluster(p, s) : sort_in_memory(p, s);
+}
+
+cudaError_t embed_clear_launch(const SortParams& p, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess)
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    p.passes = sort_passes(p.vocab);
-    p.bits = (sort_key_bits(p.vocab) + p.passes - 1) / p.passes;
-    err = p.n <= kSortClusterMax ? sort_in_cluster(p, sms, s) : sort_in_memory(p, s);
-    if (err != cudaSuccess || !p.zero || p.cluster == 1) return err;
     return launch_pdl(embed_clear_kernel, 2 * (unsigned)sms, kSortThreads, 0, s, p);
 }
 

@@ -1,19 +1,152 @@
-// embed_bwd.cu -- gradient of embedding rows from the sorted ids:
-//   dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum_{i: id_i = v} dout[i]
-// for the ids that occur (embed_sort.cu clears the rows of the others).
-//
-// Bytes bound it: dout read once, every row of the gradient written once. The
-// sorted positions are cut into chunks of 8 to 32, a lane for each position.
-// A group of threads takes one chunk and a slice of the columns, has 8 of the chunk's
-// rows in flight at a time, adds them in registers (FP32) and, where the id changes,
-// writes the id's row. An id whose positions run over a chunk's edge leaves its sum of
-// each chunk in the workspace, and a second kernel adds those in chunk order, so that an
-// id which fills half of a batch is summed by as many groups as its rows fill.
-// Every sum has a fixed order: results repeat bit for bit.
+// rn_embed.cuh -- device parts of the embedding gradient: the sort of the ids in a
+// cluster's shared memory, the sums of the sorted rows, and the joining of sums that run over
+// several chunks. embed_sort.cu and embed_bwd.cuh make kernels of them.
+#pragma once
+
 #include "rn_tokens.cuh"
 
 namespace rn {
 
+// ---- sort -------------------------------------------------------------------
+// The sort key of the id at position i.
+__device__ __forceinline__ uint32_t id_key(const SortParams& p, int64_t i) {
+    const int64_t id = ld_id(p.tokens, i, p.itype);
+    return (uint32_t)((id >= 0 && id < p.vocab) ? id : p.vocab);
+}
+
+// Sum of v over the threads before this one (all kSortThreads of them call it).
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t* wsum) {
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t q = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += q;
+    }
+    if (lane == 31) wsum[w] = incl;
+    __syncthreads();
+    uint32_t run = incl - v;
+    for (int k = 0; k < w; ++k) run += wsum[k];
+    return run;
+}
+
+// The lanes of the warp that hold an id with this lane's digit: a ballot a bit.
+__device__ __forceinline__ unsigned same_digit(uint32_t dg, bool in) {
+    unsigned same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+    for (int b = 0; b < kSortBits; ++b) {
+        const unsigned one = __ballot_sync(0xffffffffu, dg >> b & 1u);
+        same &= dg >> b & 1u ? one : ~one;
+    }
+    return same;
+}
+// The number of this lane's digit among the warp's ids so far (cnt: the warp's table,
+// advanced). All lanes; `in` false: no id.
+__device__ __forceinline__ uint32_t warp_rank(uint32_t* cnt, uint32_t dg, unsigned same, bool in,
+                                              int lane) {
+    const uint32_t r = in ? cnt[dg] : 0;
+    const unsigned below = same & ((1u << lane) - 1);
+    __syncwarp();
+    if (in && below == 0) cnt[dg] = r + __popc(same);
+    __syncwarp();
+    return r + __popc(below);
+}
+
+constexpr int cluster_fixed_bytes() { return kSortWarps * kSortBins * 4 + kSortBins * 4; }
+constexpr int cluster_bytes(int share, int passes) {
+    return cluster_fixed_bytes() + (passes > 1 ? 2 : 1) * share * 8 + share * 2;
+}
+
+// The sort of at most p.cluster * p.share ids by the CTAs of a cluster, of which this is number
+// `me`. smem: cluster_bytes(p.share, p.passes) bytes, in the same place in every CTA. Ends with
+// a barrier of the cluster.
+__device__ __forceinline__ void cluster_sort(const SortParams& p, unsigned char* smem,
+                                             uint32_t* wsum, int me) {
+    static_assert(kSortThreads == kSortBins, "one thread for each digit");
+    static_assert(kSortMaxShare <= 65536 && cluster_bytes(kSortMaxShare, 2) <= 232448 - 1024,
+                  "16-bit ranks; the shared memory of a CTA");
+    uint32_t(*cnt)[kSortBins] = (uint32_t(*)[kSortBins])smem;
+    uint32_t* const tots = (uint32_t*)smem + kSortWarps * kSortBins;
+    unsigned long long* const buf = (unsigned long long*)(smem + cluster_fixed_bytes());
+    uint16_t* const rank = (uint16_t*)(buf + (p.passes > 1 ? 2 : 1) * p.share);
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31;
+    const uint32_t mask = (1u << p.bits) - 1;
+    const int64_t base = (int64_t)me * p.share;
+    // this CTA's ids, and this warp's of them: [w0, w1)
+    const int mine = (int)max((int64_t)0, min((int64_t)p.share, p.n - base));
+    const int per = p.share / kSortWarps;
+    const int w0 = min(mine, w * per), w1 = min(mine, w0 + per);
+    if (me == 0 && t == 0) *p.zeroed = 0;
+    for (int i = w0 + lane; i < w1; i += 32)
+        buf[i] = ((unsigned long long)id_key(p, base + i) << 32) | (uint32_t)(base + i);
+    for (int pass = 0; pass < p.passes; ++pass) {
+        const int shift = pass * p.bits;
+        unsigned long long* const src = buf + (pass & 1) * p.share;
+        unsigned long long* const dst = buf + ((pass & 1) ^ 1) * p.share;
+        for (int k = 0; k < kSortWarps; ++k) cnt[k][t] = 0;
+        __syncthreads();
+        // (the ballots of 4 steps are independent of each other; the counts are not)
+        constexpr int U = 4;
+        for (int i0 = w0; i0 < w1; i0 += 32 * U) {
+            uint32_t dg[U];
+            unsigned same[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * 32 + lane;
+                dg[u] = i < w1 ? (uint32_t)(src[i] >> (32 + shift)) & mask : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * 32 < w1) same[u] = same_digit(dg[u], i0 + u * 32 + lane < w1);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * 32 + lane;
+                if (i0 + u * 32 >= w1) break;
+                const uint32_t r = warp_rank(cnt[w], dg[u], same[u], i < w1, lane);
+                if (i < w1) rank[i] = (uint16_t)r;
+            }
+        }
+        __syncthreads();
+        uint32_t sum = 0;
+        for (int k = 0; k < kSortWarps; ++k) sum += cnt[k][t];
+        tots[t] = sum;
+        cluster_sync();
+        // (all loads in flight: one after another they took half of the sort's time)
+        uint32_t c[kSortMaxCluster], before = 0, total = 0;
+#pragma unroll
+        for (int q = 0; q < kSortMaxCluster; ++q)
+            c[q] = q < p.cluster ? peer_u32(peer_addr(tots + t, q)) : 0;
+#pragma unroll
+        for (int q = 0; q < kSortMaxCluster; ++q) {
+            before += q < me ? c[q] : 0;
+            total += c[q];
+        }
+        uint32_t run = before + sum_before(total, wsum);
+        for (int k = 0; k < kSortWarps; ++k) {
+            const uint32_t c = cnt[k][t];
+            cnt[k][t] = run;
+            run += c;
+        }
+        __syncthreads();
+        const bool last = pass == p.passes - 1;
+#pragma unroll 4
+        for (int i = w0 + lane; i < w1; i += 32) {
+            const unsigned long long v = src[i];
+            const uint32_t at = cnt[w][(uint32_t)(v >> (32 + shift)) & mask] + rank[i];
+            if (last) {
+                p.key[0][at] = (uint32_t)(v >> 32);
+                p.pos[0][at] = (int32_t)v;
+            } else {
+                const uint32_t q = fast_quot(at, p.owner);
+                peer_store(peer_addr(dst + (at - q * (uint32_t)p.share), q), v);
+            }
+        }
+        // the peers' ids have arrived, and they are past their reads of tots
+        cluster_sync();
+    }
+}
+
+// ---- sums -------------------------------------------------------------------
 constexpr int kSegThreads = 256;
 constexpr int kSegU = 8;            // rows in flight
 
@@ -23,24 +156,22 @@ constexpr int seg_vectors() {
     return 16 / (NE * (int)sizeof(T)) < 4 ? 16 / (NE * (int)sizeof(T)) : 4;
 }
 
+// Sums chunk c's rows in the columns of a slice, by p.tx threads of which this is number tx: whole
+// warps, which do not wait for each other.
 template <typename T, typename G, int NE>
-__global__ void __launch_bounds__(kSegThreads, 4) embed_bwd_kernel(const EmbedBwdParams p) {
+__device__ __forceinline__ void sum_chunk(const EmbedBwdParams& p, int64_t c, int slice, int tx) {
     constexpr int M = seg_vectors<T, NE>();
     constexpr int B = NE * (int)sizeof(T);
-    pdl_launch_dependents();
     G* const DG = (G*)p.dtable;
-    const int tx = (int)threadIdx.x % p.tx, ty = (int)threadIdx.x / p.tx, lane = tx & 31;
-    const int slice = (int)blockIdx.x % p.slices;
-    const int64_t c = (int64_t)((int)blockIdx.x / p.slices) * p.ty + ty;
-    if (c >= p.chunks) return;          // whole warps: tx is a multiple of 32
+    const int lane = tx & 31;
     // this thread's vectors: every 32nd of its warp's, from column j0 on
     const int64_t j0 = (((int64_t)slice * p.tx + (tx - lane)) * M + lane) * NE;
     constexpr int step = 32 * NE;
+    if (j0 - lane * NE >= p.d) return;     // a warp past the row's end
     const int cols = (int)max((int64_t)-1, min((int64_t)(M * step), p.d - j0));   // of them in the row
     const T* const X = (const T*)p.dout + j0;
     const int64_t i0 = c * p.chunk;
     const int len = (int)min((int64_t)p.chunk, p.n - i0);
-    pdl_wait();
     const uint32_t prev = i0 > 0 ? ld_u32(p.key + i0 - 1) : 0xffffffffu;
     const uint32_t next = i0 + len < p.n ? ld_u32(p.key + i0 + len) : 0xffffffffu;
     uint32_t my_key = 0xffffffffu;
@@ -124,16 +255,16 @@ __global__ void __launch_bounds__(kSegThreads, 4) embed_bwd_kernel(const EmbedBw
 }
 
 // The ids whose positions run over a chunk's edge. Each warp of a CTA looks at one
-// chunk and, if such an id begins in it and ends within kJoinWarps chunks, adds the id's sums of
-// the chunks in order, kJoinCols blocks of 128 columns at a time so that enough loads are in
+// chunk and, if such an id begins in it and ends within as many chunks as the CTA has warps (W),
+// adds the id's sums of the chunks in order, kJoinCols blocks of 128 columns at a time so that enough loads are in
 // flight. A longer id is left to the whole CTA, whose warps take its sums in turn; the
 // warps' sums are added in order. blockIdx.y takes the blocks of columns in turn.
 // In long batches an id may have thousands of sums, and it takes two launches: the
-// first also adds the kJoinWarps sums of every CTA whose chunks lie within one id, and lists the
+// first also adds the W sums of every CTA whose chunks lie within one id, and lists the
 // long ids; the second does those, in any order, with the CTAs' sums.
 // (The sums lie in rows of their own, 16-byte aligned whatever the gradient's rows are;
 // `vec` says whether those are.)
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8;       // warps of a CTA, of the kernel that joins alone
 constexpr int kJoinCols = 4;
 constexpr int kJoinBlock = 128;
 constexpr int kJoinOnce = 64;       // chunks up to which one launch does
@@ -179,30 +310,31 @@ __device__ __forceinline__ void join_load(const EmbedBwdParams& p, float* v, int
 
 // The sum of a long id, by a CTA: its sums are the first chunk's second row, the chunks up to
 // the next CTA's, the CTAs' that lie within it (`grouped`), and the chunks that remain.
-template <typename G>
+template <typename G, int W>
 __device__ __forceinline__ void join_long(const EmbedBwdParams& p, bool vec, bool grouped,
-                                          const LongId& id, float (*sum)[kJoinBlock]) {
+                                          const LongId& id, float (*sum)[kJoinBlock], int y,
+                                          int ny) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t first = id.first, end = id.last;
-    const int64_t ga = grouped ? first / kJoinWarps + 1 : 0;
-    const int64_t gb = grouped ? end / kJoinWarps : 0;   // (ga <= gb: it spans kJoinWarps chunks more)
-    const int64_t head = grouped ? ga * kJoinWarps - first : end + 1 - first;
-    const int64_t terms = grouped ? head + (gb - ga) + (end + 1 - gb * kJoinWarps) : head;
+    const int64_t ga = grouped ? first / W + 1 : 0;
+    const int64_t gb = grouped ? end / W : 0;   // (ga <= gb: it spans W chunks more)
+    const int64_t head = grouped ? ga * W - first : end + 1 - first;
+    const int64_t terms = grouped ? head + (gb - ga) + (end + 1 - gb * W) : head;
     auto row = [&](int64_t t) {
         if (t == 0) return 2 * first + 1;
         if (t < head) return 2 * (first + t);
-        if (t < head + (gb - ga)) return 2 * (ga + t - head) * kJoinWarps;
-        return 2 * (gb * kJoinWarps + t - head - (gb - ga));
+        if (t < head + (gb - ga)) return 2 * (ga + t - head) * W;
+        return 2 * (gb * W + t - head - (gb - ga));
     };
     const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
-    for (int64_t b = blockIdx.y; b < blocks; b += gridDim.y) {
+    for (int64_t b = y; b < blocks; b += ny) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t t = w; t < terms; t += 8 * kJoinWarps) {
+        for (int64_t t = w; t < terms; t += 8 * W) {
             float v[8][4];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if (t + u * kJoinWarps < terms) {
-                    join_load(p, v[u], row(t + u * kJoinWarps), b, lane);
+                if (t + u * W < terms) {
+                    join_load(p, v[u], row(t + u * W), b, lane);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
@@ -223,40 +355,28 @@ __device__ __forceinline__ void join_long(const EmbedBwdParams& p, bool vec, boo
             for (int k = 0; k < 4; ++k) {
                 acc[k] = sum[0][lane * 4 + k];
 #pragma unroll
-                for (int r = 1; r < kJoinWarps; ++r) acc[k] += sum[r][lane * 4 + k];
+                for (int r = 1; r < W; ++r) acc[k] += sum[r][lane * 4 + k];
             }
             join_put<G>(p, vec, id.id, j, acc);
         }
     }
 }
 
-template <typename G>
-__global__ void __launch_bounds__(kJoinWarps * 32)
-    embed_long_kernel(const EmbedBwdParams p, bool vec) {
-    __shared__ float sum[kJoinWarps][kJoinBlock];
-    pdl_launch_dependents();
-    pdl_wait();
-    const uint32_t n = ld_u32(p.longs);
-    for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
-        const Raw<16> r = ld_raw<16>((const LongId*)(p.longs + 4) + i);
-        join_long<G>(p, vec, true, LongId{r.w[0], r.w[1], r.w[2], 0}, sum);
-    }
-}
-
-// `once`: the only launch, which does the long ids as well.
-template <typename G>
-__global__ void __launch_bounds__(kJoinWarps * 32, 4)
-    embed_join_kernel(const EmbedBwdParams p, bool vec, bool once) {
-    __shared__ float sum[kJoinWarps][kJoinBlock];
-    __shared__ LongId longid;           // a long id that begins here (there is one at most)
-    __shared__ bool any;
-    pdl_launch_dependents();
+// The ids that begin in chunks c0 .. c0 + W - 1, by a CTA of W warps, in the blocks of columns y,
+// y + ny, ... `once`: the long ones as well (else they are listed).
+struct JoinState {
+    LongId longid;           // a long id that begins here (there is one at most)
+    bool any;
+};
+template <typename G, int W>
+__device__ __forceinline__ void join_chunks(const EmbedBwdParams& p, bool vec, bool once, int64_t c0,
+                                            int y, int ny, JoinState& st,
+                                            float (*sum)[kJoinBlock]) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t c0 = (int64_t)blockIdx.x * kJoinWarps, c = c0 + w;
+    const int64_t c = c0 + w;
     const int64_t i0 = c * p.chunk, i1 = i0 + p.chunk;
     const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
-    if (threadIdx.x == 0) any = false;
-    pdl_wait();
+    if (threadIdx.x == 0) st.any = false;
     int64_t last = -1;
     uint32_t cur = 0xffffffffu;
     bool within = false;                // the CTA's chunks lie within one id
@@ -268,7 +388,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
         const uint32_t far = ld_u32(p.key + e);
         cur = ld_u32(p.key + i1 - 1);
         if (!once) {
-            const int64_t g0 = c0 * p.chunk, g1 = g0 + (int64_t)kJoinWarps * p.chunk;
+            const int64_t g0 = c0 * p.chunk, g1 = g0 + (int64_t)W * p.chunk;
             within = g0 > 0 && g1 < p.n && ld_u32(p.key + g0 - 1) == cur &&
                      ld_u32(p.key + g1) == cur && cur < (uint32_t)p.vocab;
         }
@@ -290,24 +410,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
             }
         }
     }
-    const bool many = last - c >= kJoinWarps;
+    const bool many = last - c >= W;
     __syncthreads();
     if (many && lane == 0) {
-        any = true;
-        longid = LongId{(uint32_t)c, (uint32_t)last, cur, 0};
-        if (!once && blockIdx.y == 0)
-            ((LongId*)(p.longs + 4))[atomicAdd(p.longs, 1u)] = longid;
+        st.any = true;
+        st.longid = LongId{(uint32_t)c, (uint32_t)last, cur, 0};
+        if (!once && y == 0)
+            ((LongId*)(p.longs + 4))[atomicAdd(p.longs, 1u)] = st.longid;
     }
     if (last >= 0 && !many) {
-        for (int64_t b0 = blockIdx.y; b0 < blocks; b0 += (int64_t)gridDim.y * kJoinCols) {
+        for (int64_t b0 = y; b0 < blocks; b0 += (int64_t)ny * kJoinCols) {
             float acc[kJoinCols][4], two[kJoinCols][4];
             // (the first two chunks, which every such id has, in one go)
 #pragma unroll
             for (int u = 0; u < kJoinCols; ++u)
-                join_load(p, acc[u], 2 * c + 1, b0 + u * gridDim.y, lane);
+                join_load(p, acc[u], 2 * c + 1, b0 + u * ny, lane);
 #pragma unroll
             for (int u = 0; u < kJoinCols; ++u)
-                join_load(p, two[u], 2 * (c + 1), b0 + u * gridDim.y, lane);
+                join_load(p, two[u], 2 * (c + 1), b0 + u * ny, lane);
             for (int64_t q = c + 2;; ++q) {
 #pragma unroll
                 for (int u = 0; u < kJoinCols; ++u)
@@ -316,24 +436,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
                 if (q > last) break;
 #pragma unroll
                 for (int u = 0; u < kJoinCols; ++u)
-                    join_load(p, two[u], 2 * q, b0 + u * gridDim.y, lane);
+                    join_load(p, two[u], 2 * q, b0 + u * ny, lane);
             }
 #pragma unroll
             for (int u = 0; u < kJoinCols; ++u) {
-                const int64_t j = (b0 + u * gridDim.y) * kJoinBlock + lane * 4;
+                const int64_t j = (b0 + u * ny) * kJoinBlock + lane * 4;
                 if (j < p.d) join_put<G>(p, vec, cur, j, acc[u]);
             }
         }
     }
     if (within) {
         // the sum of the CTA's chunks, in the place of the first one's
-        for (int64_t b = blockIdx.y + (int64_t)w * gridDim.y; b < blocks;
-             b += (int64_t)kJoinWarps * gridDim.y) {
-            float v[kJoinWarps][4];
+        for (int64_t b = y + (int64_t)w * ny; b < blocks;
+             b += (int64_t)W * ny) {
+            float v[W][4];
 #pragma unroll
-            for (int u = 0; u < kJoinWarps; ++u) join_load(p, v[u], 2 * (c0 + u), b, lane);
+            for (int u = 0; u < W; ++u) join_load(p, v[u], 2 * (c0 + u), b, lane);
 #pragma unroll
-            for (int u = 1; u < kJoinWarps; ++u)
+            for (int u = 1; u < W; ++u)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[0][k] += v[u][k];
             const int64_t j = b * kJoinBlock + lane * 4;
@@ -342,65 +462,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     }
     if (!once) return;
     __syncthreads();
-    if (any) join_long<G>(p, vec, false, longid, sum);
-}
-
-template <typename T, typename G, int NE>
-static cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
-    cudaError_t err = launch_pdl(embed_bwd_kernel<T, G, NE>,
-                                 (unsigned)((p.chunks + p.ty - 1) / p.ty * p.slices), kSegThreads,
-                                 0, s, p);
-    if (err != cudaSuccess || p.chunks < 2) return err;
-    const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
-    const int64_t ctas = (p.chunks - 1 + kJoinWarps - 1) / kJoinWarps;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const bool vec = NE % 4 == 0, once = p.chunks <= kJoinOnce;
-    // (kJoinCols blocks a step; one launch that has long ids to do as well: a block each)
-    const int64_t wide = once ? blocks : (blocks + kJoinCols - 1) / kJoinCols;
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(wide < 8 ? wide : 8), 1);
-    err = cudaLaunchKernelEx(&cfg, embed_join_kernel<G>, p, vec, once);
-    if (err != cudaSuccess || once) return err;
-    // (an id is long if it fills a CTA's chunks: there are at most as many as CTAs)
-    cfg.gridDim = dim3((unsigned)(ctas < 32 ? ctas : 32), (unsigned)(blocks < 32 ? blocks : 32), 1);
-    return cudaLaunchKernelEx(&cfg, embed_long_kernel<G>, p, vec);
-}
-
-cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams& q,
-                             cudaStream_t s) {
-    EmbedBwdParams p = q;
-    const int bytes = ne * dtype_size(dtype);
-    const int m = 16 / bytes < 4 ? 16 / bytes : 4;      // seg_vectors
-    const int64_t vpt = (p.d / ne + m - 1) / m;         // threads a row could use
-    p.tx = 32;
-    while (p.tx < kSegThreads && p.tx < vpt) p.tx *= 2;
-    p.ty = kSegThreads / p.tx;
-    p.slices = (int)((vpt + p.tx - 1) / p.tx);
-#define RN_GO(T, G)                                           \
-    {                                                         \
-        if (ne == 8) return embed_bwd_go<T, G, 8>(p, s);      \
-        if (ne == 4) return embed_bwd_go<T, G, 4>(p, s);      \
-        if (ne == 2) return embed_bwd_go<T, G, 2>(p, s);      \
-        return embed_bwd_go<T, G, 1>(p, s);                   \
-    }
-    if (dtype == DT_F32) {
-        if (ne == 4) return embed_bwd_go<float, float, 4>(p, s);
-        if (ne == 2) return embed_bwd_go<float, float, 2>(p, s);
-        return embed_bwd_go<float, float, 1>(p, s);
-    }
-    if (dtype == DT_BF16) {
-        if (gtype == DT_BF16) RN_GO(__nv_bfloat16, __nv_bfloat16)
-        RN_GO(__nv_bfloat16, float)
-    }
-    if (gtype == DT_F16) RN_GO(__half, __half)
-    RN_GO(__half, float)
-#undef RN_GO
+    if (st.any) join_long<G, W>(p, vec, false, st.longid, sum, y, ny);
 }
 
 }  // namespace rn

@@ -79,9 +79,11 @@ constexpr int sort_key_bits(int64_t vocab) {
     return b;
 }
 constexpr int sort_passes(int64_t vocab) { return (sort_key_bits(vocab) + kSortBits - 1) / kSortBits; }
-// Sorts into key[0], pos[0] and, where p.zero is given, clears the rows of the ids
-// in [0, vocab) that are not among the tokens.
+// Sorts into key[0], pos[0].
 cudaError_t embed_sort_launch(SortParams p, cudaStream_t s);
+// Clears the rows of p.zero of the ids in [0, vocab) that are not among the tokens. To be launched
+// right after a kernel that lets its dependents start only once it has waited itself.
+cudaError_t embed_clear_launch(const SortParams& p, cudaStream_t s);
 
 // dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum of dout[i] over the
 // positions i with tokens[i] == v, for the ids v that occur, from the sorted ids.
@@ -108,8 +110,9 @@ struct EmbedBwdParams {
     float scale;
     int accumulate;
 };
-cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const EmbedBwdParams& p,
-                             cudaStream_t s);
+// The whole gradient.
+cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& sp,
+                             const EmbedBwdParams& p, cudaStream_t s);
 
 // Log probabilities over the rows of a matrix of logits.
 constexpr int kMaxTop = 32;

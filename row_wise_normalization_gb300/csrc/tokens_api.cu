@@ -13,6 +13,31 @@ cudaError_t logprob_fwd_f32(const LogprobParams& p, cudaStream_t s);
 cudaError_t logprob_fwd_bf16(const LogprobParams& p, cudaStream_t s);
 cudaError_t logprob_fwd_f16(const LogprobParams& p, cudaStream_t s);
 
+cudaError_t embed_bwd_f32(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s);
+cudaError_t embed_bwd_bf16(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s);
+cudaError_t embed_bwd_f16(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s);
+
+// Sort, beside it the rows of zeros, then the sums.
+cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& sp,
+                             const EmbedBwdParams& q, cudaStream_t s) {
+    EmbedBwdParams p = q;
+    const int bytes = ne * dtype_size(dtype);
+    const int m = 16 / bytes < 4 ? 16 / bytes : 4;      // seg_vectors
+    const int64_t vpt = (p.d / ne + m - 1) / m;         // threads a row could use
+    p.tx = 32;
+    while (p.tx < 256 && p.tx < vpt) p.tx *= 2;
+    p.ty = 256 / p.tx;
+    p.slices = (int)((vpt + p.tx - 1) / p.tx);
+    cudaError_t err = embed_sort_launch(sp, s);
+    if (err == cudaSuccess && sp.zero) err = embed_clear_launch(sp, s);
+    if (err != cudaSuccess) return err;
+    switch (dtype) {
+        case DT_BF16: return embed_bwd_bf16(gtype, ne, p, s);
+        case DT_F16: return embed_bwd_f16(gtype, ne, p, s);
+        default: return embed_bwd_f32(gtype, ne, p, s);
+    }
+}
+
 cudaError_t logprob_fwd_launch(int dtype, const LogprobParams& p, cudaStream_t s) {
     switch (dtype) {
         case DT_BF16: return logprob_fwd_bf16(p, s);
@@ -210,8 +235,6 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
         sp.zero_pitch = ldg * gs;
         sp.zero_bytes = d * gs;
     }
-    cudaError_t err = embed_sort_launch(sp, s);
-    if (err != cudaSuccess) return done(err);
     EmbedBwdParams p = {};
     p.dout = dout;
     p.dtable = dtable;
@@ -230,7 +253,7 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
     p.scale = scale;
     p.accumulate = accumulate != 0;
     const int ne = access_elems(d, dout, es, lddo, dtable, gs, ldg);
-    return done(embed_bwd_launch(dtype, gtype, ne, p, s));
+    return done(embed_bwd_launch(dtype, gtype, ne, sp, p, s));
 }
 
 int logprob_fwd(int dtype, int itype, const void* logits, int64_t ldl, const void* targets,
