@@ -79,14 +79,16 @@ def logprob(logits, targets, scale, top=0):
 
 
 def logprob_backward(dlogp, dentropy, logits, targets, lse, entropy, scale):
-    """(gradient, magnitude): magnitude bounds each term of the sum that makes
-    an element. lse None: log probabilities from the logits themselves."""
+    """(gradient, magnitude, factor): magnitude bounds each term of the sum that
+    makes an element, factor what a probability below 2^-104 is multiplied by in it. lse
+    None: log probabilities from the logits themselves."""
     x = scale * np.asarray(logits, np.float64)
     lq = None
     if lse is None:
         lq, lse = log_softmax(logits, scale)
     d = np.zeros_like(x)
     mag = np.zeros_like(x)
+    factor = np.zeros((x.shape[0], 1))
     for i in range(x.shape[0]):
         t = -1 if targets is None else int(targets[i])
         there = 0 <= t < x.shape[1]
@@ -99,8 +101,9 @@ def logprob_backward(dlogp, dentropy, logits, targets, lse, entropy, scale):
         zp = np.where(p > 0, z, 0.0)
         H = float(entropy[i]) if dentropy is not None else 0.0
         d[i] = -scale * p * (g + h * (zp + H))
+        factor[i] = scale * (abs(g) + abs(h) * (104 + abs(H)))
         mag[i] = scale * p * (abs(g) + abs(h) * (np.abs(zp) + abs(H))) * (1 + np.abs(zp))
         if there:
             d[i, t] += scale * g
             mag[i, t] += scale * abs(g)
-    return d, mag
+    return d, mag, factor

@@ -36,7 +36,7 @@ def test_logprob_gradient_against_differences(scale):
     t = np.array([4, 0, -100])
     g, h = rng.normal(size=3), rng.normal(size=3)
     r = ot.logprob(x, t, scale)
-    d, _ = ot.logprob_backward(g, h, x, t, r["lse"], r["entropy"], scale)
+    d, _, _ = ot.logprob_backward(g, h, x, t, r["lse"], r["entropy"], scale)
     step = 1e-5
     for i in range(3):
         for j in range(7):

@@ -17,7 +17,7 @@ u = 2^-24 is FP32's half step, uT the storage type's (2^-8 BF16, 2^-11 FP16).
       dS + u (|W/S| (2 DEPTH + 12) + 8 E z^2) + 4 u |log S|.
 * gradient: p_j is off by u (4 |z_j| + 6) relative; the terms' magnitudes and
   (1 + |z|) come from the oracle, so 8 u covers them, with one rounding of the
-  stored value.
+  stored value; the exponential's results below 2^-126 are zero.
 """
 from __future__ import annotations
 
@@ -95,8 +95,11 @@ def check_logprob(out, want, logits, scale, what=""):
               + 6 * U * np.where(np.isfinite(w), np.abs(w), 0), what + "top_logp")
 
 
-def check_logprob_bwd(got, want, mag, dtype, what="dlogits"):
+def check_logprob_bwd(got, want, mag, factor, dtype, what="dlogits"):
     with np.errstate(invalid="ignore"):
         tol = 8 * U * mag + UT[dtype] * (np.abs(want) + 8 * U * mag) + TINY[dtype]
-        tol = tol + 2.0 ** -125 * (1 + mag)     # exponentials below FP32's range are zero
+        # Probabilities below 2^-126 are taken as zero: what is lost is at most that times
+        # scale (|g| + |h| (|log p| + H)), and |log p| < 104 down to FP32's last subnormal
+        # number (beyond, p |log p| only falls). One more rounding of each.
+        tol = tol + 2.0 ** -126 * factor * (1 + 8 * U)
     _near(got, want, tol, what)
