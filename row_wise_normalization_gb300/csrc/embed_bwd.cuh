@@ -77,14 +77,152 @@ cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, embed_long_kernel<G>, p, vec);
 }
 
-// One type of rows and of the gradient.
+// Few ids: one launch, without a sort. A CTA takes one position and a block of columns (a warp's),
+// compares all ids with the position's and leaves if an earlier position has the same id. Else it
+// lists the id's positions in order, its 8 warps add every 8th row each, and the warps' sums are
+// added in order. Other CTAs of the launch clear the rows of absent ids.
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+static_assert(kFewIds <= 32 * 32, "a lane for each word of the marks");
+
+template <typename T, typename G, int NE>
+__global__ void __launch_bounds__(kFewThreads)
+    embed_few_kernel(const SortParams z, const EmbedBwdParams p, int zero_ctas, FastDiv blocks) {
+    constexpr int M = seg_vectors<T, NE>();
+    constexpr int B = NE * (int)sizeof(T);
+    constexpr int E = M * NE;
+    constexpr int kCols = 32 * E;           // columns of a block
+    static_assert(kFewWarps * kCols * 4 <= kZeroRange / 8, "the warps' sums");
+    __shared__ __align__(16) uint32_t raw[kZeroRange / 32];
+    __shared__ uint32_t mask[32];
+    __shared__ uint16_t list[kFewIds];
+    pdl_launch_dependents();
+    pdl_wait();
+    if ((int)blockIdx.x < zero_ctas) {
+        clear_absent<kFewThreads>(z, (int)blockIdx.x, zero_ctas, raw);
+        return;
+    }
+    const int t = threadIdx.x, w = t >> 5, lane = t & 31, n = (int)p.n;
+    const uint32_t at = blockIdx.x - (unsigned)zero_ctas;
+    const int i = (int)fast_quot(at, blocks);
+    const int64_t col = (int64_t)(at - (uint32_t)i * blocks.d) * kCols;
+    const int64_t id = ld_id(z.tokens, i, z.itype);
+    if (id < 0 || id >= p.vocab) return;
+    // the positions that hold the id: a bit each
+    if (t < 32) mask[t] = 0;
+    __syncthreads();
+    for (int j0 = 0; j0 < n; j0 += kFewThreads) {
+        const int j = j0 + t;
+        const unsigned m = __ballot_sync(0xffffffffu, j < n && ld_id(z.tokens, j, z.itype) == id);
+        if (lane == 0) mask[j >> 5] = m;
+    }
+    __syncthreads();
+    const uint32_t mine = mask[lane];
+    const int word = i >> 5;
+    if (__any_sync(0xffffffffu, lane < word ? mine != 0
+                                            : lane == word && (mine & ((1u << (i & 31)) - 1)) != 0))
+        return;                             // an earlier position has it: the same in every warp
+    int before = __popc(mine);              // inclusive, then exclusive sum over the words
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int q = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += q;
+    }
+    const int rows = __shfl_sync(0xffffffffu, before, 31);
+    before -= __popc(mine);
+    for (int k = w; k < 32; k += kFewWarps) {
+        const uint32_t m = __shfl_sync(0xffffffffu, mine, k);
+        const int first = __shfl_sync(0xffffffffu, before, k);
+        if (m >> lane & 1u) list[first + __popc(m & ((1u << lane) - 1))] = (uint16_t)(k * 32 + lane);
+    }
+    __syncthreads();
+    const int64_t j0 = col + lane * NE;
+    constexpr int step = 32 * NE;
+    const int cols = (int)max((int64_t)-1, min((int64_t)kCols, p.d - j0));
+    const T* const X = (const T*)p.dout + j0;
+    F2 acc[E / 2];
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) acc[k] = f2s(0.f);
+    for (int r0 = w; r0 < rows; r0 += kSegU * kFewWarps) {
+        Raw<B> r[kSegU][M];
+#pragma unroll
+        for (int u = 0; u < kSegU; ++u) {
+            if (r0 + u * kFewWarps < rows) {
+                const int64_t pos = list[r0 + u * kFewWarps];
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    if (m * step < cols) r[u][m] = ld_raw<B>(X + pos * p.lddo + m * step);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kSegU; ++u) {
+            if (r0 + u * kFewWarps < rows) {
+                float v[E];
+#pragma unroll
+                for (int m = 0; m < M; ++m) unpack<T, NE>(v + m * NE, r[u][m]);
+#pragma unroll
+                for (int k = 0; k < E / 2; ++k) acc[k] = add2(acc[k], f2(v[2 * k], v[2 * k + 1]));
+            }
+        }
+    }
+    float s[E];
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) f2_get(acc[k], s[2 * k], s[2 * k + 1]);
+    G* const g = (G*)p.dtable + id * p.ldg + col;
+    if (rows == 1) {
+        if (w != 0) return;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            if (m * step < cols) {
+                G* const o = g + lane * NE + m * step;
+                float v[NE];
+                if (p.accumulate) ld_elems<G, NE>(v, o);
+#pragma unroll
+                for (int k = 0; k < NE; ++k)
+                    v[k] = p.accumulate ? fmaf(p.scale, s[m * NE + k], v[k]) : p.scale * s[m * NE + k];
+                st_elems<G, NE>(o, v);
+            }
+        }
+        return;
+    }
+    float(*const red)[kCols] = (float(*)[kCols])raw;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int k = 0; k < NE; ++k) red[w][m * step + lane * NE + k] = s[m * NE + k];
+    __syncthreads();
+    const int warps = rows < kFewWarps ? rows : kFewWarps;
+    for (int c = t; c < kCols && col + c < p.d; c += kFewThreads) {
+        float v = red[0][c], o[1];
+        for (int q = 1; q < warps; ++q) v += red[q][c];
+        if (p.accumulate) ld_elems<G, 1>(o, g + c);
+        o[0] = p.accumulate ? fmaf(p.scale, v, o[0]) : p.scale * v;
+        st_elems<G, 1>(g + c, o);
+    }
+}
+
+template <typename T, typename G, int NE>
+cudaError_t embed_few_go(const SortParams& z, const EmbedBwdParams& p, int sms, cudaStream_t s) {
+    const uint32_t blocks = (uint32_t)((p.d + 32 * seg_vectors<T, NE>() * NE - 1) /
+                                       (32 * seg_vectors<T, NE>() * NE));
+    const int zero_ctas = z.zero ? 4 * sms : 0;
+    return launch_pdl(embed_few_kernel<T, G, NE>, (unsigned)zero_ctas + (unsigned)p.n * blocks,
+                      kFewThreads, 0, s, z, p, zero_ctas, fast_div(blocks));
+}
+
+// One type of rows and of the gradient. z, sms: few ids, in one launch.
+template <typename T, typename G, int NE>
+cudaError_t embed_bwd_one(const SortParams* z, int sms, const EmbedBwdParams& p, cudaStream_t s) {
+    return z ? embed_few_go<T, G, NE>(*z, p, sms, s) : embed_bwd_go<T, G, NE>(p, s);
+}
 template <typename T, typename G>
-cudaError_t embed_bwd_t(int ne, const EmbedBwdParams& p, cudaStream_t s) {
+cudaError_t embed_bwd_t(int ne, const SortParams* z, int sms, const EmbedBwdParams& p,
+                        cudaStream_t s) {
     if constexpr (sizeof(T) == 2)
-        if (ne == 8) return embed_bwd_go<T, G, 8>(p, s);
-    if (ne == 4) return embed_bwd_go<T, G, 4>(p, s);
-    if (ne == 2) return embed_bwd_go<T, G, 2>(p, s);
-    return embed_bwd_go<T, G, 1>(p, s);
+        if (ne == 8) return embed_bwd_one<T, G, 8>(z, sms, p, s);
+    if (ne == 4) return embed_bwd_one<T, G, 4>(z, sms, p, s);
+    if (ne == 2) return embed_bwd_one<T, G, 2>(z, sms, p, s);
+    return embed_bwd_one<T, G, 1>(z, sms, p, s);
 }
 
 }  // namespace rn

@@ -26,73 +26,11 @@
 
 namespace rn {
 
-constexpr int kZeroRange = 65536;   // ids a CTA marks at a time (8 KB of bits)
-
-// Clears `bytes` (a multiple of 2) at p by `lanes` threads, of which this is number l.
-__device__ __forceinline__ void clear_row(char* p, int64_t bytes, int l, int lanes) {
-    const int64_t head = min((int64_t)((0u - (unsigned)(uintptr_t)p) & 15u), bytes);
-    const int64_t nv = (bytes - head) / 16, tail = head + nv * 16;
-    const Raw<16> z = {};
-    for (int64_t v = l; v < nv; v += lanes) st_raw(p + head + v * 16, z);
-    const Raw<2> h = {};
-    for (int64_t b = 2 * l; b < head; b += 2 * lanes) st_raw(p + b, h);
-    for (int64_t b = tail + 2 * l; b < bytes; b += 2 * lanes) st_raw(p + b, h);
-}
-
-// Clears the rows of the absent ids of a part of the vocabulary. What it touches no kernel of the
-// call before it does, and the one ahead has waited for all others before it let this one
-// start: it waits at its end.
+// Clears the rows of the absent ids. What it touches no kernel of the call before it does, and the
+// one ahead has waited for all others before it let this one start: it waits at its end.
 __global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(const SortParams p) {
     __shared__ uint32_t bits[kZeroRange / 32];
-    const int t = threadIdx.x;
-    // (whole groups of 32 rows: 16383 x 771 FP16 into FP32 took 69 us without, 57 us with)
-    const int64_t share = ((p.vocab + gridDim.x - 1) / gridDim.x + 31) / 32 * 32;
-    const int64_t end = min(p.vocab, (int64_t)(blockIdx.x + 1) * share);
-    // the ids as 16-byte vectors, and fewer than two vectors' before and after
-    const int64_t per = 16 / index_size(p.itype);
-    const int64_t head = min(p.n, (int64_t)((0u - (unsigned)(uintptr_t)p.tokens) & 15u) /
-                                      index_size(p.itype));
-    const int64_t nv = (p.n - head) / per;
-    const char* const body = (const char*)p.tokens + head * index_size(p.itype);
-    // threads of a row: as many 16-byte stores as it has, up to a warp's
-    int lanes = 32;
-    while (lanes > 1 && (lanes / 2) * 16 >= p.zero_bytes) lanes /= 2;
-    for (int64_t lo = (int64_t)blockIdx.x * share; lo < end; lo += kZeroRange) {
-        const int cnt = (int)min((int64_t)kZeroRange, end - lo);
-        __syncthreads();
-        for (int w = t; w < (cnt + 31) / 32; w += kSortThreads) bits[w] = 0;
-        __syncthreads();
-        auto mark = [&](int64_t id) {
-            const uint64_t k = (uint64_t)id - (uint64_t)lo;
-            if (k < (uint64_t)cnt) atomicOr(&bits[k >> 5], 1u << (k & 31));
-        };
-        // Many loads in flight: once the first CTAs store, a load waits behind their stores
-        // (8-byte loads, twice as many rounds: some CTAs read 65536 ids for 98 us).
-        constexpr int U = 8;
-        for (int64_t v = t; v < nv; v += kSortThreads * U) {
-            Raw<16> r[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (v + u * kSortThreads < nv) r[u] = ld_raw<16>(body + (v + u * kSortThreads) * 16);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (v + u * kSortThreads < nv) {
-                    if (p.itype == IT_I64) {
-                        mark((int64_t)((uint64_t)r[u].w[1] << 32 | r[u].w[0]));
-                        mark((int64_t)((uint64_t)r[u].w[3] << 32 | r[u].w[2]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mark((int32_t)r[u].w[k]);
-                    }
-                }
-            }
-        }
-        if (t < p.n - nv * per) mark(ld_id(p.tokens, t < head ? t : nv * per + t, p.itype));
-        __syncthreads();
-        for (int r = t / lanes; r < cnt; r += kSortThreads / lanes)
-            if (!((bits[r >> 5] >> (r & 31)) & 1u))
-                clear_row(p.zero + (lo + r) * p.zero_pitch, p.zero_bytes, t % lanes, lanes);
-    }
+    clear_absent<kSortThreads>(p, (int)blockIdx.x, (int)gridDim.x, bits);
     pdl_launch_dependents();
     pdl_wait();
 }
@@ -266,12 +204,7 @@ cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
     return p.n <= kSortClusterMax ? sort_in_cluster(p, s) : sort_in_memory(p, s);
 }
 
-cudaError_t embed_clear_launch(const SortParams& p, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess)
-        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (err != cudaSuccess) return err;
+cudaError_t embed_clear_launch(const SortParams& p, int sms, cudaStream_t s) {
     return launch_pdl(embed_clear_kernel, 2 * (unsigned)sms, kSortThreads, 0, s, p);
 }
 

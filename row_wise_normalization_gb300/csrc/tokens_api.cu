@@ -13,11 +13,11 @@ cudaError_t logprob_fwd_f32(const LogprobParams& p, cudaStream_t s);
 cudaError_t logprob_fwd_bf16(const LogprobParams& p, cudaStream_t s);
 cudaError_t logprob_fwd_f16(const LogprobParams& p, cudaStream_t s);
 
-cudaError_t embed_bwd_f32(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s);
-cudaError_t embed_bwd_bf16(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s);
-cudaError_t embed_bwd_f16(int gtype, int ne, const EmbedBwdParams& p, cudaStream_t s);
+cudaError_t embed_bwd_f32(int, int, const SortParams*, int, const EmbedBwdParams&, cudaStream_t);
+cudaError_t embed_bwd_bf16(int, int, const SortParams*, int, const EmbedBwdParams&, cudaStream_t);
+cudaError_t embed_bwd_f16(int, int, const SortParams*, int, const EmbedBwdParams&, cudaStream_t);
 
-// Sort, beside it the rows of zeros, then the sums.
+// Few ids: one launch. Else the sort, beside it the rows of zeros, then the sums.
 cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& sp,
                              const EmbedBwdParams& q, cudaStream_t s) {
     EmbedBwdParams p = q;
@@ -28,13 +28,19 @@ cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& sp,
     while (p.tx < 256 && p.tx < vpt) p.tx *= 2;
     p.ty = 256 / p.tx;
     p.slices = (int)((vpt + p.tx - 1) / p.tx);
-    cudaError_t err = embed_sort_launch(sp, s);
-    if (err == cudaSuccess && sp.zero) err = embed_clear_launch(sp, s);
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const bool few = embed_few(p.n, p.d, dtype_size(dtype));
+    if (err == cudaSuccess && !few) err = embed_sort_launch(sp, s);
+    if (err == cudaSuccess && !few && sp.zero) err = embed_clear_launch(sp, sms, s);
     if (err != cudaSuccess) return err;
+    const SortParams* const z = few ? &sp : nullptr;
     switch (dtype) {
-        case DT_BF16: return embed_bwd_bf16(gtype, ne, p, s);
-        case DT_F16: return embed_bwd_f16(gtype, ne, p, s);
-        default: return embed_bwd_f32(gtype, ne, p, s);
+        case DT_BF16: return embed_bwd_bf16(gtype, ne, z, sms, p, s);
+        case DT_F16: return embed_bwd_f16(gtype, ne, z, sms, p, s);
+        default: return embed_bwd_f32(gtype, ne, z, sms, p, s);
     }
 }
 
