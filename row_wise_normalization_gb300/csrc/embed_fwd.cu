@@ -16,6 +16,17 @@ namespace rn {
 constexpr int kEmbedThreads = 256;
 constexpr int kEmbedU = 4;
 
+// The NE elements of r times `scale`, rounded once. (A scale of 1 leaves the bits: no arithmetic.)
+template <typename T, int NE>
+__device__ __forceinline__ void scale_raw(Raw<NE * (int)sizeof(T)>& r, float scale) {
+    float v[NE];
+    unpack<T, NE>(v, r);
+    const F2 k = f2s(scale);
+#pragma unroll
+    for (int i = 0; i < NE; i += 2) f2_get(mul2(f2(v[i], v[i + 1]), k), v[i], v[i + 1]);
+    r = pack<T, NE>(v);
+}
+
 template <typename T, int NE>
 __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const EmbedParams p, int itype) {
     pdl_launch_dependents();
@@ -48,13 +59,10 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const EmbedPar
 #pragma unroll
     for (int u = 0; u < kEmbedU; ++u) {
         if (base + u * kEmbedThreads + threadIdx.x < p.total) {
-            float v[NE];
-            unpack<T, NE>(v, r[u]);
-            const bool there = id[u] >= 0 && id[u] < p.vocab;
             // (an absent id gives +0 whatever the sign of the scale)
-#pragma unroll
-            for (int k = 0; k < NE; ++k) v[k] = there ? v[k] * p.scale : 0.f;
-            st_elems<T, NE>((T*)p.out + row[u] * p.ldo + (int64_t)col[u] * NE, v);
+            if (p.scale != 1.f)
+                scale_raw<T, NE>(r[u], id[u] >= 0 && id[u] < p.vocab ? p.scale : 0.f);
+            st_raw((T*)p.out + row[u] * p.ldo + (int64_t)col[u] * NE, r[u]);
         }
     }
 }
@@ -116,11 +124,9 @@ __global__ void __launch_bounds__(kEmbedThreads)
                 case 2: pick(std::integral_constant<int, 2>{}); break;
                 default: pick(std::integral_constant<int, 3>{}); break;
             }
-            float x[VEC];
-            unpack<T, VEC>(x, r);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[i] = there ? x[i] * p.scale : 0.f;
-            st_elems<T, VEC>(O + head + v * VEC, x);
+            // (an absent id gives +0 whatever the sign of the scale)
+            if (p.scale != 1.f) scale_raw<T, VEC>(r, there ? p.scale : 0.f);
+            st_raw(O + head + v * VEC, r);
         }
     }
     if (piece == 0 && lane < head + (d - tail)) {
