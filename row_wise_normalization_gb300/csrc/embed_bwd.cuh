@@ -10,6 +10,12 @@
 // each chunk in the workspace, and a second kernel adds those in chunk order, so that an
 // id which fills half of a batch is summed by as many groups as its rows fill.
 // Every sum has a fixed order: results repeat bit for bit.
+//
+// 65536 x 4096 BF16 into 128000 rows (19851 of them occur): 276 us where the bytes alone
+// take 234: rows of zeros 142, sums 137 (with the write-back of the zeros' last lines; alone
+// 107 us, 0.83 of the DRAM's rate), joins 20, most of it the latency of two launches. 16383 x 771
+// FP16 into FP32, a third of it one id: 53 us (bytes 26): at odd widths an access is
+// 2 bytes, and sums are bound by instructions (17 us).
 #pragma once
 
 #include "rn_embed.cuh"
@@ -32,7 +38,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4)
     __shared__ JoinState st;
     pdl_launch_dependents();
     pdl_wait();
-    join_chunks<G, kJoinWarps>(p, vec, once, (int64_t)blockIdx.x * kJoinWarps, blockIdx.y, gridDim.y,
+    join_chunks<G>(p, vec, once, (int64_t)blockIdx.x * kJoinWarps, blockIdx.y, gridDim.y,
                                st, sum);
 }
 
@@ -45,7 +51,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const uint32_t n = ld_u32(p.longs);
     for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
         const Raw<16> r = ld_raw<16>((const LongId*)(p.longs + 4) + i);
-        join_long<G, kJoinWarps>(p, vec, true, LongId{r.w[0], r.w[1], r.w[2], 0}, sum, blockIdx.y,
+        join_long<G>(p, vec, true, LongId{r.w[0], r.w[1], r.w[2], 0}, sum, blockIdx.y,
                                  gridDim.y);
     }
 }

@@ -324,17 +324,17 @@ __device__ __forceinline__ void sum_chunk(const EmbedBwdParams& p, int64_t c, in
     put(cnt - 1, next == __shfl_sync(0xffffffffu, my_key, cnt - 1));
 }
 
-// The ids whose positions run over a chunk's edge. Each warp of a CTA looks at one
-// chunk and, if such an id begins in it and ends within as many chunks as the CTA has warps (W),
-// adds the id's sums of the chunks in order, kJoinCols blocks of 128 columns at a time so that enough loads are in
-// flight. A longer id is left to the whole CTA, whose warps take its sums in turn; the
-// warps' sums are added in order. blockIdx.y takes the blocks of columns in turn.
+// The ids whose positions run over a chunk's edge. Each warp of a CTA looks at one chunk and, if
+// such an id begins in it and ends within kJoinWarps chunks, adds the id's
+// sums of the chunks in order, kJoinCols blocks of 128 columns at a time so that enough
+// loads are in flight. A longer id is left to the whole CTA, whose warps take its sums in turn;
+// the warps' sums are added in order. The CTA takes every ny-th block of columns.
 // In long batches an id may have thousands of sums, and it takes two launches: the
-// first also adds the W sums of every CTA whose chunks lie within one id, and lists the
+// first also adds the kJoinWarps sums of every CTA whose chunks lie within one id, and lists the
 // long ids; the second does those, in any order, with the CTAs' sums.
 // (The sums lie in rows of their own, 16-byte aligned whatever the gradient's rows are;
 // `vec` says whether those are.)
-constexpr int kJoinWarps = 8;       // warps of a CTA, of the kernel that joins alone
+constexpr int kJoinWarps = 8;       // warps, and chunks, of a CTA
 constexpr int kJoinCols = 4;
 constexpr int kJoinBlock = 128;
 constexpr int kJoinOnce = 64;       // chunks up to which one launch does
@@ -380,31 +380,31 @@ __device__ __forceinline__ void join_load(const EmbedBwdParams& p, float* v, int
 
 // The sum of a long id, by a CTA: its sums are the first chunk's second row, the chunks up to
 // the next CTA's, the CTAs' that lie within it (`grouped`), and the chunks that remain.
-template <typename G, int W>
+template <typename G>
 __device__ __forceinline__ void join_long(const EmbedBwdParams& p, bool vec, bool grouped,
                                           const LongId& id, float (*sum)[kJoinBlock], int y,
                                           int ny) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t first = id.first, end = id.last;
-    const int64_t ga = grouped ? first / W + 1 : 0;
-    const int64_t gb = grouped ? end / W : 0;   // (ga <= gb: it spans W chunks more)
-    const int64_t head = grouped ? ga * W - first : end + 1 - first;
-    const int64_t terms = grouped ? head + (gb - ga) + (end + 1 - gb * W) : head;
+    const int64_t ga = grouped ? first / kJoinWarps + 1 : 0;
+    const int64_t gb = grouped ? end / kJoinWarps : 0;   // (ga <= gb: it spans kJoinWarps chunks more)
+    const int64_t head = grouped ? ga * kJoinWarps - first : end + 1 - first;
+    const int64_t terms = grouped ? head + (gb - ga) + (end + 1 - gb * kJoinWarps) : head;
     auto row = [&](int64_t t) {
         if (t == 0) return 2 * first + 1;
         if (t < head) return 2 * (first + t);
-        if (t < head + (gb - ga)) return 2 * (ga + t - head) * W;
-        return 2 * (gb * W + t - head - (gb - ga));
+        if (t < head + (gb - ga)) return 2 * (ga + t - head) * kJoinWarps;
+        return 2 * (gb * kJoinWarps + t - head - (gb - ga));
     };
     const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
     for (int64_t b = y; b < blocks; b += ny) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t t = w; t < terms; t += 8 * W) {
+        for (int64_t t = w; t < terms; t += 8 * kJoinWarps) {
             float v[8][4];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if (t + u * W < terms) {
-                    join_load(p, v[u], row(t + u * W), b, lane);
+                if (t + u * kJoinWarps < terms) {
+                    join_load(p, v[u], row(t + u * kJoinWarps), b, lane);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[u][k] = 0.f;
@@ -425,20 +425,20 @@ __device__ __forceinline__ void join_long(const EmbedBwdParams& p, bool vec, boo
             for (int k = 0; k < 4; ++k) {
                 acc[k] = sum[0][lane * 4 + k];
 #pragma unroll
-                for (int r = 1; r < W; ++r) acc[k] += sum[r][lane * 4 + k];
+                for (int r = 1; r < kJoinWarps; ++r) acc[k] += sum[r][lane * 4 + k];
             }
             join_put<G>(p, vec, id.id, j, acc);
         }
     }
 }
 
-// The ids that begin in chunks c0 .. c0 + W - 1, by a CTA of W warps, in the blocks of columns y,
+// The ids that begin in chunks c0 .. c0 + kJoinWarps - 1, by a CTA, in the blocks of columns y,
 // y + ny, ... `once`: the long ones as well (else they are listed).
 struct JoinState {
     LongId longid;           // a long id that begins here (there is one at most)
     bool any;
 };
-template <typename G, int W>
+template <typename G>
 __device__ __forceinline__ void join_chunks(const EmbedBwdParams& p, bool vec, bool once, int64_t c0,
                                             int y, int ny, JoinState& st,
                                             float (*sum)[kJoinBlock]) {
@@ -458,7 +458,7 @@ __device__ __forceinline__ void join_chunks(const EmbedBwdParams& p, bool vec, b
         const uint32_t far = ld_u32(p.key + e);
         cur = ld_u32(p.key + i1 - 1);
         if (!once) {
-            const int64_t g0 = c0 * p.chunk, g1 = g0 + (int64_t)W * p.chunk;
+            const int64_t g0 = c0 * p.chunk, g1 = g0 + (int64_t)kJoinWarps * p.chunk;
             within = g0 > 0 && g1 < p.n && ld_u32(p.key + g0 - 1) == cur &&
                      ld_u32(p.key + g1) == cur && cur < (uint32_t)p.vocab;
         }
@@ -480,7 +480,7 @@ __device__ __forceinline__ void join_chunks(const EmbedBwdParams& p, bool vec, b
             }
         }
     }
-    const bool many = last - c >= W;
+    const bool many = last - c >= kJoinWarps;
     __syncthreads();
     if (many && lane == 0) {
         st.any = true;
@@ -518,12 +518,12 @@ __device__ __forceinline__ void join_chunks(const EmbedBwdParams& p, bool vec, b
     if (within) {
         // the sum of the CTA's chunks, in the place of the first one's
         for (int64_t b = y + (int64_t)w * ny; b < blocks;
-             b += (int64_t)W * ny) {
-            float v[W][4];
+             b += (int64_t)kJoinWarps * ny) {
+            float v[kJoinWarps][4];
 #pragma unroll
-            for (int u = 0; u < W; ++u) join_load(p, v[u], 2 * (c0 + u), b, lane);
+            for (int u = 0; u < kJoinWarps; ++u) join_load(p, v[u], 2 * (c0 + u), b, lane);
 #pragma unroll
-            for (int u = 1; u < W; ++u)
+            for (int u = 1; u < kJoinWarps; ++u)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[0][k] += v[u][k];
             const int64_t j = b * kJoinBlock + lane * 4;
@@ -532,7 +532,7 @@ __device__ __forceinline__ void join_chunks(const EmbedBwdParams& p, bool vec, b
     }
     if (!once) return;
     __syncthreads();
-    if (st.any) join_long<G, W>(p, vec, false, st.longid, sum, y, ny);
+    if (st.any) join_long<G>(p, vec, false, st.longid, sum, y, ny);
 }
 
 }  // namespace rn

@@ -13,16 +13,21 @@
 // exactly (it is a reference, and the same in every term), and e^z one
 // special-function instruction. Pairs of elements go through the packed FP32
 // pipe: 4 instructions a pair beside the two exponentials, so that the pass
-// stays below the time its bytes take even for 16-bit logits.
+// stays below the time its bytes take even for 16-bit logits: 8192 x 128000 BF16 with
+// entropies 309 us, the measured copy's rate over its 2.1 GB (608 us with scalar arithmetic,
+// a test of every element for -inf and two CTAs of 512 threads an SM; four of 256 let one
+// row's end overlap another's reading).
 //
 // A masked element (-inf) gives e = 0, and 0 * -inf would be NaN in W: where entropies are
 // wanted, elements are held at -1e30 or above (NaN passes), where e is 0 as well: one packed
-// instruction a pair of BF16. A row whose largest product is beyond 2^24
+// instruction a pair of BF16 (summing masked batches twice instead: 2048 x 128000 BF16, a fifth
+// masked, 20 alternatives 157 us, this way 124 us). A row whose largest product is beyond 2^24
 // (every column at a mask's lowest value, say) cannot be referred to c in FP32: it is
 // summed again, from differences of logits (row_again).
 //
 // A row is split over the CTAs of a cluster where there are few rows; the
-// CTAs' results meet in the first one's shared memory.
+// CTAs' results meet in the first one's shared memory (one row of 128000 FP32 3.0 us, of
+// which the launch is about 2; 64 x 50001 BF16 5.3 us).
 //
 // Alternatives: the `top` largest logits, the lowest index first among equal
 // ones, found in the same pass. A candidate is a 64-bit key: the value's bits in

@@ -8,6 +8,8 @@ general ones.
 """
 from __future__ import annotations
 
+from functools import partial
+
 import torch
 
 from . import _check_f32_cuda, _empty_like_home, _rows_of, capi
@@ -77,7 +79,7 @@ def _device(*tensors):
 
 def _elsewhere(dev, stream):
     """Whether the call needs another device or stream made current first."""
-    return stream is not None or (dev >= 0 and dev != torch.cuda.current_device())
+    return stream is not None or (dev >= 0 and dev != torch._C._cuda_getDevice())
 
 
 class _On:
@@ -113,15 +115,14 @@ def _stream(dev):
             else torch.cuda.current_stream().cuda_stream)
 
 
-def _at(home, dev):
-    """The device of a call's outputs (None: host memory, like `home`)."""
-    return home.device if home.is_cuda else torch.device("cuda", dev) if dev >= 0 else None
-
-
-def _new(home, at, shape, dtype):
-    if at is not None:
-        return torch.empty(shape, dtype=dtype, device=at)
-    return _empty_like_home(home, shape, dtype)
+def _maker(home, dev):
+    """What allocates a call's outputs, given their shape and dtype: on the call's device,
+    or in host memory like `home`."""
+    if home.is_cuda:
+        return partial(torch.empty, device=home.device)
+    if dev >= 0:
+        return partial(torch.empty, device=torch.device("cuda", dev))
+    return partial(_empty_like_home, home)
 
 
 def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
@@ -145,13 +146,15 @@ def embed_fwd(tokens, table, scale: float = 1.0, *, out=None, stream=None):
             return embed_fwd(tokens, table, scale, out=out)
     n = tokens.numel()
     if out is None:
-        out, ldo = _new(table, _at(table, dev), (*tokens.shape, d), dtype), d
+        out, ldo = _maker(table, dev)((*tokens.shape, d), dtype=dtype), d
     else:
         if out.numel() != n * d or out.shape[-1:] != (d,):
             raise ValueError(f"out must hold {n} rows of {d}")
         ldo = _stride("out", out, d, dtype)
-    capi.check(_C.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt, out.data_ptr(),
-                              ldo, n, int(vocab), d, float(scale), _stream(dev)))
+    st = _C.embed_fwd(code, it, tokens.data_ptr(), table.data_ptr(), ldt, out.data_ptr(), ldo, n,
+                      int(vocab), d, float(scale), _stream(dev))
+    if st:
+        capi.check(st)
     return out
 
 
@@ -191,7 +194,7 @@ def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtabl
             return embed_bwd(dout, tokens, vocab, scale, dtype=dtype, dtable=dtable,
                              accumulate=accumulate, workspace=workspace)
     if dtable is None:
-        dtable, ldg = _new(dout, _at(dout, dev), (vocab, d), gdtype), d
+        dtable, ldg = _maker(dout, dev)((vocab, d), dtype=gdtype), d
     else:
         if tuple(dtable.shape) != (vocab, d):
             raise ValueError(f"dtable must be of shape [{vocab}, {d}]")
@@ -204,9 +207,11 @@ def embed_bwd(dout, tokens, vocab: int, scale: float = 1.0, *, dtype=None, dtabl
         if not (workspace.is_cuda and workspace.is_contiguous()):
             raise ValueError("workspace must be a contiguous CUDA tensor")
         nbytes = workspace.numel() * workspace.element_size()
-    capi.check(_C.embed_bwd(code, _FLOATS[gdtype], it, dout.data_ptr(), lddo, tokens.data_ptr(),
-                              dtable.data_ptr(), ldg, n, int(vocab), d, float(scale), 1 if accumulate else 0,
-                              workspace.data_ptr(), nbytes, _stream(dev)))
+    st = _C.embed_bwd(code, _FLOATS[gdtype], it, dout.data_ptr(), lddo, tokens.data_ptr(),
+                      dtable.data_ptr(), ldg, n, int(vocab), d, float(scale), 1 if accumulate else
+                      0, workspace.data_ptr(), nbytes, _stream(dev))
+    if st:
+        capi.check(st)
     return dtable
 
 
@@ -240,24 +245,25 @@ def logprob_fwd(logits, targets=None, scale: float = 1.0, *, top: int = 0,
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return logprob_fwd(logits, targets, scale, top=top, want_entropy=want_entropy)
-    at = _at(logits, dev)
+    new = _maker(logits, dev)
     logp = entropy = ids = top_logp = None
     a_logp = a_entropy = a_ids = a_top = 0
     if targets is not None:
-        logp = _new(logits, at, lead, _F32)
+        logp = new(lead, dtype=_F32)
         a_logp = logp.data_ptr()
     if want_entropy:
-        entropy = _new(logits, at, lead, _F32)
+        entropy = new(lead, dtype=_F32)
         a_entropy = entropy.data_ptr()
-    lse = _new(logits, at, lead, _F32)
+    lse = new(lead, dtype=_F32)
     if top > 0:
         lead = (*lead, top)
-        ids = _new(logits, at, lead, itype)
-        top_logp = _new(logits, at, lead, _F32)
+        ids = new(lead, dtype=itype)
+        top_logp = new(lead, dtype=_F32)
         a_ids, a_top = ids.data_ptr(), top_logp.data_ptr()
-    capi.check(_C.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, a_logp, a_entropy,
-                                lse.data_ptr(), a_ids, a_top, rows, vocab, int(top), float(scale),
-                                _stream(dev)))
+    st = _C.logprob_fwd(code, it, logits.data_ptr(), ldl, tgt, a_logp, a_entropy, lse.data_ptr(),
+                        a_ids, a_top, rows, vocab, int(top), float(scale), _stream(dev))
+    if st:
+        capi.check(st)
     return logp, entropy, lse, ids, top_logp
 
 
@@ -292,12 +298,13 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
             return logprob_bwd(dlogp, logits, targets, lse, scale, dentropy=dentropy,
                                entropy=entropy, dlogits=dlogits)
     if dlogits is None:
-        dlogits, ldd = _new(logits, _at(logits, dev), shape, logits.dtype), vocab
+        dlogits, ldd = _maker(logits, dev)(shape, dtype=logits.dtype), vocab
     else:
         if dlogits.shape != shape:
             raise ValueError("dlogits must be shaped like logits")
         ldd = _stride("dlogits", dlogits, vocab, logits.dtype)
-    capi.check(_C.logprob_bwd(code, it, a_dlogp, a_dentropy, logits.data_ptr(), ldl, tgt, a_lse,
-                                a_entropy, dlogits.data_ptr(), ldd, rows, vocab, float(scale),
-                                _stream(dev)))
+    st = _C.logprob_bwd(code, it, a_dlogp, a_dentropy, logits.data_ptr(), ldl, tgt, a_lse,
+                        a_entropy, dlogits.data_ptr(), ldd, rows, vocab, float(scale), _stream(dev))
+    if st:
+        capi.check(st)
     return dlogits

@@ -107,7 +107,8 @@ def _tokens(rng, kind, n, vocab):
     (33, 40, 257, "one"), (129, 100, 1030, "heavy"), (1000, 2000, 771, "uniform"),
     (4097, 600, 48, "heavy"), (5000, 3, 20, "heavy"), (700, 70000, 16, "descending"),
     (9000, 300, 4, "one"), (300, 90, 64, "outside"), (13000, 270000, 2, "uniform"),
-    (1024, 37, 9, "heavy"), (1025, 37, 9, "heavy"), (1024, 2000, 300, "one"), (64, 9, 8192, "heavy"),
+    (1024, 37, 9, "heavy"), (1025, 37, 9, "heavy"), (1024, 2000, 300, "one"),
+    (64, 9, 8192, "heavy"),
     (65, 9, 8200, "heavy"), (257, 5000, 520, "descending"), (992, 1500, 100, "uniform"),
 ])
 def test_gradient(dtype, grad, n, vocab, d, kind):

@@ -195,8 +195,9 @@ def test_gradient(dtype, which, rows, vocab, scale, masked):
     rn.logprob_bwd(g, x, t if g is not None else None, lse, scale, dentropy=h,
                    entropy=ent if h is not None else None, dlogits=d.view)
     d.check()
-    want, mag, factor = ot.logprob_backward(None if g is None else f64(g), None if h is None else f64(h),
-                                    f64(x), t.cpu().numpy(), f64(lse), f64(ent), scale)
+    want, mag, factor = ot.logprob_backward(
+        None if g is None else f64(g), None if h is None else f64(h), f64(x), t.cpu().numpy(),
+        f64(lse), f64(ent), scale)
     token_checks.check_logprob_bwd(d.f64(), want, mag, factor, dtype)
     # the gradient in the logits' place: the same bits
     y = x.clone()
@@ -223,7 +224,8 @@ def test_gradient_strides_and_phases(dtype, vocab, ldl, ldd, off_l, off_d):
     torch.cuda.synchronize()
     d.check("dlogits")
     x.check("logits")
-    want, mag, factor = ot.logprob_backward(f64(g), f64(h), f64(a), t.cpu().numpy(), f64(lse), f64(ent), 1.0)
+    want, mag, factor = ot.logprob_backward(f64(g), f64(h), f64(a), t.cpu().numpy(), f64(lse),
+                                            f64(ent), 1.0)
     token_checks.check_logprob_bwd(d.f64(), want, mag, factor, dtype)
 
 
@@ -266,7 +268,8 @@ def test_gradient_where_lse_is_too_large_to_hold(dtype):
     t = torch.tensor([4, 7, 2, 10, -1, 3000], device="cuda")
     g, h = rounded(rng, (6,), "f32"), rounded(rng, (6,), "f32")
     _, ent, lse, _, _ = rn.logprob_fwd(x, t)
-    want, mag, factor = ot.logprob_backward(f64(g), f64(h), f64(x), t.cpu().numpy(), None, f64(ent), 1.0)
+    want, mag, factor = ot.logprob_backward(f64(g), f64(h), f64(x), t.cpu().numpy(), None,
+                                            f64(ent), 1.0)
     # log S from a sum of vocab / 256 terms a thread (and 13 more), the ordinary
     # rows' lse from the forward pass
     u = token_checks.U

@@ -75,7 +75,8 @@ def test_embedding(seed):
     for f in (table, out, dout, g):
         f.check()
     there = torch.from_numpy((tok >= 0) & (tok < vocab)).cuda()
-    want = (table.view[torch.from_numpy(tok).cuda().clamp(0, vocab - 1)].float() * scale).to(DT[dtype])
+    at = torch.from_numpy(tok).cuda().clamp(0, vocab - 1)
+    want = (table.view[at].float() * scale).to(DT[dtype])
     want[~there] = 0
     assert torch.equal(out.view, want)
     want, absum, terms = ot.embed_backward(dout.f64(), tok, vocab, scale)
@@ -133,8 +134,8 @@ def test_log_probabilities(seed):
                                 _stream()))
     torch.cuda.synchronize()
     d.check()
-    ref, mag, factor = ot.logprob_backward(f64(g), None if h is None else f64(h), x.f64(), tgt, f64(lse),
-                                   f64(H), scale)
+    ref, mag, factor = ot.logprob_backward(f64(g), None if h is None else f64(h), x.f64(), tgt,
+                                           f64(lse), f64(H), scale)
     token_checks.check_logprob_bwd(d.f64(), ref, mag, factor, dtype)
 
 
@@ -191,5 +192,6 @@ def test_pinned_host_logits():
     g = torch.ones(6).pin_memory()
     d = rn.logprob_bwd(g, x, t, lse)
     torch.cuda.synchronize()
-    ref, mag, factor = ot.logprob_backward(f64(g), None, x.double().numpy(), t.numpy(), f64(lse), None, 1.0)
+    ref, mag, factor = ot.logprob_backward(f64(g), None, x.double().numpy(), t.numpy(), f64(lse),
+                                           None, 1.0)
     token_checks.check_logprob_bwd(f64(d), ref, mag, factor, "f32")

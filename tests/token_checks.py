@@ -79,7 +79,8 @@ def check_logprob(out, want, logits, scale, what=""):
     D = depth(x.shape[1])
     ds = U * (D + 4 + 4 * ez)
     base = ds + 4 * U * np.abs(ls)
-    _near(out["lse"], lse, base + 4 * U * (np.abs(m) + np.where(fine, np.abs(lse), 0)), what + "lse")
+    _near(out["lse"], lse, base + 4 * U * (np.abs(m) + np.where(fine, np.abs(lse), 0)),
+          what + "lse")
     if out.get("entropy") is not None:
         _near(out["entropy"], want["entropy"],
               base + U * (ez * (2 * D + 12) + 8 * ez2), what + "entropy")
