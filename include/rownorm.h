@@ -3,7 +3,8 @@
  *
  * Two operations over the rows of a row-major matrix x[rows][d] (FP32, or
  * BF16 / FP16 storage with FP32 arithmetic in the *_typed, *_strided and
- * *_batched entry points), with their backward passes (FP32):
+ * *_batched entry points), with their backward passes (FP32), and further down
+ * the token operators (embedding rows, log probabilities, their gradients):
  *
  *   LayerNorm:  mu_i      = (1/d) sum_j x_ij
  *               sigma_i^2 = (1/d) sum_j (x_ij - mu_i)^2
@@ -356,12 +357,12 @@ int embed_fwd(int dtype, int itype, const void *tokens, const void *table, int64
  *   dout   [n][d]      row stride lddo >= d, of type `dtype`
  *   dtable [vocab][d]  row stride ldg >= d, of type `gtype`: `dtype` or
  *                      RN_DTYPE_F32 (else RN_ERR_DTYPE)
- * Sums are FP32, in an order fixed by n, d and the ids alone (the ids are
- * sorted, stably, by a radix sort; no atomics touch a sum), so results repeat
+ * Sums are FP32, in an order fixed by n, d, the types and the ids alone (positions
+ * of an id are taken in order; no atomics touch a sum), so results repeat
  * bit for bit; each element is rounded once. `workspace` (device memory, 16-byte
  * aligned, caller-owned, contents on entry ignored) must hold the bytes that
  * embed_bwd_workspace_size gives (else RN_ERR_SIZE): 8 bytes an id (more beyond
- * 163840 ids) and d/4 bytes an id for the sums of ids that occur many times. Calls that
+ * 163840 ids) and d/4 (short batches: d) bytes an id for the sums of ids that occur many times. Calls that
  * may run at the same time on the GPU need workspaces of their own (two graphs
  * captured with one workspace count as such calls if they can overlap).
  * n up to 2^31 - 1; n == 0 zeroes dtable (accumulate: does nothing). The calls
