@@ -366,7 +366,8 @@ int embed_fwd(int dtype, int itype, const void *tokens, const void *table, int64
  * may run at the same time on the GPU need workspaces of their own (two graphs
  * captured with one workspace count as such calls if they can overlap).
  * n up to 2^31 - 1; n == 0 zeroes dtable (accumulate: does nothing). The calls
- * launch only on `stream` and can be captured into a CUDA graph.
+ * launch only on `stream`, so after one ordinary call of a configuration they can
+ * be captured into a CUDA graph (as can those of the other token operators).
  */
 int embed_bwd_workspace_size(int64_t n, int64_t vocab, int64_t d, size_t *bytes);
 

@@ -17,8 +17,9 @@
 //
 // The rows of the ids that do not occur are most of a gradient's bytes, and which
 // they are the ids alone say: a CTA that clears owns a range of the vocabulary, reads all
-// ids (from L2) and marks those of its range in shared memory. So the kernel that
-// clears runs beside the sort. It is launched as the sort's programmatic dependent, and the
+// ids (from L2) and marks those of its range in shared memory. So clearing runs beside the
+// sort: for small gradients in other clusters of its launch, else as a kernel of its own, since
+// clusters of 16 cannot cover all SMs (65536 x 4096 BF16 248 us of clearing, not 148). It is launched as the sort's programmatic dependent, and the
 // sort lets it start only after its own wait, when all work ahead of the call has
 // completed; and it waits for the sort only at its end, so that what follows it
 // follows both.
@@ -40,7 +41,11 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortPara
     __shared__ uint32_t wsum[kSortWarps];
     pdl_wait();
     pdl_launch_dependents();   // in this order: see embed_clear_kernel
-    cluster_sort(p, smem, wsum, (int)blockIdx.x);
+    static_assert(kZeroRange / 8 <= cluster_fixed_bytes(), "the marks of a range");
+    if ((int)blockIdx.x >= p.cluster)
+        clear_absent<kSortThreads>(p, (int)blockIdx.x - p.cluster, p.clear_ctas, (uint32_t*)smem);
+    else
+        cluster_sort(p, smem, wsum, (int)blockIdx.x);
 }
 
 // ---- more ids: in global memory -------------------------------------------------
@@ -140,6 +145,7 @@ __global__ void __launch_bounds__(kSortThreads)
     }
 }
 
+constexpr int kClearCtas = 128;   // in whole clusters beside the sort's
 static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
     // 2048 ids a CTA, until there are 16 CTAs
     p.cluster = 1;
@@ -163,7 +169,8 @@ static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
         prepared = ctx;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.cluster, 1, 1);
+    p.clear_ctas = p.beside ? (kClearCtas + p.cluster - 1) / p.cluster * p.cluster : 0;
+    cfg.gridDim = dim3((unsigned)(p.cluster + p.clear_ctas), 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
@@ -205,6 +212,7 @@ cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
 }
 
 cudaError_t embed_clear_launch(const SortParams& p, int sms, cudaStream_t s) {
+    if (p.beside) return cudaSuccess;
     return launch_pdl(embed_clear_kernel, 2 * (unsigned)sms, kSortThreads, 0, s, p);
 }
 

@@ -337,7 +337,9 @@ __device__ __forceinline__ void sum_chunk(const EmbedBwdParams& p, int64_t c, in
 constexpr int kJoinWarps = 8;       // warps, and chunks, of a CTA
 constexpr int kJoinCols = 4;
 constexpr int kJoinBlock = 128;
-constexpr int kJoinOnce = 64;       // chunks up to which one launch does
+// Chunks up to which one launch does: 1500 ids (188 chunks) 15.9 us in two launches, 14.4 in one;
+// 3000 ids, more than half of them one id (375 chunks), 18.3 and 18.9, and the host saves 2.5 us.
+constexpr int kJoinOnce = 512;
 struct alignas(16) LongId {          // its first and last chunk
     uint32_t first, last, id, pad;
 };

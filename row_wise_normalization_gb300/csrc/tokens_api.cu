@@ -18,9 +18,11 @@ cudaError_t embed_bwd_bf16(int, int, const SortParams*, int, const EmbedBwdParam
 cudaError_t embed_bwd_f16(int, int, const SortParams*, int, const EmbedBwdParams&, cudaStream_t);
 
 // Few ids: one launch. Else the sort, beside it the rows of zeros, then the sums.
-cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& sp,
-                             const EmbedBwdParams& q, cudaStream_t s) {
-    EmbedBwdParams p = q;
+cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& q1,
+                             const EmbedBwdParams& q2, cudaStream_t s) {
+    EmbedBwdParams p = q2;
+    SortParams sp = q1;
+    sp.beside = sp.zero && embed_clear_beside(sp.n, sp.vocab * sp.zero_bytes);
     const int bytes = ne * dtype_size(dtype);
     const int m = 16 / bytes < 4 ? 16 / bytes : 4;      // seg_vectors
     const int64_t vpt = (p.d / ne + m - 1) / m;         // threads a row could use

@@ -92,8 +92,10 @@ def test_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(want, again))
 
 
-def test_captured_and_replayed():
-    m = _model(900, 128, 500)
+@pytest.mark.parametrize("vocab,d,n", [(900, 128, 500), (2500, 96, 7000)])
+def test_captured_and_replayed(vocab, d, n):
+    """The gradient in one launch, and by the sort and its companions."""
+    m = _model(vocab, d, n)
     _step(m)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -104,7 +106,7 @@ def test_captured_and_replayed():
     with torch.cuda.graph(graph):
         outs = _step(m)
     for seed in (1, 2):
-        other = _model(900, 128, 500, seed)
+        other = _model(vocab, d, n, seed)
         for k in m:
             m[k].copy_(other[k])
         want = [t.clone() for t in _step(other)]
@@ -114,10 +116,10 @@ def test_captured_and_replayed():
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
-def test_back_to_back_calls_see_each_other():
+@pytest.mark.parametrize("vocab,d,n", [(300, 256, 2000), (300, 256, 200), (3000, 200, 20000)])
+def test_back_to_back_calls_see_each_other(vocab, d, n):
     """Chains in which each call reads what the one before wrote, against the
     same chain with a synchronization after every call."""
-    vocab, d, n = 300, 256, 2000
     gen = torch.Generator(device="cuda")
     gen.manual_seed(0)
     w0 = torch.randn(vocab, d, device="cuda", generator=gen)
@@ -175,3 +177,27 @@ def test_stream_and_device_refusals():
     with pytest.raises(ValueError):
         rn.embed_fwd(t, torch.ones(4, 8, device="cuda")[:, ::2])
     assert token_checks.depth(128000) < 200
+
+
+def test_large_and_small_gradients_in_turn():
+    """Calls of every launch path behind each other on one stream, one workspace, one
+    gradient: rows cleared by one call are read by the next."""
+    rng = np.random.default_rng(1)
+    vocab, d = 4000, 64
+    jobs = []
+    for n in (5, 40000, 300, 1500, 1, 200000, 1024, 9000):
+        tok = torch.from_numpy(rng.integers(0, vocab, n)).cuda()
+        x = torch.from_numpy(rng.integers(-3, 4, (n, d)).astype(np.float32)).cuda()
+        jobs.append((tok, x, torch.zeros(vocab, d, device="cuda").index_add_(0, tok, x)))
+    ws = torch.empty(max(capi.embed_bwd_workspace_size(t.numel(), vocab, d) for t, _, _ in jobs),
+                     dtype=torch.uint8, device="cuda")
+    g = torch.empty(vocab, d, device="cuda")
+    for _ in range(5):
+        sums = []
+        for tok, x, _ in jobs:
+            rn.embed_bwd(x, tok, vocab, dtable=g, workspace=ws)
+            sums.append(rn.embed_fwd(torch.arange(vocab, device="cuda"), g))
+            rn.embed_bwd(x, tok, vocab, dtable=g, accumulate=True, workspace=ws)
+            sums.append(g * 0.5)
+        for k, (_, _, want) in enumerate(jobs):
+            assert torch.equal(sums[2 * k], want) and torch.equal(sums[2 * k + 1], want)
