@@ -19,10 +19,10 @@
 // they are the ids alone say: a CTA that clears owns a range of the vocabulary, reads all
 // ids (from L2) and marks those of its range in shared memory. So clearing runs beside the
 // sort: for small gradients in other clusters of its launch, else as a kernel of its own, since
-// clusters of 16 cannot cover all SMs (65536 x 4096 BF16 248 us of clearing, not 148). It is launched as the sort's programmatic dependent, and the
-// sort lets it start only after its own wait, when all work ahead of the call has
-// completed; and it waits for the sort only at its end, so that what follows it
-// follows both.
+// clusters of 16 cannot cover all SMs (65536 x 4096 BF16 248 us of clearing, not 148). That one
+// is launched as the sort's programmatic dependent, and the sort lets it start only after its own
+// wait, when all work ahead of the call has completed; and it waits for the sort only at its
+// end, so that what follows it follows both.
 #include "rn_embed.cuh"
 
 namespace rn {
