@@ -86,28 +86,31 @@ cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
 // Few ids: one launch, without a sort. A CTA takes one position and a block of columns (a warp's),
 // compares all ids with the position's and leaves if an earlier position has the same id. Else it
 // lists the id's positions in order, its 8 warps add every 8th row each, and the warps' sums are
-// added in order. Other CTAs of the launch clear the rows of absent ids.
+// added in order. Other CTAs of the launch clear the rows of absent ids, and let the next kernel
+// start only once they are done: its CTAs would all go to the SMs that are free first (64 x 768
+// FP32 into 32000 rows by one such CTA an SM, call behind call: 42 us, not 23; by four 16).
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
 static_assert(kFewIds <= 32 * 32, "a lane for each word of the marks");
 
 template <typename T, typename G, int NE>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kFewThreads, 4)
     embed_few_kernel(const SortParams z, const EmbedBwdParams p, int zero_ctas, FastDiv blocks) {
     constexpr int M = seg_vectors<T, NE>();
     constexpr int B = NE * (int)sizeof(T);
     constexpr int E = M * NE;
     constexpr int kCols = 32 * E;           // columns of a block
-    static_assert(kFewWarps * kCols * 4 <= kZeroRange / 8, "the warps' sums");
-    __shared__ __align__(16) uint32_t raw[kZeroRange / 32];
+    static_assert(kFewWarps * kCols <= kClearWords, "the warps' sums");
+    __shared__ __align__(16) uint32_t raw[kClearWords];
     __shared__ uint32_t mask[32];
     __shared__ uint16_t list[kFewIds];
-    pdl_launch_dependents();
     pdl_wait();
     if ((int)blockIdx.x < zero_ctas) {
-        clear_absent<kFewThreads>(z, (int)blockIdx.x, zero_ctas, raw);
+        clear_absent<kFewThreads, true>(z, (int)blockIdx.x, zero_ctas, raw);
+        pdl_launch_dependents();
         return;
     }
+    pdl_launch_dependents();
     const int t = threadIdx.x, w = t >> 5, lane = t & 31, n = (int)p.n;
     const uint32_t at = blockIdx.x - (unsigned)zero_ctas;
     const int i = (int)fast_quot(at, blocks);

@@ -30,8 +30,8 @@ namespace rn {
 // Clears the rows of the absent ids. What it touches no kernel of the call before it does, and the
 // one ahead has waited for all others before it let this one start: it waits at its end.
 __global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(const SortParams p) {
-    __shared__ uint32_t bits[kZeroRange / 32];
-    clear_absent<kSortThreads>(p, (int)blockIdx.x, (int)gridDim.x, bits);
+    __shared__ __align__(16) uint32_t mem[kClearWords];
+    clear_absent<kSortThreads, false>(p, (int)blockIdx.x, (int)gridDim.x, mem);
     pdl_launch_dependents();
     pdl_wait();
 }
@@ -41,9 +41,9 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortPara
     __shared__ uint32_t wsum[kSortWarps];
     pdl_wait();
     pdl_launch_dependents();   // in this order: see embed_clear_kernel
-    static_assert(kZeroRange / 8 <= cluster_fixed_bytes(), "the marks of a range");
+    static_assert(kClearWords * 4 <= cluster_fixed_bytes(), "a CTA that clears");
     if ((int)blockIdx.x >= p.cluster)
-        clear_absent<kSortThreads>(p, (int)blockIdx.x - p.cluster, p.clear_ctas, (uint32_t*)smem);
+        clear_absent<kSortThreads, false>(p, (int)blockIdx.x - p.cluster, p.clear_ctas, (uint32_t*)smem);
     else
         cluster_sort(p, smem, wsum, (int)blockIdx.x);
 }

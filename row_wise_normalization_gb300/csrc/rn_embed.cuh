@@ -3,6 +3,7 @@
 // sums that run over several chunks. embed_sort.cu and embed_bwd.cuh make kernels of them.
 #pragma once
 
+#include "rn_async.cuh"
 #include "rn_tokens.cuh"
 
 namespace rn {
@@ -147,27 +148,59 @@ __device__ __forceinline__ void cluster_sort(const SortParams& p, unsigned char*
 }
 
 // ---- rows of zeros ----------------------------------------------------------
-constexpr int kZeroRange = 65536;   // ids a CTA marks at a time (8 KB of bits)
+constexpr int kZeroRange = 32768;   // ids a CTA marks at a time (4 KB of bits)
+// Zeros by the bulk-copy engine (one instruction a row, from zeros in shared memory) or by the
+// threads' stores. Measured on GB300 with the sums in other CTAs of the launch (embed_few_kernel):
+// 512 x 768 FP32 into 32000 rows 18.7 us, by stores 22.3; 512 x 1024 BF16 13.1, 15.7; 300 x 771
+// FP16 into FP32 19.5, 20.5; 16 x 512 FP32 into 50000 rows 18.6, 17.8; rows of 512 bytes 10.0,
+// 13.1. Copies of 8 KB: 1 us more. In a kernel of its own (embed_clear_kernel) there is no gain.
+constexpr int kZeroBytes = 4096;    // of a copy
+constexpr int kZeroBulk = 512;      // bytes of a row from which it is copied
+constexpr int kClearWords = kZeroRange / 32 + kZeroBytes / 4;   // shared memory of a CTA that clears
 
-// Clears `bytes` (a multiple of 2) at p by `lanes` threads, of which this is number l.
-__device__ __forceinline__ void clear_row(char* p, int64_t bytes, int l, int lanes) {
+__device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
+                 "r"(bytes)
+                 : "memory");
+}
+// Ends when this thread's copies have been written.
+__device__ __forceinline__ void bulk_s2g_wait() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Clears `bytes` (a multiple of 2) at p by `lanes` threads, of which this is number l. zeros: the
+// address of kZeroBytes of zeros in shared memory, from which the first thread has the bulk-copy
+// engine write the row's 16-byte vectors (0: the threads store them).
+__device__ __forceinline__ void clear_row(char* p, int64_t bytes, int l, int lanes,
+                                          uint32_t zeros) {
     const int64_t head = min((int64_t)((0u - (unsigned)(uintptr_t)p) & 15u), bytes);
     const int64_t nv = (bytes - head) / 16, tail = head + nv * 16;
     const Raw<16> z = {};
-    for (int64_t v = l; v < nv; v += lanes) st_raw(p + head + v * 16, z);
+    if (!zeros) {
+        for (int64_t v = l; v < nv; v += lanes) st_raw(p + head + v * 16, z);
+    } else if (l == 0) {
+        for (int64_t b = head; b < tail; b += kZeroBytes)
+            bulk_s2g(p + b, zeros, (uint32_t)min((int64_t)kZeroBytes, tail - b));
+    }
     const Raw<2> h = {};
     for (int64_t b = 2 * l; b < head; b += 2 * lanes) st_raw(p + b, h);
     for (int64_t b = tail + 2 * l; b < bytes; b += 2 * lanes) st_raw(p + b, h);
 }
 
 // Clears the rows of the absent ids of part `part` of the vocabulary, of `parts`, by a CTA of NT
-// threads. bits: kZeroRange / 32 words of shared memory.
-template <int NT>
+// threads. BULK: long rows by the bulk-copy engine. mem: kClearWords words of shared memory, 16-byte
+// aligned.
+template <int NT, bool BULK>
 __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int parts,
-                                             uint32_t* bits) {
+                                             uint32_t* mem) {
+    uint32_t* const bits = mem + kZeroBytes / 4;
     const int t = threadIdx.x;
-    // (whole groups of 32 rows: 16383 x 771 FP16 into FP32 took 69 us without, 57 us with)
-    const int64_t share = ((p.vocab + parts - 1) / parts + 31) / 32 * 32;
+    // (whole groups of 32 rows, where that leaves every CTA rows: 16383 x 771 FP16 into FP32 took 69 us
+    // without, 57 us with; 64 x 4096 BF16 into 2000 rows 11.7 us with, 6.8 us without)
+    int64_t whole = 32;
+    while (whole > 1 && whole * parts > p.vocab) whole /= 2;
+    const int64_t share = ((p.vocab + parts - 1) / parts + whole - 1) / whole * whole;
     const int64_t end = min(p.vocab, (int64_t)(part + 1) * share);
     // the ids as 16-byte vectors, and fewer than two vectors' before and after
     const int64_t per = 16 / index_size(p.itype);
@@ -175,9 +208,18 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
                                       index_size(p.itype));
     const int64_t nv = (p.n - head) / per;
     const char* const body = (const char*)p.tokens + head * index_size(p.itype);
-    // threads of a row: as many 16-byte stores as it has, up to a warp's
+    // threads of a row: as many 16-byte stores as it has, up to a warp's; one where copies do all
+    const bool bulk = BULK && p.zero_bytes >= kZeroBulk;
     int lanes = 32;
-    while (lanes > 1 && (lanes / 2) * 16 >= p.zero_bytes) lanes /= 2;
+    if (bulk) {
+        if ((((uint64_t)(uintptr_t)p.zero | (uint64_t)p.zero_pitch | (uint64_t)p.zero_bytes) & 15) == 0)
+            lanes = 1;
+        for (int k = t; k < kZeroBytes / 4; k += NT) mem[k] = 0;
+        fence_proxy_async_smem();
+    } else {
+        while (lanes > 1 && (lanes / 2) * 16 >= p.zero_bytes) lanes /= 2;
+    }
+    const uint32_t zeros = bulk ? smem_addr(mem) : 0;
     for (int64_t lo = (int64_t)part * share; lo < end; lo += kZeroRange) {
         const int cnt = (int)min((int64_t)kZeroRange, end - lo);
         __syncthreads();
@@ -212,8 +254,9 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
         __syncthreads();
         for (int r = t / lanes; r < cnt; r += NT / lanes)
             if (!((bits[r >> 5] >> (r & 31)) & 1u))
-                clear_row(p.zero + (lo + r) * p.zero_pitch, p.zero_bytes, t % lanes, lanes);
+                clear_row(p.zero + (lo + r) * p.zero_pitch, p.zero_bytes, t % lanes, lanes, zeros);
     }
+    if (bulk) bulk_s2g_wait();
 }
 
 // ---- sums -------------------------------------------------------------------

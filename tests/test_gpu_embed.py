@@ -271,3 +271,36 @@ def test_pinned_host_table():
     tok = torch.randint(0, 100, (37,), device="cuda")
     y = rn.embed_fwd(tok, table, 3.0)
     assert y.is_cuda and torch.equal(y.cpu(), table[tok.cpu()] * 3)
+
+
+@pytest.mark.parametrize("n,vocab", [(50, 21_000_000), (1500, 5_000_000), (1500, 17_000_001)])
+def test_zeros_of_a_vast_vocabulary(n, vocab):
+    # more ids than the marks of all clearing CTAs hold at a time
+    rng = np.random.default_rng(n + vocab)
+    tok = torch.from_numpy(rng.permutation(vocab)[:n]).cuda()
+    tok[0], tok[1] = 0, vocab - 1
+    tok = torch.unique(tok)
+    dout = rounded(rng, (tok.numel(), 1), "bf16")
+    want = torch.zeros(vocab, 1, dtype=torch.bfloat16, device="cuda")
+    want[tok] = dout
+    got = torch.full_like(want, float("nan"))
+    assert _bits_equal(rn.embed_bwd(dout, tok, vocab, dtable=got), want)
+
+
+@pytest.mark.parametrize("gtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [40, 1100])
+@pytest.mark.parametrize("d,ldg,off", [
+    (256, 256, 0), (256, 264, 8), (1031, 1031, 3), (2048, 2050, 1), (5000, 5000, 0), (2052, 2056, 4),
+])
+def test_zeros_of_long_rows(gtype, n, d, ldg, off):
+    # one sum an id: its bits; all else zeros, and what lies between the rows as it was
+    rng = np.random.default_rng([n, d])
+    vocab = 1500
+    tok = torch.from_numpy(rng.permutation(vocab)[:n]).cuda()
+    dout = rounded(rng, (n, d), gtype)
+    grad = Framed(vocab, d, DT[gtype], ldg, off)
+    rn.embed_bwd(dout, tok, vocab, dtable=grad.view)
+    grad.check()
+    want = torch.zeros(vocab, d, dtype=DT[gtype], device="cuda")
+    want[tok] = dout
+    assert _bits_equal(grad.view, want)
