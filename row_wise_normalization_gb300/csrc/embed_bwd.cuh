@@ -1,6 +1,6 @@
 // embed_bwd.cuh -- gradient of embedding rows from the sorted ids:
 //   dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum_{i: id_i = v} dout[i]
-// for the ids that occur (embed_sort.cu clears the rows of the others).
+// for the ids that occur; the rows of the others are zeros.
 //
 // Bytes bound it: dout read once, every row of the gradient written once. The
 // sorted positions are cut into chunks of 8 to 32, a lane for each position.
@@ -11,24 +11,39 @@
 // id which fills half of a batch is summed by as many groups as its rows fill.
 // Every sum has a fixed order: results repeat bit for bit.
 //
-// 65536 x 4096 BF16 into 128000 rows (19851 of them occur): 276 us where the bytes alone
-// take 234: rows of zeros 142, sums 137 (with the write-back of the zeros' last lines; alone
-// 107 us, 0.83 of the DRAM's rate), joins 20, most of it the latency of two launches. 16383 x 771
-// FP16 into FP32, a third of it one id: 53 us (bytes 26): at odd widths an access is
-// 2 bytes, and sums are bound by instructions (17 us).
+// The rows of ids that do not occur are most of a gradient's bytes, and which they are the ids alone
+// say. The first CTAs of the launch clear them: each owns a range of the vocabulary, reads all ids
+// (from L2) and marks those of its range in shared memory. They need not wait for the sort and run
+// beside it and then beside the sums. (In a kernel of their own between the two, for which the
+// sums had to wait: 16383 x 771 FP16 into 50001 rows 54 us, not 49; 16383 x 256 25, not 22.)
+//
+// 65536 x 4096 BF16 into 128000 rows (19851 of them occur): 277 us where the bytes alone
+// take 234: rows of zeros 142 and sums 107 by themselves, joins 20, most of it the latency of two
+// launches. 16383 x 771 FP16 into FP32, a third of it one id: 49 us (bytes 26): sort 16, joins 10,
+// sums 17, which at odd widths, an access 2 bytes, are bound by instructions.
 #pragma once
 
 #include "rn_embed.cuh"
 
 namespace rn {
 
+// The first zero_ctas CTAs clear the rows of absent ids, beside the sort: what they touch no kernel
+// of the call before touches, and the sort lets this kernel start only after its own wait, when
+// all work ahead of the call has completed.
 template <typename T, typename G, int NE>
-__global__ void __launch_bounds__(kSegThreads, 4) embed_bwd_kernel(const EmbedBwdParams p) {
+__global__ void __launch_bounds__(kSegThreads, 4)
+    embed_bwd_kernel(const SortParams z, const EmbedBwdParams p, int zero_ctas) {
+    __shared__ __align__(16) uint32_t mem[kClearWords];
+    if ((int)blockIdx.x < zero_ctas) {
+        clear_absent<kSegThreads, false>(z, (int)blockIdx.x, zero_ctas, mem);
+        return;
+    }
     pdl_launch_dependents();
-    const int64_t c = (int64_t)((int)blockIdx.x / p.slices) * p.ty + (int)threadIdx.x / p.tx;
+    const int at = (int)blockIdx.x - zero_ctas;
+    const int64_t c = (int64_t)(at / p.slices) * p.ty + (int)threadIdx.x / p.tx;
     if (c >= p.chunks) return;          // whole warps: p.tx is a multiple of 32
     pdl_wait();
-    sum_chunk<T, G, NE>(p, c, (int)blockIdx.x % p.slices, (int)threadIdx.x % p.tx);
+    sum_chunk<T, G, NE>(p, c, at % p.slices, (int)threadIdx.x % p.tx);
 }
 
 template <typename G>
@@ -57,10 +72,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 }
 
 template <typename T, typename G, int NE>
-cudaError_t embed_bwd_go(const EmbedBwdParams& p, cudaStream_t s) {
-    cudaError_t err = launch_pdl(embed_bwd_kernel<T, G, NE>,
-                                 (unsigned)((p.chunks + p.ty - 1) / p.ty * p.slices), kSegThreads,
-                                 0, s, p);
+cudaError_t embed_bwd_go(const SortParams& z, const EmbedBwdParams& p, int sms, cudaStream_t s) {
+    const int zero_ctas = z.zero ? (embed_zeros_many(p.n, z) ? 4 : 2) * sms : 0;
+    const unsigned sum_ctas = (unsigned)((p.chunks + p.ty - 1) / p.ty * p.slices);
+    cudaError_t err = launch_pdl(embed_bwd_kernel<T, G, NE>, (unsigned)zero_ctas + sum_ctas,
+                                 kSegThreads, 0, s, z, p, zero_ctas);
     if (err != cudaSuccess || p.chunks < 2) return err;
     const int64_t blocks = (p.d + kJoinBlock - 1) / kJoinBlock;
     const int64_t ctas = (p.chunks - 1 + kJoinWarps - 1) / kJoinWarps;
@@ -219,19 +235,20 @@ cudaError_t embed_few_go(const SortParams& z, const EmbedBwdParams& p, int sms, 
                       kFewThreads, 0, s, z, p, zero_ctas, fast_div(blocks));
 }
 
-// One type of rows and of the gradient. z, sms: few ids, in one launch.
+// One type of rows and of the gradient.
 template <typename T, typename G, int NE>
-cudaError_t embed_bwd_one(const SortParams* z, int sms, const EmbedBwdParams& p, cudaStream_t s) {
-    return z ? embed_few_go<T, G, NE>(*z, p, sms, s) : embed_bwd_go<T, G, NE>(p, s);
+cudaError_t embed_bwd_one(bool few, const SortParams& z, int sms, const EmbedBwdParams& p,
+                          cudaStream_t s) {
+    return few ? embed_few_go<T, G, NE>(z, p, sms, s) : embed_bwd_go<T, G, NE>(z, p, sms, s);
 }
 template <typename T, typename G>
-cudaError_t embed_bwd_t(int ne, const SortParams* z, int sms, const EmbedBwdParams& p,
+cudaError_t embed_bwd_t(int ne, bool few, const SortParams& z, int sms, const EmbedBwdParams& p,
                         cudaStream_t s) {
     if constexpr (sizeof(T) == 2)
-        if (ne == 8) return embed_bwd_one<T, G, 8>(z, sms, p, s);
-    if (ne == 4) return embed_bwd_one<T, G, 4>(z, sms, p, s);
-    if (ne == 2) return embed_bwd_one<T, G, 2>(z, sms, p, s);
-    return embed_bwd_one<T, G, 1>(z, sms, p, s);
+        if (ne == 8) return embed_bwd_one<T, G, 8>(few, z, sms, p, s);
+    if (ne == 4) return embed_bwd_one<T, G, 4>(few, z, sms, p, s);
+    if (ne == 2) return embed_bwd_one<T, G, 2>(few, z, sms, p, s);
+    return embed_bwd_one<T, G, 1>(few, z, sms, p, s);
 }
 
 }  // namespace rn

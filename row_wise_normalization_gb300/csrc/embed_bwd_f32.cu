@@ -1,9 +1,9 @@
 #include "embed_bwd.cuh"
 
 namespace rn {
-cudaError_t embed_bwd_f32(int gtype, int ne, const SortParams* z, int sms, const EmbedBwdParams& p,
-                          cudaStream_t s) {
+cudaError_t embed_bwd_f32(int gtype, int ne, bool few, const SortParams& z, int sms,
+                          const EmbedBwdParams& p, cudaStream_t s) {
     (void)gtype;
-    return embed_bwd_t<float, float>(ne, z, sms, p, s);
+    return embed_bwd_t<float, float>(ne, few, z, sms, p, s);
 }
 }  // namespace rn

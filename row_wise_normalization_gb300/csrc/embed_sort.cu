@@ -1,6 +1,5 @@
 // embed_sort.cu -- the ids of an embedding gradient in order, with their
-// positions (a stable radix sort, lowest digit first), and, beside it, the
-// gradient's rows of zeros.
+// positions (a stable radix sort, lowest digit first).
 //
 // A vocabulary needs 10 to 18 bits, so two digits of at most 9 bits sort it. Ranks
 // are stable: a warp owns consecutive ids and takes 32 at a time; equal digits
@@ -14,38 +13,16 @@
 // memory of the CTA that owns it (the last pass writes to global memory). One launch;
 // 65536 ids took 39 us in the four launches of a sort in global memory. More ids are
 // sorted there, three launches a digit.
-//
-// The rows of the ids that do not occur are most of a gradient's bytes, and which
-// they are the ids alone say: a CTA that clears owns a range of the vocabulary, reads all
-// ids (from L2) and marks those of its range in shared memory. So clearing runs beside the
-// sort: for small gradients in other clusters of its launch, else as a kernel of its own, since
-// clusters of 16 cannot cover all SMs (65536 x 4096 BF16 248 us of clearing, not 148). That one
-// is launched as the sort's programmatic dependent, and the sort lets it start only after its own
-// wait, when all work ahead of the call has completed; and it waits for the sort only at its
-// end, so that what follows it follows both.
 #include "rn_embed.cuh"
 
 namespace rn {
-
-// Clears the rows of the absent ids. What it touches no kernel of the call before it does, and the
-// one ahead has waited for all others before it let this one start: it waits at its end.
-__global__ void __launch_bounds__(kSortThreads) embed_clear_kernel(const SortParams p) {
-    __shared__ __align__(16) uint32_t mem[kClearWords];
-    clear_absent<kSortThreads, false>(p, (int)blockIdx.x, (int)gridDim.x, mem);
-    pdl_launch_dependents();
-    pdl_wait();
-}
 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint32_t wsum[kSortWarps];
     pdl_wait();
-    pdl_launch_dependents();   // in this order: see embed_clear_kernel
-    static_assert(kClearWords * 4 <= cluster_fixed_bytes(), "a CTA that clears");
-    if ((int)blockIdx.x >= p.cluster)
-        clear_absent<kSortThreads, false>(p, (int)blockIdx.x - p.cluster, p.clear_ctas, (uint32_t*)smem);
-    else
-        cluster_sort(p, smem, wsum, (int)blockIdx.x);
+    pdl_launch_dependents();   // in this order: see embed_bwd_kernel
+    cluster_sort(p, smem, wsum, (int)blockIdx.x);
 }
 
 // ---- more ids: in global memory -------------------------------------------------
@@ -107,7 +84,7 @@ __global__ void __launch_bounds__(kSortThreads)
     for (int k = 0; k < kSortWarps; ++k) cnt[k][t] = 0;
     __syncthreads();
     pdl_wait();
-    pdl_launch_dependents();   // in this order: see embed_clear_kernel
+    pdl_launch_dependents();   // in this order: see embed_bwd_kernel
     const uint32_t mask = (1u << p.bits) - 1;
     const int64_t base = (int64_t)blockIdx.x * kSortTile + w * (kSortPerThread * 32);
     uint32_t key[kSortPerThread], rank[kSortPerThread];
@@ -145,7 +122,6 @@ __global__ void __launch_bounds__(kSortThreads)
     }
 }
 
-constexpr int kClearCtas = 128;   // in whole clusters beside the sort's
 static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
     // 2048 ids a CTA, until there are 16 CTAs
     p.cluster = 1;
@@ -169,8 +145,7 @@ static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
         prepared = ctx;
     }
     cudaLaunchConfig_t cfg = {};
-    p.clear_ctas = p.beside ? (kClearCtas + p.cluster - 1) / p.cluster * p.cluster : 0;
-    cfg.gridDim = dim3((unsigned)(p.cluster + p.clear_ctas), 1, 1);
+    cfg.gridDim = dim3((unsigned)p.cluster, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
@@ -209,11 +184,6 @@ cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
     p.passes = sort_passes(p.vocab);
     p.bits = (sort_key_bits(p.vocab) + p.passes - 1) / p.passes;
     return p.n <= kSortClusterMax ? sort_in_cluster(p, s) : sort_in_memory(p, s);
-}
-
-cudaError_t embed_clear_launch(const SortParams& p, int sms, cudaStream_t s) {
-    if (p.beside) return cudaSuccess;
-    return launch_pdl(embed_clear_kernel, 2 * (unsigned)sms, kSortThreads, 0, s, p);
 }
 
 }  // namespace rn

@@ -153,7 +153,8 @@ constexpr int kZeroRange = 32768;   // ids a CTA marks at a time (4 KB of bits)
 // threads' stores. Measured on GB300 with the sums in other CTAs of the launch (embed_few_kernel):
 // 512 x 768 FP32 into 32000 rows 18.7 us, by stores 22.3; 512 x 1024 BF16 13.1, 15.7; 300 x 771
 // FP16 into FP32 19.5, 20.5; 16 x 512 FP32 into 50000 rows 18.6, 17.8; rows of 512 bytes 10.0,
-// 13.1. Copies of 8 KB: 1 us more. In a kernel of its own (embed_clear_kernel) there is no gain.
+// 13.1. Copies of 8 KB: 1 us more. Beside the sort and long sums there is no gain, and the registers
+// cost: 16383 x 771 FP16 49.9, by stores 48.8, 65536 x 4096 BF16 291, 277 (embed_bwd_kernel).
 constexpr int kZeroBytes = 4096;    // of a copy
 constexpr int kZeroBulk = 512;      // bytes of a row from which it is copied
 constexpr int kClearWords = kZeroRange / 32 + kZeroBytes / 4;   // shared memory of a CTA that clears
@@ -196,8 +197,8 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
                                              uint32_t* mem) {
     uint32_t* const bits = mem + kZeroBytes / 4;
     const int t = threadIdx.x;
-    // (whole groups of 32 rows, where that leaves every CTA rows: 16383 x 771 FP16 into FP32 took 69 us
-    // without, 57 us with; 64 x 4096 BF16 into 2000 rows 11.7 us with, 6.8 us without)
+    // (whole groups of 32 rows, where that leaves every CTA rows: 16383 x 771 FP16 into FP32 took
+    // 69 us without, 57 us with; 64 x 4096 BF16 into 2000 rows 11.7 us with, 6.8 us without)
     int64_t whole = 32;
     while (whole > 1 && whole * parts > p.vocab) whole /= 2;
     const int64_t share = ((p.vocab + parts - 1) / parts + whole - 1) / whole * whole;

@@ -69,11 +69,9 @@ struct SortParams {
     int itype;
     int cluster, share;   // CTAs that sort in shared memory, ids of each
     FastDiv owner;        // division by share
-    // Rows of ids that do not occur, cleared beside the sort (NULL: left as they are)
+    // Rows of ids that do not occur, cleared beside sort and sums (NULL: left as they are)
     char* zero;
     int64_t zero_pitch, zero_bytes;   // bytes from row to row, and of a row
-    bool beside;          // in the launch of the sort (set by embed_sort_launch's caller)
-    int clear_ctas;       // CTAs of that launch that clear
 };
 constexpr int sort_key_bits(int64_t vocab) {
     int b = 0;
@@ -83,9 +81,6 @@ constexpr int sort_key_bits(int64_t vocab) {
 constexpr int sort_passes(int64_t vocab) { return (sort_key_bits(vocab) + kSortBits - 1) / kSortBits; }
 // Sorts into key[0], pos[0].
 cudaError_t embed_sort_launch(SortParams p, cudaStream_t s);
-// Clears the rows of p.zero of the ids in [0, vocab) that are not among the tokens. To be launched
-// right after a kernel that lets its dependents start only once it has waited itself.
-cudaError_t embed_clear_launch(const SortParams& p, int sms, cudaStream_t s);
 
 // dtable[v] = (accumulate ? dtable[v] : 0) + scale * sum of dout[i] over the
 // positions i with tokens[i] == v, for the ids v that occur, from the sorted ids.
@@ -112,14 +107,14 @@ struct EmbedBwdParams {
     float scale;
     int accumulate;
 };
-// Whether the rows of zeros are cleared by other clusters of the sort's launch rather than by a
-// kernel beside it, which covers every SM but has to be launched. Measured on GB300, BF16, the
-// same launch against its own: 1500 ids, 16 MB of gradient 15.2 against 16.1 us, 66 MB 17.2 against
-// 19.5; 16000 ids, 33 MB 27.1 against 27.8, 66 MB 31.5 against 31.6, more than half of them one
-// id 37.6 against 33.9; 60000 ids, 31 MB, the same 51.9 against 48.3. The host saves 2.5 us.
-constexpr int64_t kBesideBytes = 32 << 20;
-constexpr bool embed_clear_beside(int64_t n, int64_t bytes) {
-    return n <= kSortClusterMax && bytes <= kBesideBytes;
+// Whether the zeros are many beside the sums (128 MB at least): 4 clearing CTAs an SM, which take
+// all of it until they end, rather than 2. Measured on GB300, 4 against 2: 65536 x 4096 BF16 into
+// 128000 rows 277 against 281 to 306 us, 16383 x 768 into FP32 (343 MB) 71 against 86, 4096 x 768
+// into 50001 rows (141 MB) 32 against 37; 16383 x 771 into 50001 (104 MB) 50.5 against 49, 16383 x
+// 256 27 against 22, 200000 x 1024 into 128000 182 against 157.
+constexpr int64_t kZerosMany = 128 << 20;
+constexpr bool embed_zeros_many(int64_t n, const SortParams& z) {
+    return (z.vocab - n) * z.zero_bytes >= kZerosMany;
 }
 // Few ids (embed_few_kernel): at most kFewIds, and rows of kFewBytes together. Measured on GB300,
 // added to a gradient, one launch against the sort's four: FP32 64 x 768 2.8 against 9.7 us,

@@ -13,16 +13,17 @@ cudaError_t logprob_fwd_f32(const LogprobParams& p, cudaStream_t s);
 cudaError_t logprob_fwd_bf16(const LogprobParams& p, cudaStream_t s);
 cudaError_t logprob_fwd_f16(const LogprobParams& p, cudaStream_t s);
 
-cudaError_t embed_bwd_f32(int, int, const SortParams*, int, const EmbedBwdParams&, cudaStream_t);
-cudaError_t embed_bwd_bf16(int, int, const SortParams*, int, const EmbedBwdParams&, cudaStream_t);
-cudaError_t embed_bwd_f16(int, int, const SortParams*, int, const EmbedBwdParams&, cudaStream_t);
+cudaError_t embed_bwd_f32(int, int, bool, const SortParams&, int, const EmbedBwdParams&,
+                          cudaStream_t);
+cudaError_t embed_bwd_bf16(int, int, bool, const SortParams&, int, const EmbedBwdParams&,
+                          cudaStream_t);
+cudaError_t embed_bwd_f16(int, int, bool, const SortParams&, int, const EmbedBwdParams&,
+                          cudaStream_t);
 
-// Few ids: one launch. Else the sort, beside it the rows of zeros, then the sums.
-cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& q1,
-                             const EmbedBwdParams& q2, cudaStream_t s) {
-    EmbedBwdParams p = q2;
-    SortParams sp = q1;
-    sp.beside = sp.zero && embed_clear_beside(sp.n, sp.vocab * sp.zero_bytes);
+// Few ids: one launch. Else the sort, the sums with the rows of zeros beside both, the joins.
+cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& sp,
+                             const EmbedBwdParams& q, cudaStream_t s) {
+    EmbedBwdParams p = q;
     const int bytes = ne * dtype_size(dtype);
     const int m = 16 / bytes < 4 ? 16 / bytes : 4;      // seg_vectors
     const int64_t vpt = (p.d / ne + m - 1) / m;         // threads a row could use
@@ -36,13 +37,11 @@ cudaError_t embed_bwd_launch(int dtype, int gtype, int ne, const SortParams& q1,
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const bool few = embed_few(p.n, p.d, dtype_size(dtype));
     if (err == cudaSuccess && !few) err = embed_sort_launch(sp, s);
-    if (err == cudaSuccess && !few && sp.zero) err = embed_clear_launch(sp, sms, s);
     if (err != cudaSuccess) return err;
-    const SortParams* const z = few ? &sp : nullptr;
     switch (dtype) {
-        case DT_BF16: return embed_bwd_bf16(gtype, ne, z, sms, p, s);
-        case DT_F16: return embed_bwd_f16(gtype, ne, z, sms, p, s);
-        default: return embed_bwd_f32(gtype, ne, z, sms, p, s);
+        case DT_BF16: return embed_bwd_bf16(gtype, ne, few, sp, sms, p, s);
+        case DT_F16: return embed_bwd_f16(gtype, ne, few, sp, sms, p, s);
+        default: return embed_bwd_f32(gtype, ne, few, sp, sms, p, s);
     }
 }
 
