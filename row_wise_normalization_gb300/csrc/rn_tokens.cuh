@@ -70,6 +70,10 @@ __device__ __forceinline__ void st_raw(void* p, const Raw<B>& r) {
         asm volatile("st.global.cs.u16 [%0], %1;" ::"l"(p), "h"((uint16_t)r.w[0]) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // NE elements of T between raw words and FP32.
 template <typename T, int NE>
 __device__ __forceinline__ void unpack(float* v, const Raw<NE * (int)sizeof(T)>& r) {
