@@ -14,9 +14,17 @@
 // special-function instruction. Pairs of elements go through the packed FP32
 // pipe: 4 instructions a pair beside the two exponentials, so that the pass
 // stays below the time its bytes take even for 16-bit logits: 8192 x 128000 BF16 with
-// entropies 309 us, the measured copy's rate over its 2.1 GB (608 us with scalar arithmetic,
-// a test of every element for -inf and two CTAs of 512 threads an SM; four of 256 let one
-// row's end overlap another's reading).
+// entropies 296 us, a little above the measured copy's rate over its 2.1 GB (608 us with scalar
+// arithmetic, a test of every element for -inf and two CTAs of 512 threads an SM; four of 256 let
+// one row's end overlap another's reading).
+//
+// Where there is more to do than sums, a thread keeps the next two batches under way into shared
+// memory, 32 KB a CTA, so that the memory does not wait for a row's barriers and alternatives: a
+// thread copies its own vectors and needs no barrier for them. 2048 x 128000 BF16 with entropies
+// 86 us by loads into registers, this way 82; with 8 alternatives too 108, 94 (with what is
+// below). Sums alone are better off without: 700 x 128000 30 us, this way 37. (CTAs that go on to
+// further rows, with the next one's batches under way: 2048 x 128000 with 8 alternatives 111 us,
+// where one row each took 106: rows are handed out more evenly.)
 //
 // A masked element (-inf) gives e = 0, and 0 * -inf would be NaN in W: where entropies are
 // wanted, elements are held at -1e30 or above (NaN passes), where e is 0 as well: one packed
@@ -33,17 +41,21 @@
 // ones, found in the same pass. A candidate is a 64-bit key: the value's bits in
 // an order-preserving form above the complement of its index, so that keys
 // differ and compare as wanted. Each warp keeps its newest candidates in shared
-// memory and its 32 best, sorted, in its lanes, and a new one has to exceed the
+// memory and, past 31 of them, its 32 best, sorted, in its lanes, and a new one has to exceed the
 // threshold `thr`, below which the row's `top` best cannot lie. It comes from groups of
 // threads: the top-th largest of the groups' maxima so far, since at least `top` elements
 // reach it. It is taken after the first batch, then each time the columns read have doubled, so
-// that about `top` candidates are met between two of them (2048 x 128000 BF16 with 8
-// alternatives: 139 us with the first threshold alone, 101 us with this). Past the first, no barrier is
-// needed: maxima only grow, and a stale one is a lower bound too. So is the top-th of what
-// a warp keeps. A batch without a candidate
-// costs a comparison of its maximum, which is there anyway; in one with a candidate, the warp
-// looks at the elements of the lane that has it, an element a lane. The order in which
-// warps run changes which keys are tried, not which are kept.
+// that about `top` candidates are met between two of them (with the first threshold alone 2048 x
+// 128000 BF16 with 8 alternatives took 139 us where it then took 101). Past the first, no barrier
+// is needed: maxima only grow, and a stale one is a lower bound too. So is the top-th of what a warp
+// keeps. A batch without a candidate costs a comparison of its maximum, which is there anyway; in
+// one with a candidate, the warp looks at the elements of the lane that has it, an element a lane,
+// where they lie in shared memory. At the end the keys that reach the last threshold, of all warps,
+// go into one list: mostly one or two warps' sorts (every warp sorting and keeping 32, then merging
+// 8 lists: 8 alternatives 106 us, this way 95). The order in which warps run changes which keys are
+// tried, not which are kept.
+// What alternatives cost now is instructions: a row of 128000 BF16 takes 30000 warp instructions
+// with its entropy, 41000 with 8 alternatives as well and 59000 with 32 (82, 94, 130 us for 2048).
 #pragma once
 
 #include <type_traits>
@@ -55,6 +67,7 @@ namespace rn {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpU = 4;              // vectors a thread holds of a batch
+constexpr int kLpStages = 2;         // batches a thread has under way
 constexpr int kLpMaxCluster = 16;
 constexpr int kTopCap = 64;          // candidates a warp holds unsorted: 31 and 32 more
 constexpr int kTopGroups = 64;
@@ -218,9 +231,9 @@ struct TopState {
     unsigned long long list[kLpMaxCluster][32];   // sorted lists of 32: the warps', the CTAs'
     unsigned long long thr;
     float group[kTopGroups];
-    Raw<16> batch[kLpWarps][kLpU];   // the batch of the lane a warp looks at
+    int found;                       // keys in `list`, before it is sorted
 };
-static_assert(kLpWarps <= kLpMaxCluster, "TopState::list");
+static_assert(kLpWarps * (kTopCap - 1) <= kLpMaxCluster * 32, "TopState::list");
 
 // Sorting networks over a warp's lanes, largest first, a value a lane: the last stage
 // orders a bitonic sequence, and all of them any sequence. Two sorted lists a and b
@@ -293,6 +306,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     __shared__ float parts[kLpMaxCluster][4];     // in a row's first CTA: every CTA's sums
     __shared__ unsigned long long tops[TOP ? kLpMaxCluster : 1][kMaxTop];   // and candidates
     __shared__ TopState st;
+    // batches under way: a thread copies vectors for itself (and, of a batch with a candidate, the
+    // warp reads the lane's)
+    constexpr bool RING = ENT || TOP;
+    __shared__ __align__(16) uint4 ring[RING ? kLpStages : 1][kLpU][RING ? kLpThreads : 1];
     pdl_launch_dependents();
     if (p.split > 1) cluster_arrive();            // (the peers write here: see below)
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
@@ -314,7 +331,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     a.init();
     int cnt = 0;                       // this warp's candidates
     if constexpr (TOP) {
-        if (t == 0) st.thr = 0;
+        if (t == 0) {
+            st.thr = 0;
+            st.found = 0;
+        }
     }
     pdl_wait();
     unsigned long long thr = 0;
@@ -367,63 +387,96 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
         g = __shfl_sync(0xffffffffu, g, p.top - 1);
         if (g > -INFINITY) thr = max(thr, (unsigned long long)order_bits(g) << 32);
     };
-    int turn = 0;                         // batches read
-    auto load = [&](Raw<16>* r, int v0) {
-#pragma unroll
-        for (int u = 0; u < kLpU; ++u) {
-            const int v = v0 + u * kLpThreads + t;
-            if (v < vb) {
-                r[u] = ld_raw<16>(XV + (int64_t)v * VEC);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) r[u].w[i] = raw_low<T>();
-            }
-        }
-    };
-    auto batch = [&](const Raw<16>* r, int v0) {
-        const float mx = raw_max<T>(r);
-        a.template add<T>(r, mx, k);
-        if constexpr (TOP) {
-            if ((turn & (turn + 1)) == 0) {       // 1, 2, 4, ... batches read
-                tell();
-                if (turn == 0) {
-                    __syncthreads();              // (and st.thr is set)
-                    raise();
-                } else if (w == (turn & (kLpWarps - 1))) {
-                    raise();
-                    if (lane == 0) atomicMax(&st.thr, thr);
-                }
-            }
-            ++turn;
-            // (equal values may be wanted, a NaN always is; a threshold of 0 is a NaN)
-            const bool odd = a.s != a.s;
-            unsigned lanes = __ballot_sync(0xffffffffu, !(mx < lo) || odd);
-            if (lanes) {   // with the other warps' threshold?
-                thr = max(thr, *(volatile unsigned long long*)&st.thr);
-                lo = order_value((uint32_t)(thr >> 32));
-                lanes = __ballot_sync(0xffffffffu, !(mx < lo) || odd);
-            }
-            while (lanes) {
-                const int from = __ffs(lanes) - 1;
-                lanes &= lanes - 1;
-                if (lane == from) {
-#pragma unroll
-                    for (int u = 0; u < kLpU; ++u) st.batch[w][u] = r[u];
-                }
-                __syncwarp();
-                const T* const e = reinterpret_cast<const T*>(st.batch[w]);
-                const int v = v0 + lane / VEC * kLpThreads + (w * 32 + from);
-                const bool in = lane < NB && v < vb;
-                const float x = in ? lds_f(e + lane) : 0.f;
-                append(in, x, (uint32_t)(head + v * VEC + lane % VEC));
-            }
-        }
-    };
     constexpr int kStep = kLpThreads * kLpU;
+    int turn = 0;                         // batches read
+    int slot = 0;
+    // The batch at v0, by this thread; all but a row's last are whole, and done without tests.
+    const T* const mine = XV + (int64_t)t * VEC;
+    auto ask = [&](int to, int v0) {
+        uint4* const q = &ring[to][0][t];
+        const T* const x = mine + (int64_t)v0 * VEC;
+        if (v0 + kStep <= vb) {
+#pragma unroll
+            for (int u = 0; u < kLpU; ++u) copy_async(q + u * kLpThreads, x + u * kLpThreads * VEC);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kLpU; ++u)
+                if (v0 + u * kLpThreads + t < vb)
+                    copy_async(q + u * kLpThreads, x + u * kLpThreads * VEC);
+        }
+        copy_commit();
+    };
+    auto vector = [&](int v0, int u) {
+        if constexpr (RING) {
+            const uint4 q = ring[slot][u][t];
+            return Raw<16>{{q.x, q.y, q.z, q.w}};
+        } else {
+            return ld_raw<16>(mine + (int64_t)(v0 + u * kLpThreads) * VEC);
+        }
+    };
+    auto load = [&](Raw<16>* r, int v0) {
+        if constexpr (RING) copy_wait<kLpStages - 1>();
+        if (RING && v0 + kStep <= vb) {
+#pragma unroll
+            for (int u = 0; u < kLpU; ++u) r[u] = vector(v0, u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kLpU; ++u) {
+                constexpr uint32_t low = raw_low<T>();
+                r[u] = v0 + u * kLpThreads + t < vb ? vector(v0, u)
+                                                    : Raw<16>{{low, low, low, low}};
+            }
+        }
+    };
+    // Candidates of a batch in `slot`, whose maxima are mx.
+    auto look = [&](float mx, int v0) {
+        if ((turn & (turn + 1)) == 0) {           // 1, 2, 4, ... batches read
+            tell();
+            if (turn == 0) {
+                __syncthreads();                  // (and st.thr is set)
+                raise();
+            } else if (w == (turn & (kLpWarps - 1))) {
+                raise();
+                if (lane == 0) atomicMax(&st.thr, thr);
+            }
+        }
+        ++turn;
+        // (equal values may be wanted, a NaN always is; a threshold of 0 is a NaN)
+        const bool odd = a.s != a.s;
+        unsigned lanes = __ballot_sync(0xffffffffu, !(mx < lo) || odd);
+        if (!lanes) return;
+        // with the other warps' threshold?
+        thr = max(thr, *(volatile unsigned long long*)&st.thr);
+        lo = order_value((uint32_t)(thr >> 32));
+        lanes = __ballot_sync(0xffffffffu, !(mx < lo) || odd);
+        if (!lanes) return;
+        __syncwarp();                             // (every lane's copies have arrived)
+        // this lane's element of the first lane's batch, and its vector
+        const T* const e = (const T*)&ring[slot][lane % NB / VEC][w * 32] + lane % VEC;
+        const int v = v0 + lane % NB / VEC * kLpThreads + w * 32;
+        const int end = lane < NB ? vb - v : 0;
+        const uint32_t col = (uint32_t)(head + v * VEC + lane % VEC);
+        do {
+            const int from = __ffs(lanes) - 1;
+            lanes &= lanes - 1;
+            append(from < end, lds_f(e + from * VEC), col + (uint32_t)from * VEC);
+        } while (lanes);
+        __syncwarp();
+    };
+    if constexpr (RING) {
+#pragma unroll
+        for (int q = 0; q < kLpStages; ++q) ask(q, va + q * kStep);
+    }
     Raw<16> r[kLpU];
     for (int v0 = va; v0 < vb; v0 += kStep) {
         load(r, v0);
-        batch(r, v0);
+        const float mx = raw_max<T>(r);
+        a.template add<T>(r, mx, k);
+        if constexpr (TOP) look(mx, v0);
+        if constexpr (RING) {
+            ask(slot, v0 + kLpStages * kStep);
+            slot = slot == kLpStages - 1 ? 0 : slot + 1;
+        }
     }
     // head and tail: fewer than 2 * VEC elements, one a thread
     if (t / 32 * 32 < extra) {
@@ -458,13 +511,38 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
         red[w][3] = a.w;
     }
     if constexpr (TOP) {
-        if (cnt > 0) keep();
-        st.list[w][lane] = kept;
+        // the keys that are left, of all warps, into one list
+        if (turn == 0) __syncthreads();           // (st.found is set)
+        __syncwarp();
+        const unsigned long long least = max(thr, *(volatile unsigned long long*)&st.thr);
+        const unsigned long long fresh = lane < cnt ? st.cand[w][lane] : 0;
+        const bool put1 = fresh != 0 && fresh >= least, put2 = kept != 0 && kept >= least;
+        const unsigned who1 = __ballot_sync(0xffffffffu, put1);
+        const unsigned who2 = __ballot_sync(0xffffffffu, put2);
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&st.found, __popc(who1) + __popc(who2));
+        at = __shfl_sync(0xffffffffu, at, 0);
+        const unsigned below = (1u << lane) - 1;
+        unsigned long long* const all = st.list[0];
+        if (put1) all[at + __popc(who1 & below)] = fresh;
+        if (put2) all[at + __popc(who1) + __popc(who2 & below)] = kept;
     }
     __syncthreads();
     take(red[lane % kLpWarps]);
     meet(kLpWarps);
-    if constexpr (TOP) merge_lists(st, kLpWarps, w, lane);
+    if constexpr (TOP) {
+        // 32 at a time are sorted, and the lists merged
+        const int found = st.found;
+        int lists = 1;
+        while (lists * 32 < found) lists *= 2;
+        for (int q = w; q < lists; q += kLpWarps) {
+            const int i = q * 32 + lane;
+            const unsigned long long v = warp_sort(i < found ? st.list[q][lane] : 0ull, lane);
+            st.list[q][lane] = v;
+        }
+        __syncthreads();
+        merge_lists(st, lists, w, lane);
+    }
     if (p.split > 1) {
         // every CTA leaves its results in the first one's shared memory, once that has started
         cluster_wait();

@@ -70,6 +70,21 @@ __device__ __forceinline__ void st_raw(void* p, const Raw<B>& r) {
         asm volatile("st.global.cs.u16 [%0], %1;" ::"l"(p), "h"((uint16_t)r.w[0]) : "memory");
 }
 
+// 16 bytes from global to this CTA's shared memory, without waiting; the copies up to a commit are
+// a group, and copy_wait<N> returns when all but this thread's newest N groups have arrived.
+__device__ __forceinline__ void copy_async(void* smem, const void* p) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(smem)),
+                 "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
