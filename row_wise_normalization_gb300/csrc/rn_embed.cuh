@@ -159,6 +159,30 @@ constexpr int kZeroBytes = 4096;    // of a copy
 constexpr int kZeroBulk = 512;      // bytes of a row from which it is copied
 constexpr int kClearWords = kZeroRange / 32 + kZeroBytes / 4;   // shared memory of a CTA that clears
 
+// Ids, from L2: a CTA that clears does not wait for the kernel ahead itself (embed_bwd_kernel), so
+// nothing else keeps it from an older copy in its SM's L1.
+__device__ __forceinline__ Raw<16> ld_ids(const void* p) {
+    Raw<16> r;
+    asm volatile("ld.relaxed.gpu.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ int64_t ld_id_l2(const void* p, int64_t i, int itype) {
+    if (itype == IT_I64) {
+        long long v;
+        asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];"
+                     : "=l"(v)
+                     : "l"((const long long*)p + i)
+                     : "memory");
+        return v;
+    }
+    int v;
+    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"((const int*)p + i) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void bulk_s2g(void* dst, uint32_t src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
                  "r"(bytes)
@@ -237,7 +261,7 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
             Raw<16> r[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (v + u * NT < nv) r[u] = ld_raw<16>(body + (v + u * NT) * 16);
+                if (v + u * NT < nv) r[u] = ld_ids(body + (v + u * NT) * 16);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (v + u * NT < nv) {
@@ -251,7 +275,7 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
                 }
             }
         }
-        if (t < p.n - nv * per) mark(ld_id(p.tokens, t < head ? t : nv * per + t, p.itype));
+        if (t < p.n - nv * per) mark(ld_id_l2(p.tokens, t < head ? t : nv * per + t, p.itype));
         __syncthreads();
         for (int r = t / lanes; r < cnt; r += NT / lanes)
             if (!((bits[r >> 5] >> (r & 31)) & 1u))
