@@ -21,7 +21,7 @@
 // Where there is more to do than sums, a thread keeps the next two batches under way into shared
 // memory, 32 KB a CTA, so that the memory does not wait for a row's barriers and alternatives: a
 // thread copies its own vectors and needs no barrier for them. 2048 x 128000 BF16 with entropies
-// 86 us by loads into registers, this way 82; with 8 alternatives too 108, 94 (with what is
+// 86 us by loads into registers, this way 82; with 8 alternatives too 108, 91 (with what is
 // below). Sums alone are better off without: 700 x 128000 30 us, this way 37. (CTAs that go on to
 // further rows, with the next one's batches under way: 2048 x 128000 with 8 alternatives 111 us,
 // where one row each took 106: rows are handed out more evenly.)
@@ -35,7 +35,7 @@
 //
 // A row is split over the CTAs of a cluster where there are few rows; the
 // CTAs' results meet in the first one's shared memory (one row of 128000 FP32 3.0 us, of
-// which the launch is about 2; 64 x 50001 BF16 5.3 us).
+// which the launch is about 2, 6.6 with 20 alternatives; 64 x 50001 BF16 5.3 and 9.8 us).
 //
 // Alternatives: the `top` largest logits, the lowest index first among equal
 // ones, found in the same pass. A candidate is a 64-bit key: the value's bits in
@@ -44,18 +44,19 @@
 // memory and, past 31 of them, its 32 best, sorted, in its lanes, and a new one has to exceed the
 // threshold `thr`, below which the row's `top` best cannot lie. It comes from groups of
 // threads: the top-th largest of the groups' maxima so far, since at least `top` elements
-// reach it. It is taken after the first batch, then each time the columns read have doubled, so
-// that about `top` candidates are met between two of them (with the first threshold alone 2048 x
-// 128000 BF16 with 8 alternatives took 139 us where it then took 101). Past the first, no barrier
-// is needed: maxima only grow, and a stale one is a lower bound too. So is the top-th of what a warp
-// keeps. A batch without a candidate costs a comparison of its maximum, which is there anyway; in
-// one with a candidate, the warp looks at the elements of the lane that has it, an element a lane,
-// where they lie in shared memory. At the end the keys that reach the last threshold, of all warps,
-// go into one list: mostly one or two warps' sorts (every warp sorting and keeping 32, then merging
-// 8 lists: 8 alternatives 106 us, this way 95). The order in which warps run changes which keys are
-// tried, not which are kept.
-// What alternatives cost now is instructions: a row of 128000 BF16 takes 30000 warp instructions
-// with its entropy, 41000 with 8 alternatives as well and 59000 with 32 (82, 94, 130 us for 2048).
+// reach it. It is taken after the first two batches, before either is looked at, then each time
+// the columns read have doubled, so that about `top` candidates are met between two of them (with
+// the first threshold alone 2048 x 128000 BF16 with 8 alternatives took 139 us where it then took
+// 101; the first one after one batch: 94 us, not 91, with 32 alternatives 130, not 117). Past the
+// first, no barrier is needed: maxima only grow, and a stale one is a lower bound too. So is the
+// top-th of what a warp keeps. A batch without a candidate costs a comparison of its maximum, which
+// is there anyway; in one with a candidate, the warp looks at the elements of the lane that has it,
+// an element a lane, where they lie in shared memory. At the end the keys that reach the last
+// threshold, of all warps, go into one list: mostly one or two warps' sorts (every warp sorting and
+// keeping 32, then merging 8 lists: 8 alternatives 106 us, this way 95 at the time). The order in
+// which warps run changes which keys are tried, not which are kept.
+// What alternatives cost now is instructions: a row of 128000 BF16 takes 28000 warp instructions
+// with its entropy, 38000 with 8 alternatives as well and 51000 with 32 (82, 91, 117 us for 2048).
 #pragma once
 
 #include <type_traits>
@@ -386,10 +387,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
             g = warp_sort(fmaxf(g, h), lane);
         g = __shfl_sync(0xffffffffu, g, p.top - 1);
         if (g > -INFINITY) thr = max(thr, (unsigned long long)order_bits(g) << 32);
+        lo = order_value((uint32_t)(thr >> 32));
     };
     constexpr int kStep = kLpThreads * kLpU;
     int turn = 0;                         // batches read
-    int slot = 0;
     // The batch at v0, by this thread; all but a row's last are whole, and done without tests.
     const T* const mine = XV + (int64_t)t * VEC;
     auto ask = [&](int to, int v0) {
@@ -406,41 +407,34 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
         }
         copy_commit();
     };
-    auto vector = [&](int v0, int u) {
+    auto vector = [&](int v0, int u, int from) {
         if constexpr (RING) {
-            const uint4 q = ring[slot][u][t];
+            const uint4 q = ring[from][u][t];
             return Raw<16>{{q.x, q.y, q.z, q.w}};
         } else {
             return ld_raw<16>(mine + (int64_t)(v0 + u * kLpThreads) * VEC);
         }
     };
-    auto load = [&](Raw<16>* r, int v0) {
-        if constexpr (RING) copy_wait<kLpStages - 1>();
+    // The sums of the batch at v0 (in slot `from`), which gives its maximum.
+    Raw<16> r[kLpU];
+    auto sum = [&](int v0, int from) {
         if (RING && v0 + kStep <= vb) {
 #pragma unroll
-            for (int u = 0; u < kLpU; ++u) r[u] = vector(v0, u);
+            for (int u = 0; u < kLpU; ++u) r[u] = vector(v0, u, from);
         } else {
 #pragma unroll
             for (int u = 0; u < kLpU; ++u) {
                 constexpr uint32_t low = raw_low<T>();
-                r[u] = v0 + u * kLpThreads + t < vb ? vector(v0, u)
+                r[u] = v0 + u * kLpThreads + t < vb ? vector(v0, u, from)
                                                     : Raw<16>{{low, low, low, low}};
             }
         }
+        const float mx = raw_max<T>(r);
+        a.template add<T>(r, mx, k);
+        return mx;
     };
-    // Candidates of a batch in `slot`, whose maxima are mx.
-    auto look = [&](float mx, int v0) {
-        if ((turn & (turn + 1)) == 0) {           // 1, 2, 4, ... batches read
-            tell();
-            if (turn == 0) {
-                __syncthreads();                  // (and st.thr is set)
-                raise();
-            } else if (w == (turn & (kLpWarps - 1))) {
-                raise();
-                if (lane == 0) atomicMax(&st.thr, thr);
-            }
-        }
-        ++turn;
+    // Candidates of the batch at v0 in slot `from`, whose maxima are mx.
+    auto look = [&](float mx, int v0, int from) {
         // (equal values may be wanted, a NaN always is; a threshold of 0 is a NaN)
         const bool odd = a.s != a.s;
         unsigned lanes = __ballot_sync(0xffffffffu, !(mx < lo) || odd);
@@ -452,30 +446,58 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
         if (!lanes) return;
         __syncwarp();                             // (every lane's copies have arrived)
         // this lane's element of the first lane's batch, and its vector
-        const T* const e = (const T*)&ring[slot][lane % NB / VEC][w * 32] + lane % VEC;
+        const T* const e = (const T*)&ring[from][lane % NB / VEC][w * 32] + lane % VEC;
         const int v = v0 + lane % NB / VEC * kLpThreads + w * 32;
         const int end = lane < NB ? vb - v : 0;
         const uint32_t col = (uint32_t)(head + v * VEC + lane % VEC);
         do {
-            const int from = __ffs(lanes) - 1;
+            const int at = __ffs(lanes) - 1;
             lanes &= lanes - 1;
-            append(from < end, lds_f(e + from * VEC), col + (uint32_t)from * VEC);
+            append(at < end, lds_f(e + at * VEC), col + (uint32_t)at * VEC);
         } while (lanes);
         __syncwarp();
     };
+    int v0 = va, slot = 0;
     if constexpr (RING) {
-#pragma unroll
-        for (int q = 0; q < kLpStages; ++q) ask(q, va + q * kStep);
+        static_assert(kLpStages == 2, "the loop below");
+        ask(0, va);
+        ask(1, va + kStep);
     }
-    Raw<16> r[kLpU];
-    for (int v0 = va; v0 < vb; v0 += kStep) {
-        load(r, v0);
-        const float mx = raw_max<T>(r);
-        a.template add<T>(r, mx, k);
-        if constexpr (TOP) look(mx, v0);
+    if constexpr (TOP) {
+        // the first threshold is that of two batches, which are looked at after it
+        if (va < vb) {
+            copy_wait<1>();
+            const float m0 = sum(va, 0);
+            copy_wait<0>();
+            const float m1 = sum(va + kStep, 1);
+            tell();
+            __syncthreads();                      // (and st.thr and st.found are set)
+            raise();
+            look(m0, va, 0);
+            ask(0, va + 2 * kStep);
+            look(m1, va + kStep, 1);
+            ask(1, va + 3 * kStep);
+            turn = 2;
+            v0 = va + 2 * kStep;
+        }
+    }
+    for (; v0 < vb; v0 += kStep) {
+        if constexpr (RING) copy_wait<1>();
+        const float mx = sum(v0, slot);
+        if constexpr (TOP) {
+            if ((turn & (turn + 1)) == 0) {       // 4, 8, ... batches read
+                tell();
+                if (w == (turn & (kLpWarps - 1))) {
+                    raise();
+                    if (lane == 0) atomicMax(&st.thr, thr);
+                }
+            }
+            ++turn;
+            look(mx, v0, slot);
+        }
         if constexpr (RING) {
-            ask(slot, v0 + kLpStages * kStep);
-            slot = slot == kLpStages - 1 ? 0 : slot + 1;
+            ask(slot, v0 + 2 * kStep);
+            slot ^= 1;
         }
     }
     // head and tail: fewer than 2 * VEC elements, one a thread
