@@ -156,7 +156,6 @@ constexpr int kZeroRange = 32768;   // ids a CTA marks at a time (4 KB of bits)
 // 13.1. Copies of 8 KB: 1 us more. Beside the sort and long sums there is no gain, and the registers
 // cost: 16383 x 771 FP16 49.9, by stores 48.8, 65536 x 4096 BF16 291, 277 (embed_bwd_kernel).
 constexpr int kZeroBytes = 4096;    // of a copy
-constexpr int kZeroBulk = 512;      // bytes of a row from which it is copied
 constexpr int kClearWords = kZeroRange / 32 + kZeroBytes / 4;   // shared memory of a CTA that clears
 
 // Ids, from L2: a CTA that clears does not wait for the kernel ahead itself (embed_bwd_kernel), so
@@ -234,7 +233,7 @@ __device__ __forceinline__ void clear_absent(const SortParams& p, int part, int 
     const int64_t nv = (p.n - head) / per;
     const char* const body = (const char*)p.tokens + head * index_size(p.itype);
     // threads of a row: as many 16-byte stores as it has, up to a warp's; one where copies do all
-    const bool bulk = BULK && p.zero_bytes >= kZeroBulk;
+    const bool bulk = BULK && p.bulk;
     int lanes = 32;
     if (bulk) {
         if ((((uint64_t)(uintptr_t)p.zero | (uint64_t)p.zero_pitch | (uint64_t)p.zero_bytes) & 15) == 0)

@@ -72,7 +72,9 @@ struct SortParams {
     // Rows of ids that do not occur, cleared beside sort and sums (NULL: left as they are)
     char* zero;
     int64_t zero_pitch, zero_bytes;   // bytes from row to row, and of a row
+    bool bulk;            // long rows, in device memory (embed_few_kernel)
 };
+constexpr int64_t kZeroBulk = 512;    // bytes of a row from which the bulk-copy engine clears it
 constexpr int sort_key_bits(int64_t vocab) {
     int b = 0;
     while (((int64_t)1 << b) <= vocab) ++b;   // keys 0 .. vocab

@@ -241,6 +241,8 @@ int embed_bwd(int dtype, int gtype, int itype, const void* dout, int64_t lddo, c
         sp.zero = (char*)dtable;
         sp.zero_pitch = ldg * gs;
         sp.zero_bytes = d * gs;
+        // (the bulk-copy engine is given device memory only)
+        sp.bulk = embed_few(n, d, es) && sp.zero_bytes >= kZeroBulk && !host_resident(dtable);
     }
     EmbedBwdParams p = {};
     p.dout = dout;

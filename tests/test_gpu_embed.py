@@ -304,3 +304,19 @@ def test_zeros_of_long_rows(gtype, n, d, ldg, off):
     want = torch.zeros(vocab, d, dtype=DT[gtype], device="cuda")
     want[tok] = dout
     assert _bits_equal(grad.view, want)
+
+
+@pytest.mark.parametrize("n", [40, 3000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_in_pinned_host_memory(n, accumulate):
+    """Rows read and written over the host link, long ones too."""
+    rng = np.random.default_rng(n)
+    vocab, d = 300, 640
+    tok = torch.from_numpy(rng.integers(0, vocab, n)).cuda()
+    dout = torch.from_numpy(rng.integers(-3, 4, (n, d)).astype(np.float32))
+    grad = torch.from_numpy(rng.integers(-3, 4, (vocab, d)).astype(np.float32)).pin_memory()
+    want = grad.clone() if accumulate else torch.zeros(vocab, d)
+    want.index_add_(0, tok.cpu(), dout)
+    got = rn.embed_bwd(dout.pin_memory(), tok, vocab, dtable=grad, accumulate=accumulate)
+    torch.cuda.synchronize()
+    assert got is grad and torch.equal(grad, want)

@@ -320,3 +320,18 @@ def test_shapes_and_refusals():
         rn.logprob_bwd(logp.double(), x, t, lse)
     with pytest.raises(TypeError):
         rn.logprob_bwd(logp, x, t, None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,vocab", [(3, 40001), (700, 2999)])
+def test_logits_in_pinned_host_memory(dtype, rows, vocab):
+    """Rows read over the host link: the same bits as from device memory."""
+    rng = np.random.default_rng([rows, vocab])
+    x = rounded(rng, (rows, vocab), dtype)
+    t = torch.from_numpy(rng.integers(0, vocab, rows)).cuda()
+    host = x.cpu().pin_memory()
+    for kw in ({"want_entropy": False}, {}, {"top": 7}, {"top": 32, "want_entropy": False}):
+        a, b = rn.logprob_fwd(x, t, 0.7, **kw), rn.logprob_fwd(host, t, 0.7, **kw)
+        torch.cuda.synchronize()
+        for p, q in zip(a, b):
+            assert (p is None and q is None) or torch.equal(p.cpu(), q.cpu())
