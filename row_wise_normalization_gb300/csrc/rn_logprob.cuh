@@ -271,14 +271,15 @@ __device__ __forceinline__ void merge_lists(TopState& st, int n, int w, int lane
 }
 
 // The values of a row that FP32 products cannot be referred to (see above), from
-// differences of logits: (m, log S, W / S in units of log 2). All threads.
+// differences of logits: (log S, W / S in units of log 2). All threads. (By the scale first: log2 e
+// times a scale above 2.36e38 is infinite, and 0 times that would be NaN.)
 template <typename T>
-__device__ void row_again(const T* X, int V, float k, float m, float (*red)[4], float* ls,
+__device__ void row_again(const T* X, int V, float scale, float m, float (*red)[4], float* ls,
                           float* ws) {
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     float s = 0.f, q = 0.f;
     for (int i = t; i < V; i += kLpThreads) {
-        const float z = (ldt_x1(X + i) - m) * k, e = ex2(z);
+        const float z = (ldt_x1(X + i) - m) * scale * kLog2e, e = ex2(z);
         s += e;
         if (e != 0.f) q = fmaf(e, z, q);
     }
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     const bool far = !nan && !none && fabsf(a.m) < INFINITY &&
                      (odd || !(fabsf(a.m * k) < kRef && fabsf(a.m) < -0.1f * kHeld));
     if (far) {
-        row_again<T>(X, V, k, a.m, red, &ls, &ws);
+        row_again<T>(X, V, p.scale, a.m, red, &ls, &ws);
         ref = a.m * p.scale;
     }
     // log p of a logit

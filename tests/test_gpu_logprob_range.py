@@ -1,0 +1,65 @@
+"""Log probabilities at the ends of their ranges: the largest and smallest scales,
+logits as far apart as the type allows, rows far from zero."""
+import numpy as np
+import pytest
+import torch
+
+import row_wise_normalization_gb300 as rn
+import token_checks
+from oracle import tokens as ot
+from token_util import DT, f64, rounded
+
+pytestmark = pytest.mark.gpu
+F32_MAX = float(np.finfo(np.float32).max)
+
+
+def _check(x, t, scale, top):
+    logp, ent, lse, ids, tl = rn.logprob_fwd(x, t, scale, top=top)
+    plain = rn.logprob_fwd(x, t, scale, want_entropy=False)
+    want = ot.logprob(f64(x), t.cpu().numpy(), scale, top)
+    token_checks.check_logprob({"logp": f64(logp), "entropy": f64(ent), "lse": f64(lse),
+                                "top_ids": ids.cpu().numpy(), "top_logp": f64(tl)}, want, f64(x),
+                               scale)
+    token_checks.check_logprob({"logp": f64(plain[0]), "lse": f64(plain[2])}, want, f64(x), scale)
+    return ent, lse
+
+
+def _check_gradient(x, t, scale, lse, ent, dtype, std, off_by):
+    """Against the definition from the logits themselves; off_by: what lse (or the
+    kernel's own log S) may be off by, which makes a probability off by as much."""
+    rng = np.random.default_rng(77)
+    g, h = (rounded(rng, (x.shape[0],), "f32", std) for _ in range(2))
+    d = rn.logprob_bwd(g, x, t, lse, scale, dentropy=h, entropy=ent)
+    want, mag, factor = ot.logprob_backward(f64(g), f64(h), f64(x), t.cpu().numpy(), None, f64(ent),
+                                            scale)
+    u = token_checks.U
+    more = 8 * u * mag + mag * np.reshape(off_by, (-1, 1))
+    tol = (more + token_checks.UT[dtype] * (np.abs(want) + more) + token_checks.TINY[dtype]
+           + 2.0 ** -126 * factor * 2)
+    err = np.abs(f64(d) - want)
+    assert np.all(err <= tol), (np.argwhere(~(err <= tol))[:3], err.max())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [2.0 ** 126, 2.0 ** 127, float(np.float32(3e38)), F32_MAX])
+@pytest.mark.parametrize("vocab", [3, 700, 20011])
+def test_the_largest_scales(dtype, scale, vocab):
+    """Differences of a logit are beyond the exponential's range: p is 0, or 1 over the
+    columns that share the maximum."""
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy(-rng.integers(1, 90, (6, vocab)).astype(np.float32))
+    x[0, 0] = 0.0
+    x[1, 2] = 0.0
+    x[1, 0] = float("-inf")
+    x[2, ::2] = 0.0                       # entropy: log of their number
+    x[3] = 1.0                            # lse = scale + log vocab
+    x[4, 1] = 4.0                         # lse: beyond FP32
+    x[5] = torch.finfo(DT[dtype]).min     # a mask's lowest value, and one column
+    x[5, 1] = 0.0
+    x = x.to(DT[dtype]).cuda()
+    t = torch.tensor([0, 0, 1, 2, 1, 1], device="cuda")
+    ent, lse = _check(x, t, scale, 3)
+    if dtype != "f16":                    # (whose range ends at 65504)
+        u = token_checks.U
+        off = u * (vocab / 256 + 13 + token_checks.depth(vocab) + 16)
+        _check_gradient(x, t, scale, lse, ent, dtype, 2.0 ** -20, np.full(6, off))
