@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     // (a scale with which kHeld is not far below every other product, or beyond FP32's
     // range: the sums say nothing, and the row is summed again)
     const bool odd = !(k > 1e-20f && k < 1e8f) && a.m > -INFINITY;
-    const bool nan = a.s != a.s && !odd;
+    bool nan = a.s != a.s && !odd;                  // (odd: row_again's own sum says)
     const bool none = a.m == -INFINITY && !nan;     // every logit is -inf
     float ref = a.c * kLn2, ls = logf(a.s), ws = a.w / a.s;
     const bool far = !nan && !none && fabsf(a.m) < INFINITY &&
@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     if (far) {
         row_again<T>(X, V, p.scale, a.m, red, &ls, &ws);
         ref = a.m * p.scale;
+        nan = ls != ls;
     }
     // log p of a logit
     auto logp = [&](float x) {

@@ -63,3 +63,19 @@ def test_the_largest_scales(dtype, scale, vocab):
         u = token_checks.U
         off = u * (vocab / 256 + 13 + token_checks.depth(vocab) + 16)
         _check_gradient(x, t, scale, lse, ent, dtype, 2.0 ** -20, np.full(6, off))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -70, 1.0, 2.0 ** 40, float(np.float32(3e38))])
+@pytest.mark.parametrize("vocab", [6, 2100])
+def test_nan_rows_with_masks(dtype, scale, vocab):
+    """A NaN spoils every value of its row, those of masked columns too."""
+    x = torch.full((4, vocab), float("-inf"))
+    x[:, 2] = 0.5
+    x[1, 4] = float("nan")
+    x[2, 2] = float("nan")                # nothing but NaN and -inf
+    x[3, 1] = -1.5
+    x = x.to(DT[dtype]).cuda()
+    t = torch.tensor([0, 0, 0, -1], device="cuda")
+    _check(x, t, scale, 4)
+    _check(x, torch.full_like(t, 2), scale, 1)
