@@ -279,7 +279,7 @@ __device__ void row_again(const T* X, int V, float scale, float m, float (*red)[
     const int t = threadIdx.x, w = t >> 5, lane = t & 31;
     float s = 0.f, q = 0.f;
     for (int i = t; i < V; i += kLpThreads) {
-        const float z = (ldt_x1(X + i) - m) * scale * kLog2e, e = ex2(z);
+        const float z = scaled_diff(ldt_x1(X + i), m, scale) * kLog2e, e = ex2(z);
         s += e;
         if (e != 0.f) q = fmaf(e, z, q);
     }
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     auto logp = [&](float x) {
         if (nan || a.m == INFINITY) return __uint_as_float(0x7fffffffu);
         if (none || x == -INFINITY) return -INFINITY;
-        if (far) return (x - a.m) * p.scale - ls;
+        if (far) return scaled_diff(x, a.m, p.scale) - ls;
         // (a mask's lowest value, times k, may be beyond FP32's range)
         return (fabsf(x * k) < kRef ? fmaf(x, k, -a.c) * kLn2 : x * p.scale - ref) - ls;
     };

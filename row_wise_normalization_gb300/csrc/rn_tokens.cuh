@@ -145,6 +145,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// scale * (x - m) for x <= m and scale > 0. The difference may be beyond FP32's range where its
+// product with a small scale is not; halves are exact for numbers that large.
+__device__ __forceinline__ float scaled_diff(float x, float m, float scale) {
+    const float d = x - m;
+    if (d == -INFINITY && x > -INFINITY) return (0.5f * x - 0.5f * m) * scale * 2.f;
+    return d * scale;
+}
+
 // ---- thread-block clusters --------------------------------------------------
 __device__ __forceinline__ void cluster_sync() {
     __syncwarp();

@@ -34,6 +34,10 @@ def _check_gradient(x, t, scale, lse, ent, dtype, std, off_by):
                                             scale)
     u = token_checks.U
     more = 8 * u * mag + mag * np.reshape(off_by, (-1, 1))
+    # Below 2^-126 each rounding is off by up to s = 2^-150, whatever the value. With gs = g scale,
+    # b = -h scale (s each) and a = b H - gs (s |H| + s + s), the element e^z (a + b z) + gs is
+    # off by p (s |z| + s (|H| + 2) + s) + s + s, and p |z| < 1, p <= 1: s (|H| + 6).
+    more = more + 2.0 ** -150 * (np.abs(f64(ent)[:, None]) + 6)
     tol = (more + token_checks.UT[dtype] * (np.abs(want) + more) + token_checks.TINY[dtype]
            + 2.0 ** -126 * factor * 2)
     err = np.abs(f64(d) - want)
@@ -79,3 +83,24 @@ def test_nan_rows_with_masks(dtype, scale, vocab):
     t = torch.tensor([0, 0, 0, -1], device="cuda")
     _check(x, t, scale, 4)
     _check(x, torch.full_like(t, 2), scale, 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [2.0 ** -149, 2.0 ** -130, 2.0 ** -127, 2.0 ** -126, 2.0 ** -120,
+                                   2.0 ** -60])
+@pytest.mark.parametrize("vocab", [5, 2100])
+def test_logits_as_far_apart_as_the_type_allows(dtype, scale, vocab):
+    """Differences of logits beyond FP32's range, whose products with the scale are ordinary."""
+    rng = np.random.default_rng(vocab)
+    top = torch.finfo(DT[dtype]).max
+    a = rng.uniform(-1.0, 1.0, (4, vocab))
+    a[1] = np.where(rng.random(vocab) < 0.5, 1.0, -1.0)
+    a[2, ::2] = -np.inf
+    a[0, :2], a[1, :2], a[2, 1] = (1.0, -1.0), (-1.0, 1.0), 1.0
+    x = torch.from_numpy(a * top).to(DT[dtype]).cuda()
+    t = torch.tensor([1, 0, 3, 2], device="cuda")
+    ent, lse = _check(x, t, scale, 4)
+    u = token_checks.U
+    off = 4 * u * (np.abs(f64(lse)) + np.log(vocab)) + u * (token_checks.depth(vocab) + 32)
+    if dtype != "f16":                    # (all of whose logits are alike at such scales)
+        _check_gradient(x, t, scale, lse, ent, dtype, 1.0, off)
