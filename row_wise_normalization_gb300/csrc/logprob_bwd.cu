@@ -12,10 +12,11 @@
 // 4.2 GB (1373 us with scalar arithmetic and a comparison an element).
 // Rows with g = h = 0 (padding) are written as zeros without being read. p_j = 0
 // makes both terms zero: e^-128 is below the smallest FP32 number the exponential
-// gives, so log p_j is held above -128 and 0 * -inf cannot arise. Where |lse| >= 4096 (a mask
-// of the type's lowest value on every column, or logits far from zero), 24 bits no longer hold
-// log S beside the maximum and x - lse would be off by 2^-12 or more: the first CTA of
-// such a row takes m and log S from the logits again and does the whole row, and the row's
+// gives, so log p_j is held above -128 and 0 * -inf cannot arise. lse is rounded to 24 bits, and
+// every p_j of a row is off by what that leaves off: half a step, 2^-24 |lse| at most, so 2^-13
+// just below 4096 (and below the half step of 16-bit gradients everywhere). Where |lse| >= 4096 (a
+// mask of the type's lowest value on every column, or logits far from zero) the first CTA of
+// the row takes m and log S from the logits again and does the whole row, and the row's
 // other CTAs leave. dlogits may be logits itself: a thread writes only what it, or its CTA, has
 // read.
 #include "rn_tokens.cuh"

@@ -593,12 +593,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     const bool odd = !(k > 1e-20f && k < 1e8f) && a.m > -INFINITY;
     bool nan = a.s != a.s && !odd;                  // (odd: row_again's own sum says)
     const bool none = a.m == -INFINITY && !nan;     // every logit is -inf
-    float ref = a.c * kLn2, ls = logf(a.s), ws = a.w / a.s;
+    const float ref = a.m * p.scale;
+    float ls = logf(a.s), ws = a.w / a.s;
     const bool far = !nan && !none && fabsf(a.m) < INFINITY &&
                      (odd || !(fabsf(a.m * k) < kRef && fabsf(a.m) < -0.1f * kHeld));
     if (far) {
         row_again<T>(X, V, p.scale, a.m, red, &ls, &ws);
-        ref = a.m * p.scale;
         nan = ls != ls;
     }
     // log p of a logit
@@ -612,7 +612,15 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     if (t == 0) {
         const float bad = __uint_as_float(0x7fffffffu);
         const bool spoilt = nan || a.m == INFINITY;
-        if (p.lse) p.lse[row] = spoilt ? bad : none ? -INFINITY : ref + ls;
+        if (p.lse) {
+            // The largest product with what its rounding left off, and log S referred to it rather
+            // than to c, which is m k rounded: one rounding of a large number in all. (c ln 2 + log S
+            // has two more, and was off by 2.8e-4 at 3900, where half a step is 1.2e-4.)
+            const float left = fmaf(a.m, p.scale, -ref);
+            const float log_s = far ? ls : ls - fmaf(a.m, k, -a.c) * kLn2;
+            const float lse = fabsf(ref) < INFINITY ? ref + (log_s + left) : ref;
+            p.lse[row] = spoilt ? bad : none ? -INFINITY : lse;
+        }
         if (ENT) p.entropy[row] = spoilt ? bad : none ? 0.f : ls - ws * kLn2;
         if (p.logp) {
             const int64_t id = ld_id(p.targets, row, p.itype);

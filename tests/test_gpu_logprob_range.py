@@ -104,3 +104,29 @@ def test_logits_as_far_apart_as_the_type_allows(dtype, scale, vocab):
     off = 4 * u * (np.abs(f64(lse)) + np.log(vocab)) + u * (token_checks.depth(vocab) + 32)
     if dtype != "f16":                    # (all of whose logits are alike at such scales)
         _check_gradient(x, t, scale, lse, ent, dtype, 1.0, off)
+
+
+@pytest.mark.parametrize("offset", [300.0, 1000.0, 3900.0, -3000.0])
+@pytest.mark.parametrize("scale", [0.7, 0.8125, 1.0, 1.0333])
+@pytest.mark.parametrize("vocab", [64, 5003])
+def test_lse_far_from_zero(offset, scale, vocab):
+    """lse is what log S adds to the largest product, rounded once: half a step of its own, and
+    S's and the logarithm's errors. A gradient from it is off by as much."""
+    rng = np.random.default_rng([vocab, int(abs(offset))])
+    scale = float(np.float32(scale))
+    x = (rounded(rng, (40, vocab), "f32", 2.0) + offset).contiguous()
+    t = torch.from_numpy(rng.integers(0, vocab, 40)).cuda()
+    ent, lse = _check(x, t, scale, 2)
+    a = scale * f64(x)
+    m = a.max(1)
+    z = np.abs(a - m[:, None])
+    p = np.exp(-z) / np.exp(-z).sum(1, keepdims=True)
+    want = m + np.log(np.exp(-z).sum(1))
+    u = token_checks.U
+    # S along its chain and its elements' exponents (token_checks), the logarithm, and the two
+    # sums of small numbers that precede the rounding
+    off = (u * np.abs(want) + u * (token_checks.depth(vocab) + 4 + 4 * (p * z).sum(1))
+           + 6 * u * np.log(vocab) + 4 * u)
+    err = np.abs(f64(lse) - want)
+    assert np.all(err <= off), (err.max(), off.min())
+    _check_gradient(x, t, scale, lse, ent, "f32", 1.0, off)
