@@ -137,16 +137,16 @@ static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
     static thread_local unsigned long long prepared = 0;
     unsigned long long ctx = 0;
     cudaError_t err = current_context_id(&ctx);
+    if (err == cudaSuccess)
+        err = once_in_context(ctx, prepared, [] {
+            const cudaError_t e =
+                cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     cluster_bytes(kSortMaxShare, 2));
+            if (e != cudaSuccess) return e;
+            return cudaFuncSetAttribute(embed_sort_kernel,
+                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        });
     if (err != cudaSuccess) return err;
-    if (ctx == 0 || prepared != ctx) {
-        err = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   cluster_bytes(kSortMaxShare, 2));
-        if (err == cudaSuccess)
-            err = cudaFuncSetAttribute(embed_sort_kernel,
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (err != cudaSuccess) return err;
-        prepared = ctx;
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.cluster, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);

@@ -666,10 +666,11 @@ static cudaError_t logprob_fwd_go(const LogprobParams& q, cudaStream_t s) {
         static thread_local unsigned long long prepared = 0;
         unsigned long long ctx = 0;
         err = current_context_id(&ctx);
-        if (err == cudaSuccess && (ctx == 0 || prepared != ctx)) {
-            err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            prepared = ctx;
-        }
+        if (err == cudaSuccess)
+            err = once_in_context(ctx, prepared, [&] {
+                return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                            1);
+            });
         if (err != cudaSuccess) return err;
     }
     cudaLaunchConfig_t cfg = {};

@@ -31,6 +31,16 @@ inline FastDiv fast_div(uint32_t d) {
     return f;
 }
 
+// Function attributes belong to a context: `set` runs once in each, in each thread, and again after
+// it has failed. `done`: the context it last succeeded in (a thread's own); ctx 0: none is current.
+template <typename Set>
+inline cudaError_t once_in_context(unsigned long long ctx, unsigned long long& done, Set set) {
+    if (ctx != 0 && done == ctx) return cudaSuccess;
+    const cudaError_t err = set();
+    if (err == cudaSuccess) done = ctx;
+    return err;
+}
+
 // out[i] = scale * table[tokens[i]], zeros where the id is outside [0, vocab).
 struct EmbedParams {
     const void* tokens;
