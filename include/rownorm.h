@@ -361,8 +361,8 @@ int embed_fwd(int dtype, int itype, const void *tokens, const void *table, int64
  * of an id are taken in order; no atomics touch a sum), so results repeat
  * bit for bit; each element is rounded once. `workspace` (device memory, 16-byte
  * aligned, caller-owned, contents on entry ignored) must hold the bytes that
- * embed_bwd_workspace_size gives (else RN_ERR_SIZE): 8 bytes an id (more beyond
- * 163840 ids) and d/4 (short batches: d) bytes an id for the sums of ids that occur many times. Calls that
+ * embed_bwd_workspace_size gives (else RN_ERR_SIZE): 8 bytes an id (16.5 beyond
+ * 10240 ids) and d/4 (short batches: d) bytes an id for the sums of ids that occur many times. Calls that
  * may run at the same time on the GPU need workspaces of their own (two graphs
  * captured with one workspace count as such calls if they can overlap).
  * n up to 2^31 - 1; n == 0 zeroes dtable (accumulate: does nothing). The calls

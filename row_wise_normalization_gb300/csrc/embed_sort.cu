@@ -7,8 +7,8 @@
 // for each warp carries the number from one 32 to the next. Nothing depends on the
 // order in which CTAs or atomics run.
 //
-// Up to kSortClusterMax ids are sorted by one thread-block cluster of 1 to 16 CTAs
-// that keeps them in its CTAs' shared memory: a pass counts its digits, the CTAs
+// Up to 163840 ids (10240 a CTA of the largest cluster that the GPU places, 16 on a whole
+// GB300) are sorted by one thread-block cluster of 1 to 16 CTAs that keeps them in its CTAs' shared memory: a pass counts its digits, the CTAs
 // read each other's counts, and every id goes straight to its place in the shared
 // memory of the CTA that owns it (the last pass writes to global memory). One launch;
 // 65536 ids took 39 us in the four launches of a sort in global memory. More ids are
@@ -122,31 +122,12 @@ __global__ void __launch_bounds__(kSortThreads)
     }
 }
 
-static cudaError_t sort_in_cluster(SortParams& p, cudaStream_t s) {
-    // 512 ids a CTA, one for each thread, up to 8 CTAs, and 1024 before there are 16, whose barriers
-    // cost more: with the sums of 8 columns 2048 ids 12.7 us, 16.0 by one CTA; 4096 ids 13.3, 16.6
-    // by two; 8192 ids 16.2, 17.0 by 16 CTAs, 18.3 by four; 16383 ids 18.9, 20.1 by 8.
-    p.cluster = 1;
-    while (p.cluster < kSortMaxCluster && p.n > (int64_t)p.cluster * (p.cluster < 8 ? 512 : 1024))
-        p.cluster *= 2;
+static cudaError_t sort_in_cluster(SortParams& p, int ctas, cudaStream_t s) {
+    p.cluster = ctas;
     const int64_t per = (p.n + p.cluster - 1) / p.cluster;
     p.share = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
     p.owner = fast_div((uint32_t)p.share);
     const int smem = cluster_bytes(p.share, p.passes);
-    // the function's limits belong to a context: raised once in each, by each thread
-    static thread_local unsigned long long prepared = 0;
-    unsigned long long ctx = 0;
-    cudaError_t err = current_context_id(&ctx);
-    if (err == cudaSuccess)
-        err = once_in_context(ctx, prepared, [] {
-            const cudaError_t e =
-                cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     cluster_bytes(kSortMaxShare, 2));
-            if (e != cudaSuccess) return e;
-            return cudaFuncSetAttribute(embed_sort_kernel,
-                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        });
-    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.cluster, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
@@ -183,10 +164,38 @@ static cudaError_t sort_in_memory(const SortParams& p, cudaStream_t s) {
     return cudaSuccess;
 }
 
+// The largest cluster of the sort that the GPU places, with all the shared memory a CTA may need.
+static cudaError_t sort_most(int* most) {
+    static thread_local unsigned long long prepared = 0;
+    static thread_local int found = 1;
+    unsigned long long ctx = 0;
+    const cudaError_t err = current_context_id(&ctx);
+    if (err != cudaSuccess) return err;
+    const cudaError_t set = once_in_context(ctx, prepared, [] {
+        constexpr int smem = cluster_bytes(kSortMaxShare, 2);
+        cudaError_t e = cudaFuncSetAttribute(
+            embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(embed_sort_kernel,
+                                     cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess)
+            found = placeable_cluster(kSortMaxCluster, [](int c) {
+                return resident_clusters((const void*)embed_sort_kernel, c, kSortThreads, smem);
+            });
+        return e;
+    });
+    *most = found;
+    return set;
+}
+
 cudaError_t embed_sort_launch(SortParams p, cudaStream_t s) {
     p.passes = sort_passes(p.vocab);
     p.bits = (sort_key_bits(p.vocab) + p.passes - 1) / p.passes;
-    return p.n <= kSortClusterMax ? sort_in_cluster(p, s) : sort_in_memory(p, s);
+    int most = 1;
+    const cudaError_t err = sort_most(&most);
+    if (err != cudaSuccess) return err;
+    const int ctas = sort_cluster(p.n, most);
+    return ctas > 0 ? sort_in_cluster(p, ctas, s) : sort_in_memory(p, s);
 }
 
 }  // namespace rn

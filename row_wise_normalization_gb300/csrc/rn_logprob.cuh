@@ -65,11 +65,8 @@
 
 namespace rn {
 
-constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpU = 4;              // vectors a thread holds of a batch
 constexpr int kLpStages = 2;         // batches a thread has under way
-constexpr int kLpMaxCluster = 16;
 constexpr int kTopCap = 64;          // candidates a warp holds unsorted: 31 and 32 more
 constexpr int kTopGroups = 64;
 constexpr float kRef = 16777216.f;  // references stay within 2^24: their rounding is below 1
@@ -642,15 +639,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_fwd_kernel(const Logpro
     }
 }
 
-// CTAs a row is split over: as many as keep every SM at its four resident CTAs, while
-// each still has a whole batch of its threads to read. A power of two.
-inline int logprob_split(int64_t rows, int vocab, int vec, int sms) {
-    const int64_t batches = (vocab / vec + kLpThreads * kLpU - 1) / (kLpThreads * kLpU);
-    int c = 1;
-    while (c < kLpMaxCluster && rows * c * 2 <= 4 * (int64_t)sms && c * 2 <= batches) c *= 2;
-    return c;
-}
-
 template <typename T, bool ENT, bool TOP>
 static cudaError_t logprob_fwd_go(const LogprobParams& q, cudaStream_t s) {
     LogprobParams p = q;
@@ -660,18 +648,26 @@ static cudaError_t logprob_fwd_go(const LogprobParams& q, cudaStream_t s) {
     if (err == cudaSuccess)
         err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    p.split = logprob_split(p.rows, p.vocab, Elem<T>::kVec, sms);
-    if (p.split > 8) {
-        // clusters of more than 8 CTAs have to be asked for: once in each context, by each thread
+    p.split = logprob_split(p.rows, p.vocab, Elem<T>::kVec, sms, kLpMaxCluster);
+    if (p.split > 1) {
+        // clusters of more than 8 CTAs have to be asked for, and may not fit: once in each context,
+        // by each thread
         static thread_local unsigned long long prepared = 0;
+        static thread_local int most = 1;
         unsigned long long ctx = 0;
         err = current_context_id(&ctx);
         if (err == cudaSuccess)
             err = once_in_context(ctx, prepared, [&] {
-                return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                            1);
+                const cudaError_t e =
+                    cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                if (e == cudaSuccess)
+                    most = placeable_cluster(kLpMaxCluster, [&](int c) {
+                        return resident_clusters((const void*)kernel, c, kLpThreads, 0);
+                    });
+                return e;
             });
         if (err != cudaSuccess) return err;
+        p.split = logprob_split(p.rows, p.vocab, Elem<T>::kVec, sms, most);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.rows * p.split), 1, 1);

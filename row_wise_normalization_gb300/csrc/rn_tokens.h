@@ -41,6 +41,34 @@ inline cudaError_t once_in_context(unsigned long long ctx, unsigned long long& d
     return err;
 }
 
+// The largest cluster that the context's GPU can place, a power of two up to `most`: fits(c) says
+// how many clusters of c CTAs can be resident (cudaOccupancyMaxActiveClusters; a partition of a GPU
+// may have no 16 SMs side by side). 1 where nothing larger fits.
+template <typename Fits>
+inline int placeable_cluster(int most, Fits fits) {
+    while (most > 1 && fits(most) < 1) most /= 2;
+    return most;
+}
+inline int resident_clusters(const void* kernel, int ctas, int threads, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
 // out[i] = scale * table[tokens[i]], zeros where the id is outside [0, vocab).
 struct EmbedParams {
     const void* tokens;
@@ -66,13 +94,25 @@ constexpr int kSortBits = 9;                               // bits of a digit, a
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortMaxCluster = 16;
 constexpr int kSortMaxShare = 10240;   // ids of a CTA, sorting in shared memory
-constexpr int64_t kSortClusterMax = (int64_t)kSortMaxCluster * kSortMaxShare;
+// CTAs of the cluster that sorts n ids, where the GPU places up to `most` (a power of two): 0, more
+// ids than it holds, for the sort in global memory. 512 ids a CTA, one for each thread, up to 8
+// CTAs, and 1024 before there are 16, whose barriers cost more: with the sums of 8 columns 2048 ids
+// 12.7 us, 16.0 by one CTA; 4096 ids 13.3, 16.6 by two; 8192 ids 16.2, 17.0 by 16 CTAs, 18.3 by
+// four; 16383 ids 18.9, 20.1 by 8.
+constexpr int sort_cluster(int64_t n, int most) {
+    if (n > (int64_t)most * kSortMaxShare) return 0;
+    int c = 1;
+    while (c < most && n > (int64_t)c * (c < 8 ? 512 : 1024)) c *= 2;
+    return c;
+}
+// Whether some GPU (one that places no cluster at all) sorts n ids in global memory.
+constexpr bool sort_may_use_memory(int64_t n) { return sort_cluster(n, 1) == 0; }
 struct SortParams {
     const void* tokens;
     int64_t n, vocab;
-    uint32_t* key[2];     // [n] each: the result in [0]; [1] beyond kSortClusterMax only
+    uint32_t* key[2];     // [n] each: the result in [0]; [1] where sort_may_use_memory only
     int32_t* pos[2];
-    uint32_t* hist;       // [tiles][kSortBins], beyond kSortClusterMax
+    uint32_t* hist;       // [tiles][kSortBins], where sort_may_use_memory
     uint32_t* zeroed;     // a word that the sort clears for the kernels after it
     int tiles;
     int bits, passes;     // bits of a digit, digits
@@ -157,6 +197,17 @@ struct LogprobParams {
     int split;              // CTAs of a row
     float scale;
 };
+constexpr int kLpThreads = 256;
+constexpr int kLpU = 4;              // vectors a thread holds of a batch
+constexpr int kLpMaxCluster = 16;
+// CTAs a row is split over: as many as keep every SM at its four resident CTAs, while each still
+// has a whole batch of its threads to read. A power of two up to `most`, what the GPU places.
+constexpr int logprob_split(int64_t rows, int vocab, int vec, int sms, int most) {
+    const int64_t batches = (vocab / vec + kLpThreads * kLpU - 1) / (kLpThreads * kLpU);
+    int c = 1;
+    while (c < most && rows * c * 2 <= 4 * (int64_t)sms && c * 2 <= batches) c *= 2;
+    return c;
+}
 cudaError_t logprob_fwd_launch(int dtype, const LogprobParams& p, cudaStream_t s);
 
 struct LogprobBwdParams {

@@ -124,7 +124,7 @@ EmbedWorkspace embed_workspace(int64_t n, int64_t d) {
     w.tiles = (n + kSortTile - 1) / kSortTile;
     w.chunks = (n + embed_chunk(n, d) - 1) / embed_chunk(n, d);
     w.dpad = (d + 7) / 8 * 8;
-    const bool global = n > kSortClusterMax;   // the sort's second arrays and its counts
+    const bool global = sort_may_use_memory(n);   // the sort's second arrays and its counts
     for (int k = 0; k < 2; ++k) {
         w.key[k] = take(k == 0 || global ? n * 4 : 0);
         w.pos[k] = take(k == 0 || global ? n * 4 : 0);

@@ -47,3 +47,44 @@ def test_a_failed_preparation_is_tried_again(tmp_path):
     printf("%d", calls);
     """)
     assert out.split() == ["1", "1", "1", "1", "1", "3", "4", "6"]
+
+
+def test_clusters_follow_what_the_gpu_places(tmp_path):
+    out = _run(tmp_path, r"""
+    // the largest power of two that fits, down to one CTA
+    for (int limit : {16, 15, 8, 5, 2, 1, 0})
+        printf("%d ", placeable_cluster(16, [&](int c) { return c <= limit ? 3 : 0; }));
+    // the sort: what each CTA holds, and the sort in global memory beyond that
+    bool ok = true;
+    for (int most = 1; most <= 16; most *= 2)
+        for (int64_t n = 1; n < 400000; n += n < 3000 ? 1 : 97) {
+            const int c = sort_cluster(n, most);
+            if (c == 0) {
+                ok = ok && n > (int64_t)most * kSortMaxShare && sort_may_use_memory(n);
+                continue;
+            }
+            const int64_t per = (n + c - 1) / c;
+            ok = ok && c <= most && (c & (c - 1)) == 0 &&
+                 (per + kSortThreads - 1) / kSortThreads * kSortThreads <= kSortMaxShare;
+        }
+    printf("%d ", ok);
+    printf("%d %d %d %d ", sort_cluster(163840, 16), sort_cluster(163841, 16),
+           sort_cluster(81920, 8), sort_cluster(81921, 8));
+    // a row's CTAs
+    printf("%d %d %d %d", logprob_split(1, 128000, 4, 152, 16), logprob_split(1, 128000, 4, 152, 8),
+           logprob_split(1, 128000, 4, 152, 1), logprob_split(700, 128000, 8, 152, 16));
+    """)
+    assert out.split() == ["16", "8", "8", "4", "2", "1", "1", "1", "16", "0", "8", "0",
+                           "16", "8", "1", "1"]
+
+
+@pytest.mark.parametrize("n", [10241, 16383, 163840, 163841])
+def test_workspace_holds_the_sort_in_memory(n):
+    """Whatever cluster a GPU places, the workspace of a call is one size."""
+    from row_wise_normalization_gb300 import capi
+
+    small = capi.embed_bwd_workspace_size(10240, 1000, 8)
+    assert small < 10240 * 8 + (10240 // 8) * (2 * 8 * 4 + 2) + 4096
+    # keys and positions twice, counts of 512 digits for each 4096 ids, sums of the chunks
+    chunks = -(-n // 32)
+    assert capi.embed_bwd_workspace_size(n, 1000, 8) >= 16 * n + -(-n // 4096) * 2048 + 64 * chunks
