@@ -344,7 +344,8 @@ enum { RN_INDEX_I32 = 0, RN_INDEX_I64 = 1 };
  *   out    [n][d]      row stride ldo >= d, of type `dtype`
  * The product is computed in FP32 and rounded once, to nearest even; scale must
  * be finite (RN_ERR_SCALE). vocab and d up to 2^30, n * (d / 512 + 1) up to 2^31 - 1.
- * One kernel launch. Rows of any alignment are written 16 bytes at a time.
+ * One kernel launch. Rows of any alignment are written 16 bytes at a time, their ends
+ * (fewer than 32 bytes each) by elements.
  */
 int embed_fwd(int dtype, int itype, const void *tokens, const void *table, int64_t ldt, void *out,
               int64_t ldo, int64_t n, int64_t vocab, int64_t d, float scale, void *stream);

@@ -69,10 +69,11 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_fwd_kernel(const EmbedPar
 
 // Rows at any phase (odd widths or strides, offset bases): 16-byte stores to the aligned part of
 // the output row, each from the two aligned 16-byte vectors of the table row that hold its
-// elements, shifted by the row's common phase. An aligned vector that holds one byte of the
-// row lies in the same allocation, so nothing out of reach is touched. A warp takes 128 vectors of
-// a row; the row's first warp also its unaligned head and tail. (One element an access, as
-// above with NE = 1, took 8.1 us for 4097 x 771 FP16.)
+// elements, shifted by the row's common phase. Nothing beside the row is read: where an end vector's
+// two would reach beyond it, its elements are copied one at a time with the row's unaligned head
+// and tail, by the row's first warp. A warp takes 128 vectors of a row. (4097 x 771 FP16 3.0 us,
+// one element an access throughout 8.1. With whole vectors at the row's ends, which read up to 14
+// bytes of what lies beside it, 65536 x 37 BF16 took 17.3 us, not 18.6; the wider ones gained nothing.)
 constexpr int kShiftVectors = 32 * kEmbedU;
 
 template <typename T>
@@ -85,13 +86,14 @@ __global__ void __launch_bounds__(kEmbedThreads)
     const uint32_t row = fast_quot(k, pieces), piece = k - row * pieces.d;
     if (row >= p.n) return;
     T* const O = (T*)p.out + row * p.ldo;
-    const int64_t head = head_peel_t(O, d), nv = (d - head) / VEC, tail = head + nv * VEC;
     pdl_wait();
     const int64_t id = ld_id(p.tokens, row, itype);
     const bool there = id >= 0 && id < p.vocab;
     const T* const S = (const T*)p.table + (there ? id : 0) * p.ldt;
+    const ShiftSpan span = shift_span((uintptr_t)O, (uintptr_t)S, d, (int)sizeof(T));
+    const int64_t head = span.head, nv = span.nv, tail = head + nv * VEC;
     // the phase of every vector's source
-    const uint32_t q = (uint32_t)(uintptr_t)(S + head) & 15u;
+    const uint32_t q = span.phase;
     const char* const A = (const char*)(S + head) - q;
     const int64_t v0 = (int64_t)piece * kShiftVectors + lane;
     Raw<16> a[kEmbedU], b[kEmbedU];
@@ -104,6 +106,11 @@ __global__ void __launch_bounds__(kEmbedThreads)
             if (q) b[u] = ld_raw<16>(A + v * 16 + 16);
         }
     }
+    // an element of the row's ends
+    const int64_t j = lane < head ? lane : tail + lane - head;
+    const bool ends = piece == 0 && j < d;
+    Raw<(int)sizeof(T)> e = {};
+    if (ends && there) e = ld_raw<(int)sizeof(T)>(S + j);
 #pragma unroll
     for (int u = 0; u < kEmbedU; ++u) {
         const int64_t v = v0 + u * 32;
@@ -129,11 +136,14 @@ __global__ void __launch_bounds__(kEmbedThreads)
             st_raw(O + head + v * VEC, r);
         }
     }
-    if (piece == 0 && lane < head + (d - tail)) {
-        const int64_t j = lane < head ? lane : tail + lane - head;
-        float x[1] = {0.f};
-        if (there) x[0] = ldt_x1(S + j) * p.scale;
-        st_elems<T, 1>(O + j, x);
+    if (ends) {
+        if (p.scale != 1.f) {
+            float x[1];
+            unpack<T, 1>(x, e);
+            x[0] = there ? x[0] * p.scale : 0.f;
+            e = pack<T, 1>(x);
+        }
+        st_raw(O + j, e);
     }
 }
 

@@ -84,6 +84,32 @@ struct EmbedParams {
 cudaError_t embed_fwd_launch(int dtype, int itype, int ne, int64_t d, const EmbedParams& p,
                              cudaStream_t s);
 
+// An output row of d elements of `es` bytes, written by aligned 16-byte vectors that are each
+// put together from the two aligned 16-byte vectors of the source row that hold their elements:
+// elements [head, head + nv * (16 / es)) are written so, the rest one at a time. A vector whose two
+// would reach beyond the source row is left to those: fewer than 4 * 16 / es of them, a warp's.
+struct ShiftSpan {
+    int64_t head, nv;
+    uint32_t phase;       // bytes from the source's aligned vector to the first vector's elements
+};
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+constexpr ShiftSpan shift_span(uintptr_t out, uintptr_t src, int64_t d, int es) {
+    const int64_t vec = 16 / es;
+    int64_t head = (int64_t)((0u - (uint32_t)out) & 15u) / es;
+    if (head > d) head = d;
+    int64_t nv = (d - head) / vec;
+    const uint32_t phase = ((uint32_t)src + (uint32_t)(head * es)) & 15u;
+    if (phase != 0 && nv > 0 && (int64_t)phase > head * es) {   // its first vector begins before the row
+        head += vec;
+        nv -= 1;
+    }
+    if (phase != 0 && nv > 0 && (int64_t)(16 - phase) > (d - head - nv * vec) * es)   // ends behind it
+        nv -= 1;
+    return {head, nv, phase};
+}
+
 // Stable sort of the n ids by value, with their positions. Ids outside
 // [0, vocab) are given the key `vocab`, so that they come last.
 constexpr int kSortThreads = 512;

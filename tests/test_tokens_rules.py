@@ -88,3 +88,31 @@ def test_workspace_holds_the_sort_in_memory(n):
     # keys and positions twice, counts of 512 digits for each 4096 ids, sums of the chunks
     chunks = -(-n // 32)
     assert capi.embed_bwd_workspace_size(n, 1000, 8) >= 16 * n + -(-n // 4096) * 2048 + 64 * chunks
+
+
+def test_realigned_rows_read_nothing_beside_the_row(tmp_path):
+    """Every phase of both rows: the aligned vectors that are read lie within the source row,
+    every element is written once, and what is left over is at most a warp's."""
+    out = _run(tmp_path, r"""
+    long bad = 0, rows = 0, vectors = 0;
+    for (int es = 2; es <= 4; es += 2)
+        for (int64_t d = 1; d <= 100; ++d)
+            for (uintptr_t o = 4096; o < 4112; o += es)
+                for (uintptr_t s = 8192; s < 8208; s += es) {
+                    const ShiftSpan p = shift_span(o, s, d, es);
+                    const int64_t vec = 16 / es, tail = p.head + p.nv * vec;
+                    const uintptr_t first = s + p.head * es - p.phase;
+                    const uintptr_t last = first + p.nv * 16 + (p.phase ? 16 : 0);
+                    ++rows;
+                    vectors += p.nv;
+                    bad += p.head < 0 || p.nv < 0 || tail > d || p.head + (d - tail) > 32;
+                    if (p.nv > 0) {
+                        bad += (o + p.head * es) % 16 != 0 || first % 16 != 0;
+                        bad += first < s || last > s + d * es;
+                    }
+                    // an end leaves at most one vector, and fewer elements than one, behind
+                    bad += p.head >= 2 * vec || d - tail >= 2 * vec;
+                }
+    printf("%ld %d", bad, rows > 0 && vectors > 0);
+    """)
+    assert out.split() == ["0", "1"]
