@@ -18,7 +18,18 @@ _FLOATS = {torch.float32: capi.RN_DTYPE_F32, torch.bfloat16: capi.RN_DTYPE_BF16,
            torch.float16: capi.RN_DTYPE_F16}
 _INDEX = {torch.int32: capi.RN_INDEX_I32, torch.int64: capi.RN_INDEX_I64}
 _F32 = torch.float32
-_C = capi.load()
+
+
+class _Unloaded:
+    """Loads the library at the first call, and stands aside."""
+
+    def __getattr__(self, name):
+        global _C
+        _C = capi.load()
+        return getattr(_C, name)
+
+
+_C = _Unloaded()
 
 
 def _values(name, t):
