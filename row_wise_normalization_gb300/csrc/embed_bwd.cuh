@@ -29,7 +29,7 @@ namespace rn {
 
 // The first zero_ctas CTAs clear the rows of absent ids, beside the sort: what they touch no kernel
 // of the call before touches, and the sort lets this kernel start only after its own wait, when
-// all work ahead of the call has completed.
+// all work ahead of the call has completed (the exception that rn_device.cuh names).
 template <typename T, typename G, int NE>
 __global__ void __launch_bounds__(kSegThreads, 4)
     embed_bwd_kernel(const SortParams z, const EmbedBwdParams p, int zero_ctas) {

@@ -41,6 +41,15 @@ namespace rn {
 // which every call overwrote the buffer the previous call read, and read the
 // one it wrote, returned stale values for about 1 % of the elements.
 // Prefetches after the wait are safe.
+// One exception to (2): the CTAs of embed_bwd_kernel that clear rows of absent ids do not wait.
+// The kernel ahead of theirs is always the sort of the same call, whose CTAs let
+// them be scheduled only after their own wait. What precedes the sort on the stream has then
+// completed, so nothing still reads or writes the gradient, and the sort touches neither the
+// gradient nor the ids' memory but to read it. PTX promises visibility only to a kernel that
+// waits, so their one kind of load, the ids, is a relaxed one at GPU scope, which an SM's L1 does
+// not answer. (Chains on GB300 in which the kernel ahead of the call wrote the ids, in the same
+// memory every time: no stale id in 68000.) A kernel put between the sort and embed_bwd_kernel,
+// or a sort that signals before its wait, would break this.
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
