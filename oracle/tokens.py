@@ -80,8 +80,9 @@ def logprob(logits, targets, scale, top=0):
 
 def logprob_backward(dlogp, dentropy, logits, targets, lse, entropy, scale):
     """(gradient, magnitude, factor): magnitude bounds each term of the sum that
-    makes an element, factor what a probability below 2^-104 is multiplied by in it. lse
-    None: log probabilities from the logits themselves."""
+    makes an element, factor what a probability below 2^-126 is multiplied by in it (its
+    logarithm taken as -104, that of FP32's last subnormal number). lse None: log
+    probabilities from the logits themselves."""
     x = scale * np.asarray(logits, np.float64)
     lq = None
     if lse is None:

