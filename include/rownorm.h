@@ -414,8 +414,8 @@ int logprob_fwd(int dtype, int itype, const void *logits, int64_t ldl, const voi
  *                           rounded once. May be logits itself (same pointer and
  *                           stride): the one exception to the aliasing rule.
  * A target outside [0, vocab) takes no part (its dlogp is ignored). A row whose
- * dlogp and dentropy are both zero or ignored, or whose lse is -inf, gets zeros (its
- * logits are not read). A row's probabilities are off by what FP32 leaves off its
+ * dlogp and dentropy are both zero or ignored gets zeros (its logits are not read),
+ * and so does one of nothing but -inf. A row's probabilities are off by what FP32 leaves off its
  * lse, 2^-24 |lse| at most; rows with |lse| >= 4096 have their sums taken again
  * from the logits. One kernel launch.
  */

@@ -15,7 +15,8 @@
 // gives, so log p_j is held above -128 and 0 * -inf cannot arise. lse is rounded to 24 bits, and
 // every p_j of a row is off by what that leaves off: half a step, 2^-24 |lse| at most, so 2^-13
 // just below 4096 (and below the half step of 16-bit gradients everywhere). Where |lse| >= 4096 (a
-// mask of the type's lowest value on every column, or logits far from zero) the first CTA of
+// mask of the type's lowest value on every column, times a scale above 1 beyond FP32's range even,
+// or logits far from zero; or nothing but -inf) the first CTA of
 // the row takes m and log S from the logits again and does the whole row, and the row's
 // other CTAs leave (2048 x 128000 BF16 of such rows 724 us, ordinary ones 151). Rows of logits and
 // gradient in different 16-byte phases are done an element an access: 2048 x 50001 BF16 at a stride
@@ -51,6 +52,7 @@ __device__ float2 row_sums(const T* X, int V, float scale) {
     float m = -INFINITY;
     for (int c = t; c < V; c += kLpbThreads) m = fmaxf(m, ldt_x1(X + c));
     m = meet(m, false);
+    if (m == -INFINITY) return make_float2(m, m);
     float s = 0.f;
     for (int c = t; c < V; c += kLpbThreads) s += ex2((ldt_x1(X + c) - m) * scale * kLog2e);
     return make_float2(m, logf(meet(s, true)));
@@ -75,10 +77,8 @@ __global__ void __launch_bounds__(kLpbThreads) logprob_bwd_kernel(const LogprobB
     float g = p.dlogp && id >= 0 ? ld_p1(p.dlogp + row) : 0.f;
     float h = p.dentropy ? ld_p1(p.dentropy + row) : 0.f;
     const float H = p.dentropy ? ld_p1(p.entropy + row) : 0.f;
-    // a row of -inf: no probability depends on a logit
-    if (lse == -INFINITY) g = h = 0.f;
+    const Raw<VEC * (int)sizeof(T)> z = {};
     if (g == 0.f && h == 0.f) {
-        const Raw<VEC * (int)sizeof(T)> z = {};
 #pragma unroll
         for (int u = 0; u < kLpbU; ++u) {
             const int v = v0 + u * kLpbThreads;
@@ -98,6 +98,14 @@ __global__ void __launch_bounds__(kLpbThreads) logprob_bwd_kernel(const LogprobB
     if (fabsf(lse) >= kLpbFar) {
         if (tile == 0) {
             const float2 ms = row_sums<T>(X, V, p.scale);
+            if (ms.x == -INFINITY) {   // nothing but -inf: no probability depends on a logit
+                for (int v = t; v < nv; v += kLpbThreads) st_raw(D + head + (int64_t)v * VEC, z);
+                if (t < head + (V - tail0)) {
+                    const float o[1] = {0.f};
+                    st_elems<T, 1>(D + (t < head ? t : tail0 + t - head), o);
+                }
+                return;
+            }
             for (int c = t; c < V; c += kLpbThreads) {
                 const float o[1] = {grad((ldt_x1(X + c) - ms.x) * p.scale - ms.y, c)};
                 st_elems<T, 1>(D + c, o);

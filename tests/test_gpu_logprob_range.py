@@ -130,3 +130,26 @@ def test_lse_far_from_zero(offset, scale, vocab):
     err = np.abs(f64(lse) - want)
     assert np.all(err <= off), (err.max(), off.min())
     _check_gradient(x, t, scale, lse, ent, "f32", 1.0, off)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [1.0, 1.25, 64.0, 2.0 ** 30])
+@pytest.mark.parametrize("vocab,pad", [(7, 0), (700, 0), (5003, 5)])
+def test_rows_of_masks_alone(dtype, scale, vocab, pad):
+    """Nothing but a mask's lowest value: its columns share the row, although lse may be beyond
+    FP32. Nothing but -inf: no gradient."""
+    low = torch.finfo(DT[dtype]).min
+    x = torch.full((4, vocab + pad), low, dtype=DT[dtype], device="cuda")[:, :vocab]
+    x[1, ::2] = float("-inf")
+    x[2] = float("-inf")
+    x[3, 3:] = 0.25
+    t = torch.tensor([1, 3, 0, 2], device="cuda")
+    ent, lse = _check(x, t, scale, 3)
+    assert ent[2] == 0 and lse[2] == -np.inf
+    u = token_checks.U
+    off = u * (vocab / 256 + 13 + token_checks.depth(vocab) + 16 + np.abs(0.25 * scale)
+               * (0.25 * scale < 4096))
+    if dtype != "f16" or scale < 100:
+        _check_gradient(x, t, scale, lse, ent, dtype, 2.0 ** -8, np.full(4, off))
+        d = rn.logprob_bwd(torch.ones(4, device="cuda"), x, t, lse, scale, dlogits=x.clone())
+        assert not bool(d[2].any()) and bool(d[0].any())
