@@ -18,7 +18,7 @@
 // mask of the type's lowest value on every column, times a scale above 1 beyond FP32's range even,
 // or logits far from zero; or nothing but -inf) the first CTA of
 // the row takes m and log S from the logits again and does the whole row, and the row's
-// other CTAs leave (2048 x 128000 BF16 of such rows 724 us, ordinary ones 151). Rows of logits and
+// other CTAs leave (2048 x 128000 BF16 of such rows 690 us, of nothing but -inf 166, ordinary ones 151). Rows of logits and
 // gradient in different 16-byte phases are done an element an access: 2048 x 50001 BF16 at a stride
 // of 50048 into a contiguous gradient 139 us, into one of the same stride 61. dlogits may be logits itself: a thread writes only what it, or its CTA, has
 // read.
@@ -32,7 +32,7 @@ constexpr float kLpbFar = 4096.f;
 
 // (m, log S) of a row: its largest logit, and the logarithm of the sum of
 // e^{scale (x_j - m)}. All threads of the CTA.
-template <typename T>
+template <typename T, int VEC>
 __device__ float2 row_sums(const T* X, int V, float scale) {
     __shared__ float red[kLpbThreads / 32];
     const int t = threadIdx.x;
@@ -50,7 +50,23 @@ __device__ float2 row_sums(const T* X, int V, float scale) {
         return v;
     };
     float m = -INFINITY;
-    for (int c = t; c < V; c += kLpbThreads) m = fmaxf(m, ldt_x1(X + c));
+    const int head = VEC > 1 ? head_peel_t(X, V) : 0, nv = (V - head) / VEC, tail0 = head + nv * VEC;
+    constexpr int U = 2;   // (8 CTAs of ordinary rows an SM leave registers for no more)
+    for (int v = t; v < nv; v += kLpbThreads * U) {
+        Raw<VEC * (int)sizeof(T)> r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)   // (past the end: the first again)
+            r[u] = ld_raw<VEC * (int)sizeof(T)>(
+                X + head + (int64_t)(v + u * kLpbThreads < nv ? v + u * kLpbThreads : v) * VEC);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[VEC];
+            unpack<T, VEC>(x, r[u]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) m = fmaxf(m, x[i]);
+        }
+    }
+    if (t < head + (V - tail0)) m = fmaxf(m, ldt_x1(X + (t < head ? t : tail0 + t - head)));
     m = meet(m, false);
     if (m == -INFINITY) return make_float2(m, m);
     float s = 0.f;
@@ -59,7 +75,7 @@ __device__ float2 row_sums(const T* X, int V, float scale) {
 }
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kLpbThreads) logprob_bwd_kernel(const LogprobBwdParams p) {
+__global__ void __launch_bounds__(kLpbThreads, 8) logprob_bwd_kernel(const LogprobBwdParams p) {
     pdl_launch_dependents();
     const int t = threadIdx.x, V = p.vocab;
     const uint32_t row = fast_quot(blockIdx.x, p.tiles);
@@ -97,7 +113,7 @@ __global__ void __launch_bounds__(kLpbThreads) logprob_bwd_kernel(const LogprobB
     };
     if (fabsf(lse) >= kLpbFar) {
         if (tile == 0) {
-            const float2 ms = row_sums<T>(X, V, p.scale);
+            const float2 ms = row_sums<T, VEC>(X, V, p.scale);
             if (ms.x == -INFINITY) {   // nothing but -inf: no probability depends on a logit
                 for (int v = t; v < nv; v += kLpbThreads) st_raw(D + head + (int64_t)v * VEC, z);
                 if (t < head + (V - tail0)) {
