@@ -383,7 +383,7 @@ int embed_bwd(int dtype, int gtype, int itype, const void *dout, int64_t lddo, c
  *   logp     [rows]       x_t - lse for the row's target t; 0 where t is outside
  *                         [0, vocab) (a padded row). Needs targets.
  *   entropy  [rows]       H = -sum_j p_j log p_j, p_j = e^{x_j - lse}
- *   lse      [rows]
+ *   lse      [rows]       (infinite where FP32 cannot hold it)
  *   top_ids, top_logp     [rows][top]: the `top` (0 .. RN_LOGPROB_MAX_TOP, at
  *                         most vocab) largest logits' columns (of type `itype`)
  *                         and log probabilities, largest first, equal logits by
@@ -395,8 +395,9 @@ int embed_bwd(int dtype, int gtype, int itype, const void *dout, int64_t lddo, c
  * Logits of -inf (masked columns) have probability zero; a row of nothing else
  * gives lse = logp = -inf and entropy 0. A row that holds a NaN or a +inf gives
  * NaN for all its values (its top_ids count NaN as the largest). All
- * arithmetic and sums are FP32, over one read of the logits. vocab up to 2^30,
- * rows up to 2^31 - 1.
+ * arithmetic and sums are FP32, over one read of the logits; rows whose largest
+ * x_j is beyond 10^7 or so, and all rows at a scale outside 10^-20 .. 5 * 10^7, are
+ * read once more. vocab up to 2^30, rows up to 2^31 - 1.
  * One kernel launch.
  */
 #define RN_LOGPROB_MAX_TOP 32
