@@ -12,16 +12,17 @@
 // 4.2 GB (1373 us with scalar arithmetic and a comparison an element).
 // Rows with g = h = 0 (padding) are written as zeros without being read. p_j = 0
 // makes both terms zero: e^-128 is below the smallest FP32 number the exponential
-// gives, so log p_j is held above -128 and 0 * -inf cannot arise. lse is rounded to 24 bits, and
-// every p_j of a row is off by what that leaves off: half a step, 2^-24 |lse| at most, so 2^-13
-// just below 4096 (and below the half step of 16-bit gradients everywhere). Where |lse| >= 4096 (a
-// mask of the type's lowest value on every column, times a scale above 1 beyond FP32's range even,
-// or logits far from zero; or nothing but -inf) the first CTA of
-// the row takes m and log S from the logits again and does the whole row, and the row's
-// other CTAs leave (2048 x 128000 BF16 of such rows 690 us, of nothing but -inf 166, ordinary ones 151). Rows of logits and
-// gradient in different 16-byte phases are done an element an access: 2048 x 50001 BF16 at a stride
-// of 50048 into a contiguous gradient 139 us, into one of the same stride 61. dlogits may be logits itself: a thread writes only what it, or its CTA, has
-// read.
+// gives, so log p_j is held above -128 and 0 * -inf cannot arise. dlogits may be logits itself: a
+// thread writes only what it, or its CTA, has read.
+//
+// lse is rounded to 24 bits, and every p_j of a row is off by what that leaves off: half a step,
+// 2^-24 |lse| at most, so 2^-13 just below 4096 (and below the half step of 16-bit gradients
+// everywhere). Where |lse| >= 4096 (logits far from zero; a mask of the type's lowest value on every
+// column, beyond FP32's range even at a scale above 1; or nothing but -inf) the first CTA of the
+// row takes m and log S from the logits again and does the whole row, and the row's other CTAs
+// leave: 2048 x 128000 BF16 of such rows 690 us, of nothing but -inf 166, ordinary ones 151.
+// Rows of logits and gradient in different 16-byte phases are done an element an access: 2048 x
+// 50001 BF16 at a stride of 50048 into a contiguous gradient 139 us, into one of that stride 61.
 #include "rn_tokens.cuh"
 
 namespace rn {
