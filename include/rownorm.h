@@ -108,7 +108,9 @@ typedef enum rn_status {
 enum {
     RN_DTYPE_F32 = 0,
     RN_DTYPE_BF16 = 1,   /* bfloat16: 8 exponent bits, 7 stored mantissa bits */
-    RN_DTYPE_F16 = 2     /* IEEE binary16                                      */
+    RN_DTYPE_F16 = 2,    /* IEEE binary16                                      */
+    RN_DTYPE_E4M3 = 3    /* 8 bits: 4 exponent, 3 stored mantissa bits, largest
+                            value 448, no infinities (paged caches only)       */
 };
 
 /*
@@ -424,6 +426,125 @@ int logprob_bwd(int dtype, int itype, const float *dlogp, const float *dentropy,
                 const void *logits, int64_t ldl, const void *targets, const float *lse,
                 const float *entropy, void *dlogits, int64_t ldd, int64_t rows, int64_t vocab,
                 float scale, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Head operators: between a network's projections and its attention. A row is one
+ * head of one token, d values (d even, up to RN_MAX_HEAD_DIM); tokens are counted
+ * through the batch, batch * len of them. What is said above of memory, streams,
+ * errors, aliasing, ids and threads holds for them (programmatic launches included).
+ * ------------------------------------------------------------------------ */
+#define RN_MAX_HEAD_DIM 512
+#define RN_MAX_HEADS 65535
+
+/* Rows of some heads: head h of token t of sequence b begins at
+ * data + b * batch_stride + t * token_stride + h * head_stride (elements, >= 0) and is
+ * contiguous. Column blocks of a packed projection and head-major layouts are such;
+ * what lies between rows is neither read nor written, so that outputs may be disjoint
+ * blocks of one matrix. Inputs may repeat rows (strides of 0); outputs may not
+ * (RN_ERR_ALIAS). heads == 0: none (data may be NULL). */
+typedef struct rn_heads {
+    void *data;
+    int64_t heads;
+    int64_t batch_stride, token_stride, head_stride;
+} rn_heads;
+
+/* Queries and keys, and what is done to their rows.
+ * norm != 0: n_j = x_j r w_j with r = (mean_j x_j^2 + eps)^(-1/2), w = wq [d] for queries
+ *   and wk [d] for keys, of the rows' type (NULL: ones); else n = x.
+ * rot (even, 0 .. d): the first rot values of n are turned. With c, s the cosine and sine
+ *   of pair i, row positions_t of table [table_rows][table_stride]: rot / 2 cosines,
+ *   then rot / 2 sines, FP32:
+ *     y_a = n_a c - n_b s,  y_b = n_b c + n_a s
+ *   a = i, b = i + rot / 2 or, with interleaved != 0, a = 2i, b = 2i + 1. The others pass.
+ *   A token whose position is outside [0, table_rows) has rows of zeros (padding).
+ *   rot == 0: table and positions are not read.
+ * All arithmetic is FP32 (squares beyond its range give r = 0, as in rms_fwd); each value
+ * is rounded once. */
+typedef struct rn_qk {
+    rn_heads q, k;
+    const void *wq, *wk;
+    const void *positions;       /* [batch * len], of type itype */
+    const float *table;
+    int64_t table_rows, table_stride, rot;
+    int64_t batch, len, d;
+    int32_t dtype, itype, norm, interleaved;
+    float eps;                   /* finite, >= 0 with norm (RN_ERR_EPS) */
+    int32_t reserved;            /* 0 */
+} rn_qk;
+
+/* Queries and keys normed and rotated: q_out, k_out of the inputs' heads and type. Each may
+ * be its input itself (same address and strides). One kernel launch. */
+int qk_rope_fwd(const rn_qk *in, const rn_heads *q_out, const rn_heads *k_out, void *stream);
+
+/*
+ * Gradient: with g the transposed rotation of what reaches q_out (dq_out) or k_out (dk_out),
+ *   dx_j = r (w_j g_j - x_j r^2 mean_k(w_k g_k x_k)),   dw_j = sum over rows g_j x_j r,
+ * or dx = g without norm (in->q.data, in->k.data may then be NULL). r is taken again from x.
+ *   dq, dk    of the inputs' heads; each may be dq_out / dk_out or q / k itself
+ *   dwq, dwk  [d], of the rows' type, each may be NULL; they need norm and their weights
+ *             (RN_ERR_NULL). Every token counts but those with positions outside the table.
+ * With dwq or dwk, `workspace` (16-byte aligned, caller-owned, contents ignored) must hold
+ * the bytes that qk_rope_bwd_workspace_size gives (RN_ERR_SIZE), and there are two launches; the sums are
+ * FP32 in an order that sizes, strides and addresses' alignment alone fix (no atomics), so
+ * results repeat bit for bit. Calls that may run at the same time need workspaces of their own.
+ * batch * len == 0 gives dwq and dwk of zeros.
+ */
+int qk_rope_bwd_workspace_size(int64_t d, size_t *bytes);
+int qk_rope_bwd(const rn_qk *in, const rn_heads *dq_out, const rn_heads *dk_out,
+                const rn_heads *dq, const rn_heads *dk, void *dwq, void *dwk, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+/* A paged cache: token i of page g has its key of head h at
+ * k + g * k_page_stride + i * k_slot_stride + h * k_head_stride, d contiguous elements, and
+ * its value likewise with d_v. Its slot is g * page_size + i. pages * page_size up to
+ * 2^31 - 1. k and v may be disjoint blocks of one tensor. With dtype RN_DTYPE_E4M3 a value y
+ * is held as y / scale, rounded to nearest even, at most 448 in size; scales are finite
+ * and > 0 (RN_ERR_SCALE), and 1 for the other types. */
+typedef struct rn_cache {
+    void *k, *v;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+    int64_t pages, page_size, d_v;
+    int32_t dtype;               /* the rows' type, or RN_DTYPE_E4M3 */
+    float k_scale, v_scale;
+    int32_t reserved;            /* 0 */
+} rn_cache;
+
+/*
+ * Appends to a cache: the keys, normed and rotated as in qk_rope_fwd, and the values v (as many
+ * heads, d_v wide, as they are) of each token into its slot, slots [batch * len] of type itype;
+ * and, in the same launch, the queries (in->q, if it has heads) to q_out. Tokens whose slot is
+ * outside [0, pages * page_size) leave the cache alone (their queries are still written); all
+ * other slots are left as they are. Slots must differ from one another: a slot given twice
+ * holds some mixture of its tokens' rows afterwards. One kernel launch.
+ */
+int kv_append(const rn_qk *in, const rn_heads *q_out, const rn_heads *v, const rn_cache *cache,
+              const void *slots, void *stream);
+
+/*
+ * Rows of slots out of a cache: k_out[t] and v_out[t] (heads and token strides as given; batch
+ * strides are not used) are those of slots_t, zeros where it is outside the cache; slots may
+ * repeat. dtype: the cache's, or any of the three for an 8-bit cache, whose values are multiplied
+ * by their scale in FP32 and rounded once. n up to 2^31 - 1. One kernel launch.
+ */
+int kv_gather(const rn_cache *cache, int64_t d, const void *slots, int itype, int64_t n,
+              int dtype, const rn_heads *k_out, const rn_heads *v_out, void *stream);
+
+/*
+ * Slots of a ragged batch: tokens offsets_b <= t < offsets_{b+1} belong to sequence b, whose first
+ * new token has position starts_b and whose pages page_table[b][0 .. width) (row stride
+ * ld >= width) are. For each of the n tokens
+ *   positions_t = starts_b + t - offsets_b
+ *   slots_t     = page_table[b][positions_t / page_size] * page_size + positions_t % page_size
+ * Tokens of no sequence (behind the last, before the first) get -1 for both, as do those whose position is
+ * negative or beyond 2^31 - 1; a position beyond the table's width, or a page that is
+ * negative or would end beyond slot 2^31 - 1, has slot -1. offsets must not fall. Sequences may be empty;
+ * seqs == 0 gives -1 throughout. All ids are of type itype; positions may be NULL.
+ * With starts of 0 it gives the slots of whole sequences, for kv_gather. One kernel launch.
+ */
+int kv_slots(int itype, const void *page_table, int64_t ld, int64_t width, const void *starts,
+             const void *offsets, int64_t seqs, int64_t page_size, void *slots, void *positions,
+             int64_t n, void *stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *rn_status_str(int status);

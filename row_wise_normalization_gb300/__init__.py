@@ -1,5 +1,7 @@
-"""Row-wise LayerNorm / RMSNorm on GB300 (sm_103a), and the token operators on
-either side of them (embedding rows, log probabilities).
+"""Row-wise LayerNorm / RMSNorm on GB300 (sm_103a), the token operators on
+either side of them (embedding rows, log probabilities), and the head operators
+between a network's projections and its attention (norms of queries and keys with
+the position rotation, the paged cache).
 
 A thin torch-facing binding over the C ABI of ``librownorm.so``
 (include/rownorm.h): it checks tensor shapes and dtypes, allocates outputs
@@ -14,7 +16,8 @@ from .capi import RowNormError, load  # noqa: F401
 
 __all__ = ["ln_fwd", "rms_fwd", "ln_fwd_residual", "rms_fwd_residual", "ln_fwd_batched",
            "rms_fwd_batched", "ln_bwd", "rms_bwd", "embed_fwd", "embed_bwd", "logprob_fwd",
-           "logprob_bwd", "capi", "RowNormError", "load"]
+           "logprob_bwd", "qk_rope_fwd", "qk_rope_bwd", "kv_slots", "kv_append", "kv_gather",
+           "capi", "RowNormError", "load"]
 
 
 def _stream_handle(t, stream):
@@ -344,11 +347,12 @@ def rms_bwd(dy, x, w, eps: float = 1e-5, *, dx=None, dw=None, param_grads: bool 
 
 
 
-_TOKENS = ("embed_fwd", "embed_bwd", "logprob_fwd", "logprob_bwd")
+_TOKENS = ("embed_fwd", "embed_bwd", "logprob_fwd", "logprob_bwd", "qk_rope_fwd", "qk_rope_bwd",
+           "kv_slots", "kv_append", "kv_gather")
 
 
 def __getattr__(name):
-    # the token operators, whose module imports torch
+    # the token and head operators, whose module imports torch
     if name in _TOKENS:
         from . import tokens
 

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librownorm.so")
 
@@ -40,11 +41,14 @@ RN_NOALLOC_MAX_D = 4096
 RN_DTYPE_F32 = 0
 RN_DTYPE_BF16 = 1
 RN_DTYPE_F16 = 2
+RN_DTYPE_E4M3 = 3   # paged caches only
 
 # type of ids (tokens, targets)
 RN_INDEX_I32 = 0
 RN_INDEX_I64 = 1
 RN_LOGPROB_MAX_TOP = 32
+RN_MAX_HEAD_DIM = 512
+RN_MAX_HEADS = 65535
 
 RN_VARIANT_AUTO = 0
 RN_VARIANT_WARP = 1
@@ -77,6 +81,15 @@ class rn_problem(ctypes.Structure):
                 ("y", ctypes.c_void_p), ("mean_out", ctypes.c_void_p),
                 ("rstd_out", ctypes.c_void_p), ("rows", ctypes.c_int64), ("d", ctypes.c_int64)]
 
+
+# Structs of the head operators, as packed bytes (one conversion a call in place of
+# one a field).
+heads = struct.Struct("Q4q").pack            # data, heads, batch, token and head strides
+# q, k (as `heads` packs them), wq, wk, positions, table, table_rows, table_stride, rot, batch,
+# len, d, dtype, itype, norm, interleaved, eps, 0
+qk = struct.Struct("40s40s4Q6q4ifi").pack
+# k, v, their page, slot and head strides, pages, page_size, d_v, dtype, scales, 0
+cache = struct.Struct("2Q6q3qi2fi").pack
 
 SIGNATURES = {
     "ln_fwd": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _F, _P]),
@@ -121,6 +134,12 @@ SIGNATURES = {
                            _P]),
     "logprob_bwd": (_INT, [_INT, _INT, _P, _P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _F,
                            _P]),
+    "qk_rope_fwd": (_INT, [_P, _P, _P, _P]),
+    "qk_rope_bwd_workspace_size": (_INT, [_I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "qk_rope_bwd": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "kv_append": (_INT, [_P, _P, _P, _P, _P, _P]),
+    "kv_gather": (_INT, [_P, _I64, _P, _INT, _I64, _INT, _P, _P, _P]),
+    "kv_slots": (_INT, [_INT, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _P]),
     "rn_pageable_host_access": (_INT, [ctypes.POINTER(_INT)]),
 }
 
@@ -360,3 +379,34 @@ def logprob_bwd(dtype, itype, dlogp, dentropy, logits, ldl, targets, lse, entrop
                 rows, vocab, scale, stream=0) -> int:
     return load().logprob_bwd(dtype, itype, dlogp, dentropy, logits, ldl, targets, lse, entropy,
                               dlogits, ldd, rows, vocab, scale, stream)
+
+
+def qk_rope_fwd(qk, q_out, k_out, stream=0) -> int:
+    """qk, q_out, k_out: packed structs (`qk`, `heads`)."""
+    return load().qk_rope_fwd(qk, q_out, k_out, stream)
+
+
+def qk_rope_bwd_workspace_size(d: int) -> int:
+    out = ctypes.c_size_t(0)
+    check(load().qk_rope_bwd_workspace_size(d, ctypes.byref(out)))
+    return out.value
+
+
+def qk_rope_bwd(qk, dq_out, dk_out, dq, dk, dwq, dwk, workspace, workspace_bytes,
+                stream=0) -> int:
+    return load().qk_rope_bwd(qk, dq_out, dk_out, dq, dk, dwq, dwk, workspace, workspace_bytes,
+                              stream)
+
+
+def kv_append(qk, q_out, v, cache, slots, stream=0) -> int:
+    return load().kv_append(qk, q_out, v, cache, slots, stream)
+
+
+def kv_gather(cache, d, slots, itype, n, dtype, k_out, v_out, stream=0) -> int:
+    return load().kv_gather(cache, d, slots, itype, n, dtype, k_out, v_out, stream)
+
+
+def kv_slots(itype, page_table, ld, width, starts, offsets, seqs, page_size, slots, positions, n,
+             stream=0) -> int:
+    return load().kv_slots(itype, page_table, ld, width, starts, offsets, seqs, page_size, slots,
+                           positions, n, stream)

@@ -1,0 +1,8 @@
+// heads_bwd_f32.cu -- the gradient of norms of queries and keys with the position rotation, f32 rows.
+#include "rn_heads.cuh"
+
+namespace rn {
+cudaError_t heads_bwd_f32(HeadShape sh, const HeadsParams& p, int ctas, cudaStream_t s) {
+    return heads_bwd_t<float>(sh, p, ctas, s);
+}
+}  // namespace rn

@@ -1,0 +1,9 @@
+// heads_fwd_f16.cu -- norms of queries and keys with the position rotation, f16 rows.
+#include "rn_heads.cuh"
+
+namespace rn {
+cudaError_t heads_fwd_f16(bool append, bool e4m3, HeadShape sh, const HeadsParams& p,
+                         cudaStream_t s) {
+    return heads_fwd_t<__half>(append, e4m3, sh, p, s);
+}
+}  // namespace rn

@@ -1,0 +1,111 @@
+// rn_heads.h -- kernel arguments of the head operators (norms of queries and
+// keys with the position rotation, their gradient, the paged cache of keys and
+// values), shared by the C-ABI unit and the kernel units.
+#pragma once
+
+#include "rn_tokens.h"
+
+namespace rn {
+
+constexpr int DT_E4M3 = 3;         // 8-bit floating point, caches only
+constexpr int64_t kMaxHeadDim = 512;
+constexpr int kHeadsThreads = 256;
+constexpr int kHeadsWarps = kHeadsThreads / 32;
+
+// Rows of one kind (queries, keys, values): one for each head of each token.
+struct HeadSeg {
+    const void* x;
+    const void* dy;            // the gradient's kernel: what reaches the rows' outputs
+    void* y;
+    const void* w;             // may be NULL: ones
+    int64_t xb, xt, xh;        // strides in elements: batch, token, head
+    int64_t gb, gt, gh;        // of dy
+    int64_t yb, yt, yh;        // of y; into a cache: page, slot, head
+    int heads;
+    int groups;                // warps' units that a token's rows take
+    FastDiv per;               // division by groups
+};
+
+// How a warp holds rows: lpr lanes each, every lane ch pairs of vectors of v elements.
+struct HeadShape {
+    int v, lpr, ch;
+};
+
+struct HeadsParams {
+    HeadSeg seg[3];            // queries, keys, values (append only)
+    FastDiv units;             // units of a token, over its segments
+    FastDiv len;               // tokens of a sequence of the batch
+    uint32_t total;            // units in all
+    int64_t tokens;
+    const void* positions;
+    const float* table;        // [table_rows][ldt]: rot / 2 cosines, rot / 2 sines
+    int64_t table_rows, ldt;
+    const void* slots;         // append
+    int64_t nslots;
+    FastDiv page;
+    float* part;               // gradient: [CTAs][2 d] sums for the weights, or NULL
+    float eps;
+    float store[3];            // factor of a row before it is stored
+    int d[3];                  // width of each segment's rows
+    int rot, itype;
+    bool norm, interleaved, back;   // back: the transposed rotation
+};
+
+// Pairs of vectors of v elements that fill a row of d, and the lanes that hold them.
+constexpr HeadShape head_shape(int v, int vec, int64_t d) {
+    const int64_t pairs = (d / 2 + v - 1) / v;
+    if (v == vec) {
+        int lpr = 4;
+        while (lpr < 32 && lpr < pairs) lpr *= 2;
+        return {v, lpr, pairs > 32 ? 2 : 1};
+    }
+    const int few = v == 2 ? 1 : 2, many = v == 2 ? 4 : 8;
+    return {v, 32, pairs > 32 * few ? many : few};
+}
+
+// Rows that a lane group takes of a unit: so many times 32 / lpr heads of a token.
+constexpr int heads_fwd_rows(int ch) { return ch > 2 ? 1 : 2; }
+constexpr int heads_bwd_rows(int ch) { return ch > 2 ? 1 : 2; }
+
+// cache_dtype: -1 without a cache.
+cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape shape, const HeadsParams& p,
+                             cudaStream_t s);
+// ctas: rows of p.part.
+cudaError_t heads_bwd_launch(int dtype, HeadShape shape, const HeadsParams& p, int ctas,
+                             cudaStream_t s);
+constexpr int kHeadsBwdCtas = 304;   // two a GB300's SM: rows of the gradient's workspace, at most
+
+struct SlotsParams {
+    const void* page_table;    // [seqs][ld]
+    const void* starts;        // [seqs]
+    const void* offsets;       // [seqs + 1]
+    void* slots;               // [n]
+    void* positions;           // [n], may be NULL
+    int64_t n, ld, width, pages;
+    int seqs;
+    int64_t page;
+    int itype;
+};
+cudaError_t kv_slots_launch(const SlotsParams& p, cudaStream_t s);
+
+struct GatherSide {
+    const void* cache;
+    void* out;
+    int64_t cp, cs, ch;        // page, slot, head strides of the cache
+    int64_t ot, oh;            // token, head strides of out
+    int64_t total;             // n * heads * vectors of a head's row
+    FastDiv token, head;       // vectors of a token, of a head
+    float scale;
+};
+struct GatherParams {
+    GatherSide side[2];
+    const void* slots;
+    int64_t nslots;
+    FastDiv page;
+    int itype;
+};
+// ne: elements of an access, one for both sides.
+cudaError_t kv_gather_launch(int cache_dtype, int dtype, int ne, const GatherParams& p,
+                             cudaStream_t s);
+
+}  // namespace rn

@@ -1,5 +1,7 @@
-"""The token operators: embedding rows and their gradient, log probabilities and
-their gradient (torch binding; the C entry points are in include/rownorm.h).
+"""The token operators (embedding rows and their gradient, log probabilities and their
+gradient) and the head operators (norms of queries and keys with the position rotation, their
+gradient, a paged cache of keys and values): torch binding; the C entry points are in
+include/rownorm.h.
 
 A decoding step waits for the host side of these calls, not for their kernels
 (a few microseconds each), so the checks take the common case (contiguous CUDA
@@ -18,6 +20,7 @@ _FLOATS = {torch.float32: capi.RN_DTYPE_F32, torch.bfloat16: capi.RN_DTYPE_BF16,
            torch.float16: capi.RN_DTYPE_F16}
 _INDEX = {torch.int32: capi.RN_INDEX_I32, torch.int64: capi.RN_INDEX_I64}
 _F32 = torch.float32
+_E4M3 = torch.float8_e4m3fn
 
 
 class _Unloaded:
@@ -319,3 +322,354 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
     if st:
         capi.check(st)
     return dlogits
+
+
+# ---------------------------------------------------------------------------
+# The head operators. Rows are heads of tokens: tensors of shape [tokens, heads, d] or
+# [batch, len, heads, d] with contiguous rows and any other strides (column blocks of a packed
+# projection, transposed head-major tensors).
+# ---------------------------------------------------------------------------
+_NONE = capi.heads(0, 0, 0, 0, 0)
+
+
+def _rows(name, t, lead, heads, d, dtype):
+    """Packed rn_heads of a tensor of rows; what is given of lead, heads, d, dtype has to be
+    so."""
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if shape[-2:] != (heads, d) or shape[:-2] != lead:
+        raise ValueError(f"{name} must be of shape {[*lead, heads, d]}, got {list(shape)}")
+    if not t.is_cuda or t.dtype is not dtype:
+        _check_f32_cuda(name, t, dtype, contiguous=False)
+    st = t.stride()
+    if st[-1] != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous rows")
+    if len(shape) == 3:
+        return capi.heads(t.data_ptr(), heads, 0, st[0], st[1])
+    return capi.heads(t.data_ptr(), heads, st[0], st[1], st[2])
+
+
+def _first(name, t):
+    """Storage code, leading shape, heads and width of the tensor that sets them."""
+    code = _values(name, t)
+    shape = t.shape
+    if len(shape) not in (3, 4):
+        raise ValueError(f"{name} must be [tokens, heads, d] or [batch, len, heads, d]")
+    return code, shape[:-2], shape[-2], shape[-1]
+
+
+def _weight(name, w, d, dtype):
+    if w is None:
+        return 0
+    if not (isinstance(w, torch.Tensor) and w.is_cuda and w.dtype is dtype and w.is_contiguous()):
+        _check_f32_cuda(name, w, dtype)
+    if w.numel() != d:
+        raise ValueError(f"{name} must have {d} elements")
+    return w.data_ptr()
+
+
+def _count(lead):
+    return lead[0] if len(lead) == 1 else lead[0] * lead[1]
+
+
+def _turn(positions, table, n):
+    """(address of positions, of table, rows, stride, rot, index code)."""
+    if table is None or table.shape[-1] == 0:
+        return 0, 0, 0, 0, 0, 0
+    if not (isinstance(table, torch.Tensor) and table.is_cuda and table.dtype is torch.float32):
+        _check_f32_cuda("table", table, torch.float32, contiguous=False)
+    if table.dim() != 2 or table.stride(1) != 1:
+        raise ValueError("table must be 2-D with contiguous rows")
+    it = _ids("positions", positions)
+    if positions.numel() != n:
+        raise ValueError(f"positions must have {n} elements")
+    rows, rot = table.shape
+    return (positions.data_ptr(), table.data_ptr(), rows, table.stride(0) if rows > 1 else rot,
+            rot, it)
+
+
+def qk_rope_fwd(q, k, positions=None, table=None, wq=None, wk=None, eps: float = 1e-5, *,
+                norm=None, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Queries and keys, each head normed (RMS) and turned by its token's position.
+
+    q, k: ``[tokens, heads, d]`` or ``[batch, len, heads, d]`` (float32, bfloat16 or
+    float16, one type; d even, at most 512); k may be None. table: float32 ``[positions,
+    rot]``, a row the cosines of rot / 2 angles, then their sines; the first ``rot`` values
+    of a row are turned, in pairs (i, i + rot / 2) or, with ``interleaved``, (2i, 2i + 1).
+    positions: int32 or int64, one a token; a token whose position is outside the table gets
+    rows of zeros. Without a table nothing is turned. wq, wk: ``[d]``, the norms' weights;
+    without ``norm`` rows are normed if one of them is given. Returns ``(q_out, k_out)``
+    (allocated contiguous unless given; each may be its input itself).
+    """
+    code, lead, hq, d = _first("q", q)
+    dtype = q.dtype
+    hk = 0
+    if k is not None:
+        hk = k.shape[-2] if k.dim() > 1 else -1
+    if norm is None:
+        norm = wq is not None or wk is not None
+    n = _count(lead)
+    pos, tab, trows, tstride, rot, it = _turn(positions, table, n)
+    dev = _device(q, k, positions, table, wq, wk, q_out, k_out)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return qk_rope_fwd(q, k, positions, table, wq, wk, eps, norm=norm,
+                               interleaved=interleaved, q_out=q_out, k_out=k_out)
+    a_q = _rows("q", q, lead, hq, d, dtype)
+    a_k = _rows("k", k, lead, hk, d, dtype) if k is not None else _NONE
+    if q_out is None:
+        q_out = _maker(q, dev)(q.shape, dtype=dtype)
+    a_qo = _rows("q_out", q_out, lead, hq, d, dtype)
+    a_ko = _NONE
+    if k is not None:
+        if k_out is None:
+            k_out = _maker(k, dev)(k.shape, dtype=dtype)
+        a_ko = _rows("k_out", k_out, lead, hk, d, dtype)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    st = _C.qk_rope_fwd(
+        capi.qk(a_q, a_k, _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype), pos, tab,
+                trows, tstride, rot, 1 if len(lead) == 1 else lead[0], lead[-1], d, code, it,
+                1 if norm else 0, 1 if interleaved else 0, eps, 0), a_qo, a_ko, _stream(dev))
+    if st:
+        capi.check(st)
+    return q_out, k_out
+
+
+def qk_rope_bwd(dq_out, dk_out, q, k, positions=None, table=None, wq=None, wk=None,
+                eps: float = 1e-5, *, norm=None, interleaved: bool = False,
+                param_grads: bool = True, dq=None, dk=None, dwq=None, dwk=None, workspace=None,
+                stream=None):
+    """Gradient of ``qk_rope_fwd``: dq_out and dk_out are what reaches its outputs, the other
+    arguments are as there (without a norm q and k may be None). Returns ``(dq, dk, dwq,
+    dwk)`` in the inputs' type, dk None without dk_out, dwq and dwk None without their weights
+    or without ``param_grads``. dq and dk may be passed in, dq_out and dk_out (or q and k)
+    themselves among them. ``workspace``: a contiguous CUDA tensor of at least
+    ``capi.qk_rope_bwd_workspace_size(d)`` bytes (allocated if not given).
+    """
+    code, lead, hq, d = _first("dq_out", dq_out)
+    dtype = dq_out.dtype
+    hk = 0
+    if dk_out is not None:
+        hk = dk_out.shape[-2] if dk_out.dim() > 1 else -1
+    if norm is None:
+        norm = wq is not None or wk is not None
+    n = _count(lead)
+    pos, tab, trows, tstride, rot, it = _turn(positions, table, n)
+    dev = _device(dq_out, dk_out, q, k, positions, table, wq, wk, dq, dk, dwq, dwk, workspace)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return qk_rope_bwd(dq_out, dk_out, q, k, positions, table, wq, wk, eps, norm=norm,
+                               interleaved=interleaved, param_grads=param_grads, dq=dq, dk=dk,
+                               dwq=dwq, dwk=dwk, workspace=workspace)
+    a_gq = _rows("dq_out", dq_out, lead, hq, d, dtype)
+    a_gk = _rows("dk_out", dk_out, lead, hk, d, dtype) if hk else _NONE
+    if norm:
+        a_q = _rows("q", q, lead, hq, d, dtype)
+        a_k = _rows("k", k, lead, hk, d, dtype) if hk else _NONE
+    else:
+        a_q, a_k = capi.heads(0, hq, 0, 0, 0), capi.heads(0, hk, 0, 0, 0)
+    if dq is None:
+        dq = _maker(dq_out, dev)(dq_out.shape, dtype=dtype)
+    a_dq = _rows("dq", dq, lead, hq, d, dtype)
+    a_dk = _NONE
+    if hk:
+        if dk is None:
+            dk = _maker(dk_out, dev)(dk_out.shape, dtype=dtype)
+        a_dk = _rows("dk", dk, lead, hk, d, dtype)
+    elif dk is not None:
+        raise ValueError("dk without dk_out")
+    a_wq, a_wk = _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype)
+    a_dwq = a_dwk = a_ws = nbytes = 0
+    if param_grads and norm:
+        if wq is not None:
+            if dwq is None:
+                dwq = _maker(dq_out, dev)((d,), dtype=dtype)
+            a_dwq = _weight("dwq", dwq, d, dtype)
+        if wk is not None:
+            if dwk is None:
+                dwk = _maker(dq_out, dev)((d,), dtype=dtype)
+            a_dwk = _weight("dwk", dwk, d, dtype)
+    if (dwq is not None and not a_dwq) or (dwk is not None and not a_dwk):
+        raise ValueError("dwq and dwk need param_grads, the norm and its weights")
+    if a_dwq or a_dwk:
+        if workspace is None:
+            nbytes = capi.qk_rope_bwd_workspace_size(d)
+            workspace = torch.empty(nbytes, dtype=torch.uint8,
+                                    device=dq_out.device if dq_out.is_cuda else "cuda")
+        else:
+            if not (workspace.is_cuda and workspace.is_contiguous()):
+                raise ValueError("workspace must be a contiguous CUDA tensor")
+            nbytes = workspace.numel() * workspace.element_size()
+        a_ws = workspace.data_ptr()
+    st = _C.qk_rope_bwd(
+        capi.qk(a_q, a_k, a_wq, a_wk, pos, tab, trows, tstride, rot,
+                1 if len(lead) == 1 else lead[0], lead[-1], d, code, it, 1 if norm else 0,
+                1 if interleaved else 0, eps, 0), a_gq, a_gk, a_dq, a_dk, a_dwq, a_dwk, a_ws,
+        nbytes, _stream(dev))
+    if st:
+        capi.check(st)
+    return dq, dk, dwq, dwk
+
+
+def _cache(k_cache, v_cache, dtype, k_scale, v_scale):
+    """Packed rn_cache of ``[pages, page_size, heads, d]`` tensors, heads, d, d_v."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != 4 or (t.stride(3) != 1 and t.numel()):
+            raise ValueError(f"{name} must be [pages, page_size, heads, d] with contiguous rows")
+    cdtype = k_cache.dtype
+    if cdtype is not _E4M3 and cdtype is not dtype:
+        raise TypeError(f"k_cache must be {dtype} or {_E4M3}, got {cdtype}")
+    if not (k_cache.is_cuda and v_cache.is_cuda and v_cache.dtype is cdtype):
+        _check_f32_cuda("k_cache", k_cache, cdtype, contiguous=False)
+        _check_f32_cuda("v_cache", v_cache, cdtype, contiguous=False)
+    pages, page, heads, d = k_cache.shape
+    if v_cache.shape[:3] != k_cache.shape[:3]:
+        raise ValueError("k_cache and v_cache must hold the same pages, tokens and heads")
+    dv = v_cache.shape[3]
+    sk, sv = k_cache.stride(), v_cache.stride()
+    return (capi.cache(k_cache.data_ptr(), v_cache.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1],
+                       sv[2], pages, page, dv, capi.RN_DTYPE_E4M3 if cdtype is _E4M3 else
+                       _FLOATS[cdtype], k_scale, v_scale, 0), heads, d, dv)
+
+
+def kv_append(k, v, slots, k_cache, v_cache, positions=None, table=None, wk=None,
+              eps: float = 1e-5, *, q=None, wq=None, norm=None, interleaved: bool = False,
+              k_scale: float = 1.0, v_scale: float = 1.0, q_out=None, stream=None):
+    """Appends keys and values to a paged cache, the keys normed and turned as by
+    ``qk_rope_fwd`` on the way; with ``q``, its queries too, in the same launch.
+
+    k, v (and q): ``[tokens, heads, d]`` or ``[batch, len, heads, d]``; v may have a width of
+    its own. slots: int32 or int64, one a token (of positions' type): page times page size
+    plus the token's place in its page, each at most once; a token whose slot is outside the
+    cache (-1: padding) is not stored. k_cache, v_cache: ``[pages, page_size, heads, d]`` with
+    contiguous rows and any other strides, of k's type or float8_e4m3fn; an 8-bit cache holds
+    values divided by k_scale and v_scale, at most 448 in size. Returns ``q_out`` (None
+    without q), which may be passed in, q itself among them.
+    """
+    code, lead, hk, d = _first("k", k)
+    dtype = k.dtype
+    if norm is None:
+        norm = wq is not None or wk is not None
+    n = _count(lead)
+    it = _ids("slots", slots)
+    if slots.numel() != n:
+        raise ValueError(f"slots must have {n} elements")
+    pos, tab, trows, tstride, rot, pit = _turn(positions, table, n)
+    if rot and pit != it:
+        raise TypeError(f"slots and positions must have one type, got {slots.dtype} and "
+                        f"{positions.dtype}")
+    dev = _device(k, v, slots, k_cache, v_cache, positions, table, wk, q, wq, q_out)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_append(k, v, slots, k_cache, v_cache, positions, table, wk, eps, q=q, wq=wq,
+                             norm=norm, interleaved=interleaved, k_scale=k_scale,
+                             v_scale=v_scale, q_out=q_out)
+    a_c, heads, dk, dv = _cache(k_cache, v_cache, dtype, k_scale, v_scale)
+    if (heads, dk) != (hk, d):
+        raise ValueError(f"k_cache holds {heads} heads of {dk}, k has {hk} of {d}")
+    a_k = _rows("k", k, lead, hk, d, dtype)
+    a_v = _rows("v", v, lead, hk, dv, dtype)
+    a_q = a_qo = _NONE
+    if q is not None:
+        hq = q.shape[-2] if q.dim() > 1 else -1
+        a_q = _rows("q", q, lead, hq, d, dtype)
+        if q_out is None:
+            q_out = _maker(q, dev)(q.shape, dtype=dtype)
+        a_qo = _rows("q_out", q_out, lead, hq, d, dtype)
+    elif q_out is not None or wq is not None:
+        raise ValueError("q_out and wq need q")
+    st = _C.kv_append(
+        capi.qk(a_q, a_k, _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype), pos, tab,
+                trows, tstride, rot, 1 if len(lead) == 1 else lead[0], lead[-1], d, code, it,
+                1 if norm else 0, 1 if interleaved else 0, eps, 0), a_qo, a_v, a_c,
+        slots.data_ptr(), _stream(dev))
+    if st:
+        capi.check(st)
+    return q_out
+
+
+def kv_gather(k_cache, v_cache, slots, *, dtype=None, k_scale: float = 1.0, v_scale: float = 1.0,
+              k_out=None, v_out=None, stream=None):
+    """The rows of ``slots`` (int32 or int64, any shape of them, repeats allowed) out of a
+    paged cache: ``(k, v)`` of shape ``[tokens, heads, d]``, rows of zeros where a slot is
+    outside the cache. An 8-bit cache's values are multiplied by their scales and come in
+    ``dtype`` (bfloat16 unless given); otherwise dtype is the cache's. k_out, v_out may be
+    passed in (contiguous rows, any other strides).
+    """
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    if dtype is None:
+        dtype = (k_out.dtype if k_out is not None else
+                 torch.bfloat16 if k_cache.dtype is _E4M3 else k_cache.dtype)
+    code = _FLOATS.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (float32, bfloat16 or float16)")
+    it = _ids("slots", slots)
+    n = slots.numel()
+    dev = _device(k_cache, v_cache, slots, k_out, v_out)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_gather(k_cache, v_cache, slots, dtype=dtype, k_scale=k_scale,
+                             v_scale=v_scale, k_out=k_out, v_out=v_out)
+    a_c, heads, d, dv = _cache(k_cache, v_cache, dtype, k_scale, v_scale)
+    if k_out is None:
+        k_out = _maker(k_cache, dev)((n, heads, d), dtype=dtype)
+    if v_out is None:
+        v_out = _maker(v_cache, dev)((n, heads, dv), dtype=dtype)
+    lead = (n,)
+    st = _C.kv_gather(a_c, d, slots.data_ptr(), it, n, code,
+                      _rows("k_out", k_out, lead, heads, d, dtype),
+                      _rows("v_out", v_out, lead, heads, dv, dtype), _stream(dev))
+    if st:
+        capi.check(st)
+    return k_out, v_out
+
+
+def kv_slots(page_table, starts, offsets, n: int, page_size: int, *, slots=None, positions=None,
+             stream=None):
+    """Slots and positions of the ``n`` tokens of a ragged batch: ``(slots, positions)``.
+
+    Tokens ``offsets[b] .. offsets[b + 1]`` belong to sequence b, whose first new token has
+    position ``starts[b]`` and whose pages are ``page_table[b]``; tokens of no sequence get -1.
+    page_table ``[sequences, width]`` (contiguous rows), starts ``[sequences]``, offsets
+    ``[sequences + 1]``: int32 or int64, one type, which is the outputs' too. The results are
+    what ``kv_append`` and ``qk_rope_fwd`` take for every layer of a step; with starts of 0,
+    what ``kv_gather`` takes for whole sequences.
+    """
+    if not isinstance(page_table, torch.Tensor):
+        raise TypeError("page_table must be a torch.Tensor")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be 2-D")
+    it = _ids("offsets", offsets)
+    dtype = offsets.dtype
+    seqs, width = page_table.shape
+    if not page_table.is_cuda or page_table.dtype is not dtype:
+        _check_f32_cuda("page_table", page_table, dtype, contiguous=False)
+    if width > 1 and seqs and page_table.stride(1) != 1:
+        raise ValueError("page_table must have contiguous rows")
+    if _ids("starts", starts) != it:
+        raise TypeError(f"starts must be {dtype}, got {starts.dtype}")
+    if starts.numel() != seqs or offsets.numel() != seqs + 1:
+        raise ValueError(f"starts must have {seqs} elements, offsets {seqs + 1}")
+    dev = _device(page_table, starts, offsets, slots, positions)
+    if _elsewhere(dev, stream):
+        with _On(dev, stream):
+            return kv_slots(page_table, starts, offsets, n, page_size, slots=slots,
+                            positions=positions)
+    if slots is None:
+        slots = _maker(offsets, dev)((n,), dtype=dtype)
+    if positions is None:
+        positions = _maker(offsets, dev)((n,), dtype=dtype)
+    for name, t in (("slots", slots), ("positions", positions)):
+        if _ids(name, t) != it or t.numel() != n:
+            raise ValueError(f"{name} must be {dtype} with {n} elements")
+    st = _C.kv_slots(it, page_table.data_ptr(), page_table.stride(0) if seqs > 1 else width, width,
+                     starts.data_ptr(), offsets.data_ptr(), seqs, page_size, slots.data_ptr(),
+                     positions.data_ptr(), n, _stream(dev))
+    if st:
+        capi.check(st)
+    return slots, positions
