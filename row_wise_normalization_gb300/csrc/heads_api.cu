@@ -135,8 +135,8 @@ bool row_suits(const rn_qk& in, int v, int es) {
     return !in.norm || (!misaligned(in.wq, v * es) && !misaligned(in.wk, v * es));
 }
 
-// The parameters that calls on queries and keys share; rows: heads that a unit's lane group takes.
-HeadsParams qk_params(const rn_qk& in, const HeadShape& sh, int rows) {
+// The parameters that calls on queries and keys share; per: heads of a unit.
+HeadsParams qk_params(const rn_qk& in, int per) {
     HeadsParams p = {};
     p.len = fast_div((uint32_t)in.len);
     p.tokens = in.batch * in.len;
@@ -162,13 +162,7 @@ HeadsParams qk_params(const rn_qk& in, const HeadShape& sh, int rows) {
         p.d[i] = (int)in.d;
         p.store[i] = 1.f;
     }
-    for (int i = 0; i < 3; ++i) p.seg[i].per = fast_div(1);
-    const int per = rows * (32 / sh.lpr);
-    for (int i = 0; i < 2; ++i) {
-        HeadSeg& g = p.seg[i];
-        g.groups = (g.heads + per - 1) / per;
-        if (g.groups > 0) g.per = fast_div((uint32_t)g.groups);
-    }
+    p.per = per;
     return p;
 }
 void set_y(HeadSeg& g, const rn_heads* h) {
@@ -178,12 +172,17 @@ void set_y(HeadSeg& g, const rn_heads* h) {
     g.yt = h->token_stride;
     g.yh = h->head_stride;
 }
-// Units of a token and in all; false where they are too many for one launch.
+// The units of every segment; false where they are too many for one launch.
 bool set_units(HeadsParams& p) {
-    const int64_t u = p.seg[0].groups + p.seg[1].groups + p.seg[2].groups;
-    if (u * p.tokens > kMaxCount) return false;
-    p.units = fast_div((uint32_t)u);
-    p.total = (uint32_t)(u * p.tokens);
+    int64_t total = 0;
+    for (HeadSeg& g : p.seg) {
+        const int64_t groups = (g.heads + p.per - 1) / p.per;
+        g.per = fast_div((uint32_t)(groups > 0 ? groups : 1));
+        total += groups * p.tokens;
+        if (total > kMaxCount) return false;
+        g.units = (uint32_t)(groups * p.tokens);
+    }
+    p.total = (uint32_t)total;
     return true;
 }
 
@@ -259,7 +258,7 @@ int qk_rope_fwd(const rn_qk* in, const rn_heads* q_out, const rn_heads* k_out, v
                suits(*k_out, batch, len, w, es);
     });
     const HeadShape sh = head_shape(v, vec, d);
-    HeadsParams p = qk_params(*in, sh, heads_fwd_rows(sh.ch));
+    HeadsParams p = qk_params(*in, heads_fwd_per(sh, in->q.heads + in->k.heads, batch * len));
     set_y(p.seg[0], q_out);
     set_y(p.seg[1], k_out);
     if (!set_units(p)) return RN_ERR_SIZE;
@@ -339,7 +338,8 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         at.q = *dq_out;
         at.k = *dk_out;
     }
-    HeadsParams p = qk_params(at, sh, plain ? heads_fwd_rows(sh.ch) : heads_bwd_rows(sh.ch));
+    HeadsParams p = qk_params(at, plain ? heads_fwd_per(sh, at.q.heads + at.k.heads, batch * len)
+                                     : heads_bwd_rows(sh.ch) * (32 / sh.lpr));
     set_y(p.seg[0], dq);
     set_y(p.seg[1], dk);
     p.back = true;
@@ -352,8 +352,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         p.seg[i].gb = g[i]->batch_stride;
         p.seg[i].gt = g[i]->token_stride;
         p.seg[i].gh = g[i]->head_stride;
-        const int64_t n = p.seg[i].groups * p.tokens;
-        if (n > units) units = n;
+        if (p.seg[i].units > units) units = p.seg[i].units;
     }
     p.part = params ? (float*)workspace : nullptr;
     const int64_t want = (units + kHeadsWarps - 1) / kHeadsWarps;
@@ -403,7 +402,7 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
                cache_suits(bk, e, cs) && cache_suits(bv, e, cs);
     });
     const HeadShape sh = head_shape(w, vec, d > cache->d_v ? d : cache->d_v);
-    HeadsParams p = qk_params(*in, sh, heads_fwd_rows(sh.ch));
+    HeadsParams p = qk_params(*in, heads_fwd_per(sh, in->q.heads + in->k.heads, batch * len));
     set_y(p.seg[0], q_out);
     HeadSeg& k = p.seg[1];
     k.y = cache->k;
@@ -420,7 +419,6 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
     g.yt = cache->v_slot_stride;
     g.yh = cache->v_head_stride;
     g.heads = (int)v->heads;
-    g.groups = k.groups;
     p.d[2] = (int)cache->d_v;
     p.store[1] = 1.f / cache->k_scale;
     p.store[2] = 1.f / cache->v_scale;

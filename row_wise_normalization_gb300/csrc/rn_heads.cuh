@@ -143,139 +143,268 @@ __device__ __forceinline__ void st_e4m3(uint8_t* p, const float* v) {
     }
 }
 
-// The unit of a warp: a token, a segment and its first head. False beyond the last unit.
+// The unit of a warp: a token, a segment and its first head. Units of one segment lie together, so
+// that the warps of a CTA take about the same time: token by token they left a CTA's place half
+// empty beside its last warps (queries of 64 heads beside keys of 8).
 struct HeadUnit {
-    int64_t token;
+    uint32_t token;
     int seg, head;
 };
-__device__ __forceinline__ HeadUnit head_unit(const HeadsParams& p, uint32_t unit, int rows) {
-    const uint32_t t = fast_quot(unit, p.units);
-    int g = (int)(unit - t * p.units.d), seg = 0;
-    if (g >= p.seg[0].groups) {
-        g -= p.seg[0].groups;
-        seg = 1;
-        if (g >= p.seg[1].groups) {
-            g -= p.seg[1].groups;
-            seg = 2;
-        }
+__device__ __forceinline__ HeadUnit head_unit(const HeadsParams& p, uint32_t unit) {
+    int seg = 0;
+    while (seg < 2 && unit >= p.seg[seg].units) {
+        unit -= p.seg[seg].units;
+        ++seg;
     }
-    return {(int64_t)t, seg, g * rows};
+    const uint32_t t = fast_quot(unit, p.seg[seg].per);
+    return {t, seg, (int)(unit - t * p.seg[seg].per.d) * p.per};
 }
 
-// APPEND: keys and values (segments 1 and 2) go into the cache, at the token's slot.
-template <typename T, int V, int LPR, int CH, int U, bool APPEND, bool E4M3>
-__global__ void __launch_bounds__(kHeadsThreads) heads_fwd_kernel(const HeadsParams p) {
-    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T);
+// A row's rotation and weights as two factors a value: y_j = r (x_j A_j + x_partner B_j), where the
+// partner is the other value of j's pair: A = w c, B = -+ w_partner s. They are a token's, so that a
+// row costs three packed products for two values. Values that are not turned have no second term.
+template <int V>
+struct Factors {
+    float a1[V], b1[V], a2[V], b2[V];      // of the first and the second vector
+};
+
+// Factors of a lane's pair of vectors, from weights w1, w2 and the table's cosines and sines.
+template <int V>
+__device__ __forceinline__ void set_factors(Factors<V>& f, const float (&w1)[V], const float (&w2)[V],
+                                            const float (&c)[V], const float (&s)[V],
+                                            bool interleaved) {
+    if (V == 1 || !interleaved) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            f.a1[i] = w1[i] * c[i];
+            f.b1[i] = -(w2[i] * s[i]);
+            f.a2[i] = w2[i] * c[i];
+            f.b2[i] = w1[i] * s[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            f.a1[2 * i] = w1[2 * i] * c[i];
+            f.b1[2 * i] = -(w1[2 * i + 1] * s[i]);
+            f.a1[2 * i + 1] = w1[2 * i + 1] * c[i];
+            f.b1[2 * i + 1] = w1[2 * i] * s[i];
+            f.a2[2 * i] = w2[2 * i] * c[V / 2 + i];
+            f.b2[2 * i] = -(w2[2 * i + 1] * s[V / 2 + i]);
+            f.a2[2 * i + 1] = w2[2 * i + 1] * c[V / 2 + i];
+            f.b2[2 * i + 1] = w2[2 * i] * s[V / 2 + i];
+        }
+    }
+}
+
+// x1, x2 := r (x A + partner B), or r x A where nothing is turned.
+template <int V>
+__device__ __forceinline__ void apply_factors(float (&x1)[V], float (&x2)[V], const Factors<V>& f,
+                                              float r, bool turned, bool interleaved) {
+    if constexpr (V == 1) {
+        const float t = x1[0];
+        x1[0] = r * (turned ? t * f.a1[0] + x2[0] * f.b1[0] : t * f.a1[0]);
+        x2[0] = r * (turned ? x2[0] * f.a2[0] + t * f.b2[0] : x2[0] * f.a2[0]);
+    } else {
+        const F2 r2 = f2s(r);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const F2 u = f2(x1[i], x1[i + 1]), v = f2(x2[i], x2[i + 1]);
+            F2 a = mul2(u, f2(f.a1[i], f.a1[i + 1])), b = mul2(v, f2(f.a2[i], f.a2[i + 1]));
+            if (turned) {
+                const F2 pu = interleaved ? f2(x1[i + 1], x1[i]) : v;
+                const F2 pv = interleaved ? f2(x2[i + 1], x2[i]) : u;
+                a = fma2(pu, f2(f.b1[i], f.b1[i + 1]), a);
+                b = fma2(pv, f2(f.b2[i], f.b2[i + 1]), b);
+            }
+            f2_get(mul2(a, r2), x1[i], x1[i + 1]);
+            f2_get(mul2(b, r2), x2[i], x2[i + 1]);
+        }
+    }
+}
+
+// A lane's share of a row's sum of squares.
+template <int V, int CH>
+__device__ __forceinline__ float squares(const float (&x1)[CH][V], const float (&x2)[CH][V]) {
+    if constexpr (V == 1) {
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) ss = fmaf(x1[k][0], x1[k][0], fmaf(x2[k][0], x2[k][0], ss));
+        return ss;
+    } else {
+        F2 t = f2s(0.f);
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const F2 u = f2(x1[k][i], x1[k][i + 1]), v = f2(x2[k][i], x2[k][i + 1]);
+                t = fma2(u, u, t);
+                t = fma2(v, v, t);
+            }
+        }
+        float lo, hi;
+        f2_get(t, lo, hi);
+        return lo + hi;
+    }
+}
+
+#ifndef RN_FWD_MINB
+#define RN_FWD_MINB 3
+#endif
+#ifndef RN_FWD_RING
+#define RN_FWD_RING 4
+#endif
+// Row groups that a warp copies ahead, where accesses are 16 bytes (asynchronous copies take no
+// fewer than 4, and narrow rows hold several chunks a lane): else one, in registers.
+template <int V, typename T>
+constexpr int heads_ring() {
+    return V == Elem<T>::kVec ? RN_FWD_RING : 1;
+}
+
+// APPEND: keys and values (segments 1 and 2) go into the cache, at the token's slot. A warp takes
+// p.per heads of its token, a row for each lane group at a time, with the next rows under way.
+template <typename T, int V, int LPR, int CH, bool APPEND, bool E4M3>
+__global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(const HeadsParams p) {
+    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<V, T>();
+    __shared__ uint4 ring[RING > 1 ? kHeadsWarps : 1][RING > 1 ? RING : 1][RING > 1 ? 2 * CH : 1][32];
     pdl_launch_dependents();
-    const uint32_t unit = blockIdx.x * kHeadsWarps + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5;
+    const uint32_t unit = blockIdx.x * kHeadsWarps + warp;
     if (unit >= p.total) return;
     const int lane = threadIdx.x & 31, l = lane % LPR, sg = lane / LPR;
-    const HeadUnit u0 = head_unit(p, unit, SG * U);
+    const HeadUnit u0 = head_unit(p, unit);
     const HeadSeg& S = p.seg[u0.seg];
     const bool value = APPEND && u0.seg == 2;
     const int d = p.d[u0.seg], rp = value ? 0 : p.rot / 2 / V;
-    const uint32_t b = fast_quot((uint32_t)u0.token, p.len);
-    const int64_t t = u0.token - (int64_t)b * p.len.d;
-    pdl_wait();
-    Raw<B> xa[U][CH], xb[U][CH];
-    const T* const X = (const T*)S.x + b * S.xb + t * S.xt;
+    const uint32_t b = fast_quot(u0.token, p.len), t = u0.token - b * p.len.d;
+    const int end = S.heads < u0.head + p.per ? S.heads : u0.head + p.per;
+    int lo[CH], hi[CH];
+    bool in[CH];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = u0.head + u * SG + sg;
+    for (int k = 0; k < CH; ++k) {
+        const int q = l + k * LPR;
+        in[k] = 2 * q * V < d;
+        pair_at<V>(q, rp, p.interleaved, lo[k], hi[k]);
+    }
+    int h = u0.head + sg;
+    const T* X = (const T*)S.x + b * S.xb + t * S.xt + h * S.xh;
+    // the next row of the lane group, whose first head is `first`: into the ring, or registers
+    Raw<B> n1[CH], n2[CH];
+    int ahead = u0.head, put = 0, get = 0;
+    auto load = [&]() {
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int q = l + k * LPR;
-            xa[u][k] = xb[u][k] = Raw<B>{};
-            if (h < S.heads && 2 * q * V < d) {
-                int lo, hi;
-                pair_at<V>(q, rp, p.interleaved, lo, hi);
-                xa[u][k] = ld_raw<B>(X + h * S.xh + lo);
-                xb[u][k] = ld_raw<B>(X + h * S.xh + hi);
+            const bool there = ahead + sg < end && in[k];
+            if constexpr (RING > 1) {
+                if (there) {
+                    copy_async(&ring[warp][put][2 * k][lane], X + lo[k]);
+                    copy_async(&ring[warp][put][2 * k + 1][lane], X + hi[k]);
+                }
+            } else {
+                n1[k] = n2[k] = Raw<B>{};
+                if (there) {
+                    n1[k] = ld_raw<B>(X + lo[k]);
+                    n2[k] = ld_raw<B>(X + hi[k]);
+                }
             }
         }
-    }
-    char* Y = (char*)S.y;
-    int64_t ybase = b * S.yb + t * S.yt;
+        if constexpr (RING > 1) {
+            copy_commit();
+            put = put + 1 == RING ? 0 : put + 1;
+        }
+        ahead += SG;
+        X += SG * S.xh;
+    };
+    pdl_wait();
+#pragma unroll
+    for (int k = 0; k < (RING > 1 ? RING - 1 : 1); ++k) load();
+    int64_t at = b * S.yb + t * S.yt + h * S.yh;
     if (APPEND && u0.seg > 0) {
         const int64_t slot = ld_id(p.slots, u0.token, p.itype);
-        if (slot < 0 || slot >= p.nslots) return;     // (the whole warp: one token)
+        if (slot < 0 || slot >= p.nslots) {     // (the whole warp: one token)
+            if constexpr (RING > 1) copy_wait<0>();
+            return;
+        }
         const uint32_t page = fast_quot((uint32_t)slot, p.page);
-        ybase = page * S.yb + (int64_t)((uint32_t)slot - page * p.page.d) * S.yt;
+        at = page * S.yb + (int64_t)((uint32_t)slot - page * p.page.d) * S.yt + h * S.yh;
     }
-    float c[CH][V], s[CH][V];
     bool there = true;
-    if (rp > 0) {
-        const int64_t pos = ld_id(p.positions, u0.token, p.itype);
-        there = pos >= 0 && pos < p.table_rows;
-        ld_turn<V, CH, LPR>(c, s, p.table + (there ? pos : 0) * p.ldt, l, rp, p.back);
-    }
-    float wa[CH][V], wb[CH][V];
     const bool norm = p.norm && !value;
-    if (norm) {
+    Factors<V> f[CH];
+    {
+        const float* row = nullptr;
+        if (rp > 0) {
+            const int64_t pos = ld_id(p.positions, u0.token, p.itype);
+            there = pos >= 0 && pos < p.table_rows;
+            row = p.table + (there ? pos : 0) * p.ldt;
+        }
+        float c[CH][V], s[CH][V];
+        ld_turn<V, CH, LPR>(c, s, row, l, rp, p.back);
+        const T* const w = norm ? (const T*)S.w : nullptr;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int q = l + k * LPR;
-            if (2 * q * V < d) {
-                int lo, hi;
-                pair_at<V>(q, rp, p.interleaved, lo, hi);
-                ld_weight<T, V>(wa[k], (const T*)S.w, lo);
-                ld_weight<T, V>(wb[k], (const T*)S.w, hi);
+            float w1[V] = {}, w2[V] = {};
+            if (in[k]) {
+                ld_weight<T, V>(w1, w, lo[k]);
+                ld_weight<T, V>(w2, w, hi[k]);
             }
+            set_factors<V>(f[k], w1, w2, c[k], s[k], p.interleaved);
         }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+    const float store = E4M3 && u0.seg > 0 ? p.store[u0.seg] : 1.f;
+    for (; h - sg < end; h += SG) {
         float a[CH][V], e[CH][V];
-        float ss = 0.f;
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-            unpack<T, V>(a[k], xa[u][k]);
-            unpack<T, V>(e[k], xb[u][k]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) ss = fmaf(a[k][i], a[k][i], fmaf(e[k][i], e[k][i], ss));
-        }
-        if (norm) {
-            const float r = rsqrtf(row_sum<LPR>(ss) / (float)d + p.eps);
+        if constexpr (RING > 1) {
+            load();
+            copy_wait<RING - 1>();
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    a[k][i] = a[k][i] * r * wa[k][i];
-                    e[k][i] = e[k][i] * r * wb[k][i];
+                if (h < end && in[k]) {       // (a lane reads what it copied itself)
+                    n1[k] = *reinterpret_cast<const Raw<B>*>(&ring[warp][get][2 * k][lane]);
+                    n2[k] = *reinterpret_cast<const Raw<B>*>(&ring[warp][get][2 * k + 1][lane]);
+                } else {
+                    n1[k] = n2[k] = Raw<B>{};
                 }
             }
+            get = get + 1 == RING ? 0 : get + 1;
         }
-        const int h = u0.head + u * SG + sg;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int q = l + k * LPR;
-            if (h < S.heads && 2 * q * V < d) {
-                int lo, hi;
-                pair_at<V>(q, rp, p.interleaved, lo, hi);
-                if (rp > 0) {
-                    turn<V>(a[k], e[k], c[k], s[k], p.interleaved);
-                    if (!there) {
+            unpack<T, V>(a[k], n1[k]);
+            unpack<T, V>(e[k], n2[k]);
+        }
+        if constexpr (RING == 1) load();
+        float r = 1.f;
+        if (norm) r = rsqrtf(row_sum<LPR>(squares<V, CH>(a, e)) / (float)d + p.eps);
+        if (h < end) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) a[k][i] = e[k][i] = 0.f;
-                    }
+            for (int k = 0; k < CH; ++k) {
+                if (!in[k]) continue;
+                const bool turned = l + k * LPR < rp;
+                if (p.interleaved)
+                    apply_factors<V>(a[k], e[k], f[k], r, turned, true);
+                else
+                    apply_factors<V>(a[k], e[k], f[k], r, turned, false);
+                if (!there) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) a[k][i] = e[k][i] = 0.f;
                 }
-                const int64_t at = ybase + h * S.yh;
                 if (E4M3 && u0.seg > 0) {
-                    const float f = p.store[u0.seg];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        a[k][i] *= f;
-                        e[k][i] *= f;
+                        a[k][i] *= store;
+                        e[k][i] *= store;
                     }
-                    st_e4m3<V>((uint8_t*)Y + at + lo, a[k]);
-                    st_e4m3<V>((uint8_t*)Y + at + hi, e[k]);
+                    st_e4m3<V>((uint8_t*)S.y + at + lo[k], a[k]);
+                    st_e4m3<V>((uint8_t*)S.y + at + hi[k], e[k]);
                 } else {
-                    st_elems<T, V>((T*)Y + at + lo, a[k]);
-                    st_elems<T, V>((T*)Y + at + hi, e[k]);
+                    st_elems<T, V>((T*)S.y + at + lo[k], a[k]);
+                    st_elems<T, V>((T*)S.y + at + hi[k], e[k]);
                 }
             }
         }
+        at += SG * S.yh;
     }
+    if constexpr (RING > 1) copy_wait<0>();
 }
 
 // The gradient. With g the transposed rotation of dy (sines negated) and r the row's, taken
@@ -310,7 +439,7 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
                 ld_weight<T, V>(wb[k], (const T*)S.w, hi[k]);
             }
         }
-        const uint32_t total = (uint32_t)(p.tokens * S.groups);
+        const uint32_t total = S.units;
         for (uint32_t unit = blockIdx.x * kHeadsWarps + warp; unit < total;
              unit += gridDim.x * kHeadsWarps) {
             const uint32_t token = fast_quot(unit, S.per);
@@ -440,8 +569,7 @@ struct FwdRun {
     cudaStream_t s;
     template <int V, int LPR, int CH>
     cudaError_t run() {
-        constexpr int U = heads_fwd_rows(CH);
-        return launch_pdl(heads_fwd_kernel<T, V, LPR, CH, U, APPEND, E4M3>,
+        return launch_pdl(heads_fwd_kernel<T, V, LPR, CH, APPEND, E4M3>,
                           (p.total + kHeadsWarps - 1) / kHeadsWarps, kHeadsThreads, 0, s, p);
     }
 };

@@ -22,8 +22,8 @@ struct HeadSeg {
     int64_t gb, gt, gh;        // of dy
     int64_t yb, yt, yh;        // of y; into a cache: page, slot, head
     int heads;
-    int groups;                // warps' units that a token's rows take
-    FastDiv per;               // division by groups
+    FastDiv per;               // warps' units that a token's rows take
+    uint32_t units;            // of all tokens
 };
 
 // How a warp holds rows: lpr lanes each, every lane ch pairs of vectors of v elements.
@@ -33,9 +33,9 @@ struct HeadShape {
 
 struct HeadsParams {
     HeadSeg seg[3];            // queries, keys, values (append only)
-    FastDiv units;             // units of a token, over its segments
     FastDiv len;               // tokens of a sequence of the batch
     uint32_t total;            // units in all
+    int per;                   // heads of a unit
     int64_t tokens;
     const void* positions;
     const float* table;        // [table_rows][ldt]: rot / 2 cosines, rot / 2 sines
@@ -63,9 +63,17 @@ constexpr HeadShape head_shape(int v, int vec, int64_t d) {
     return {v, 32, pairs > 32 * few ? many : few};
 }
 
-// Rows that a lane group takes of a unit: so many times 32 / lpr heads of a token.
-constexpr int heads_fwd_rows(int ch) { return ch > 2 ? 1 : 2; }
 constexpr int heads_bwd_rows(int ch) { return ch > 2 ? 1 : 2; }
+#ifndef RN_FWD_LOOPS
+#define RN_FWD_LOOPS 16
+#endif
+// Heads of a forward unit
+constexpr int heads_fwd_per(HeadShape sh, int64_t heads, int64_t tokens) {
+    const int at_once = 32 / sh.lpr;
+    int loops = RN_FWD_LOOPS;
+    while (loops > 1 && tokens * ((heads + at_once * loops - 1) / (at_once * loops)) < 152 * 32) loops /= 2;
+    return loops * at_once;
+}
 
 // cache_dtype: -1 without a cache.
 cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape shape, const HeadsParams& p,
