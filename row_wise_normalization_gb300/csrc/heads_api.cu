@@ -186,6 +186,30 @@ bool set_units(HeadsParams& p) {
     return true;
 }
 
+// CTAs of the gradient's kernel: enough for a unit a warp, at most kHeadsBwdCtas, shared in
+// proportion to the rows that warps hold at once.
+struct BwdCtas {
+    int q, k;
+};
+BwdCtas bwd_ctas(const HeadsParams& p, int at_once) {
+    int64_t want[2], work[2];
+    for (int i = 0; i < 2; ++i) {
+        want[i] = ((int64_t)p.seg[i].units + kHeadsWarps - 1) / kHeadsWarps;
+        work[i] = (p.seg[i].heads + at_once - 1) / at_once;
+    }
+    if (want[0] + want[1] <= kHeadsBwdCtas) return {(int)want[0], (int)want[1]};
+    if (want[0] == 0) return {0, kHeadsBwdCtas};
+    if (want[1] == 0) return {kHeadsBwdCtas, 0};
+    int64_t q = (kHeadsBwdCtas * work[0] + (work[0] + work[1]) / 2) / (work[0] + work[1]);
+    if (q < 1) q = 1;
+    if (q > kHeadsBwdCtas - 1) q = kHeadsBwdCtas - 1;
+    // (no more than there are units: the other segment then has enough)
+    if (q > want[0]) q = want[0];
+    int64_t k = kHeadsBwdCtas - q;
+    if (k > want[1]) k = want[1];
+    return {(int)q, (int)k};
+}
+
 // The widest access, of the vector, 2 or 1 elements, that `ok` accepts.
 template <typename F>
 int widest(int vec, F ok) {
@@ -258,7 +282,7 @@ int qk_rope_fwd(const rn_qk* in, const rn_heads* q_out, const rn_heads* k_out, v
                suits(*k_out, batch, len, w, es);
     });
     const HeadShape sh = head_shape(v, vec, d);
-    HeadsParams p = qk_params(*in, heads_fwd_per(sh, in->q.heads + in->k.heads, batch * len));
+    HeadsParams p = qk_params(*in, heads_per_unit(sh.lpr, in->q.heads + in->k.heads, batch * len));
     set_y(p.seg[0], q_out);
     set_y(p.seg[1], k_out);
     if (!set_units(p)) return RN_ERR_SIZE;
@@ -338,25 +362,23 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         at.q = *dq_out;
         at.k = *dk_out;
     }
-    HeadsParams p = qk_params(at, plain ? heads_fwd_per(sh, at.q.heads + at.k.heads, batch * len)
-                                     : heads_bwd_rows(sh.ch) * (32 / sh.lpr));
+    HeadsParams p = qk_params(at, heads_per_unit(sh.lpr, in->q.heads + in->k.heads, batch * len));
     set_y(p.seg[0], dq);
     set_y(p.seg[1], dk);
     p.back = true;
     if (!set_units(p)) return RN_ERR_SIZE;
     if (plain) return done(heads_fwd_launch(in->dtype, -1, sh, p, s));
     const rn_heads* const g[2] = {dq_out, dk_out};
-    int64_t units = 0;
     for (int i = 0; i < 2; ++i) {
         p.seg[i].dy = g[i]->data;
         p.seg[i].gb = g[i]->batch_stride;
         p.seg[i].gt = g[i]->token_stride;
         p.seg[i].gh = g[i]->head_stride;
-        if (p.seg[i].units > units) units = p.seg[i].units;
     }
     p.part = params ? (float*)workspace : nullptr;
-    const int64_t want = (units + kHeadsWarps - 1) / kHeadsWarps;
-    const int ctas = (int)(want < kHeadsBwdCtas ? want : kHeadsBwdCtas);
+    const BwdCtas c = bwd_ctas(p, 32 / sh.lpr);
+    p.first_k = c.q;
+    const int ctas = c.q + c.k;
     cudaError_t err = heads_bwd_launch(in->dtype, sh, p, ctas, s);
     if (err == cudaSuccess && params)
         err = column_reduce(in->dtype, (const float*)workspace, ctas, 2 * d, d, dwq, dwk, s);
@@ -402,7 +424,7 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
                cache_suits(bk, e, cs) && cache_suits(bv, e, cs);
     });
     const HeadShape sh = head_shape(w, vec, d > cache->d_v ? d : cache->d_v);
-    HeadsParams p = qk_params(*in, heads_fwd_per(sh, in->q.heads + in->k.heads, batch * len));
+    HeadsParams p = qk_params(*in, heads_per_unit(sh.lpr, in->q.heads + in->k.heads, batch * len));
     set_y(p.seg[0], q_out);
     HeadSeg& k = p.seg[1];
     k.y = cache->k;

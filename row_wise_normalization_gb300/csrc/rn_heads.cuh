@@ -82,25 +82,68 @@ __device__ __forceinline__ void ld_turn(float (&c)[CH][V], float (&s)[CH][V], co
     }
 }
 
-// The rotation of one lane's vectors a (first values) and b (second ones).
+// The transposed rotation of one lane's vectors a (first values) and b (second ones).
 template <int V>
-__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float (&c)[V],
-                                     const float (&s)[V], bool interleaved) {
-    if (V == 1 || !interleaved) {
+__device__ __forceinline__ void turn_back(float (&a)[V], float (&b)[V], const float (&c)[V],
+                                          const float (&s)[V], bool interleaved) {
+    if constexpr (V == 1) {
+        const float t = a[0];
+        a[0] = fmaf(b[0], s[0], t * c[0]);
+        b[0] = fmaf(-t, s[0], b[0] * c[0]);
+    } else if (!interleaved) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float t = a[i];
-            a[i] = t * c[i] - b[i] * s[i];
-            b[i] = b[i] * c[i] + t * s[i];
+        for (int i = 0; i < V; i += 2) {
+            const F2 u = f2(a[i], a[i + 1]), v = f2(b[i], b[i + 1]), c2 = f2(c[i], c[i + 1]);
+            f2_get(fma2(v, f2(s[i], s[i + 1]), mul2(u, c2)), a[i], a[i + 1]);
+            f2_get(fma2(u, f2(-s[i], -s[i + 1]), mul2(v, c2)), b[i], b[i + 1]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
-            const float t = a[2 * i], u = b[2 * i];
-            a[2 * i] = t * c[i] - a[2 * i + 1] * s[i];
-            a[2 * i + 1] = a[2 * i + 1] * c[i] + t * s[i];
-            b[2 * i] = u * c[V / 2 + i] - b[2 * i + 1] * s[V / 2 + i];
-            b[2 * i + 1] = b[2 * i + 1] * c[V / 2 + i] + u * s[V / 2 + i];
+            const F2 u = f2(a[2 * i], a[2 * i + 1]), v = f2(b[2 * i], b[2 * i + 1]);
+            const float cu = c[i], su = s[i], cv = c[V / 2 + i], sv = s[V / 2 + i];
+            f2_get(fma2(f2(a[2 * i + 1], a[2 * i]), f2(su, -su), mul2(u, f2s(cu))), a[2 * i],
+                   a[2 * i + 1]);
+            f2_get(fma2(f2(b[2 * i + 1], b[2 * i]), f2(sv, -sv), mul2(v, f2s(cv))), b[2 * i],
+                   b[2 * i + 1]);
+        }
+    }
+}
+
+// A lane's share of a row's sum of w g x.
+template <int V>
+__device__ __forceinline__ float dots(const float (&x1)[V], const float (&x2)[V],
+                                      const float (&g1)[V], const float (&g2)[V],
+                                      const float (&w1)[V], const float (&w2)[V]) {
+    if constexpr (V == 1) {
+        return fmaf(w1[0] * g1[0], x1[0], w2[0] * g2[0] * x2[0]);
+    } else {
+        F2 t = f2s(0.f);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            t = fma2(mul2(f2(g1[i], g1[i + 1]), f2(w1[i], w1[i + 1])), f2(x1[i], x1[i + 1]), t);
+            t = fma2(mul2(f2(g2[i], g2[i + 1]), f2(w2[i], w2[i + 1])), f2(x2[i], x2[i + 1]), t);
+        }
+        float lo, hi;
+        f2_get(t, lo, hi);
+        return lo + hi;
+    }
+}
+
+// dw += g x r, x := r (w g + x m).
+template <int V>
+__device__ __forceinline__ void grads(float (&x)[V], const float (&g)[V], const float (&w)[V],
+                                      float (&dw)[V], float r, float m) {
+    if constexpr (V == 1) {
+        dw[0] = fmaf(g[0], x[0] * r, dw[0]);
+        x[0] = r * fmaf(x[0], m, w[0] * g[0]);
+    } else {
+        const F2 r2 = f2s(r), m2 = f2s(m);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const F2 xx = f2(x[i], x[i + 1]), gg = f2(g[i], g[i + 1]);
+            f2_get(fma2(mul2(xx, r2), gg, f2(dw[i], dw[i + 1])), dw[i], dw[i + 1]);
+            f2_get(mul2(fma2(xx, m2, mul2(gg, f2(w[i], w[i + 1]))), r2), x[i], x[i + 1]);
         }
     }
 }
@@ -411,135 +454,205 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
 // again from x:
 //   dx_j = r (w_j g_j - x_j r^2 mean_k(w_k g_k x_k)),   dw_j = sum over rows of g_j x_j r.
 // A lane meets the same columns in every row, so its shares of dw stay in registers over all the
-// rows of a warp; the CTA joins its warps' and writes one row of p.part, which the column
-// reduction adds in order: no atomics, the same bits for the same sizes and grid.
-template <typename T, int V, int LPR, int CH, int U>
+// rows of a warp. A CTA works on one segment and writes one row of p.part (zeros for the other
+// segment), which the column reduction adds in order: no atomics, the same bits for the same sizes
+// and grid. A warp goes through its units in turn, and its copies run ahead over their borders.
+#ifndef RN_BWD_RING
+#define RN_BWD_RING 4
+#endif
+template <typename T, int V, int CH>
+constexpr int heads_bwd_ring() {
+    return V != Elem<T>::kVec ? 1 : CH == 1 ? RN_BWD_RING : 2;
+}
+template <typename T, int V, int CH>
+constexpr int heads_bwd_smem(int d) {
+    const int ring = heads_bwd_ring<T, V, CH>() > 1
+                         ? kHeadsWarps * heads_bwd_ring<T, V, CH>() * 4 * CH * 32 * 16 : 0;
+    const int sums = kHeadsWarps * d * 4;
+    return ring > sums ? ring : sums;
+}
+
+template <typename T, int V, int LPR, int CH>
 __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const HeadsParams p) {
-    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T);
-    __shared__ float sums[kHeadsWarps][2 * V * LPR * CH];
+    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_bwd_ring<T, V, CH>();
+    extern __shared__ uint4 shared[];      // the warps' rings; at the end their sums
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sg = lane / LPR;
+    const int seg = (int)blockIdx.x >= p.first_k ? 1 : 0;
+    const HeadSeg& S = p.seg[seg];
     const int d = p.d[0], rp = p.rot / 2 / V;
     const float inv = 1.f / (float)d;
-    pdl_wait();
-    for (int seg = 0; seg < 2; ++seg) {
-        const HeadSeg& S = p.seg[seg];
-        float da[CH][V], db[CH][V], wa[CH][V], wb[CH][V];
-        int lo[CH], hi[CH];
-        bool in[CH];
+    const uint32_t stride = (seg ? gridDim.x - p.first_k : p.first_k) * kHeadsWarps;
+    uint32_t unit = (blockIdx.x - (seg ? p.first_k : 0)) * kHeadsWarps + warp;
+    int lo[CH], hi[CH];
+    bool in[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        const int q = l + k * LPR;
+        in[k] = 2 * q * V < d;
+        pair_at<V>(q, rp, p.interleaved, lo[k], hi[k]);
+    }
+    uint4* const ring = shared + warp * (RING * 4 * CH * 32) + lane;
+    // what is loaded next: its unit, the lane group's row, heads that are left
+    uint32_t next = unit;
+    const T *X = nullptr, *G = nullptr;
+    int left = 0, put = 0, get = 0;
+    Raw<B> x1[CH], x2[CH], g1[CH], g2[CH];
+    auto enter = [&]() {
+        const uint32_t token = fast_quot(next, S.per);
+        const int head = (int)(next - token * S.per.d) * p.per;
+        const uint32_t b = fast_quot(token, p.len), t = token - b * p.len.d;
+        left = S.heads - head < p.per ? S.heads - head : p.per;
+        X = (const T*)S.x + b * S.xb + t * S.xt + (head + sg) * S.xh;
+        G = (const T*)S.dy + b * S.gb + t * S.gt + (head + sg) * S.gh;
+    };
+    auto load = [&]() {
+        const bool more = next < S.units;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int q = l + k * LPR;
-            in[k] = 2 * q * V < d;
-            pair_at<V>(q, rp, p.interleaved, lo[k], hi[k]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) da[k][i] = db[k][i] = wa[k][i] = wb[k][i] = 0.f;
-            if (in[k]) {
-                ld_weight<T, V>(wa[k], (const T*)S.w, lo[k]);
-                ld_weight<T, V>(wb[k], (const T*)S.w, hi[k]);
-            }
-        }
-        const uint32_t total = S.units;
-        for (uint32_t unit = blockIdx.x * kHeadsWarps + warp; unit < total;
-             unit += gridDim.x * kHeadsWarps) {
-            const uint32_t token = fast_quot(unit, S.per);
-            const int head = (int)(unit - token * S.per.d) * (SG * U);
-            const uint32_t b = fast_quot(token, p.len);
-            const int64_t t = token - b * p.len.d;
-            const T* const X = (const T*)S.x + b * S.xb + t * S.xt;
-            const T* const G = (const T*)S.dy + b * S.gb + t * S.gt;
-            T* const Y = (T*)S.y + b * S.yb + t * S.yt;
-            Raw<B> xa[U][CH], xb[U][CH], ga[U][CH], gb[U][CH];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = head + u * SG + sg;
-#pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    xa[u][k] = xb[u][k] = ga[u][k] = gb[u][k] = Raw<B>{};
-                    if (h < S.heads && in[k]) {
-                        xa[u][k] = ld_raw<B>(X + h * S.xh + lo[k]);
-                        xb[u][k] = ld_raw<B>(X + h * S.xh + hi[k]);
-                        ga[u][k] = ld_raw<B>(G + h * S.gh + lo[k]);
-                        gb[u][k] = ld_raw<B>(G + h * S.gh + hi[k]);
-                    }
+            const bool there = more && sg < left && in[k];
+            if constexpr (RING > 1) {
+                if (there) {
+                    uint4* const at = ring + (put * CH + k) * 128;
+                    copy_async(at, X + lo[k]);
+                    copy_async(at + 32, X + hi[k]);
+                    copy_async(at + 64, G + lo[k]);
+                    copy_async(at + 96, G + hi[k]);
                 }
-            }
-            float c[CH][V], s[CH][V];
-            bool there = true;
-            if (rp > 0) {
-                const int64_t pos = ld_id(p.positions, token, p.itype);
-                there = pos >= 0 && pos < p.table_rows;
-                ld_turn<V, CH, LPR>(c, s, p.table + (there ? pos : 0) * p.ldt, l, rp, true);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = head + u * SG + sg;
-                float x1[CH][V], x2[CH][V], g1[CH][V], g2[CH][V];
-                float ss = 0.f, dot = 0.f;
-#pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    unpack<T, V>(x1[k], xa[u][k]);
-                    unpack<T, V>(x2[k], xb[u][k]);
-                    unpack<T, V>(g1[k], ga[u][k]);
-                    unpack<T, V>(g2[k], gb[u][k]);
-                    if (rp > 0) turn<V>(g1[k], g2[k], c[k], s[k], p.interleaved);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        ss = fmaf(x1[k][i], x1[k][i], fmaf(x2[k][i], x2[k][i], ss));
-                        dot = fmaf(wa[k][i] * g1[k][i], x1[k][i],
-                                   fmaf(wb[k][i] * g2[k][i], x2[k][i], dot));
-                    }
-                }
-                ss = row_sum<LPR>(ss);
-                dot = row_sum<LPR>(dot);
-                const float r = rsqrtf(ss * inv + p.eps);
-                const float m = dot * inv * r * r;
-                if (h < S.heads) {
-#pragma unroll
-                    for (int k = 0; k < CH; ++k) {
-                        if (!in[k]) continue;
-                        float y1[V], y2[V];
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            y1[i] = there ? r * (wa[k][i] * g1[k][i] - x1[k][i] * m) : 0.f;
-                            y2[i] = there ? r * (wb[k][i] * g2[k][i] - x2[k][i] * m) : 0.f;
-                            if (there) {
-                                da[k][i] = fmaf(g1[k][i], x1[k][i] * r, da[k][i]);
-                                db[k][i] = fmaf(g2[k][i], x2[k][i] * r, db[k][i]);
-                            }
-                        }
-                        st_elems<T, V>(Y + h * S.yh + lo[k], y1);
-                        st_elems<T, V>(Y + h * S.yh + hi[k], y2);
-                    }
+            } else {
+                x1[k] = x2[k] = g1[k] = g2[k] = Raw<B>{};
+                if (there) {
+                    x1[k] = ld_raw<B>(X + lo[k]);
+                    x2[k] = ld_raw<B>(X + hi[k]);
+                    g1[k] = ld_raw<B>(G + lo[k]);
+                    g2[k] = ld_raw<B>(G + hi[k]);
                 }
             }
         }
-        if (p.part) {
-            // the warp's row groups, then the CTA's warps in order
+        if constexpr (RING > 1) {
+            copy_commit();
+            put = put + 1 == RING ? 0 : put + 1;
+        }
+        X += SG * S.xh;
+        G += SG * S.gh;
+        left -= SG;
+        if (left <= 0 && more) {
+            next += stride;
+            if (next < S.units) enter();
+        }
+    };
+    pdl_wait();
+    if (next < S.units) enter();
+#pragma unroll
+    for (int k = 0; k < (RING > 1 ? RING - 1 : 1); ++k) load();
+    float da[CH][V], db[CH][V], wa[CH][V], wb[CH][V];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) da[k][i] = db[k][i] = wa[k][i] = wb[k][i] = 0.f;
+        if (in[k]) {
+            ld_weight<T, V>(wa[k], (const T*)S.w, lo[k]);
+            ld_weight<T, V>(wb[k], (const T*)S.w, hi[k]);
+        }
+    }
+    uint32_t token = fast_quot(unit, S.per);
+    int64_t pos = rp > 0 && unit < S.units ? ld_id(p.positions, token, p.itype) : 0;
+    while (unit < S.units) {
+        const int head = (int)(unit - token * S.per.d) * p.per;
+        const uint32_t b = fast_quot(token, p.len), t = token - b * p.len.d;
+        const int rows = S.heads - head < p.per ? S.heads - head : p.per;
+        int64_t at = b * S.yb + t * S.yt + (head + sg) * S.yh;
+        const bool there = rp == 0 || (pos >= 0 && pos < p.table_rows);
+        float c[CH][V], s[CH][V];
+        ld_turn<V, CH, LPR>(c, s, p.table + (there ? pos : 0) * p.ldt, l, rp, false);
+        unit += stride;
+        token = fast_quot(unit, S.per);
+        if (rp > 0 && unit < S.units) pos = ld_id(p.positions, token, p.itype);
+        for (int h = sg; h - sg < rows; h += SG) {
+            if constexpr (RING > 1) {
+                load();
+                copy_wait<RING - 1>();
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    x1[k] = x2[k] = g1[k] = g2[k] = Raw<B>{};
+                    if (h < rows && in[k]) {       // (a lane reads what it copied itself)
+                        const uint4* const at = ring + (get * CH + k) * 128;
+                        x1[k] = *reinterpret_cast<const Raw<B>*>(at);
+                        x2[k] = *reinterpret_cast<const Raw<B>*>(at + 32);
+                        g1[k] = *reinterpret_cast<const Raw<B>*>(at + 64);
+                        g2[k] = *reinterpret_cast<const Raw<B>*>(at + 96);
+                    }
+                }
+                get = get + 1 == RING ? 0 : get + 1;
+            }
+            float u1[CH][V], u2[CH][V], v1[CH][V], v2[CH][V];     // x and g
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-#pragma unroll
-                    for (int o = LPR; o < 32; o <<= 1) {
-                        da[k][i] += __shfl_xor_sync(0xffffffffu, da[k][i], o);
-                        db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], o);
-                    }
-                    if (sg == 0 && in[k]) {
-                        sums[warp][lo[k] + i] = da[k][i];
-                        sums[warp][hi[k] + i] = db[k][i];
-                    }
+                unpack<T, V>(u1[k], x1[k]);
+                unpack<T, V>(u2[k], x2[k]);
+                unpack<T, V>(v1[k], g1[k]);
+                unpack<T, V>(v2[k], g2[k]);
+                if (l + k * LPR < rp) {
+                    if (p.interleaved)
+                        turn_back<V>(v1[k], v2[k], c[k], s[k], true);
+                    else
+                        turn_back<V>(v1[k], v2[k], c[k], s[k], false);
                 }
             }
-            __syncthreads();
-            for (int j = threadIdx.x; j < d; j += kHeadsThreads) {
-                float v = 0.f;
+            if constexpr (RING == 1) load();
+            const float ss = row_sum<LPR>(squares<V, CH>(u1, u2));
+            float dot = 0.f;
 #pragma unroll
-                for (int w = 0; w < kHeadsWarps; ++w) v += sums[w][j];
-                p.part[((int64_t)blockIdx.x * 2 + seg) * d + j] = v;
+            for (int k = 0; k < CH; ++k) dot += dots<V>(u1[k], u2[k], v1[k], v2[k], wa[k], wb[k]);
+            dot = row_sum<LPR>(dot);
+            const float r = rsqrtf(ss * inv + p.eps);
+            const float m = -(dot * inv * r * r);
+            if (h < rows) {
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    if (!in[k]) continue;
+                    if (there) {
+                        grads<V>(u1[k], v1[k], wa[k], da[k], r, m);
+                        grads<V>(u2[k], v2[k], wb[k], db[k], r, m);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) u1[k][i] = u2[k][i] = 0.f;
+                    }
+                    st_elems<T, V>((T*)S.y + at + lo[k], u1[k]);
+                    st_elems<T, V>((T*)S.y + at + hi[k], u2[k]);
+                }
             }
-            __syncthreads();
+            at += SG * S.yh;
         }
+    }
+    if constexpr (RING > 1) copy_wait<0>();
+    if (!p.part) return;
+    // the warp's row groups, then the CTA's warps in order
+    __syncthreads();
+    float* const sums = reinterpret_cast<float*>(shared);
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+            for (int o = LPR; o < 32; o <<= 1) {
+                da[k][i] += __shfl_xor_sync(0xffffffffu, da[k][i], o);
+                db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], o);
+            }
+            if (sg == 0 && in[k]) {
+                sums[warp * d + lo[k] + i] = da[k][i];
+                sums[warp * d + hi[k] + i] = db[k][i];
+            }
+        }
+    }
+    __syncthreads();
+    float* const row = p.part + (int64_t)blockIdx.x * 2 * d;
+    for (int j = threadIdx.x; j < d; j += kHeadsThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kHeadsWarps; ++w) v += sums[w * d + j];
+        row[seg * d + j] = v;
+        row[(1 - seg) * d + j] = 0.f;
     }
 }
 
@@ -580,8 +693,21 @@ struct BwdRun {
     cudaStream_t s;
     template <int V, int LPR, int CH>
     cudaError_t run() {
-        constexpr int U = heads_bwd_rows(CH);
-        return launch_pdl(heads_bwd_kernel<T, V, LPR, CH, U>, (unsigned)ctas, kHeadsThreads, 0, s,
+        const int smem = heads_bwd_smem<T, V, CH>(p.d[0]);
+        constexpr int MOST = heads_bwd_smem<T, V, CH>((int)kMaxHeadDim);
+        if constexpr (MOST > 48 * 1024) {
+            // (an attribute of the function in a context)
+            static thread_local unsigned long long done = 0;
+            unsigned long long ctx = 0;
+            cudaError_t err = current_context_id(&ctx);
+            if (err == cudaSuccess)
+                err = once_in_context(ctx, done, [] {
+                    return cudaFuncSetAttribute(heads_bwd_kernel<T, V, LPR, CH>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
+                });
+            if (err != cudaSuccess) return err;
+        }
+        return launch_pdl(heads_bwd_kernel<T, V, LPR, CH>, (unsigned)ctas, kHeadsThreads, smem, s,
                           p);
     }
 };

@@ -44,6 +44,7 @@ struct HeadsParams {
     int64_t nslots;
     FastDiv page;
     float* part;               // gradient: [CTAs][2 d] sums for the weights, or NULL
+    int first_k;               // gradient: the first CTA of the keys
     float eps;
     float store[3];            // factor of a row before it is stored
     int d[3];                  // width of each segment's rows
@@ -63,15 +64,21 @@ constexpr HeadShape head_shape(int v, int vec, int64_t d) {
     return {v, 32, pairs > 32 * few ? many : few};
 }
 
-constexpr int heads_bwd_rows(int ch) { return ch > 2 ? 1 : 2; }
-#ifndef RN_FWD_LOOPS
-#define RN_FWD_LOOPS 16
+// Heads of a unit: a multiple of what a warp holds at once (32 / lpr rows), up to kHeadsLoops times,
+// fewer where that leaves warps without one.
+#ifndef RN_LOOPS
+#define RN_LOOPS 16
 #endif
-// Heads of a forward unit
-constexpr int heads_fwd_per(HeadShape sh, int64_t heads, int64_t tokens) {
-    const int at_once = 32 / sh.lpr;
-    int loops = RN_FWD_LOOPS;
-    while (loops > 1 && tokens * ((heads + at_once * loops - 1) / (at_once * loops)) < 152 * 32) loops /= 2;
+#ifndef RN_MINU
+#define RN_MINU 32
+#endif
+constexpr int kHeadsLoops = RN_LOOPS;
+constexpr int heads_per_unit(int lpr, int64_t heads, int64_t tokens) {
+    const int at_once = 32 / lpr;
+    int loops = kHeadsLoops;
+    while (loops > 1 &&
+           tokens * ((heads + at_once * loops - 1) / (at_once * loops)) < 152 * RN_MINU)
+        loops /= 2;
     return loops * at_once;
 }
 

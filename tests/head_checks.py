@@ -47,8 +47,9 @@ def check_rope_bwd(got, want, norm, dtype, what="dx"):
 
 
 def check_dw(got, want, tokens, heads, dtype, what="dw"):
-    """A warp takes units of a token's heads in turn: at least 8 warps of 304 CTAs, or one
-    unit each; a unit adds at most 2 rows to a lane's sums."""
-    chain = 2 * -(-tokens * heads // (304 * 8)) + 5 + 8 + 4
+    """heads: of queries and keys together. 304 CTAs of 8 warps share the rows of both about
+    evenly (within a factor of 2), and a lane adds at most one of a warp's rows at once; a warp's
+    unit is 16 of them at most."""
+    chain = 2 * -(-tokens * heads // (304 * 8)) + 16 + 5 + 8 + 4
     tol = (21 + chain) * U * want["dw_abs"]
     _near(got, want["dw"], _stored(tol, want["dw"], dtype), what)

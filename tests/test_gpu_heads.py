@@ -109,7 +109,7 @@ def test_backward(n, hq, hk, d, rot, norm, interleaved, itype, param_grads, dtyp
         want = c.want_bwd(which, g)
         head_checks.check_rope_bwd(f64(dx), want, norm, dtype, "d" + which)
         if norm and param_grads:
-            head_checks.check_dw(f64(dw), want, n, heads, dtype, "dw" + which)
+            head_checks.check_dw(f64(dw), want, n, hq + hk, dtype, "dw" + which)
         else:
             assert dw is None
 
@@ -193,8 +193,8 @@ def test_layouts(layout, d, rot, dtype):
     dq, dk, dwq, dwk = rn.qk_rope_bwd(go_q, go_k, q, k, *c.args(), dq=qo, dk=ko)
     head_checks.check_rope_bwd(f64(dq.reshape(n, hq, d)), want_q, True, dtype)
     head_checks.check_rope_bwd(f64(dk.reshape(n, hk, d)), want_k, True, dtype)
-    head_checks.check_dw(f64(dwq), want_q, n, hq, dtype)
-    head_checks.check_dw(f64(dwk), want_k, n, hk, dtype)
+    head_checks.check_dw(f64(dwq), want_q, n, hq + hk, dtype)
+    head_checks.check_dw(f64(dwk), want_k, n, hq + hk, dtype)
     inplace = rn.qk_rope_bwd(go_q, go_k, q, k, *c.args(), dq=go_q, dk=go_k)
     assert torch.equal(go_q, dq) and torch.equal(go_k, dk)
     assert torch.equal(inplace[2], dwq) and torch.equal(inplace[3], dwk)
@@ -251,7 +251,7 @@ def test_norm_without_weights_and_one_weight(dtype):
     head_checks.check_rope(f64(k2), *c.want("k"), True, dtype)
     dq2, dk2, dwq, dwk = rn.qk_rope_bwd(*g, c.q, c.k, *c.args())
     assert dwq is None and torch.equal(dq, dq2)
-    head_checks.check_dw(f64(dwk), c.want_bwd("k", g[1]), 12, 2, dtype)
+    head_checks.check_dw(f64(dwk), c.want_bwd("k", g[1]), 12, 6, dtype)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -323,10 +323,10 @@ def test_many_tokens_gradient_of_weights():
     mag = torch.cat([gd[..., :half].abs() * cs.abs() + gd[..., half:].abs() * sn.abs(),
                      gd[..., half:].abs() * cs.abs() + gd[..., :half].abs() * sn.abs()], -1)
     r = (xd.square().mean(-1, keepdim=True) + EPS).rsqrt()
-    for sl, dw, heads in ((slice(0, hq), dwq, hq), (slice(hq, None), dwk, hk)):
+    for sl, dw in ((slice(0, hq), dwq), (slice(hq, None), dwk)):
         want = {"dw": (t * xd * r)[:, sl].sum((0, 1)).cpu().numpy(),
                 "dw_abs": (mag * xd.abs() * r)[:, sl].sum((0, 1)).cpu().numpy()}
-        head_checks.check_dw(f64(dw), want, n, heads, "bf16")
+        head_checks.check_dw(f64(dw), want, n, hq + hk, "bf16")
 
 
 def test_graph_replays_follow_their_inputs():
