@@ -13,9 +13,9 @@ namespace rn {
 cudaError_t heads_fwd_f32(bool, bool, HeadShape, const HeadsParams&, cudaStream_t);
 cudaError_t heads_fwd_bf16(bool, bool, HeadShape, const HeadsParams&, cudaStream_t);
 cudaError_t heads_fwd_f16(bool, bool, HeadShape, const HeadsParams&, cudaStream_t);
-cudaError_t heads_bwd_f32(HeadShape, const HeadsParams&, int, cudaStream_t);
-cudaError_t heads_bwd_bf16(HeadShape, const HeadsParams&, int, cudaStream_t);
-cudaError_t heads_bwd_f16(HeadShape, const HeadsParams&, int, cudaStream_t);
+cudaError_t heads_bwd_f32(HeadShape, const HeadsParams&, int, void*, void*, cudaStream_t);
+cudaError_t heads_bwd_bf16(HeadShape, const HeadsParams&, int, void*, void*, cudaStream_t);
+cudaError_t heads_bwd_f16(HeadShape, const HeadsParams&, int, void*, void*, cudaStream_t);
 
 cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape sh, const HeadsParams& p,
                              cudaStream_t s) {
@@ -26,12 +26,12 @@ cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape sh, const Hea
         default: return heads_fwd_f32(append, e4m3, sh, p, s);
     }
 }
-cudaError_t heads_bwd_launch(int dtype, HeadShape sh, const HeadsParams& p, int ctas,
-                             cudaStream_t s) {
+cudaError_t heads_bwd_launch(int dtype, HeadShape sh, const HeadsParams& p, int ctas, void* dwq,
+                             void* dwk, cudaStream_t s) {
     switch (dtype) {
-        case DT_BF16: return heads_bwd_bf16(sh, p, ctas, s);
-        case DT_F16: return heads_bwd_f16(sh, p, ctas, s);
-        default: return heads_bwd_f32(sh, p, ctas, s);
+        case DT_BF16: return heads_bwd_bf16(sh, p, ctas, dwq, dwk, s);
+        case DT_F16: return heads_bwd_f16(sh, p, ctas, dwq, dwk, s);
+        default: return heads_bwd_f32(sh, p, ctas, dwq, dwk, s);
     }
 }
 }  // namespace rn
@@ -186,27 +186,33 @@ bool set_units(HeadsParams& p) {
     return true;
 }
 
-// CTAs of the gradient's kernel: enough for a unit a warp, at most kHeadsBwdCtas, shared in
-// proportion to the rows that warps hold at once.
+// CTAs of the gradient's kernel, shared in proportion to the row groups (what a warp holds at
+// once): kBwdGroups of them a warp, so that a CTA's start and its sums weigh little, at
+// most kHeadsBwdCtas (several rounds of what the GPU holds at once, which evens out CTAs that
+// take longer) and no more than there are units.
 struct BwdCtas {
     int q, k;
 };
+#ifndef RN_BWD_GROUPS
+#define RN_BWD_GROUPS 16
+#endif
+constexpr int kBwdGroups = RN_BWD_GROUPS;
 BwdCtas bwd_ctas(const HeadsParams& p, int at_once) {
-    int64_t want[2], work[2];
+    int64_t most[2], work[2];
     for (int i = 0; i < 2; ++i) {
-        want[i] = ((int64_t)p.seg[i].units + kHeadsWarps - 1) / kHeadsWarps;
-        work[i] = (p.seg[i].heads + at_once - 1) / at_once;
+        most[i] = ((int64_t)p.seg[i].units + kHeadsWarps - 1) / kHeadsWarps;
+        work[i] = (p.seg[i].heads + at_once - 1) / at_once * p.tokens;
     }
-    if (want[0] + want[1] <= kHeadsBwdCtas) return {(int)want[0], (int)want[1]};
-    if (want[0] == 0) return {0, kHeadsBwdCtas};
-    if (want[1] == 0) return {kHeadsBwdCtas, 0};
-    int64_t q = (kHeadsBwdCtas * work[0] + (work[0] + work[1]) / 2) / (work[0] + work[1]);
-    if (q < 1) q = 1;
-    if (q > kHeadsBwdCtas - 1) q = kHeadsBwdCtas - 1;
-    // (no more than there are units: the other segment then has enough)
-    if (q > want[0]) q = want[0];
-    int64_t k = kHeadsBwdCtas - q;
-    if (k > want[1]) k = want[1];
+    const int64_t all = work[0] + work[1];
+    int64_t ctas = all / (kHeadsWarps * kBwdGroups);
+    if (ctas < 304) ctas = 304;
+    if (ctas > kHeadsBwdCtas) ctas = kHeadsBwdCtas;
+    int64_t q = (ctas * work[0] + all / 2) / all;
+    if (q > ctas - 1 && work[1] > 0) q = ctas - 1;
+    if (q < 1 && work[0] > 0) q = 1;
+    int64_t k = ctas - q;
+    if (q > most[0]) q = most[0];
+    if (k > most[1]) k = most[1];
     return {(int)q, (int)k};
 }
 
@@ -293,7 +299,7 @@ int qk_rope_bwd_workspace_size(int64_t d, size_t* bytes) {
     if (!bytes) return RN_ERR_NULL;
     *bytes = 0;
     if (d < 2 || d > kMaxHeadDim || d % 2) return RN_ERR_SIZE;
-    *bytes = (size_t)(kHeadsBwdCtas * 2 * d * 4);
+    *bytes = (size_t)(kHeadsBwdCtas * d * 4);
     return RN_OK;
 }
 
@@ -322,7 +328,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         if (st != RN_OK) return st;
         if (!*h) *h = &none;
     }
-    const size_t need = (size_t)(kHeadsBwdCtas * 2 * d * 4);
+    const size_t need = (size_t)(kHeadsBwdCtas * d * 4);
     if (params) {
         if (!workspace) return RN_ERR_NULL;
         if (misaligned(workspace, 16)) return RN_ERR_ALIGN;
@@ -379,10 +385,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
     const BwdCtas c = bwd_ctas(p, 32 / sh.lpr);
     p.first_k = c.q;
     const int ctas = c.q + c.k;
-    cudaError_t err = heads_bwd_launch(in->dtype, sh, p, ctas, s);
-    if (err == cudaSuccess && params)
-        err = column_reduce(in->dtype, (const float*)workspace, ctas, 2 * d, d, dwq, dwk, s);
-    return done(err);
+    return done(heads_bwd_launch(in->dtype, sh, p, ctas, dwq, dwk, s));
 }
 
 int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const rn_cache* cache,

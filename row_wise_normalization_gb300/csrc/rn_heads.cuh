@@ -454,9 +454,8 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
 // again from x:
 //   dx_j = r (w_j g_j - x_j r^2 mean_k(w_k g_k x_k)),   dw_j = sum over rows of g_j x_j r.
 // A lane meets the same columns in every row, so its shares of dw stay in registers over all the
-// rows of a warp. A CTA works on one segment and writes one row of p.part (zeros for the other
-// segment), which the column reduction adds in order: no atomics, the same bits for the same sizes
-// and grid. A warp goes through its units in turn, and its copies run ahead over their borders.
+// rows of a warp. A CTA works on one segment and writes one row of p.part, and heads_join_kernel adds
+// those in a fixed order: no atomics, the same bits for the same sizes and grid. A warp goes through its units in turn, and its copies run ahead over their borders.
 #ifndef RN_BWD_RING
 #define RN_BWD_RING 4
 #endif
@@ -545,14 +544,21 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
     if (next < S.units) enter();
 #pragma unroll
     for (int k = 0; k < (RING > 1 ? RING - 1 : 1); ++k) load();
-    float da[CH][V], db[CH][V], wa[CH][V], wb[CH][V];
+    float da[CH][V], db[CH][V];
+    Raw<B> wa[CH], wb[CH];      // (as they are stored: registers)
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) da[k][i] = db[k][i] = wa[k][i] = wb[k][i] = 0.f;
-        if (in[k]) {
-            ld_weight<T, V>(wa[k], (const T*)S.w, lo[k]);
-            ld_weight<T, V>(wb[k], (const T*)S.w, hi[k]);
+        for (int i = 0; i < V; ++i) da[k][i] = db[k][i] = 0.f;
+        wa[k] = wb[k] = Raw<B>{};
+        if (in[k] && S.w) {
+            wa[k] = ld_raw<B>((const T*)S.w + lo[k]);
+            wb[k] = ld_raw<B>((const T*)S.w + hi[k]);
+        } else if (in[k]) {
+            float ones[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) ones[i] = 1.f;
+            wa[k] = wb[k] = pack<T, V>(ones);
         }
     }
     uint32_t token = fast_quot(unit, S.per);
@@ -603,7 +609,12 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
             const float ss = row_sum<LPR>(squares<V, CH>(u1, u2));
             float dot = 0.f;
 #pragma unroll
-            for (int k = 0; k < CH; ++k) dot += dots<V>(u1[k], u2[k], v1[k], v2[k], wa[k], wb[k]);
+            for (int k = 0; k < CH; ++k) {
+                float w1[V], w2[V];
+                unpack<T, V>(w1, wa[k]);
+                unpack<T, V>(w2, wb[k]);
+                dot += dots<V>(u1[k], u2[k], v1[k], v2[k], w1, w2);
+            }
             dot = row_sum<LPR>(dot);
             const float r = rsqrtf(ss * inv + p.eps);
             const float m = -(dot * inv * r * r);
@@ -612,8 +623,11 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
                 for (int k = 0; k < CH; ++k) {
                     if (!in[k]) continue;
                     if (there) {
-                        grads<V>(u1[k], v1[k], wa[k], da[k], r, m);
-                        grads<V>(u2[k], v2[k], wb[k], db[k], r, m);
+                        float w1[V], w2[V];
+                        unpack<T, V>(w1, wa[k]);
+                        unpack<T, V>(w2, wb[k]);
+                        grads<V>(u1[k], v1[k], w1, da[k], r, m);
+                        grads<V>(u2[k], v2[k], w2, db[k], r, m);
                     } else {
 #pragma unroll
                         for (int i = 0; i < V; ++i) u1[k][i] = u2[k][i] = 0.f;
@@ -646,13 +660,46 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
         }
     }
     __syncthreads();
-    float* const row = p.part + (int64_t)blockIdx.x * 2 * d;
     for (int j = threadIdx.x; j < d; j += kHeadsThreads) {
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kHeadsWarps; ++w) v += sums[w * d + j];
-        row[seg * d + j] = v;
-        row[(1 - seg) * d + j] = 0.f;
+        p.part[(int64_t)blockIdx.x * d + j] = v;
+    }
+}
+
+// The CTAs' rows into the weights' gradients: columns of queries from the first first_k rows, of
+// keys from the others. 8 columns a CTA, 128 rows of them at a time, so that each thread has about ten loads,
+// none of which waits for another; then the warp's four rows, then the warps in order.
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinCols = 8;
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads)
+    heads_join_kernel(const float* part, int d, int first_k, int ctas, T* dwq, T* dwk) {
+    __shared__ float sums[kJoinThreads / 32][kJoinCols];
+    const int per = (d + kJoinCols - 1) / kJoinCols;
+    const bool key = (int)blockIdx.x >= per;
+    const int col = ((int)blockIdx.x - (key ? per : 0)) * kJoinCols + threadIdx.x % kJoinCols;
+    const int begin = key ? first_k : 0, end = key ? ctas : first_k;
+    T* const out = key ? dwk : dwq;
+    pdl_wait();
+    if (!out) return;
+    float v = 0.f;
+    if (col < d) {
+#pragma unroll 10
+        for (int r = begin + threadIdx.x / kJoinCols; r < end; r += kJoinThreads / kJoinCols)
+            v += __ldcg(part + (int64_t)r * d + col);
+    }
+#pragma unroll
+    for (int o = kJoinCols; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int lane = threadIdx.x & 31;
+    if (lane < kJoinCols) sums[threadIdx.x >> 5][lane] = v;
+    __syncthreads();
+    if (threadIdx.x < kJoinCols && col < d) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) t += sums[w][threadIdx.x];
+        stt_y1(out + col, t);
     }
 }
 
@@ -720,8 +767,13 @@ cudaError_t heads_fwd_t(bool append, bool e4m3, HeadShape sh, const HeadsParams&
     return for_shape<T>(sh, FwdRun<T, true, false>{p, s});
 }
 template <typename T>
-cudaError_t heads_bwd_t(HeadShape sh, const HeadsParams& p, int ctas, cudaStream_t s) {
-    return for_shape<T>(sh, BwdRun<T>{p, ctas, s});
+cudaError_t heads_bwd_t(HeadShape sh, const HeadsParams& p, int ctas, void* dwq, void* dwk,
+                        cudaStream_t s) {
+    const cudaError_t err = for_shape<T>(sh, BwdRun<T>{p, ctas, s});
+    if (err != cudaSuccess || !p.part) return err;
+    return launch_pdl(heads_join_kernel<T>, 2 * ((p.d[0] + kJoinCols - 1) / kJoinCols),
+                      kJoinThreads, 0, s, (const float*)p.part, p.d[0], p.first_k, ctas, (T*)dwq,
+                      (T*)dwk);
 }
 
 }  // namespace rn

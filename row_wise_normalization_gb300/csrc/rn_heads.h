@@ -43,7 +43,7 @@ struct HeadsParams {
     const void* slots;         // append
     int64_t nslots;
     FastDiv page;
-    float* part;               // gradient: [CTAs][2 d] sums for the weights, or NULL
+    float* part;               // gradient: [CTAs][d] sums for the weights, or NULL
     int first_k;               // gradient: the first CTA of the keys
     float eps;
     float store[3];            // factor of a row before it is stored
@@ -86,9 +86,12 @@ constexpr int heads_per_unit(int lpr, int64_t heads, int64_t tokens) {
 cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape shape, const HeadsParams& p,
                              cudaStream_t s);
 // ctas: rows of p.part.
-cudaError_t heads_bwd_launch(int dtype, HeadShape shape, const HeadsParams& p, int ctas,
-                             cudaStream_t s);
-constexpr int kHeadsBwdCtas = 304;   // two a GB300's SM: rows of the gradient's workspace, at most
+cudaError_t heads_bwd_launch(int dtype, HeadShape shape, const HeadsParams& p, int ctas, void* dwq,
+                             void* dwk, cudaStream_t s);
+#ifndef RN_BWD_CTAS
+#define RN_BWD_CTAS 1216
+#endif
+constexpr int kHeadsBwdCtas = RN_BWD_CTAS;   // two a GB300's SM: rows of the gradient's workspace, at most
 
 struct SlotsParams {
     const void* page_table;    // [seqs][ld]

@@ -12,7 +12,7 @@ u = 2^-24 is FP32's half step, uT the storage type's (2^-8 BF16, 2^-11 FP16, 2^-
   = 22 u of its magnitude. The second term x r^3 mean(w g x): its terms 3 + 2, their sum 24, the
   products with 1 / d and r twice 3 + 32, with x and r 2 + 16 and the difference 1: 83 u.
 * dw: terms g x r 3 + 2 + 16 = 21 u, their sum one u for each addition of the longest chain:
-  a lane's rows, 5 shuffles, 8 warps; the CTAs' rows are added with compensation (2 u each way).
+  a lane's rows, 5 shuffles, 8 warps, then the CTAs' rows.
 * storage adds uT of the result, half the smallest subnormal step at least.
 * e4m3: the product with the scale's reciprocal 2 u more, then uT = 2^-4, half of 2^-9 at least.
 """
@@ -47,9 +47,10 @@ def check_rope_bwd(got, want, norm, dtype, what="dx"):
 
 
 def check_dw(got, want, tokens, heads, dtype, what="dw"):
-    """heads: of queries and keys together. 304 CTAs of 8 warps share the rows of both about
-    evenly (within a factor of 2), and a lane adds at most one of a warp's rows at once; a warp's
-    unit is 16 of them at most."""
-    chain = 2 * -(-tokens * heads // (304 * 8)) + 16 + 5 + 8 + 4
+    """heads: of queries and keys together. CTAs of 8 warps, at least 304 of them where there is
+    work for as many, share the rows of both about evenly (within a factor of 2); a lane adds at
+    most one of a warp's rows at once, and a warp's unit is 16 of them at most. At most 1216 CTAs
+    are joined: 10 a thread, 2 shuffles, 32 warps."""
+    chain = 2 * -(-tokens * heads // (304 * 8)) + 16 + 5 + 8 + 10 + 2 + 32
     tol = (21 + chain) * U * want["dw_abs"]
     _near(got, want["dw"], _stored(tol, want["dw"], dtype), what)

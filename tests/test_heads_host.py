@@ -209,7 +209,7 @@ def test_qk_rope_bwd_checks(kw, want):
 
 
 def test_workspace_size():
-    assert capi.qk_rope_bwd_workspace_size(128) == 304 * 2 * 128 * 4
+    assert capi.qk_rope_bwd_workspace_size(128) == 1216 * 128 * 4
     for bad in (0, 3, -2, 514):
         with pytest.raises(capi.RowNormError):
             capi.qk_rope_bwd_workspace_size(bad)
