@@ -83,12 +83,12 @@ class rn_problem(ctypes.Structure):
 
 
 # Structs of the head operators, as packed bytes (one conversion a call in place of
-# one a field).
-heads = struct.Struct("Q4q").pack            # data, heads, batch, token and head strides
-# q, k (as `heads` packs them), wq, wk, positions, table, table_rows, table_stride, rot, batch,
-# len, d, dtype, itype, norm, interleaved, eps, 0
-qk = struct.Struct("40s40s4Q6q4ifi").pack
-# k, v, their page, slot and head strides, pages, page_size, d_v, dtype, scales, 0
+# one a field). rn_heads: data, heads, batch, token and head strides. rn_qk: q, k (as in
+# rn_heads), wq, wk, positions, table, table_rows, table_stride, rot, batch, len, d, dtype, itype,
+# norm, interleaved, eps, 0. rn_cache: k, v, their page, slot and head strides, pages, page_size, d_v,
+# dtype, scales, 0.
+heads = struct.Struct("Q4q").pack
+qk = struct.Struct("Q4qQ4q4Q6q4ifi").pack
 cache = struct.Struct("2Q6q3qi2fi").pack
 
 SIGNATURES = {

@@ -70,7 +70,7 @@ constexpr HeadShape head_shape(int v, int vec, int64_t d) {
 #define RN_LOOPS 16
 #endif
 #ifndef RN_MINU
-#define RN_MINU 32
+#define RN_MINU 4
 #endif
 constexpr int kHeadsLoops = RN_LOOPS;
 constexpr int heads_per_unit(int lpr, int64_t heads, int64_t tokens) {
@@ -89,7 +89,7 @@ cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape shape, const 
 cudaError_t heads_bwd_launch(int dtype, HeadShape shape, const HeadsParams& p, int ctas, void* dwq,
                              void* dwk, cudaStream_t s);
 #ifndef RN_BWD_CTAS
-#define RN_BWD_CTAS 1216
+#define RN_BWD_CTAS 2432
 #endif
 constexpr int kHeadsBwdCtas = RN_BWD_CTAS;   // two a GB300's SM: rows of the gradient's workspace, at most
 

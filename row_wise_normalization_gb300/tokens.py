@@ -327,36 +327,55 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
 # ---------------------------------------------------------------------------
 # The head operators. Rows are heads of tokens: tensors of shape [tokens, heads, d] or
 # [batch, len, heads, d] with contiguous rows and any other strides (column blocks of a packed
-# projection, transposed head-major tensors).
+# projection, transposed head-major tensors). A tensor's rows go to the library as its address,
+# heads, and batch, token and head strides.
 # ---------------------------------------------------------------------------
-_NONE = capi.heads(0, 0, 0, 0, 0)
+_NO_ROWS = (0, 0, 0, 0, 0)
+_heads, _qk = capi.heads, capi.qk
+_NONE = _heads(*_NO_ROWS)
 
 
-def _rows(name, t, lead, heads, d, dtype):
-    """Packed rn_heads of a tensor of rows; what is given of lead, heads, d, dtype has to be
-    so."""
+def _rows(name, t, want, dtype):
+    """A tensor's rows; its shape and dtype have to be as given."""
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
-    shape = t.shape
-    if shape[-2:] != (heads, d) or shape[:-2] != lead:
-        raise ValueError(f"{name} must be of shape {[*lead, heads, d]}, got {list(shape)}")
+    if t.shape != want:
+        raise ValueError(f"{name} must be of shape {list(want)}, got {list(t.shape)}")
     if not t.is_cuda or t.dtype is not dtype:
         _check_f32_cuda(name, t, dtype, contiguous=False)
-    st = t.stride()
-    if st[-1] != 1 and t.numel():
+    if len(want) == 3:
+        ts, hs, one = t.stride()
+        bs = 0
+    else:
+        bs, ts, hs, one = t.stride()
+    if one != 1 and t.numel():
         raise ValueError(f"{name} must have contiguous rows")
-    if len(shape) == 3:
-        return capi.heads(t.data_ptr(), heads, 0, st[0], st[1])
-    return capi.heads(t.data_ptr(), heads, st[0], st[1], st[2])
+    return t.data_ptr(), want[-2], bs, ts, hs
+
+
+def _new_rows(home, shape, dtype, dev):
+    """(tensor, packed rows) of an output that the call allocates, contiguous."""
+    t = home.new_empty(shape) if home.is_cuda else _maker(home, dev)(shape, dtype=dtype)
+    h, d = shape[-2:]
+    return t, _heads(t.data_ptr(), h, shape[1] * h * d if len(shape) == 4 else 0, h * d, d)
 
 
 def _first(name, t):
-    """Storage code, leading shape, heads and width of the tensor that sets them."""
+    """Storage code and shape of the tensor that sets them."""
     code = _values(name, t)
     shape = t.shape
-    if len(shape) not in (3, 4):
+    if len(shape) != 3 and len(shape) != 4:
         raise ValueError(f"{name} must be [tokens, heads, d] or [batch, len, heads, d]")
-    return code, shape[:-2], shape[-2], shape[-1]
+    return code, shape
+
+
+def _beside(name, t, shape):
+    """The shape that a tensor of other heads of the same tokens has to have."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    heads = t.shape[-2] if t.dim() > 1 else -1
+    return ((shape[0], heads, shape[2]) if len(shape) == 3 else
+            (shape[0], shape[1], heads, shape[3]))
 
 
 def _weight(name, w, d, dtype):
@@ -369,22 +388,21 @@ def _weight(name, w, d, dtype):
     return w.data_ptr()
 
 
-def _count(lead):
-    return lead[0] if len(lead) == 1 else lead[0] * lead[1]
-
-
 def _turn(positions, table, n):
     """(address of positions, of table, rows, stride, rot, index code)."""
-    if table is None or table.shape[-1] == 0:
+    if table is None:
         return 0, 0, 0, 0, 0, 0
-    if not (isinstance(table, torch.Tensor) and table.is_cuda and table.dtype is torch.float32):
-        _check_f32_cuda("table", table, torch.float32, contiguous=False)
-    if table.dim() != 2 or table.stride(1) != 1:
+    if not (isinstance(table, torch.Tensor) and table.is_cuda and table.dtype is _F32):
+        _check_f32_cuda("table", table, _F32, contiguous=False)
+    shape = table.shape
+    if len(shape) != 2 or table.stride(1) != 1:
         raise ValueError("table must be 2-D with contiguous rows")
+    rows, rot = shape
+    if rot == 0:
+        return 0, 0, 0, 0, 0, 0
     it = _ids("positions", positions)
     if positions.numel() != n:
         raise ValueError(f"positions must have {n} elements")
-    rows, rot = table.shape
     return (positions.data_ptr(), table.data_ptr(), rows, table.stride(0) if rows > 1 else rot,
             rot, it)
 
@@ -399,42 +417,45 @@ def qk_rope_fwd(q, k, positions=None, table=None, wq=None, wk=None, eps: float =
     of a row are turned, in pairs (i, i + rot / 2) or, with ``interleaved``, (2i, 2i + 1).
     positions: int32 or int64, one a token; a token whose position is outside the table gets
     rows of zeros. Without a table nothing is turned. wq, wk: ``[d]``, the norms' weights;
-    without ``norm`` rows are normed if one of them is given. Returns ``(q_out, k_out)``
+    unless ``norm`` says so, rows are normed if one of them is given. Returns ``(q_out, k_out)``
     (allocated contiguous unless given; each may be its input itself).
     """
-    code, lead, hq, d = _first("q", q)
-    dtype = q.dtype
-    hk = 0
-    if k is not None:
-        hk = k.shape[-2] if k.dim() > 1 else -1
+    code, shape = _first("q", q)
+    dtype, d, len_ = q.dtype, shape[-1], shape[-3]
+    batch = 1 if len(shape) == 3 else shape[0]
     if norm is None:
         norm = wq is not None or wk is not None
-    n = _count(lead)
-    pos, tab, trows, tstride, rot, it = _turn(positions, table, n)
+    pos, tab, trows, tstride, rot, it = _turn(positions, table, batch * len_)
     dev = _device(q, k, positions, table, wq, wk, q_out, k_out)
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return qk_rope_fwd(q, k, positions, table, wq, wk, eps, norm=norm,
                                interleaved=interleaved, q_out=q_out, k_out=k_out)
-    a_q = _rows("q", q, lead, hq, d, dtype)
-    a_k = _rows("k", k, lead, hk, d, dtype) if k is not None else _NONE
+    r_q = _rows("q", q, shape, dtype)
     if q_out is None:
-        q_out = _maker(q, dev)(q.shape, dtype=dtype)
-    a_qo = _rows("q_out", q_out, lead, hq, d, dtype)
-    a_ko = _NONE
+        q_out, p_q = _new_rows(q, shape, dtype, dev)
+    else:
+        p_q = _heads(*_rows("q_out", q_out, shape, dtype))
+    r_k, p_k = _NO_ROWS, _NONE
     if k is not None:
+        kshape = _beside("k", k, shape)
+        r_k = _rows("k", k, kshape, dtype)
         if k_out is None:
-            k_out = _maker(k, dev)(k.shape, dtype=dtype)
-        a_ko = _rows("k_out", k_out, lead, hk, d, dtype)
+            k_out, p_k = _new_rows(k, kshape, dtype, dev)
+        else:
+            p_k = _heads(*_rows("k_out", k_out, kshape, dtype))
     elif k_out is not None:
         raise ValueError("k_out without k")
     st = _C.qk_rope_fwd(
-        capi.qk(a_q, a_k, _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype), pos, tab,
-                trows, tstride, rot, 1 if len(lead) == 1 else lead[0], lead[-1], d, code, it,
-                1 if norm else 0, 1 if interleaved else 0, eps, 0), a_qo, a_ko, _stream(dev))
+        _qk(*r_q, *r_k, _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype), pos, tab, trows,
+            tstride, rot, batch, len_, d, code, it, 1 if norm else 0, 1 if interleaved else 0, eps,
+            0), p_q, p_k, _stream(dev))
     if st:
         capi.check(st)
     return q_out, k_out
+
+
+_BWD_BYTES = {}      # workspace of qk_rope_bwd by width
 
 
 def qk_rope_bwd(dq_out, dk_out, q, k, positions=None, table=None, wq=None, wk=None,
@@ -448,36 +469,33 @@ def qk_rope_bwd(dq_out, dk_out, q, k, positions=None, table=None, wq=None, wk=No
     themselves among them. ``workspace``: a contiguous CUDA tensor of at least
     ``capi.qk_rope_bwd_workspace_size(d)`` bytes (allocated if not given).
     """
-    code, lead, hq, d = _first("dq_out", dq_out)
-    dtype = dq_out.dtype
-    hk = 0
-    if dk_out is not None:
-        hk = dk_out.shape[-2] if dk_out.dim() > 1 else -1
+    code, shape = _first("dq_out", dq_out)
+    dtype, d, len_ = dq_out.dtype, shape[-1], shape[-3]
+    batch = 1 if len(shape) == 3 else shape[0]
     if norm is None:
         norm = wq is not None or wk is not None
-    n = _count(lead)
-    pos, tab, trows, tstride, rot, it = _turn(positions, table, n)
+    pos, tab, trows, tstride, rot, it = _turn(positions, table, batch * len_)
     dev = _device(dq_out, dk_out, q, k, positions, table, wq, wk, dq, dk, dwq, dwk, workspace)
     if _elsewhere(dev, stream):
         with _On(dev, stream):
             return qk_rope_bwd(dq_out, dk_out, q, k, positions, table, wq, wk, eps, norm=norm,
                                interleaved=interleaved, param_grads=param_grads, dq=dq, dk=dk,
                                dwq=dwq, dwk=dwk, workspace=workspace)
-    a_gq = _rows("dq_out", dq_out, lead, hq, d, dtype)
-    a_gk = _rows("dk_out", dk_out, lead, hk, d, dtype) if hk else _NONE
-    if norm:
-        a_q = _rows("q", q, lead, hq, d, dtype)
-        a_k = _rows("k", k, lead, hk, d, dtype) if hk else _NONE
-    else:
-        a_q, a_k = capi.heads(0, hq, 0, 0, 0), capi.heads(0, hk, 0, 0, 0)
+    p_gq = _heads(*_rows("dq_out", dq_out, shape, dtype))
     if dq is None:
-        dq = _maker(dq_out, dev)(dq_out.shape, dtype=dtype)
-    a_dq = _rows("dq", dq, lead, hq, d, dtype)
-    a_dk = _NONE
-    if hk:
+        dq, p_dq = _new_rows(dq_out, shape, dtype, dev)
+    else:
+        p_dq = _heads(*_rows("dq", dq, shape, dtype))
+    r_q = _rows("q", q, shape, dtype) if norm else (0, shape[-2], 0, 0, 0)
+    r_k, p_gk, p_dk = _NO_ROWS, _NONE, _NONE
+    if dk_out is not None:
+        kshape = _beside("dk_out", dk_out, shape)
+        p_gk = _heads(*_rows("dk_out", dk_out, kshape, dtype))
         if dk is None:
-            dk = _maker(dk_out, dev)(dk_out.shape, dtype=dtype)
-        a_dk = _rows("dk", dk, lead, hk, d, dtype)
+            dk, p_dk = _new_rows(dk_out, kshape, dtype, dev)
+        else:
+            p_dk = _heads(*_rows("dk", dk, kshape, dtype))
+        r_k = _rows("k", k, kshape, dtype) if norm else (0, kshape[-2], 0, 0, 0)
     elif dk is not None:
         raise ValueError("dk without dk_out")
     a_wq, a_wk = _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype)
@@ -495,7 +513,9 @@ def qk_rope_bwd(dq_out, dk_out, q, k, positions=None, table=None, wq=None, wk=No
         raise ValueError("dwq and dwk need param_grads, the norm and its weights")
     if a_dwq or a_dwk:
         if workspace is None:
-            nbytes = capi.qk_rope_bwd_workspace_size(d)
+            nbytes = _BWD_BYTES.get(d)
+            if nbytes is None:
+                nbytes = _BWD_BYTES[d] = capi.qk_rope_bwd_workspace_size(d)
             workspace = torch.empty(nbytes, dtype=torch.uint8,
                                     device=dq_out.device if dq_out.is_cuda else "cuda")
         else:
@@ -504,10 +524,9 @@ def qk_rope_bwd(dq_out, dk_out, q, k, positions=None, table=None, wq=None, wk=No
             nbytes = workspace.numel() * workspace.element_size()
         a_ws = workspace.data_ptr()
     st = _C.qk_rope_bwd(
-        capi.qk(a_q, a_k, a_wq, a_wk, pos, tab, trows, tstride, rot,
-                1 if len(lead) == 1 else lead[0], lead[-1], d, code, it, 1 if norm else 0,
-                1 if interleaved else 0, eps, 0), a_gq, a_gk, a_dq, a_dk, a_dwq, a_dwk, a_ws,
-        nbytes, _stream(dev))
+        _qk(*r_q, *r_k, a_wq, a_wk, pos, tab, trows, tstride, rot, batch, len_, d, code, it,
+            1 if norm else 0, 1 if interleaved else 0, eps, 0), p_gq, p_gk, p_dq, p_dk, a_dwq,
+        a_dwk, a_ws, nbytes, _stream(dev))
     if st:
         capi.check(st)
     return dq, dk, dwq, dwk
@@ -518,22 +537,25 @@ def _cache(k_cache, v_cache, dtype, k_scale, v_scale):
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dim() != 4 or (t.stride(3) != 1 and t.numel()):
-            raise ValueError(f"{name} must be [pages, page_size, heads, d] with contiguous rows")
-    cdtype = k_cache.dtype
+    kshape, vshape, cdtype = k_cache.shape, v_cache.shape, k_cache.dtype
     if cdtype is not _E4M3 and cdtype is not dtype:
         raise TypeError(f"k_cache must be {dtype} or {_E4M3}, got {cdtype}")
     if not (k_cache.is_cuda and v_cache.is_cuda and v_cache.dtype is cdtype):
         _check_f32_cuda("k_cache", k_cache, cdtype, contiguous=False)
         _check_f32_cuda("v_cache", v_cache, cdtype, contiguous=False)
-    pages, page, heads, d = k_cache.shape
-    if v_cache.shape[:3] != k_cache.shape[:3]:
+    if len(kshape) != 4 or len(vshape) != 4:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, heads, d]")
+    pages, page, heads, d = kshape
+    if vshape != kshape and vshape[:3] != kshape[:3]:
         raise ValueError("k_cache and v_cache must hold the same pages, tokens and heads")
-    dv = v_cache.shape[3]
-    sk, sv = k_cache.stride(), v_cache.stride()
-    return (capi.cache(k_cache.data_ptr(), v_cache.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1],
-                       sv[2], pages, page, dv, capi.RN_DTYPE_E4M3 if cdtype is _E4M3 else
-                       _FLOATS[cdtype], k_scale, v_scale, 0), heads, d, dv)
+    dv = vshape[3]
+    kp, ks, kh, k1 = k_cache.stride()
+    vp, vs, vh, v1 = v_cache.stride()
+    if (k1 != 1 or v1 != 1) and k_cache.numel():
+        raise ValueError("k_cache and v_cache must have contiguous rows")
+    return (capi.cache(k_cache.data_ptr(), v_cache.data_ptr(), kp, ks, kh, vp, vs, vh, pages, page,
+                       dv, capi.RN_DTYPE_E4M3 if cdtype is _E4M3 else _FLOATS[cdtype], k_scale,
+                       v_scale, 0), heads, d, dv)
 
 
 def kv_append(k, v, slots, k_cache, v_cache, positions=None, table=None, wk=None,
@@ -550,11 +572,12 @@ def kv_append(k, v, slots, k_cache, v_cache, positions=None, table=None, wk=None
     values divided by k_scale and v_scale, at most 448 in size. Returns ``q_out`` (None
     without q), which may be passed in, q itself among them.
     """
-    code, lead, hk, d = _first("k", k)
-    dtype = k.dtype
+    code, shape = _first("k", k)
+    dtype, hk, d, len_ = k.dtype, shape[-2], shape[-1], shape[-3]
+    batch = 1 if len(shape) == 3 else shape[0]
+    n = batch * len_
     if norm is None:
         norm = wq is not None or wk is not None
-    n = _count(lead)
     it = _ids("slots", slots)
     if slots.numel() != n:
         raise ValueError(f"slots must have {n} elements")
@@ -569,24 +592,24 @@ def kv_append(k, v, slots, k_cache, v_cache, positions=None, table=None, wk=None
                              norm=norm, interleaved=interleaved, k_scale=k_scale,
                              v_scale=v_scale, q_out=q_out)
     a_c, heads, dk, dv = _cache(k_cache, v_cache, dtype, k_scale, v_scale)
-    if (heads, dk) != (hk, d):
+    if heads != hk or dk != d:
         raise ValueError(f"k_cache holds {heads} heads of {dk}, k has {hk} of {d}")
-    a_k = _rows("k", k, lead, hk, d, dtype)
-    a_v = _rows("v", v, lead, hk, dv, dtype)
-    a_q = a_qo = _NONE
+    r_k = _rows("k", k, shape, dtype)
+    p_v = _heads(*_rows("v", v, shape if dv == d else (*shape[:-1], dv), dtype))
+    r_q, p_q = _NO_ROWS, _NONE
     if q is not None:
-        hq = q.shape[-2] if q.dim() > 1 else -1
-        a_q = _rows("q", q, lead, hq, d, dtype)
+        qshape = _beside("q", q, shape)
+        r_q = _rows("q", q, qshape, dtype)
         if q_out is None:
-            q_out = _maker(q, dev)(q.shape, dtype=dtype)
-        a_qo = _rows("q_out", q_out, lead, hq, d, dtype)
+            q_out, p_q = _new_rows(q, qshape, dtype, dev)
+        else:
+            p_q = _heads(*_rows("q_out", q_out, qshape, dtype))
     elif q_out is not None or wq is not None:
         raise ValueError("q_out and wq need q")
     st = _C.kv_append(
-        capi.qk(a_q, a_k, _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype), pos, tab,
-                trows, tstride, rot, 1 if len(lead) == 1 else lead[0], lead[-1], d, code, it,
-                1 if norm else 0, 1 if interleaved else 0, eps, 0), a_qo, a_v, a_c,
-        slots.data_ptr(), _stream(dev))
+        _qk(*r_q, *r_k, _weight("wq", wq, d, dtype), _weight("wk", wk, d, dtype), pos, tab, trows,
+            tstride, rot, batch, len_, d, code, it, 1 if norm else 0, 1 if interleaved else 0, eps,
+            0), p_q, p_v, a_c, slots.data_ptr(), _stream(dev))
     if st:
         capi.check(st)
     return q_out
@@ -618,12 +641,15 @@ def kv_gather(k_cache, v_cache, slots, *, dtype=None, k_scale: float = 1.0, v_sc
     a_c, heads, d, dv = _cache(k_cache, v_cache, dtype, k_scale, v_scale)
     if k_out is None:
         k_out = _maker(k_cache, dev)((n, heads, d), dtype=dtype)
+        p_k = _heads(k_out.data_ptr(), heads, 0, heads * d, d)
+    else:
+        p_k = _heads(*_rows("k_out", k_out, (n, heads, d), dtype))
     if v_out is None:
         v_out = _maker(v_cache, dev)((n, heads, dv), dtype=dtype)
-    lead = (n,)
-    st = _C.kv_gather(a_c, d, slots.data_ptr(), it, n, code,
-                      _rows("k_out", k_out, lead, heads, d, dtype),
-                      _rows("v_out", v_out, lead, heads, dv, dtype), _stream(dev))
+        p_v = _heads(v_out.data_ptr(), heads, 0, heads * dv, dv)
+    else:
+        p_v = _heads(*_rows("v_out", v_out, (n, heads, dv), dtype))
+    st = _C.kv_gather(a_c, d, slots.data_ptr(), it, n, code, p_k, p_v, _stream(dev))
     if st:
         capi.check(st)
     return k_out, v_out
@@ -642,14 +668,16 @@ def kv_slots(page_table, starts, offsets, n: int, page_size: int, *, slots=None,
     """
     if not isinstance(page_table, torch.Tensor):
         raise TypeError("page_table must be a torch.Tensor")
-    if page_table.dim() != 2:
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be 2-D")
     it = _ids("offsets", offsets)
     dtype = offsets.dtype
-    seqs, width = page_table.shape
+    seqs, width = shape
     if not page_table.is_cuda or page_table.dtype is not dtype:
         _check_f32_cuda("page_table", page_table, dtype, contiguous=False)
-    if width > 1 and seqs and page_table.stride(1) != 1:
+    ld, one = page_table.stride()
+    if one != 1 and width > 1 and seqs:
         raise ValueError("page_table must have contiguous rows")
     if _ids("starts", starts) != it:
         raise TypeError(f"starts must be {dtype}, got {starts.dtype}")
@@ -661,13 +689,15 @@ def kv_slots(page_table, starts, offsets, n: int, page_size: int, *, slots=None,
             return kv_slots(page_table, starts, offsets, n, page_size, slots=slots,
                             positions=positions)
     if slots is None:
-        slots = _maker(offsets, dev)((n,), dtype=dtype)
+        slots = offsets.new_empty(n) if offsets.is_cuda else _maker(offsets, dev)((n,), dtype=dtype)
+    elif _ids("slots", slots) != it or slots.numel() != n:
+        raise ValueError(f"slots must be {dtype} with {n} elements")
     if positions is None:
-        positions = _maker(offsets, dev)((n,), dtype=dtype)
-    for name, t in (("slots", slots), ("positions", positions)):
-        if _ids(name, t) != it or t.numel() != n:
-            raise ValueError(f"{name} must be {dtype} with {n} elements")
-    st = _C.kv_slots(it, page_table.data_ptr(), page_table.stride(0) if seqs > 1 else width, width,
+        positions = (offsets.new_empty(n) if offsets.is_cuda else
+                     _maker(offsets, dev)((n,), dtype=dtype))
+    elif _ids("positions", positions) != it or positions.numel() != n:
+        raise ValueError(f"positions must be {dtype} with {n} elements")
+    st = _C.kv_slots(it, page_table.data_ptr(), ld if seqs > 1 else width, width,
                      starts.data_ptr(), offsets.data_ptr(), seqs, page_size, slots.data_ptr(),
                      positions.data_ptr(), n, _stream(dev))
     if st:

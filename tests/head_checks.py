@@ -49,8 +49,8 @@ def check_rope_bwd(got, want, norm, dtype, what="dx"):
 def check_dw(got, want, tokens, heads, dtype, what="dw"):
     """heads: of queries and keys together. CTAs of 8 warps, at least 304 of them where there is
     work for as many, share the rows of both about evenly (within a factor of 2); a lane adds at
-    most one of a warp's rows at once, and a warp's unit is 16 of them at most. At most 1216 CTAs
-    are joined: 10 a thread, 2 shuffles, 32 warps."""
-    chain = 2 * -(-tokens * heads // (304 * 8)) + 16 + 5 + 8 + 10 + 2 + 32
+    most one of a warp's rows at once, and a warp's unit is 16 of them at most. At most 2432 CTAs
+    are joined: 19 a thread, 2 shuffles, 32 warps."""
+    chain = 2 * -(-tokens * heads // (304 * 8)) + 16 + 5 + 8 + 19 + 2 + 32
     tol = (21 + chain) * U * want["dw_abs"]
     _near(got, want["dw"], _stored(tol, want["dw"], dtype), what)

@@ -4,6 +4,7 @@ rows (no GPU needed)."""
 import math
 import os
 import shutil
+import struct
 import subprocess
 
 import numpy as np
@@ -93,12 +94,15 @@ def _h(at, heads=4, bs=0, ts=32, hs=8):
     return capi.heads(at, heads, bs, ts, hs)
 
 
+_PARTS = struct.Struct("Q4q").unpack
+
+
 def _qk(**kw):
     a = dict(q=_h(A), k=_h(A + STEP), wq=A + 2 * STEP, wk=A + 3 * STEP, positions=A + 4 * STEP,
              table=A + 5 * STEP, table_rows=100, table_stride=8, rot=8, batch=1, len=5, d=8, dtype=0,
              itype=1, norm=1, interleaved=0, eps=1e-5, zero=0)
     a.update(kw)
-    return capi.qk(*a.values())
+    return capi.qk(*_PARTS(a.pop("q")), *_PARTS(a.pop("k")), *a.values())
 
 
 _IN = set("q k wq wk positions table table_rows table_stride rot batch len d dtype itype norm "
@@ -209,7 +213,7 @@ def test_qk_rope_bwd_checks(kw, want):
 
 
 def test_workspace_size():
-    assert capi.qk_rope_bwd_workspace_size(128) == 1216 * 128 * 4
+    assert capi.qk_rope_bwd_workspace_size(128) == 2432 * 128 * 4
     for bad in (0, 3, -2, 514):
         with pytest.raises(capi.RowNormError):
             capi.qk_rope_bwd_workspace_size(bad)
