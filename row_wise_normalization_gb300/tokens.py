@@ -331,7 +331,7 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
 # heads, and batch, token and head strides.
 # ---------------------------------------------------------------------------
 _NO_ROWS = (0, 0, 0, 0, 0)
-_heads, _qk = capi.heads, capi.qk
+_heads, _qk, _empty = capi.heads, capi.qk, torch.empty
 _NONE = _heads(*_NO_ROWS)
 
 
@@ -355,7 +355,8 @@ def _rows(name, t, want, dtype):
 
 def _new_rows(home, shape, dtype, dev):
     """(tensor, packed rows) of an output that the call allocates, contiguous."""
-    t = home.new_empty(shape) if home.is_cuda else _maker(home, dev)(shape, dtype=dtype)
+    t = (_empty(shape, dtype=dtype, device=home.device) if home.is_cuda else
+         _maker(home, dev)(shape, dtype=dtype))
     h, d = shape[-2:]
     return t, _heads(t.data_ptr(), h, shape[1] * h * d if len(shape) == 4 else 0, h * d, d)
 
@@ -689,12 +690,11 @@ def kv_slots(page_table, starts, offsets, n: int, page_size: int, *, slots=None,
             return kv_slots(page_table, starts, offsets, n, page_size, slots=slots,
                             positions=positions)
     if slots is None:
-        slots = offsets.new_empty(n) if offsets.is_cuda else _maker(offsets, dev)((n,), dtype=dtype)
+        slots = _maker(offsets, dev)(n, dtype=dtype)
     elif _ids("slots", slots) != it or slots.numel() != n:
         raise ValueError(f"slots must be {dtype} with {n} elements")
     if positions is None:
-        positions = (offsets.new_empty(n) if offsets.is_cuda else
-                     _maker(offsets, dev)((n,), dtype=dtype))
+        positions = _maker(offsets, dev)(n, dtype=dtype)
     elif _ids("positions", positions) != it or positions.numel() != n:
         raise ValueError(f"positions must be {dtype} with {n} elements")
     st = _C.kv_slots(it, page_table.data_ptr(), ld if seqs > 1 else width, width,
