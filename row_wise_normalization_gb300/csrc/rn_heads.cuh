@@ -58,26 +58,16 @@ __device__ __forceinline__ void ld_table(float* v, const float* p) {
     }
 }
 
-// A lane's cosines and sines for its pairs; 1 and 0 where nothing is turned.
+// A lane's cosines and sines for its pairs. Lanes whose pairs are not turned load none.
 template <int V, int CH, int LPR>
 __device__ __forceinline__ void ld_turn(float (&c)[CH][V], float (&s)[CH][V], const float* row,
-                                        int l, int rp, bool back) {
+                                        int l, int rp) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int p = l + k * LPR;
         if (p < rp) {
             ld_table<V>(c[k], row + p * V);
             ld_table<V>(s[k], row + (rp + p) * V);
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                c[k][i] = 1.f;
-                s[k][i] = 0.f;
-            }
-        }
-        if (back) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) s[k][i] = -s[k][i];
         }
     }
 }
@@ -155,18 +145,6 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// Weights at a row's vectors; ones without any.
-template <typename T, int V>
-__device__ __forceinline__ void ld_weight(float* v, const T* w, int at) {
-    if (w) {
-        const Raw<V * (int)sizeof(T)> r = ld_raw<V * (int)sizeof(T)>(w + at);
-        unpack<T, V>(v, r);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 1.f;
-    }
-}
-
 // V values as e4m3, to nearest even, those beyond its largest to that.
 template <int V>
 __device__ __forceinline__ void st_e4m3(uint8_t* p, const float* v) {
@@ -205,36 +183,42 @@ __device__ __forceinline__ HeadUnit head_unit(const HeadsParams& p, uint32_t uni
 
 // A row's rotation and weights as two factors a value: y_j = r (x_j A_j + x_partner B_j), where the
 // partner is the other value of j's pair: A = w c, B = -+ w_partner s. They are a token's, so that a
-// row costs three packed products for two values. Values that are not turned have no second term.
+// row costs three packed products for two values. Values that are not turned have A alone. What a
+// row is multiplied by before it is stored is in them too.
 template <int V>
 struct Factors {
-    float a1[V], b1[V], a2[V], b2[V];      // of the first and the second vector
+    F2 a1[(V + 1) / 2], b1[(V + 1) / 2], a2[(V + 1) / 2], b2[(V + 1) / 2];   // first, second vector
 };
 
-// Factors of a lane's pair of vectors, from weights w1, w2 and the table's cosines and sines.
+// Factors of a lane's pair of vectors, from weights w1, w2 and, where it is turned, the table's
+// cosines c and sines s.
 template <int V>
 __device__ __forceinline__ void set_factors(Factors<V>& f, const float (&w1)[V], const float (&w2)[V],
-                                            const float (&c)[V], const float (&s)[V],
+                                            const float (&c)[V], const float (&s)[V], bool turned,
                                             bool interleaved) {
-    if (V == 1 || !interleaved) {
+    if constexpr (V == 1) {
+        f.a1[0] = f2(turned ? w1[0] * c[0] : w1[0], turned ? w2[0] * c[0] : w2[0]);
+        f.b1[0] = f2(-(w2[0] * s[0]), w1[0] * s[0]);
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            f.a1[i] = w1[i] * c[i];
-            f.b1[i] = -(w2[i] * s[i]);
-            f.a2[i] = w2[i] * c[i];
-            f.b2[i] = w1[i] * s[i];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            f.a1[2 * i] = w1[2 * i] * c[i];
-            f.b1[2 * i] = -(w1[2 * i + 1] * s[i]);
-            f.a1[2 * i + 1] = w1[2 * i + 1] * c[i];
-            f.b1[2 * i + 1] = w1[2 * i] * s[i];
-            f.a2[2 * i] = w2[2 * i] * c[V / 2 + i];
-            f.b2[2 * i] = -(w2[2 * i + 1] * s[V / 2 + i]);
-            f.a2[2 * i + 1] = w2[2 * i + 1] * c[V / 2 + i];
-            f.b2[2 * i + 1] = w2[2 * i] * s[V / 2 + i];
+    for (int i = 0; i < V / 2; ++i) {
+        const F2 u = f2(w1[2 * i], w1[2 * i + 1]), v = f2(w2[2 * i], w2[2 * i + 1]);
+        if (!turned) {
+            f.a1[i] = u;
+            f.a2[i] = v;
+        } else if (!interleaved) {
+            const F2 cc = f2(c[2 * i], c[2 * i + 1]);
+            f.a1[i] = mul2(u, cc);
+            f.a2[i] = mul2(v, cc);
+            f.b1[i] = mul2(v, f2(-s[2 * i], -s[2 * i + 1]));
+            f.b2[i] = mul2(u, f2(s[2 * i], s[2 * i + 1]));
+        } else {
+            const float su = s[i], sv = s[V / 2 + i];
+            f.a1[i] = mul2(u, f2s(c[i]));
+            f.a2[i] = mul2(v, f2s(c[V / 2 + i]));
+            f.b1[i] = mul2(f2(w1[2 * i + 1], w1[2 * i]), f2(-su, su));
+            f.b2[i] = mul2(f2(w2[2 * i + 1], w2[2 * i]), f2(-sv, sv));
         }
     }
 }
@@ -244,20 +228,21 @@ template <int V>
 __device__ __forceinline__ void apply_factors(float (&x1)[V], float (&x2)[V], const Factors<V>& f,
                                               float r, bool turned, bool interleaved) {
     if constexpr (V == 1) {
-        const float t = x1[0];
-        x1[0] = r * (turned ? t * f.a1[0] + x2[0] * f.b1[0] : t * f.a1[0]);
-        x2[0] = r * (turned ? x2[0] * f.a2[0] + t * f.b2[0] : x2[0] * f.a2[0]);
+        float a1, a2, b1, b2;
+        f2_get(f.a1[0], a1, a2);
+        f2_get(f.b1[0], b1, b2);
+        const float t = x1[0], u = x2[0];
+        x1[0] = r * (turned ? t * a1 + u * b1 : t * a1);
+        x2[0] = r * (turned ? u * a2 + t * b2 : u * a2);
     } else {
         const F2 r2 = f2s(r);
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
             const F2 u = f2(x1[i], x1[i + 1]), v = f2(x2[i], x2[i + 1]);
-            F2 a = mul2(u, f2(f.a1[i], f.a1[i + 1])), b = mul2(v, f2(f.a2[i], f.a2[i + 1]));
+            F2 a = mul2(u, f.a1[i / 2]), b = mul2(v, f.a2[i / 2]);
             if (turned) {
-                const F2 pu = interleaved ? f2(x1[i + 1], x1[i]) : v;
-                const F2 pv = interleaved ? f2(x2[i + 1], x2[i]) : u;
-                a = fma2(pu, f2(f.b1[i], f.b1[i + 1]), a);
-                b = fma2(pv, f2(f.b2[i], f.b2[i + 1]), b);
+                a = fma2(interleaved ? f2(x1[i + 1], x1[i]) : v, f.b1[i / 2], a);
+                b = fma2(interleaved ? f2(x2[i + 1], x2[i]) : u, f.b2[i / 2], b);
             }
             f2_get(mul2(a, r2), x1[i], x1[i + 1]);
             f2_get(mul2(b, r2), x2[i], x2[i + 1]);
@@ -358,11 +343,59 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
         X += SG * S.xh;
     };
     pdl_wait();
+    // All that does not wait for anything is under way before the first wait, the position's, for
+    // the table's row.
+    const bool norm = p.norm && !value, eight = E4M3 && u0.seg > 0;
+    int64_t pos = 0, slot = 0;
+    if (rp > 0) pos = ld_id(p.positions, u0.token, p.itype);
+    if (APPEND && u0.seg > 0) slot = ld_id(p.slots, u0.token, p.itype);
 #pragma unroll
     for (int k = 0; k < (RING > 1 ? RING - 1 : 1); ++k) load();
+    Raw<B> wa[CH], wb[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        wa[k] = wb[k] = Raw<B>{};
+        if (norm && S.w && in[k]) {
+            wa[k] = ld_raw<B>((const T*)S.w + lo[k]);
+            wb[k] = ld_raw<B>((const T*)S.w + hi[k]);
+        }
+    }
+    bool there = true;
+    Factors<V> f[CH];
+    // (values in their own type are copied: no factors)
+    if (!value || E4M3) {
+        const float* row = nullptr;
+        if (rp > 0) {
+            there = pos >= 0 && pos < p.table_rows;
+            row = p.table + (there ? pos : 0) * p.ldt;
+        }
+        float c[CH][V], s[CH][V];
+        ld_turn<V, CH, LPR>(c, s, row, l, rp);
+        const float scale = eight ? p.store[u0.seg] : 1.f;
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            float w1[V], w2[V];
+            unpack<T, V>(w1, wa[k]);
+            unpack<T, V>(w2, wb[k]);
+            if (!norm || !S.w) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) w1[i] = w2[i] = scale;
+            } else if (eight) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    w1[i] *= scale;
+                    w2[i] *= scale;
+                }
+            }
+            if (p.back) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[k][i] = -s[k][i];
+            }
+            set_factors<V>(f[k], w1, w2, c[k], s[k], l + k * LPR < rp, p.interleaved);
+        }
+    }
     int64_t at = b * S.yb + t * S.yt + h * S.yh;
     if (APPEND && u0.seg > 0) {
-        const int64_t slot = ld_id(p.slots, u0.token, p.itype);
         if (slot < 0 || slot >= p.nslots) {     // (the whole warp: one token)
             if constexpr (RING > 1) copy_wait<0>();
             return;
@@ -370,78 +403,67 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
         const uint32_t page = fast_quot((uint32_t)slot, p.page);
         at = page * S.yb + (int64_t)((uint32_t)slot - page * p.page.d) * S.yt + h * S.yh;
     }
-    bool there = true;
-    const bool norm = p.norm && !value;
-    Factors<V> f[CH];
-    {
-        const float* row = nullptr;
-        if (rp > 0) {
-            const int64_t pos = ld_id(p.positions, u0.token, p.itype);
-            there = pos >= 0 && pos < p.table_rows;
-            row = p.table + (there ? pos : 0) * p.ldt;
-        }
-        float c[CH][V], s[CH][V];
-        ld_turn<V, CH, LPR>(c, s, row, l, rp, p.back);
-        const T* const w = norm ? (const T*)S.w : nullptr;
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-            float w1[V] = {}, w2[V] = {};
-            if (in[k]) {
-                ld_weight<T, V>(w1, w, lo[k]);
-                ld_weight<T, V>(w2, w, hi[k]);
-            }
-            set_factors<V>(f[k], w1, w2, c[k], s[k], p.interleaved);
-        }
-    }
-    const float store = E4M3 && u0.seg > 0 ? p.store[u0.seg] : 1.f;
+    const float inv = 1.f / (float)d;
     for (; h - sg < end; h += SG) {
-        float a[CH][V], e[CH][V];
         if constexpr (RING > 1) {
             load();
             copy_wait<RING - 1>();
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
+                n1[k] = n2[k] = Raw<B>{};
                 if (h < end && in[k]) {       // (a lane reads what it copied itself)
                     n1[k] = *reinterpret_cast<const Raw<B>*>(&ring[warp][get][2 * k][lane]);
                     n2[k] = *reinterpret_cast<const Raw<B>*>(&ring[warp][get][2 * k + 1][lane]);
-                } else {
-                    n1[k] = n2[k] = Raw<B>{};
                 }
             }
             get = get + 1 == RING ? 0 : get + 1;
         }
+        Raw<B> o1[CH], o2[CH];
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            unpack<T, V>(a[k], n1[k]);
-            unpack<T, V>(e[k], n2[k]);
+            o1[k] = n1[k];
+            o2[k] = n2[k];
         }
         if constexpr (RING == 1) load();
-        float r = 1.f;
-        if (norm) r = rsqrtf(row_sum<LPR>(squares<V, CH>(a, e)) / (float)d + p.eps);
-        if (h < end) {
+        char* const Y = (char*)S.y + (eight ? at : at * (int)sizeof(T));
+        if (value && !E4M3) {
+            if (h < end) {
+#pragma unroll
+                for (int k = 0; k < CH; ++k) {
+                    if (!in[k]) continue;
+                    st_raw<B>((T*)Y + lo[k], o1[k]);
+                    st_raw<B>((T*)Y + hi[k], o2[k]);
+                }
+            }
+        } else {
+            float a[CH][V], e[CH][V];
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
-                if (!in[k]) continue;
-                const bool turned = l + k * LPR < rp;
-                if (p.interleaved)
-                    apply_factors<V>(a[k], e[k], f[k], r, turned, true);
-                else
-                    apply_factors<V>(a[k], e[k], f[k], r, turned, false);
-                if (!there) {
+                unpack<T, V>(a[k], o1[k]);
+                unpack<T, V>(e[k], o2[k]);
+            }
+            float r = 1.f;
+            if (norm) r = rsqrtf(fmaf(row_sum<LPR>(squares<V, CH>(a, e)), inv, p.eps));
+            if (h < end) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) a[k][i] = e[k][i] = 0.f;
-                }
-                if (E4M3 && u0.seg > 0) {
+                for (int k = 0; k < CH; ++k) {
+                    if (!in[k]) continue;
+                    const bool turned = l + k * LPR < rp;
+                    if (p.interleaved)
+                        apply_factors<V>(a[k], e[k], f[k], r, turned, true);
+                    else
+                        apply_factors<V>(a[k], e[k], f[k], r, turned, false);
+                    if (!there) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        a[k][i] *= store;
-                        e[k][i] *= store;
+                        for (int i = 0; i < V; ++i) a[k][i] = e[k][i] = 0.f;
                     }
-                    st_e4m3<V>((uint8_t*)S.y + at + lo[k], a[k]);
-                    st_e4m3<V>((uint8_t*)S.y + at + hi[k], e[k]);
-                } else {
-                    st_elems<T, V>((T*)S.y + at + lo[k], a[k]);
-                    st_elems<T, V>((T*)S.y + at + hi[k], e[k]);
+                    if (eight) {
+                        st_e4m3<V>((uint8_t*)Y + lo[k], a[k]);
+                        st_e4m3<V>((uint8_t*)Y + hi[k], e[k]);
+                    } else {
+                        st_elems<T, V>((T*)Y + lo[k], a[k]);
+                        st_elems<T, V>((T*)Y + hi[k], e[k]);
+                    }
                 }
             }
         }
@@ -570,7 +592,7 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
         int64_t at = b * S.yb + t * S.yt + (head + sg) * S.yh;
         const bool there = rp == 0 || (pos >= 0 && pos < p.table_rows);
         float c[CH][V], s[CH][V];
-        ld_turn<V, CH, LPR>(c, s, p.table + (there ? pos : 0) * p.ldt, l, rp, false);
+        ld_turn<V, CH, LPR>(c, s, p.table + (there ? pos : 0) * p.ldt, l, rp);
         unit += stride;
         token = fast_quot(unit, S.per);
         if (rp > 0 && unit < S.units) pos = ld_id(p.positions, token, p.itype);
