@@ -197,15 +197,15 @@ struct BwdCtas {
 #define RN_BWD_GROUPS 16
 #endif
 constexpr int kBwdGroups = RN_BWD_GROUPS;
-BwdCtas bwd_ctas(const HeadsParams& p, int at_once) {
+BwdCtas bwd_ctas(const HeadsParams& p, int at_once, int warps, int ctas_per_sm) {
     int64_t most[2], work[2];
     for (int i = 0; i < 2; ++i) {
-        most[i] = ((int64_t)p.seg[i].units + kHeadsWarps - 1) / kHeadsWarps;
+        most[i] = ((int64_t)p.seg[i].units + warps - 1) / warps;
         work[i] = (p.seg[i].heads + at_once - 1) / at_once * p.tokens;
     }
     const int64_t all = work[0] + work[1];
-    int64_t ctas = all / (kHeadsWarps * kBwdGroups);
-    if (ctas < 304) ctas = 304;
+    int64_t ctas = all / (warps * kBwdGroups);
+    if (ctas < 152 * ctas_per_sm) ctas = 152 * ctas_per_sm;
     if (ctas > kHeadsBwdCtas) ctas = kHeadsBwdCtas;
     int64_t q = (ctas * work[0] + all / 2) / all;
     if (q > ctas - 1 && work[1] > 0) q = ctas - 1;
@@ -216,10 +216,10 @@ BwdCtas bwd_ctas(const HeadsParams& p, int at_once) {
     return {(int)q, (int)k};
 }
 
-// The widest access, of the vector, 2 or 1 elements, that `ok` accepts.
+// The widest access, of the vector (16 bytes of rows), 4, 2 or 1 elements, that `ok` accepts.
 template <typename F>
 int widest(int vec, F ok) {
-    return ok(vec) ? vec : ok(2) ? 2 : 1;
+    return ok(vec) ? vec : vec > 4 && ok(4) ? 4 : ok(2) ? 2 : 1;
 }
 
 int check_cache(const rn_cache* c, int64_t heads, int64_t d, int dtype, int* cs, Box* k, Box* v) {
@@ -382,7 +382,8 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         p.seg[i].gh = g[i]->head_stride;
     }
     p.part = params ? (float*)workspace : nullptr;
-    const BwdCtas c = bwd_ctas(p, 32 / sh.lpr);
+    const BwdCtas c = bwd_ctas(p, 32 / sh.lpr, heads_bwd_warps(sh.v),
+                               heads_bwd_ctas_per_sm(sh.v));
     p.first_k = c.q;
     const int ctas = c.q + c.k;
     return done(heads_bwd_launch(in->dtype, sh, p, ctas, dwq, dwk, s));

@@ -178,6 +178,7 @@ template <typename T>
 cudaError_t gather_e4m3(int ne, const GatherParams& p, cudaStream_t s) {
     switch (ne) {
         case 8: return gather_run<T, 8, 1>(p, s);
+        case 4: return gather_run<T, 4, 1>(p, s);
         case 2: return gather_run<T, 2, 1>(p, s);
         default: return gather_run<T, 1, 1>(p, s);
     }
@@ -202,6 +203,7 @@ cudaError_t kv_gather_launch(int cache_dtype, int dtype, int ne, const GatherPar
     }
     switch (ne) {
         case 8: return gather_run<void, 8, 2>(p, s);
+        case 4: return gather_run<void, 4, 2>(p, s);
         case 2: return gather_run<void, 2, 2>(p, s);
         default: return gather_run<void, 1, 2>(p, s);
     }

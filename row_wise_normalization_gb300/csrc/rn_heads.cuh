@@ -58,7 +58,7 @@ __device__ __forceinline__ void ld_table(float* v, const float* p) {
     }
 }
 
-// A lane's cosines and sines for its pairs. Lanes whose pairs are not turned load none.
+// A lane's cosines and sines for its pairs; 1 and 0 where nothing is turned.
 template <int V, int CH, int LPR>
 __device__ __forceinline__ void ld_turn(float (&c)[CH][V], float (&s)[CH][V], const float* row,
                                         int l, int rp) {
@@ -68,6 +68,12 @@ __device__ __forceinline__ void ld_turn(float (&c)[CH][V], float (&s)[CH][V], co
         if (p < rp) {
             ld_table<V>(c[k], row + p * V);
             ld_table<V>(s[k], row + (rp + p) * V);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                c[k][i] = 1.f;
+                s[k][i] = 0.f;
+            }
         }
     }
 }
@@ -84,8 +90,9 @@ __device__ __forceinline__ void turn_back(float (&a)[V], float (&b)[V], const fl
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
             const F2 u = f2(a[i], a[i + 1]), v = f2(b[i], b[i + 1]), c2 = f2(c[i], c[i + 1]);
-            f2_get(fma2(v, f2(s[i], s[i + 1]), mul2(u, c2)), a[i], a[i + 1]);
-            f2_get(fma2(u, f2(-s[i], -s[i + 1]), mul2(v, c2)), b[i], b[i + 1]);
+            const F2 s2 = f2(s[i], s[i + 1]);
+            f2_get(fma2(v, s2, mul2(u, c2)), a[i], a[i + 1]);
+            f2_get(sub2(mul2(v, c2), mul2(u, s2)), b[i], b[i + 1]);
         }
     } else {
 #pragma unroll
@@ -281,19 +288,51 @@ __device__ __forceinline__ float squares(const float (&x1)[CH][V], const float (
 #ifndef RN_FWD_RING
 #define RN_FWD_RING 4
 #endif
-// Row groups that a warp copies ahead, where accesses are 16 bytes (asynchronous copies take no
-// fewer than 4, and narrow rows hold several chunks a lane): else one, in registers.
-template <int V, typename T>
+// Row groups that a warp copies ahead: in shared memory, where each lane reads what it copied
+// itself; one, in registers, where accesses are of 2 bytes (asynchronous copies take no fewer
+// than 4) or a lane holds many chunks of a row.
+template <typename T, int V, int CH>
 constexpr int heads_ring() {
-    return V == Elem<T>::kVec ? RN_FWD_RING : 1;
+    return V * (int)sizeof(T) >= 4 && CH <= 2 ? RN_FWD_RING : 1;
+}
+
+template <int B>
+__device__ __forceinline__ Raw<B> ld_ring(const Raw<B>* p) {
+    Raw<B> r;
+    if constexpr (B == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+        r.w[2] = v.z;
+        r.w[3] = v.w;
+    } else if constexpr (B == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+    } else {
+        r.w[0] = p->w[0];
+    }
+    return r;
+}
+// B bytes (4, 8 or 16) to shared memory, without waiting.
+template <int B>
+__device__ __forceinline__ void copy_raw(Raw<B>* smem, const void* p) {
+    if constexpr (B == 16)
+        copy_async(smem, p);
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(smem)),
+                     "l"(p), "n"(B)
+                     : "memory");
 }
 
 // APPEND: keys and values (segments 1 and 2) go into the cache, at the token's slot. A warp takes
 // p.per heads of its token, a row for each lane group at a time, with the next rows under way.
 template <typename T, int V, int LPR, int CH, bool APPEND, bool E4M3>
 __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(const HeadsParams p) {
-    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<V, T>();
-    __shared__ uint4 ring[RING > 1 ? kHeadsWarps : 1][RING > 1 ? RING : 1][RING > 1 ? 2 * CH : 1][32];
+    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<T, V, CH>();
+    __shared__ __align__(16) Raw<B> ring[RING > 1 ? kHeadsWarps : 1][RING > 1 ? RING : 1]
+                                        [RING > 1 ? 2 * CH : 1][32];
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5;
     const uint32_t unit = blockIdx.x * kHeadsWarps + warp;
@@ -324,8 +363,8 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
             const bool there = ahead + sg < end && in[k];
             if constexpr (RING > 1) {
                 if (there) {
-                    copy_async(&ring[warp][put][2 * k][lane], X + lo[k]);
-                    copy_async(&ring[warp][put][2 * k + 1][lane], X + hi[k]);
+                    copy_raw<B>(&ring[warp][put][2 * k][lane], X + lo[k]);
+                    copy_raw<B>(&ring[warp][put][2 * k + 1][lane], X + hi[k]);
                 }
             } else {
                 n1[k] = n2[k] = Raw<B>{};
@@ -412,8 +451,8 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
             for (int k = 0; k < CH; ++k) {
                 n1[k] = n2[k] = Raw<B>{};
                 if (h < end && in[k]) {       // (a lane reads what it copied itself)
-                    n1[k] = *reinterpret_cast<const Raw<B>*>(&ring[warp][get][2 * k][lane]);
-                    n2[k] = *reinterpret_cast<const Raw<B>*>(&ring[warp][get][2 * k + 1][lane]);
+                    n1[k] = ld_ring(&ring[warp][get][2 * k][lane]);
+                    n2[k] = ld_ring(&ring[warp][get][2 * k + 1][lane]);
                 }
             }
             get = get + 1 == RING ? 0 : get + 1;
@@ -483,19 +522,22 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
 #endif
 template <typename T, int V, int CH>
 constexpr int heads_bwd_ring() {
-    return V != Elem<T>::kVec ? 1 : CH == 1 ? RN_BWD_RING : 2;
+    return heads_ring<T, V, CH>() == 1 ? 1 : CH == 1 ? RN_BWD_RING : 2;
 }
 template <typename T, int V, int CH>
 constexpr int heads_bwd_smem(int d) {
+    constexpr int WARPS = heads_bwd_warps(V);
     const int ring = heads_bwd_ring<T, V, CH>() > 1
-                         ? kHeadsWarps * heads_bwd_ring<T, V, CH>() * 4 * CH * 32 * 16 : 0;
-    const int sums = kHeadsWarps * d * 4;
+                         ? WARPS * heads_bwd_ring<T, V, CH>() * 4 * CH * 32 * V * (int)sizeof(T)
+                         : 0;
+    const int sums = WARPS * d * 4;
     return ring > sums ? ring : sums;
 }
 
-template <typename T, int V, int LPR, int CH>
-__global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const HeadsParams p) {
+template <typename T, int V, int LPR, int CH, bool INTER>
+__global__ void __launch_bounds__(heads_bwd_warps(V) * 32, heads_bwd_ctas_per_sm(V)) heads_bwd_kernel(const HeadsParams p) {
     constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_bwd_ring<T, V, CH>();
+    constexpr int WARPS = heads_bwd_warps(V);
     extern __shared__ uint4 shared[];      // the warps' rings; at the end their sums
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sg = lane / LPR;
@@ -503,17 +545,17 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
     const HeadSeg& S = p.seg[seg];
     const int d = p.d[0], rp = p.rot / 2 / V;
     const float inv = 1.f / (float)d;
-    const uint32_t stride = (seg ? gridDim.x - p.first_k : p.first_k) * kHeadsWarps;
-    uint32_t unit = (blockIdx.x - (seg ? p.first_k : 0)) * kHeadsWarps + warp;
+    const uint32_t stride = (seg ? gridDim.x - p.first_k : p.first_k) * WARPS;
+    uint32_t unit = (blockIdx.x - (seg ? p.first_k : 0)) * WARPS + warp;
     int lo[CH], hi[CH];
     bool in[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int q = l + k * LPR;
         in[k] = 2 * q * V < d;
-        pair_at<V>(q, rp, p.interleaved, lo[k], hi[k]);
+        pair_at<V>(q, rp, INTER, lo[k], hi[k]);
     }
-    uint4* const ring = shared + warp * (RING * 4 * CH * 32) + lane;
+    Raw<B>* const ring = reinterpret_cast<Raw<B>*>(shared) + warp * (RING * 4 * CH * 32) + lane;
     // what is loaded next: its unit, the lane group's row, heads that are left
     uint32_t next = unit;
     const T *X = nullptr, *G = nullptr;
@@ -534,11 +576,11 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
             const bool there = more && sg < left && in[k];
             if constexpr (RING > 1) {
                 if (there) {
-                    uint4* const at = ring + (put * CH + k) * 128;
-                    copy_async(at, X + lo[k]);
-                    copy_async(at + 32, X + hi[k]);
-                    copy_async(at + 64, G + lo[k]);
-                    copy_async(at + 96, G + hi[k]);
+                    Raw<B>* const at = ring + (put * CH + k) * 128;
+                    copy_raw<B>(at, X + lo[k]);
+                    copy_raw<B>(at + 32, X + hi[k]);
+                    copy_raw<B>(at + 64, G + lo[k]);
+                    copy_raw<B>(at + 96, G + hi[k]);
                 }
             } else {
                 x1[k] = x2[k] = g1[k] = g2[k] = Raw<B>{};
@@ -604,11 +646,11 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
                 for (int k = 0; k < CH; ++k) {
                     x1[k] = x2[k] = g1[k] = g2[k] = Raw<B>{};
                     if (h < rows && in[k]) {       // (a lane reads what it copied itself)
-                        const uint4* const at = ring + (get * CH + k) * 128;
-                        x1[k] = *reinterpret_cast<const Raw<B>*>(at);
-                        x2[k] = *reinterpret_cast<const Raw<B>*>(at + 32);
-                        g1[k] = *reinterpret_cast<const Raw<B>*>(at + 64);
-                        g2[k] = *reinterpret_cast<const Raw<B>*>(at + 96);
+                        const Raw<B>* const at = ring + (get * CH + k) * 128;
+                        x1[k] = ld_ring(at);
+                        x2[k] = ld_ring(at + 32);
+                        g1[k] = ld_ring(at + 64);
+                        g2[k] = ld_ring(at + 96);
                     }
                 }
                 get = get + 1 == RING ? 0 : get + 1;
@@ -620,12 +662,7 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
                 unpack<T, V>(u2[k], x2[k]);
                 unpack<T, V>(v1[k], g1[k]);
                 unpack<T, V>(v2[k], g2[k]);
-                if (l + k * LPR < rp) {
-                    if (p.interleaved)
-                        turn_back<V>(v1[k], v2[k], c[k], s[k], true);
-                    else
-                        turn_back<V>(v1[k], v2[k], c[k], s[k], false);
-                }
+                if (l + k * LPR < rp) turn_back<V>(v1[k], v2[k], c[k], s[k], INTER);
             }
             if constexpr (RING == 1) load();
             const float ss = row_sum<LPR>(squares<V, CH>(u1, u2));
@@ -682,10 +719,10 @@ __global__ void __launch_bounds__(kHeadsThreads, 2) heads_bwd_kernel(const Heads
         }
     }
     __syncthreads();
-    for (int j = threadIdx.x; j < d; j += kHeadsThreads) {
+    for (int j = threadIdx.x; j < d; j += WARPS * 32) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kHeadsWarps; ++w) v += sums[w * d + j];
+        for (int w = 0; w < WARPS; ++w) v += sums[w * d + j];
         p.part[(int64_t)blockIdx.x * d + j] = v;
     }
 }
@@ -741,6 +778,16 @@ cudaError_t for_shape(HeadShape sh, F f) {
                 return f.template run<V, 32, 1>();
         }
     }
+    if constexpr (V == 8) {
+        if (sh.v == 4) {
+            switch (sh.lpr) {
+                case 8: return f.template run<4, 8, 1>();
+                case 16: return f.template run<4, 16, 1>();
+                default:
+                    return sh.ch == 2 ? f.template run<4, 32, 2>() : f.template run<4, 32, 1>();
+            }
+        }
+    }
     if (sh.v == 2) return sh.ch == 1 ? f.template run<2, 32, 1>() : f.template run<2, 32, 4>();
     return sh.ch == 2 ? f.template run<1, 32, 2>() : f.template run<1, 32, 8>();
 }
@@ -760,8 +807,9 @@ struct BwdRun {
     const HeadsParams& p;
     int ctas;
     cudaStream_t s;
-    template <int V, int LPR, int CH>
-    cudaError_t run() {
+    template <int V, int LPR, int CH, bool INTER>
+    cudaError_t launch() {
+        const auto kernel = heads_bwd_kernel<T, V, LPR, CH, INTER>;
         const int smem = heads_bwd_smem<T, V, CH>(p.d[0]);
         constexpr int MOST = heads_bwd_smem<T, V, CH>((int)kMaxHeadDim);
         if constexpr (MOST > 48 * 1024) {
@@ -770,14 +818,17 @@ struct BwdRun {
             unsigned long long ctx = 0;
             cudaError_t err = current_context_id(&ctx);
             if (err == cudaSuccess)
-                err = once_in_context(ctx, done, [] {
-                    return cudaFuncSetAttribute(heads_bwd_kernel<T, V, LPR, CH>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
+                err = once_in_context(ctx, done, [&] {
+                    return cudaFuncSetAttribute(
+                        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
                 });
             if (err != cudaSuccess) return err;
         }
-        return launch_pdl(heads_bwd_kernel<T, V, LPR, CH>, (unsigned)ctas, kHeadsThreads, smem, s,
-                          p);
+        return launch_pdl(kernel, (unsigned)ctas, heads_bwd_warps(V) * 32, smem, s, p);
+    }
+    template <int V, int LPR, int CH>
+    cudaError_t run() {
+        return p.interleaved ? launch<V, LPR, CH, true>() : launch<V, LPR, CH, false>();
     }
 };
 

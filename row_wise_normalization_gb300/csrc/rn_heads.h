@@ -11,6 +11,14 @@ constexpr int DT_E4M3 = 3;         // 8-bit floating point, caches only
 constexpr int64_t kMaxHeadDim = 512;
 constexpr int kHeadsThreads = 256;
 constexpr int kHeadsWarps = kHeadsThreads / 32;
+#ifndef RN_BWD_WARPS
+#define RN_BWD_WARPS 6
+#define RN_BWD_PER 2
+#endif
+// Warps of a CTA of the gradient's kernel, and CTAs of an SM: vectors of 8 elements take
+// about 150 registers a thread.
+constexpr int heads_bwd_warps(int v) { return v == 8 ? RN_BWD_WARPS : 8; }
+constexpr int heads_bwd_ctas_per_sm(int v) { return v == 8 ? RN_BWD_PER : 2; }
 
 // Rows of one kind (queries, keys, values): one for each head of each token.
 struct HeadSeg {
@@ -52,11 +60,13 @@ struct HeadsParams {
     bool norm, interleaved, back;   // back: the transposed rotation
 };
 
-// Pairs of vectors of v elements that fill a row of d, and the lanes that hold them.
+// Pairs of vectors of v elements that fill a row of d, and the lanes that hold them: vectors of 16
+// bytes (vec elements), of 8 where 16-bit rows have a rotation that 16 do not divide (32768 tokens of
+// 32 + 8 heads of 80, 40 of them turned, BF16: RN_T4 us, RN_T2 by two elements), else 2 or 1 elements.
 constexpr HeadShape head_shape(int v, int vec, int64_t d) {
     const int64_t pairs = (d / 2 + v - 1) / v;
-    if (v == vec) {
-        int lpr = 4;
+    if (v >= 4) {
+        int lpr = v == vec ? 4 : 8;
         while (lpr < 32 && lpr < pairs) lpr *= 2;
         return {v, lpr, pairs > 32 ? 2 : 1};
     }
