@@ -193,11 +193,8 @@ bool set_units(HeadsParams& p) {
 struct BwdCtas {
     int q, k;
 };
-#ifndef RN_BWD_GROUPS
-#define RN_BWD_GROUPS 16
-#endif
-constexpr int kBwdGroups = RN_BWD_GROUPS;
-BwdCtas bwd_ctas(const HeadsParams& p, int at_once, int warps, int ctas_per_sm) {
+constexpr int kBwdGroups = 16;
+BwdCtas bwd_ctas(const HeadsParams& p, int at_once, int warps) {
     int64_t most[2], work[2];
     for (int i = 0; i < 2; ++i) {
         most[i] = ((int64_t)p.seg[i].units + warps - 1) / warps;
@@ -205,7 +202,7 @@ BwdCtas bwd_ctas(const HeadsParams& p, int at_once, int warps, int ctas_per_sm) 
     }
     const int64_t all = work[0] + work[1];
     int64_t ctas = all / (warps * kBwdGroups);
-    if (ctas < 152 * ctas_per_sm) ctas = 152 * ctas_per_sm;
+    if (ctas < 152 * kHeadsBwdPerSm) ctas = 152 * kHeadsBwdPerSm;
     if (ctas > kHeadsBwdCtas) ctas = kHeadsBwdCtas;
     int64_t q = (ctas * work[0] + all / 2) / all;
     if (q > ctas - 1 && work[1] > 0) q = ctas - 1;
@@ -382,8 +379,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         p.seg[i].gh = g[i]->head_stride;
     }
     p.part = params ? (float*)workspace : nullptr;
-    const BwdCtas c = bwd_ctas(p, 32 / sh.lpr, heads_bwd_warps(sh.v),
-                               heads_bwd_ctas_per_sm(sh.v));
+    const BwdCtas c = bwd_ctas(p, 32 / sh.lpr, heads_bwd_warps(sh.v, sh.ch));
     p.first_k = c.q;
     const int ctas = c.q + c.k;
     return done(heads_bwd_launch(in->dtype, sh, p, ctas, dwq, dwk, s));

@@ -70,10 +70,7 @@ cudaError_t kv_slots_launch(const SlotsParams& p, cudaStream_t s) {
 // the flat list of the output's vectors, kGatherU of them a thread, whose slots are loaded first,
 // then all their rows, then all are stored: two waits for memory whatever the widths.
 constexpr int kGatherThreads = 256;
-#ifndef RN_GATHER_U
-#define RN_GATHER_U 4
-#endif
-constexpr int kGatherU = RN_GATHER_U;
+constexpr int kGatherU = 4;          // (131072 x 8 x 128 from e4m3 130 us; 2 144, 8 137)
 
 // NE e4m3 values, each an FP32 one times scale, rounded once. Pairs go through FP16, which holds
 // every e4m3 value: one conversion for two (131072 x 8 x 128 to BF16 with one for each value 146 us,

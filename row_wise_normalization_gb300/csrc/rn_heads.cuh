@@ -282,18 +282,13 @@ __device__ __forceinline__ float squares(const float (&x1)[CH][V], const float (
     }
 }
 
-#ifndef RN_FWD_MINB
-#define RN_FWD_MINB 3
-#endif
-#ifndef RN_FWD_RING
-#define RN_FWD_RING 4
-#endif
-// Row groups that a warp copies ahead: in shared memory, where each lane reads what it copied
-// itself; one, in registers, where accesses are of 2 bytes (asynchronous copies take no fewer
-// than 4) or a lane holds many chunks of a row.
+// Row groups that a warp copies ahead, in shared memory, where each lane reads what it copied
+// itself (32768 tokens of 64 + 8 heads of 128 BF16: 182 us; rows loaded into registers 226): four,
+// as deep as that gains anything; one, in registers, where accesses are of 2 bytes (asynchronous
+// copies take no fewer than 4) or a lane holds many chunks of a row.
 template <typename T, int V, int CH>
 constexpr int heads_ring() {
-    return V * (int)sizeof(T) >= 4 && CH <= 2 ? RN_FWD_RING : 1;
+    return V * (int)sizeof(T) < 4 || CH > 2 ? 1 : CH == 2 ? 2 : 4;
 }
 
 template <int B>
@@ -329,7 +324,8 @@ __device__ __forceinline__ void copy_raw(Raw<B>* smem, const void* p) {
 // APPEND: keys and values (segments 1 and 2) go into the cache, at the token's slot. A warp takes
 // p.per heads of its token, a row for each lane group at a time, with the next rows under way.
 template <typename T, int V, int LPR, int CH, bool APPEND, bool E4M3>
-__global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(const HeadsParams p) {
+__global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
+    heads_fwd_kernel(const HeadsParams p) {
     constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<T, V, CH>();
     __shared__ __align__(16) Raw<B> ring[RING > 1 ? kHeadsWarps : 1][RING > 1 ? RING : 1]
                                         [RING > 1 ? 2 * CH : 1][32];
@@ -517,27 +513,20 @@ __global__ void __launch_bounds__(kHeadsThreads, RN_FWD_MINB) heads_fwd_kernel(c
 // A lane meets the same columns in every row, so its shares of dw stay in registers over all the
 // rows of a warp. A CTA works on one segment and writes one row of p.part, and heads_join_kernel adds
 // those in a fixed order: no atomics, the same bits for the same sizes and grid. A warp goes through its units in turn, and its copies run ahead over their borders.
-#ifndef RN_BWD_RING
-#define RN_BWD_RING 4
-#endif
-template <typename T, int V, int CH>
-constexpr int heads_bwd_ring() {
-    return heads_ring<T, V, CH>() == 1 ? 1 : CH == 1 ? RN_BWD_RING : 2;
-}
 template <typename T, int V, int CH>
 constexpr int heads_bwd_smem(int d) {
-    constexpr int WARPS = heads_bwd_warps(V);
-    const int ring = heads_bwd_ring<T, V, CH>() > 1
-                         ? WARPS * heads_bwd_ring<T, V, CH>() * 4 * CH * 32 * V * (int)sizeof(T)
+    constexpr int WARPS = heads_bwd_warps(V, CH);
+    const int ring = heads_ring<T, V, CH>() > 1
+                         ? WARPS * heads_ring<T, V, CH>() * 4 * CH * 32 * V * (int)sizeof(T)
                          : 0;
     const int sums = WARPS * d * 4;
     return ring > sums ? ring : sums;
 }
 
 template <typename T, int V, int LPR, int CH, bool INTER>
-__global__ void __launch_bounds__(heads_bwd_warps(V) * 32, heads_bwd_ctas_per_sm(V)) heads_bwd_kernel(const HeadsParams p) {
-    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_bwd_ring<T, V, CH>();
-    constexpr int WARPS = heads_bwd_warps(V);
+__global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm) heads_bwd_kernel(const HeadsParams p) {
+    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<T, V, CH>();
+    constexpr int WARPS = heads_bwd_warps(V, CH);
     extern __shared__ uint4 shared[];      // the warps' rings; at the end their sums
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sg = lane / LPR;
@@ -824,7 +813,7 @@ struct BwdRun {
                 });
             if (err != cudaSuccess) return err;
         }
-        return launch_pdl(kernel, (unsigned)ctas, heads_bwd_warps(V) * 32, smem, s, p);
+        return launch_pdl(kernel, (unsigned)ctas, heads_bwd_warps(V, CH) * 32, smem, s, p);
     }
     template <int V, int LPR, int CH>
     cudaError_t run() {

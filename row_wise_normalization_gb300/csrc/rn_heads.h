@@ -9,16 +9,16 @@ namespace rn {
 
 constexpr int DT_E4M3 = 3;         // 8-bit floating point, caches only
 constexpr int64_t kMaxHeadDim = 512;
-constexpr int kHeadsThreads = 256;
-constexpr int kHeadsWarps = kHeadsThreads / 32;
-#ifndef RN_BWD_WARPS
-#define RN_BWD_WARPS 6
-#define RN_BWD_PER 2
-#endif
-// Warps of a CTA of the gradient's kernel, and CTAs of an SM: vectors of 8 elements take
-// about 150 registers a thread.
-constexpr int heads_bwd_warps(int v) { return v == 8 ? RN_BWD_WARPS : 8; }
-constexpr int heads_bwd_ctas_per_sm(int v) { return v == 8 ? RN_BWD_PER : 2; }
+// Warps of a CTA of the forward kernel: few, since a CTA's place is free again when its last warp
+// ends, and warps take different times (65536 keys' and values' rows a head into an 8-bit cache: two
+// warps a CTA 52 us, eight 56).
+constexpr int kHeadsWarps = 2;
+constexpr int kHeadsThreads = kHeadsWarps * 32;
+// Warps of a CTA of the gradient's kernel, of which an SM holds two: a lane that holds 16 values of a
+// row takes about 150 registers (six warps; with eight at 128 registers, some of them in memory,
+// 32768 tokens of 64 + 8 heads of 128 BF16 took 282 us, not 273).
+constexpr int heads_bwd_warps(int v, int ch) { return v * ch >= 8 ? 6 : 8; }
+constexpr int kHeadsBwdPerSm = 2;
 
 // Rows of one kind (queries, keys, values): one for each head of each token.
 struct HeadSeg {
@@ -61,8 +61,8 @@ struct HeadsParams {
 };
 
 // Pairs of vectors of v elements that fill a row of d, and the lanes that hold them: vectors of 16
-// bytes (vec elements), of 8 where 16-bit rows have a rotation that 16 do not divide (32768 tokens of
-// 32 + 8 heads of 80, 40 of them turned, BF16: RN_T4 us, RN_T2 by two elements), else 2 or 1 elements.
+// bytes (vec elements); of 8 bytes where 16 do not divide a 16-bit row's rotation (32768 tokens of 32
+// + 8 heads of 80, 40 values of each turned, BF16 105 us, 140 by two elements); else 2 or 1 elements.
 constexpr HeadShape head_shape(int v, int vec, int64_t d) {
     const int64_t pairs = (d / 2 + v - 1) / v;
     if (v >= 4) {
@@ -74,20 +74,14 @@ constexpr HeadShape head_shape(int v, int vec, int64_t d) {
     return {v, 32, pairs > 32 * few ? many : few};
 }
 
-// Heads of a unit: a multiple of what a warp holds at once (32 / lpr rows), up to kHeadsLoops times,
-// fewer where that leaves warps without one.
-#ifndef RN_LOOPS
-#define RN_LOOPS 16
-#endif
-#ifndef RN_MINU
-#define RN_MINU 4
-#endif
-constexpr int kHeadsLoops = RN_LOOPS;
+// Heads of a unit, one token's: what a warp holds at once (32 / lpr rows), kHeadsLoops times, so
+// that a token's factors serve many rows (16 times 182 us for 32768 tokens of 64 + 8 heads of 128 BF16,
+// four times 198); fewer where that leaves an SM fewer than four units.
+constexpr int kHeadsLoops = 16;
 constexpr int heads_per_unit(int lpr, int64_t heads, int64_t tokens) {
     const int at_once = 32 / lpr;
     int loops = kHeadsLoops;
-    while (loops > 1 &&
-           tokens * ((heads + at_once * loops - 1) / (at_once * loops)) < 152 * RN_MINU)
+    while (loops > 1 && tokens * ((heads + at_once * loops - 1) / (at_once * loops)) < 152 * 4)
         loops /= 2;
     return loops * at_once;
 }
@@ -98,10 +92,10 @@ cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape shape, const 
 // ctas: rows of p.part.
 cudaError_t heads_bwd_launch(int dtype, HeadShape shape, const HeadsParams& p, int ctas, void* dwq,
                              void* dwk, cudaStream_t s);
-#ifndef RN_BWD_CTAS
-#define RN_BWD_CTAS 2432
-#endif
-constexpr int kHeadsBwdCtas = RN_BWD_CTAS;   // two a GB300's SM: rows of the gradient's workspace, at most
+// CTAs of the gradient's kernel, and rows of its workspace, at most: eight rounds of what a GB300
+// holds, since CTAs take different times (32768 tokens of 64 + 8 heads of 128 BF16: one round 365 us,
+// four 309, eight 289, sixteen 290).
+constexpr int kHeadsBwdCtas = 2432;
 
 struct SlotsParams {
     const void* page_table;    // [seqs][ld]
