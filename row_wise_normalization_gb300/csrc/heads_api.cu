@@ -501,6 +501,7 @@ int kv_gather(const rn_cache* cache, int64_t d, const void* slots, int itype, in
         g.token = fast_div((uint32_t)(heads * per));
         g.head = fast_div((uint32_t)per);
         g.scale = i == 0 ? cache->k_scale : cache->v_scale;
+        if (g.total / 1024 >= kMaxCount) return RN_ERR_SIZE;     // (the grid of one launch)
     }
     return done(kv_gather_launch(cache->dtype, dtype, ne, p, (cudaStream_t)stream));
 }

@@ -13,9 +13,10 @@
 // weights are shared by a token's heads. LPR lanes hold a row, so that 32 / LPR
 // rows fill a warp, and a lane holds whole pairs, its vector of first values and
 // its vector of second ones: the rotation then needs no exchange, and the only
-// one left is the row's sum, log2(LPR) shuffles. A warp takes one token and
-// U * 32 / LPR of its heads: cosines, sines and weights are read once for U rows.
-// Arithmetic is FP32, each value is rounded once, to its storage type.
+// one left is the row's sum, log2(LPR) shuffles. A warp takes one token and up to
+// kHeadsLoops * 32 / LPR of its heads, for which cosines, sines and weights are
+// read once. Arithmetic is FP32 (packed in pairs), each value is rounded once, to its
+// storage type.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -152,18 +153,22 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// V values as e4m3, to nearest even, those beyond its largest to that.
+// V values times f as e4m3, to nearest even, those beyond its largest to that. (f comes last: the
+// rotation of values near FP32's largest stays finite.)
 template <int V>
-__device__ __forceinline__ void st_e4m3(uint8_t* p, const float* v) {
+__device__ __forceinline__ void st_e4m3(uint8_t* p, const float* v, float f) {
     if constexpr (V == 1) {
-        *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+        *p = __nv_cvt_float_to_fp8(v[0] * f, __NV_SATFINITE, __NV_E4M3);
     } else {
         uint32_t w[(V + 3) / 4] = {};
+        const F2 f22 = f2s(f);
 #pragma unroll
-        for (int k = 0; k < V; k += 2)
-            w[k / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[k], v[k + 1]),
-                                                           __NV_SATFINITE, __NV_E4M3)
+        for (int k = 0; k < V; k += 2) {
+            float2 t;
+            f2_get(mul2(f2(v[k], v[k + 1]), f22), t.x, t.y);
+            w[k / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(t, __NV_SATFINITE, __NV_E4M3)
                         << (8 * (k % 4));
+        }
         Raw<V> r;
 #pragma unroll
         for (int k = 0; k < (V + 3) / 4; ++k) r.w[k] = w[k];
@@ -188,14 +193,20 @@ __device__ __forceinline__ HeadUnit head_unit(const HeadsParams& p, uint32_t uni
     return {t, seg, (int)(unit - t * p.seg[seg].per.d) * p.per};
 }
 
-// A row's rotation and weights as two factors a value: y_j = r (x_j A_j + x_partner B_j), where the
+// A row's rotation and weights as two factors a value: y_j = r x_j A_j + r x_partner B_j, where the
 // partner is the other value of j's pair: A = w c, B = -+ w_partner s. They are a token's, so that a
-// row costs three packed products for two values. Values that are not turned have A alone. What a
-// row is multiplied by before it is stored is in them too.
+// row costs three packed products for two values. Values that are not turned have A alone. (r comes
+// first, as in rms_fwd: r x stays within sqrt(d) whatever x and w.)
 template <int V>
 struct Factors {
     F2 a1[(V + 1) / 2], b1[(V + 1) / 2], a2[(V + 1) / 2], b2[(V + 1) / 2];   // first, second vector
 };
+
+__device__ __forceinline__ F2 swap2(F2 v) {
+    float a, b;
+    f2_get(v, a, b);
+    return f2(b, a);
+}
 
 // Factors of a lane's pair of vectors, from weights w1, w2 and, where it is turned, the table's
 // cosines c and sines s.
@@ -230,7 +241,7 @@ __device__ __forceinline__ void set_factors(Factors<V>& f, const float (&w1)[V],
     }
 }
 
-// x1, x2 := r (x A + partner B), or r x A where nothing is turned.
+// x1, x2 := (r x) A + (r partner) B, or (r x) A where nothing is turned.
 template <int V>
 __device__ __forceinline__ void apply_factors(float (&x1)[V], float (&x2)[V], const Factors<V>& f,
                                               float r, bool turned, bool interleaved) {
@@ -238,21 +249,21 @@ __device__ __forceinline__ void apply_factors(float (&x1)[V], float (&x2)[V], co
         float a1, a2, b1, b2;
         f2_get(f.a1[0], a1, a2);
         f2_get(f.b1[0], b1, b2);
-        const float t = x1[0], u = x2[0];
-        x1[0] = r * (turned ? t * a1 + u * b1 : t * a1);
-        x2[0] = r * (turned ? u * a2 + t * b2 : u * a2);
+        const float t = r * x1[0], u = r * x2[0];
+        x1[0] = turned ? t * a1 + u * b1 : t * a1;
+        x2[0] = turned ? u * a2 + t * b2 : u * a2;
     } else {
         const F2 r2 = f2s(r);
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
-            const F2 u = f2(x1[i], x1[i + 1]), v = f2(x2[i], x2[i + 1]);
+            const F2 u = mul2(f2(x1[i], x1[i + 1]), r2), v = mul2(f2(x2[i], x2[i + 1]), r2);
             F2 a = mul2(u, f.a1[i / 2]), b = mul2(v, f.a2[i / 2]);
             if (turned) {
-                a = fma2(interleaved ? f2(x1[i + 1], x1[i]) : v, f.b1[i / 2], a);
-                b = fma2(interleaved ? f2(x2[i + 1], x2[i]) : u, f.b2[i / 2], b);
+                a = fma2(interleaved ? swap2(u) : v, f.b1[i / 2], a);
+                b = fma2(interleaved ? swap2(v) : u, f.b2[i / 2], b);
             }
-            f2_get(mul2(a, r2), x1[i], x1[i + 1]);
-            f2_get(mul2(b, r2), x2[i], x2[i + 1]);
+            f2_get(a, x1[i], x1[i + 1]);
+            f2_get(b, x2[i], x2[i + 1]);
         }
     }
 }
@@ -406,7 +417,6 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
         }
         float c[CH][V], s[CH][V];
         ld_turn<V, CH, LPR>(c, s, row, l, rp);
-        const float scale = eight ? p.store[u0.seg] : 1.f;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             float w1[V], w2[V];
@@ -414,13 +424,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
             unpack<T, V>(w2, wb[k]);
             if (!norm || !S.w) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) w1[i] = w2[i] = scale;
-            } else if (eight) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    w1[i] *= scale;
-                    w2[i] *= scale;
-                }
+                for (int i = 0; i < V; ++i) w1[i] = w2[i] = 1.f;
             }
             if (p.back) {
 #pragma unroll
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
         const uint32_t page = fast_quot((uint32_t)slot, p.page);
         at = page * S.yb + (int64_t)((uint32_t)slot - page * p.page.d) * S.yt + h * S.yh;
     }
-    const float inv = 1.f / (float)d;
+    const float inv = 1.f / (float)d, store = eight ? p.store[u0.seg] : 1.f;
     for (; h - sg < end; h += SG) {
         if constexpr (RING > 1) {
             load();
@@ -493,8 +497,8 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
                         for (int i = 0; i < V; ++i) a[k][i] = e[k][i] = 0.f;
                     }
                     if (eight) {
-                        st_e4m3<V>((uint8_t*)Y + lo[k], a[k]);
-                        st_e4m3<V>((uint8_t*)Y + hi[k], e[k]);
+                        st_e4m3<V>((uint8_t*)Y + lo[k], a[k], store);
+                        st_e4m3<V>((uint8_t*)Y + hi[k], e[k], store);
                     } else {
                         st_elems<T, V>((T*)Y + lo[k], a[k]);
                         st_elems<T, V>((T*)Y + hi[k], e[k]);
@@ -511,8 +515,11 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
 // again from x:
 //   dx_j = r (w_j g_j - x_j r^2 mean_k(w_k g_k x_k)),   dw_j = sum over rows of g_j x_j r.
 // A lane meets the same columns in every row, so its shares of dw stay in registers over all the
-// rows of a warp. A CTA works on one segment and writes one row of p.part, and heads_join_kernel adds
-// those in a fixed order: no atomics, the same bits for the same sizes and grid. A warp goes through its units in turn, and its copies run ahead over their borders.
+// rows of a warp. A CTA works on one segment and writes one row of p.part, and heads_join_kernel
+// adds those in a fixed order: no atomics, the same bits for the same sizes and grid. A warp goes
+// through its units in turn, and its copies run ahead over their borders. (The forward kernel's warps
+// have one unit each: with several, 32768 tokens of 64 + 8 heads of 128 BF16 took 187 us and not 184,
+// since fewer of them even out less.)
 template <typename T, int V, int CH>
 constexpr int heads_bwd_smem(int d) {
     constexpr int WARPS = heads_bwd_warps(V, CH);
@@ -524,7 +531,8 @@ constexpr int heads_bwd_smem(int d) {
 }
 
 template <typename T, int V, int LPR, int CH, bool INTER>
-__global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm) heads_bwd_kernel(const HeadsParams p) {
+__global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
+    heads_bwd_kernel(const HeadsParams p) {
     constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<T, V, CH>();
     constexpr int WARPS = heads_bwd_warps(V, CH);
     extern __shared__ uint4 shared[];      // the warps' rings; at the end their sums
@@ -717,10 +725,12 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm) h
 }
 
 // The CTAs' rows into the weights' gradients: columns of queries from the first first_k rows, of
-// keys from the others. 8 columns a CTA, 128 rows of them at a time, so that each thread has about ten loads,
-// none of which waits for another; then the warp's four rows, then the warps in order.
+// keys from the others. Latency bounds it: 8 columns a CTA and 128 rows of them at a time, so that
+// a thread has at most 19 rows, in two batches whose loads do not wait for one another; then the
+// warp's four rows, then the warps in order.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinCols = 8;
+constexpr int kJoinBatch = 10;     // rows a thread loads together
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
     heads_join_kernel(const float* part, int d, int first_k, int ctas, T* dwq, T* dwk) {
@@ -734,9 +744,15 @@ __global__ void __launch_bounds__(kJoinThreads)
     if (!out) return;
     float v = 0.f;
     if (col < d) {
-#pragma unroll 10
-        for (int r = begin + threadIdx.x / kJoinCols; r < end; r += kJoinThreads / kJoinCols)
-            v += __ldcg(part + (int64_t)r * d + col);
+        constexpr int ROWS = kJoinThreads / kJoinCols;
+        for (int r = begin + threadIdx.x / kJoinCols; r < end; r += kJoinBatch * ROWS) {
+            float x[kJoinBatch];
+#pragma unroll
+            for (int u = 0; u < kJoinBatch; ++u)
+                x[u] = r + u * ROWS < end ? __ldcg(part + (int64_t)(r + u * ROWS) * d + col) : 0.f;
+#pragma unroll
+            for (int u = 0; u < kJoinBatch; ++u) v += x[u];
+        }
     }
 #pragma unroll
     for (int o = kJoinCols; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -752,7 +768,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 // ---- instances -----------------------------------------------------------------
-// Calls f.template operator()<V, LPR, CH>() for a shape.
+// Calls f.run<V, LPR, CH>() for a shape.
 template <typename T, typename F>
 cudaError_t for_shape(HeadShape sh, F f) {
     constexpr int V = Elem<T>::kVec;

@@ -407,3 +407,69 @@ def test_host_rows():
                          k_out=torch.empty_like(k).pin_memory())
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0].cpu()) and torch.equal(got[1], want[1].cpu())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_keys_alone_through_the_c_abi(dtype):
+    """No queries: every unit and every partial sum belongs to the keys."""
+    c = Case(37, 1, 3, 64, 64, dtype)
+    code = {"f32": 0, "bf16": 1, "f16": 2}[dtype]
+    n, hk, d = 37, 3, 64
+    k, none = c.k.contiguous(), capi.heads(0, 0, 0, 0, 0)
+    rows = lambda t: (t.data_ptr(), hk, 0, hk * d, d)  # noqa: E731
+    g = rounded(c.rng, (n, hk, d), dtype)
+    out, dk = torch.empty_like(k), torch.empty_like(k)
+    dw = torch.empty(d, dtype=DT[dtype], device="cuda")
+    ws = torch.empty(capi.qk_rope_bwd_workspace_size(d), dtype=torch.uint8, device="cuda")
+    qk = capi.qk(0, 0, 0, 0, 0, *rows(k), 0, c.wk.data_ptr(), c.pos.data_ptr(), c.table.data_ptr(), 50, 64,
+                 64, 1, n, d, code, 1, 1, 0, EPS, 0)
+    st = torch.cuda.current_stream().cuda_stream
+    capi.check(capi.qk_rope_fwd(qk, none, capi.heads(*rows(out)), st))
+    capi.check(capi.qk_rope_bwd(qk, none, capi.heads(*rows(g)), none, capi.heads(*rows(dk)), 0,
+                                dw.data_ptr(), ws.data_ptr(), ws.numel(), st))
+    head_checks.check_rope(f64(out), *c.want("k"), True, dtype)
+    want = c.want_bwd("k", g)
+    head_checks.check_rope_bwd(f64(dk), want, True, dtype)
+    head_checks.check_dw(f64(dw), want, n, hk, dtype)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_calls(seed):
+    """Shapes, strides, alignments, types and modes at random."""
+    rng = np.random.default_rng([77, seed])
+    dtype = TYPES[rng.integers(3)]
+    d = 2 * int(rng.integers(1, 100)) if rng.random() < 0.6 else int(rng.choice([64, 80, 96, 112, 128, 192, 256, 384]))
+    rot = int(rng.choice([d, d // 4 * 2, 2 * rng.integers(0, d // 2 + 1)]))
+    n, hq, hk = int(rng.integers(1, 90)), int(rng.integers(1, 14)), int(rng.integers(0, 6))
+    norm = bool(rng.random() < 0.7)
+    c = Case(n, hq, hk, d, rot, dtype, norm, bool(rng.random() < 0.5), "i32" if seed % 2 else "i64")
+
+    def place(x):
+        """The values of x in memory with gaps between tokens and heads, at some element offset."""
+        if x is None:
+            return None
+        gap, head, off = int(rng.integers(0, 9)), int(rng.integers(0, 5)), int(rng.integers(0, 9))
+        if rng.random() < 0.4:
+            gap, head, off = 0, 0, 0
+        hs = d + head
+        ts = x.shape[1] * hs + gap
+        t = _guarded((off + n * ts,), x.dtype)[off:].as_strided(x.shape, (ts, hs, 1))
+        t.copy_(x)
+        return t
+
+    q, k = place(c.q), place(c.k)
+    qo, ko = place(torch.zeros_like(q)), place(torch.zeros_like(k)) if hk else None
+    rn.qk_rope_fwd(q, k, *c.args(), norm=norm, q_out=qo, k_out=ko, **c.kw)
+    head_checks.check_rope(f64(qo), *c.want("q"), norm, dtype, "q")
+    gq, gk = place(rounded(rng, (n, hq, d), dtype)), place(rounded(rng, (n, hk, d), dtype)) if hk else None
+    dq, dk, dwq, dwk = rn.qk_rope_bwd(gq, gk, q, k, *c.args(), norm=norm, dq=qo, dk=ko, **c.kw)
+    want = c.want_bwd("q", gq)
+    head_checks.check_rope_bwd(f64(dq), want, norm, dtype, "dq")
+    if norm:
+        head_checks.check_dw(f64(dwq), want, n, hq + hk, dtype, "dwq")
+    if hk:
+        rn.qk_rope_fwd(q, k, *c.args(), norm=norm, k_out=ko, **c.kw)
+        head_checks.check_rope(f64(ko), *c.want("k"), norm, dtype, "k")
+        want = c.want_bwd("k", gk)
+        rn.qk_rope_bwd(gq, gk, q, k, *c.args(), norm=norm, dk=gk, **c.kw)
+        head_checks.check_rope_bwd(f64(gk), want, norm, dtype, "dk in place")

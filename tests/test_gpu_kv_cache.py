@@ -200,6 +200,23 @@ def test_append_saturates_and_keeps_nan():
         assert got[:6] == want and got[6] != got[6] and got[7] == 0
 
 
+def test_append_turns_the_largest_values_without_nan():
+    """The rotation comes before the scale: what it leaves finite is held at 448, not as NaN."""
+    big = torch.finfo(torch.bfloat16).max * 0.5
+    k = torch.full((1, 1, 64), big, dtype=torch.bfloat16, device="cuda")
+    table = torch.cat([torch.full((1, 32), 0.6), torch.full((1, 32), 0.8)], 1).cuda()
+    pos = torch.zeros(1, dtype=torch.int64, device="cuda")
+    kc, vc = (torch.zeros(1, 1, 1, 64, device="cuda").to(E4M3) for _ in range(2))
+    rn.kv_append(k, -k, pos, kc, vc, pos, table, k_scale=0.001, v_scale=0.001)
+    got = kc.float().flatten()
+    assert bool((got[:32] == -448).all()) and bool((got[32:] == 448).all())
+    assert bool((vc.float() == -448).all())
+    # a norm's factor comes before the weights: a row beyond the squares' range gives zeros
+    w = torch.full((64,), 1e30, dtype=torch.bfloat16, device="cuda")
+    q, _ = rn.qk_rope_fwd(k, None, pos, table, w)
+    assert not bool(q.any())
+
+
 def test_every_e4m3_value_comes_out():
     bits = torch.arange(256, dtype=torch.uint8, device="cuda")
     kc = bits.view(E4M3).view(8, 1, 1, 32)
@@ -477,16 +494,17 @@ def test_calls_of_several_threads():
     assert not wrong
 
 
-def test_calls_back_to_back_wait_for_one_another():
+@pytest.mark.parametrize("d,rot", [(128, 128), (80, 40), (132, 132), (34, 34)])
+def test_calls_back_to_back_wait_for_one_another(d, rot):
     """Each call reads what the one ahead of it wrote, without a pause: append, gather, rotate back
     and append elsewhere, over and over, against the same chain with a synchronisation after every
     call."""
-    c = Case(600, 8, 8, 128, 128, "bf16", outside=False)
+    c = Case(600, 8, 8, d, rot, "bf16", outside=False)
     n = c.n
     slots = [torch.from_numpy(c.rng.permutation(700)[:n]).cuda() for _ in range(2)]
 
     def chain(wait):
-        caches = [torch.zeros(100, 7, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        caches = [torch.zeros(100, 7, 8, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
         k, v = c.q.contiguous(), c.k.contiguous()
         for i in range(40):
             q = rn.kv_append(k, v, slots[i % 2], *caches, c.pos, c.table, q=v)
