@@ -175,7 +175,8 @@ void set_y(HeadSeg& g, const rn_heads* h) {
 // The units of every segment; false where they are too many for one launch.
 bool set_units(HeadsParams& p) {
     int64_t total = 0;
-    for (HeadSeg& g : p.seg) {
+    for (int i = 0; i < 2; ++i) {           // (values go with their keys)
+        HeadSeg& g = p.seg[i];
         const int64_t groups = (g.heads + p.per - 1) / p.per;
         g.per = fast_div((uint32_t)(groups > 0 ? groups : 1));
         total += groups * p.tokens;

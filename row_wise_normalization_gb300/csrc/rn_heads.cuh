@@ -184,6 +184,8 @@ struct HeadUnit {
     int seg, head;
 };
 __device__ __forceinline__ HeadUnit head_unit(const HeadsParams& p, uint32_t unit) {
+    // (a loop, though only two segments have units: from a choice of two the compiler selects every
+    // field of theirs, which cost 32768 tokens' keys and values 5 us of 45)
     int seg = 0;
     while (seg < 2 && unit >= p.seg[seg].units) {
         unit -= p.seg[seg].units;
@@ -332,14 +334,18 @@ __device__ __forceinline__ void copy_raw(Raw<B>* smem, const void* p) {
                      : "memory");
 }
 
-// APPEND: keys and values (segments 1 and 2) go into the cache, at the token's slot. A warp takes
+// APPEND: keys (segment 1) go into the cache, at the token's slot, and with each the value of the same
+// head (segment 2, which has no units of its own: 32768 tokens of 8 heads of 128, BF16 into 8 bits,
+// without queries 45 us, 52 with units for values; three groups ahead there, 46 with four). A warp takes
 // p.per heads of its token, a row for each lane group at a time, with the next rows under way.
 template <typename T, int V, int LPR, int CH, bool APPEND, bool E4M3>
 __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
     heads_fwd_kernel(const HeadsParams p) {
-    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<T, V, CH>();
+    constexpr int SG = 32 / LPR, B = V * (int)sizeof(T);
+    constexpr int DEEP = heads_ring<T, V, CH>(), RING = APPEND && DEEP > 3 ? 3 : DEEP;
+    constexpr int SIDES = APPEND ? 4 : 2;      // vectors of a group: a key's two, its value's two
     __shared__ __align__(16) Raw<B> ring[RING > 1 ? kHeadsWarps : 1][RING > 1 ? RING : 1]
-                                        [RING > 1 ? 2 * CH : 1][32];
+                                        [RING > 1 ? SIDES * CH : 1][32];
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5;
     const uint32_t unit = blockIdx.x * kHeadsWarps + warp;
@@ -347,8 +353,9 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
     const int lane = threadIdx.x & 31, l = lane % LPR, sg = lane / LPR;
     const HeadUnit u0 = head_unit(p, unit);
     const HeadSeg& S = p.seg[u0.seg];
-    const bool value = APPEND && u0.seg == 2;
-    const int d = p.d[u0.seg], rp = value ? 0 : p.rot / 2 / V;
+    const bool key = APPEND && u0.seg == 1;
+    const HeadSeg& W = p.seg[2];               // the values beside keys
+    const int d = p.d[0], rp = p.rot / 2 / V;
     const uint32_t b = fast_quot(u0.token, p.len), t = u0.token - b * p.len.d;
     const int end = S.heads < u0.head + p.per ? S.heads : u0.head + p.per;
     int lo[CH], hi[CH];
@@ -361,17 +368,34 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
     }
     int h = u0.head + sg;
     const T* X = (const T*)S.x + b * S.xb + t * S.xt + h * S.xh;
-    // the next row of the lane group, whose first head is `first`: into the ring, or registers
-    Raw<B> n1[CH], n2[CH];
+    const T* Z = key ? (const T*)W.x + b * W.xb + t * W.xt + h * W.xh : nullptr;
+    // the lane group's next row (and value): into the ring, or registers
+    Raw<B> n1[CH], n2[CH], z1[CH], z2[CH];
     int ahead = u0.head, put = 0, get = 0;
     auto load = [&]() {
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const bool there = ahead + sg < end && in[k];
+            if (APPEND && key) {
+                const int q = 2 * (l + k * LPR) * V;
+                const bool beside = ahead + sg < end && q < p.d[2];
+                if constexpr (RING > 1) {
+                    if (beside) {
+                        copy_raw<B>(&ring[warp][put][SIDES * k + 2][lane], Z + q);
+                        copy_raw<B>(&ring[warp][put][SIDES * k + 3][lane], Z + q + V);
+                    }
+                } else {
+                    z1[k] = z2[k] = Raw<B>{};
+                    if (beside) {
+                        z1[k] = ld_raw<B>(Z + q);
+                        z2[k] = ld_raw<B>(Z + q + V);
+                    }
+                }
+            }
             if constexpr (RING > 1) {
                 if (there) {
-                    copy_raw<B>(&ring[warp][put][2 * k][lane], X + lo[k]);
-                    copy_raw<B>(&ring[warp][put][2 * k + 1][lane], X + hi[k]);
+                    copy_raw<B>(&ring[warp][put][SIDES * k][lane], X + lo[k]);
+                    copy_raw<B>(&ring[warp][put][SIDES * k + 1][lane], X + hi[k]);
                 }
             } else {
                 n1[k] = n2[k] = Raw<B>{};
@@ -387,14 +411,15 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
         }
         ahead += SG;
         X += SG * S.xh;
+        if (APPEND && key) Z += SG * W.xh;
     };
     pdl_wait();
     // All that does not wait for anything is under way before the first wait, the position's, for
     // the table's row.
-    const bool norm = p.norm && !value, eight = E4M3 && u0.seg > 0;
+    const bool norm = p.norm, eight = E4M3 && key;
     int64_t pos = 0, slot = 0;
     if (rp > 0) pos = ld_id(p.positions, u0.token, p.itype);
-    if (APPEND && u0.seg > 0) slot = ld_id(p.slots, u0.token, p.itype);
+    if (key) slot = ld_id(p.slots, u0.token, p.itype);
 #pragma unroll
     for (int k = 0; k < (RING > 1 ? RING - 1 : 1); ++k) load();
     Raw<B> wa[CH], wb[CH];
@@ -408,8 +433,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
     }
     bool there = true;
     Factors<V> f[CH];
-    // (values in their own type are copied: no factors)
-    if (!value || E4M3) {
+    {
         const float* row = nullptr;
         if (rp > 0) {
             there = pos >= 0 && pos < p.table_rows;
@@ -433,16 +457,18 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
             set_factors<V>(f[k], w1, w2, c[k], s[k], l + k * LPR < rp, p.interleaved);
         }
     }
-    int64_t at = b * S.yb + t * S.yt + h * S.yh;
-    if (APPEND && u0.seg > 0) {
+    int64_t at = b * S.yb + t * S.yt + h * S.yh, zat = 0;
+    if (key) {
         if (slot < 0 || slot >= p.nslots) {     // (the whole warp: one token)
             if constexpr (RING > 1) copy_wait<0>();
             return;
         }
         const uint32_t page = fast_quot((uint32_t)slot, p.page);
-        at = page * S.yb + (int64_t)((uint32_t)slot - page * p.page.d) * S.yt + h * S.yh;
+        const int64_t i = (uint32_t)slot - page * p.page.d;
+        at = page * S.yb + i * S.yt + h * S.yh;
+        zat = page * W.yb + i * W.yt + h * W.yh;
     }
-    const float inv = 1.f / (float)d, store = eight ? p.store[u0.seg] : 1.f;
+    const float inv = 1.f / (float)d;
     for (; h - sg < end; h += SG) {
         if constexpr (RING > 1) {
             load();
@@ -451,58 +477,66 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
             for (int k = 0; k < CH; ++k) {
                 n1[k] = n2[k] = Raw<B>{};
                 if (h < end && in[k]) {       // (a lane reads what it copied itself)
-                    n1[k] = ld_ring(&ring[warp][get][2 * k][lane]);
-                    n2[k] = ld_ring(&ring[warp][get][2 * k + 1][lane]);
+                    n1[k] = ld_ring(&ring[warp][get][SIDES * k][lane]);
+                    n2[k] = ld_ring(&ring[warp][get][SIDES * k + 1][lane]);
                 }
             }
-            get = get + 1 == RING ? 0 : get + 1;
         }
-        Raw<B> o1[CH], o2[CH];
+        float a[CH][V], e[CH][V];
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            o1[k] = n1[k];
-            o2[k] = n2[k];
+            unpack<T, V>(a[k], n1[k]);
+            unpack<T, V>(e[k], n2[k]);
         }
-        if constexpr (RING == 1) load();
-        char* const Y = (char*)S.y + (eight ? at : at * (int)sizeof(T));
-        if (value && !E4M3) {
-            if (h < end) {
-#pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    if (!in[k]) continue;
-                    st_raw<B>((T*)Y + lo[k], o1[k]);
-                    st_raw<B>((T*)Y + hi[k], o2[k]);
-                }
-            }
-        } else {
-            float a[CH][V], e[CH][V];
+        if (key && h < end) {
+            // the value, as it is or in 8 bits
+            char* const Y = (char*)W.y + zat * (E4M3 ? 1 : (int)sizeof(T));
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
-                unpack<T, V>(a[k], o1[k]);
-                unpack<T, V>(e[k], o2[k]);
+                const int q = 2 * (l + k * LPR) * V;
+                if (q >= p.d[2]) continue;
+                if constexpr (RING > 1) {
+                    z1[k] = ld_ring(&ring[warp][get][SIDES * k + 2][lane]);
+                    z2[k] = ld_ring(&ring[warp][get][SIDES * k + 3][lane]);
+                }
+                if constexpr (E4M3) {
+                    float v[V];
+                    unpack<T, V>(v, z1[k]);
+                    st_e4m3<V>((uint8_t*)Y + q, v, p.store[2]);
+                    unpack<T, V>(v, z2[k]);
+                    st_e4m3<V>((uint8_t*)Y + q + V, v, p.store[2]);
+                } else {
+                    st_raw<B>((T*)Y + q, z1[k]);
+                    st_raw<B>((T*)Y + q + V, z2[k]);
+                }
             }
-            float r = 1.f;
-            if (norm) r = rsqrtf(fmaf(row_sum<LPR>(squares<V, CH>(a, e)), inv, p.eps));
-            if (h < end) {
+            zat += SG * W.yh;
+        }
+        if constexpr (RING == 1)
+            load();
+        else
+            get = get + 1 == RING ? 0 : get + 1;
+        float r = 1.f;
+        if (norm) r = rsqrtf(fmaf(row_sum<LPR>(squares<V, CH>(a, e)), inv, p.eps));
+        if (h < end) {
 #pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    if (!in[k]) continue;
-                    const bool turned = l + k * LPR < rp;
-                    if (p.interleaved)
-                        apply_factors<V>(a[k], e[k], f[k], r, turned, true);
-                    else
-                        apply_factors<V>(a[k], e[k], f[k], r, turned, false);
-                    if (!there) {
+            for (int k = 0; k < CH; ++k) {
+                if (!in[k]) continue;
+                const bool turned = l + k * LPR < rp;
+                if (p.interleaved)
+                    apply_factors<V>(a[k], e[k], f[k], r, turned, true);
+                else
+                    apply_factors<V>(a[k], e[k], f[k], r, turned, false);
+                if (!there) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) a[k][i] = e[k][i] = 0.f;
-                    }
-                    if (eight) {
-                        st_e4m3<V>((uint8_t*)Y + lo[k], a[k], store);
-                        st_e4m3<V>((uint8_t*)Y + hi[k], e[k], store);
-                    } else {
-                        st_elems<T, V>((T*)Y + lo[k], a[k]);
-                        st_elems<T, V>((T*)Y + hi[k], e[k]);
-                    }
+                    for (int i = 0; i < V; ++i) a[k][i] = e[k][i] = 0.f;
+                }
+                if (eight) {
+                    st_e4m3<V>((uint8_t*)S.y + at + lo[k], a[k], p.store[1]);
+                    st_e4m3<V>((uint8_t*)S.y + at + hi[k], e[k], p.store[1]);
+                } else {
+                    st_elems<T, V>((T*)S.y + at + lo[k], a[k]);
+                    st_elems<T, V>((T*)S.y + at + hi[k], e[k]);
                 }
             }
         }

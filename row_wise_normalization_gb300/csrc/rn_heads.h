@@ -40,7 +40,7 @@ struct HeadShape {
 };
 
 struct HeadsParams {
-    HeadSeg seg[3];            // queries, keys, values (append only)
+    HeadSeg seg[3];            // queries, keys; append: the values beside keys
     FastDiv len;               // tokens of a sequence of the batch
     uint32_t total;            // units in all
     int per;                   // heads of a unit
