@@ -10,21 +10,27 @@
 #include "rn_heads.h"
 
 namespace rn {
-cudaError_t heads_fwd_f32(bool, bool, HeadShape, const HeadsParams&, cudaStream_t);
-cudaError_t heads_fwd_bf16(bool, bool, HeadShape, const HeadsParams&, cudaStream_t);
-cudaError_t heads_fwd_f16(bool, bool, HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_fwd_f32(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_fwd_bf16(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_fwd_f16(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_append_f32(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_append_bf16(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_append_f16(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_append8_f32(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_append8_bf16(HeadShape, const HeadsParams&, cudaStream_t);
+cudaError_t heads_append8_f16(HeadShape, const HeadsParams&, cudaStream_t);
 cudaError_t heads_bwd_f32(HeadShape, const HeadsParams&, int, void*, void*, cudaStream_t);
 cudaError_t heads_bwd_bf16(HeadShape, const HeadsParams&, int, void*, void*, cudaStream_t);
 cudaError_t heads_bwd_f16(HeadShape, const HeadsParams&, int, void*, void*, cudaStream_t);
 
 cudaError_t heads_fwd_launch(int dtype, int cache_dtype, HeadShape sh, const HeadsParams& p,
                              cudaStream_t s) {
-    const bool append = cache_dtype >= 0, e4m3 = cache_dtype == DT_E4M3;
-    switch (dtype) {
-        case DT_BF16: return heads_fwd_bf16(append, e4m3, sh, p, s);
-        case DT_F16: return heads_fwd_f16(append, e4m3, sh, p, s);
-        default: return heads_fwd_f32(append, e4m3, sh, p, s);
-    }
+    const int kind = cache_dtype < 0 ? 0 : cache_dtype != DT_E4M3 ? 1 : 2;
+    using Run = cudaError_t (*)(HeadShape, const HeadsParams&, cudaStream_t);
+    static const Run runs[3][3] = {{heads_fwd_f32, heads_fwd_bf16, heads_fwd_f16},
+                                   {heads_append_f32, heads_append_bf16, heads_append_f16},
+                                   {heads_append8_f32, heads_append8_bf16, heads_append8_f16}};
+    return runs[kind][dtype](sh, p, s);        // (DT_F32, DT_BF16, DT_F16: 0, 1, 2)
 }
 cudaError_t heads_bwd_launch(int dtype, HeadShape sh, const HeadsParams& p, int ctas, void* dwq,
                              void* dwk, cudaStream_t s) {

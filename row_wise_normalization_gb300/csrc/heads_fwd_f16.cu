@@ -2,8 +2,7 @@
 #include "rn_heads.cuh"
 
 namespace rn {
-cudaError_t heads_fwd_f16(bool append, bool e4m3, HeadShape sh, const HeadsParams& p,
-                         cudaStream_t s) {
-    return heads_fwd_t<__half>(append, e4m3, sh, p, s);
+cudaError_t heads_fwd_f16(HeadShape sh, const HeadsParams& p, cudaStream_t s) {
+    return heads_fwd_t<__half, false, false>(sh, p, s);
 }
 }  // namespace rn

@@ -156,11 +156,26 @@ __device__ __forceinline__ void grads(float (&x)[V], const float (&g)[V], const 
     }
 }
 
+// The sum over a row's LPR lanes, in each of them. Of a number that is no power of two: each lane adds
+// the sums of 1, 2 and 4 lanes from its own on, around the row, to those of the lanes that are left.
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_sum(float v, int lane) {
+    if constexpr ((LPR & (LPR - 1)) == 0) {
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+        for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    } else {
+        const int l = lane % LPR;
+        auto from = [&](float x, int o) {
+            return __shfl_sync(0xffffffffu, x, lane + (l + o < LPR ? o : o - LPR));
+        };
+        const float two = v + from(v, 1), four = two + from(two, 2);
+        if constexpr (LPR == 5) return four + from(v, 4);
+        if constexpr (LPR == 6) return four + from(two, 4);
+        static_assert(LPR == 5 || LPR == 6 || LPR == 10 || (LPR & (LPR - 1)) == 0, "lanes of a row");
+        const float eight = four + from(four, 4);
+        return eight + from(two, 8);
+    }
 }
 
 // V values times f as e4m3, to nearest even, those beyond its largest to that. (f comes last: the
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int q = l + k * LPR;
-        in[k] = 2 * q * V < d;
+        in[k] = 2 * q * V < d && sg < SG;      // (lanes behind the last row stand aside)
         pair_at<V>(q, rp, d, p.interleaved, lo[k], hi[k]);
     }
     int h = u0.head + sg;
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
             const bool there = ahead + sg < end && in[k];
             if (APPEND && key) {
                 const int q = (l + k * LPR) * V, half = p.d[2] / 2;
-                const bool beside = ahead + sg < end && q < half;
+                const bool beside = ahead + sg < end && q < half && sg < SG;
                 if constexpr (RING > 1) {
                     if (beside) {
                         copy_raw<B>(&ring[warp][put][SIDES * k + 2][lane], Z + q);
@@ -504,7 +519,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 const int q = (l + k * LPR) * V, half = p.d[2] / 2;
-                if (q >= half) continue;
+                if (q >= half || sg >= SG) continue;
                 if constexpr (RING > 1) {
                     z1[k] = ld_ring(&ring[warp][get][SIDES * k + 2][lane]);
                     z2[k] = ld_ring(&ring[warp][get][SIDES * k + 3][lane]);
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
         else
             get = get + 1 == RING ? 0 : get + 1;
         float r = 1.f;
-        if (norm) r = rsqrtf(fmaf(row_sum<LPR>(squares<V, CH>(a, e)), inv, p.eps));
+        if (norm) r = rsqrtf(fmaf(row_sum<LPR>(squares<V, CH>(a, e), lane), inv, p.eps));
         if (h < end) {
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
@@ -593,7 +608,7 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int q = l + k * LPR;
-        in[k] = 2 * q * V < d;
+        in[k] = 2 * q * V < d && sg < SG;      // (lanes behind the last row stand aside)
         pair_at<V>(q, rp, d, INTER, lo[k], hi[k]);
     }
     Raw<B>* const ring = reinterpret_cast<Raw<B>*>(shared) + warp * (RING * 4 * CH * 32) + lane;
@@ -706,7 +721,7 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
                 if (l + k * LPR < rp) turn_back<V>(v1[k], v2[k], c[k], s[k], INTER);
             }
             if constexpr (RING == 1) load();
-            const float ss = row_sum<LPR>(squares<V, CH>(u1, u2));
+            const float ss = row_sum<LPR>(squares<V, CH>(u1, u2), lane);
             float dot = 0.f;
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
@@ -715,7 +730,7 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
                 unpack<T, V>(w2, wb[k]);
                 dot += dots<V>(u1[k], u2[k], v1[k], v2[k], w1, w2);
             }
-            dot = row_sum<LPR>(dot);
+            dot = row_sum<LPR>(dot, lane);
             const float r = rsqrtf(ss * inv + p.eps);
             const float m = -(dot * inv * r * r);
             if (h < rows) {
@@ -744,19 +759,35 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
     // the warp's row groups, then the CTA's warps in order
     __syncthreads();
     float* const sums = reinterpret_cast<float*>(shared);
+    if constexpr ((LPR & (LPR - 1)) == 0) {
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
+        for (int k = 0; k < CH; ++k) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < V; ++i) {
 #pragma unroll
-            for (int o = LPR; o < 32; o <<= 1) {
-                da[k][i] += __shfl_xor_sync(0xffffffffu, da[k][i], o);
-                db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], o);
+                for (int o = LPR; o < 32; o <<= 1) {
+                    da[k][i] += __shfl_xor_sync(0xffffffffu, da[k][i], o);
+                    db[k][i] += __shfl_xor_sync(0xffffffffu, db[k][i], o);
+                }
+                if (sg == 0 && in[k]) {
+                    sums[warp * d + lo[k] + i] = da[k][i];
+                    sums[warp * d + hi[k] + i] = db[k][i];
+                }
             }
-            if (sg == 0 && in[k]) {
-                sums[warp * d + lo[k] + i] = da[k][i];
-                sums[warp * d + hi[k] + i] = db[k][i];
+        }
+    } else {
+        static_assert(CH == 1, "rows of one chunk a lane");
+        for (int g = 0; g < SG; ++g) {
+            if (sg == g && in[0]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    float* const u = sums + warp * d + lo[0] + i;
+                    float* const v = sums + warp * d + hi[0] + i;
+                    *u = g ? *u + da[0][i] : da[0][i];
+                    *v = g ? *v + db[0][i] : db[0][i];
+                }
             }
+            __syncwarp();
         }
     }
     __syncthreads();
@@ -830,7 +861,11 @@ cudaError_t for_shape(HeadShape sh, F f) {
     if constexpr (V == 8) {
         if (sh.v == 4) {
             switch (sh.lpr) {
+                case 4: return f.template run<4, 4, 1>();
+                case 5: return f.template run<4, 5, 1>();
+                case 6: return f.template run<4, 6, 1>();
                 case 8: return f.template run<4, 8, 1>();
+                case 10: return f.template run<4, 10, 1>();
                 case 16: return f.template run<4, 16, 1>();
                 default:
                     return sh.ch == 2 ? f.template run<4, 32, 2>() : f.template run<4, 32, 1>();
@@ -881,12 +916,9 @@ struct BwdRun {
     }
 };
 
-template <typename T>
-cudaError_t heads_fwd_t(bool append, bool e4m3, HeadShape sh, const HeadsParams& p,
-                        cudaStream_t s) {
-    if (!append) return for_shape<T>(sh, FwdRun<T, false, false>{p, s});
-    if (e4m3) return for_shape<T>(sh, FwdRun<T, true, true>{p, s});
-    return for_shape<T>(sh, FwdRun<T, true, false>{p, s});
+template <typename T, bool APPEND, bool E4M3>
+cudaError_t heads_fwd_t(HeadShape sh, const HeadsParams& p, cudaStream_t s) {
+    return for_shape<T>(sh, FwdRun<T, APPEND, E4M3>{p, s});
 }
 template <typename T>
 cudaError_t heads_bwd_t(HeadShape sh, const HeadsParams& p, int ctas, void* dwq, void* dwk,

@@ -62,13 +62,16 @@ struct HeadsParams {
 
 // Pairs of vectors of v elements that fill a row of d, and the lanes that hold them: vectors of 16
 // bytes (vec elements); of 8 bytes where 16 do not divide a 16-bit row's rotation (32768 tokens of 32
-// + 8 heads of 80, 40 values of each turned, BF16 105 us, 140 by two elements); else 2 or 1 elements.
+// + 8 heads of 80, 40 values of each turned, BF16 89 us, 140 by two elements); else 2 or 1 elements.
+// Lanes of a row: a power of two, or with 8-byte vectors 5, 6 or 10 too, of which more rows fit a warp
+// (that case 89 us, 105 by 16 lanes; with 16-byte vectors nothing gained: heads of 96 by 6 lanes 98 us,
+// by 8 98, their gradient 154 and 151).
 constexpr HeadShape head_shape(int v, int vec, int64_t d) {
     const int64_t pairs = (d / 2 + v - 1) / v;
     if (v >= 4) {
-        int lpr = v == vec ? 4 : 8;
-        while (lpr < 32 && lpr < pairs) lpr *= 2;
-        return {v, lpr, pairs > 32 ? 2 : 1};
+        for (int lpr : {4, 5, 6, 8, 10, 16})
+            if (pairs <= lpr && (v != vec || (lpr & (lpr - 1)) == 0)) return {v, lpr, 1};
+        return {v, 32, pairs > 32 ? 2 : 1};
     }
     const int few = v == 2 ? 1 : 2, many = v == 2 ? 4 : 8;
     return {v, 32, pairs > 32 * few ? many : few};
