@@ -1,4 +1,6 @@
-"""Build the CUDA library ``librownorm.so`` in-tree with nvcc for sm_103a.
+"""Build the CUDA library ``librownorm.so`` in-tree with nvcc for sm_103a, and beside it
+``_binding.so``, which marshals the head operators' plain calls from Python (C++ against the
+installed PyTorch; where that cannot be compiled, the package does the same in Python).
 
 Each ``csrc/*.cu`` translation unit is compiled to an object in
 ``_build/`` (in parallel), then linked into ``librownorm.so`` next to this
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +26,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librownorm.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -51,6 +55,43 @@ def _stale(target, deps):
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_binding(force: bool = False) -> bool:
+    """Compile ``_binding.so``; False (and no such file) where that does not succeed."""
+    src = os.path.join(CSRC, "binding.cpp")
+    stamp = os.path.join(BUILD, "binding.stamp")
+    try:
+        import torch
+
+        made_for = f"{torch.__version__} {sys.version}"
+        if (not force and not _stale(BINDING, [src] + _headers()) and os.path.exists(stamp)
+                and open(stamp).read() == made_for):
+            return True
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+        inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+               "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), src, "-o",
+               tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+               f"-Wl,-rpath,{lib}"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stderr if r.returncode else ""
+    except (ImportError, OSError) as e:
+        why = str(e)
+    if why:
+        print(f"[build] _binding.so: not built, calls are marshalled in Python\n{why[-2000:]}",
+              file=sys.stderr, flush=True)
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        return False
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(made_for)
+    return True
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     """Compile and link the library; returns its path."""
     nvcc = _nvcc()
@@ -77,10 +118,11 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         if verbose:
             print(f"[build] {os.path.basename(src)}", flush=True)
 
-    if todo:
-        n = jobs or min(len(todo), os.cpu_count() or 1)
-        with ThreadPoolExecutor(n) as ex:
-            list(ex.map(compile_one, todo))
+    n = jobs or min(len(todo) + 1, os.cpu_count() or 1)
+    with ThreadPoolExecutor(n) as ex:
+        binding = ex.submit(build_binding, force)
+        list(ex.map(compile_one, todo))
+        binding.result()
     if force or todo or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs

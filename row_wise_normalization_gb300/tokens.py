@@ -10,6 +10,7 @@ general ones.
 """
 from __future__ import annotations
 
+import ctypes
 from functools import partial
 
 import torch
@@ -328,11 +329,53 @@ def logprob_bwd(dlogp, logits, targets, lse, scale: float = 1.0, *, dentropy=Non
 # The head operators. Rows are heads of tokens: tensors of shape [tokens, heads, d] or
 # [batch, len, heads, d] with contiguous rows and any other strides (column blocks of a packed
 # projection, transposed head-major tensors). A tensor's rows go to the library as its address,
-# heads, and batch, token and head strides.
+# heads, and batch, token and head strides. Plain calls are made by the native module (see _Unfound);
+# what follows each of those is the general way: outputs passed in, host memory, another device or
+# stream, and what is wrong with a call.
 # ---------------------------------------------------------------------------
+class _InPython:
+    """Takes no call: each goes the way below, in Python."""
+
+    def _none(self, *args):
+        return None
+
+    qk_rope_fwd = qk_rope_bwd = kv_append = kv_gather = kv_slots = _none
+
+
+class _Unfound:
+    """Finds the native module that marshals plain calls (csrc/binding.cpp), at the first one,
+    and stands aside for it. Its functions take a call whole and return its outputs as a
+    tuple, or None for one that is not plain, which the functions here then check and make."""
+
+    def __getattr__(self, name):
+        global _B
+        lib = capi.load()
+        _B = _InPython()
+        try:
+            from . import _binding
+        except ImportError:
+            pass
+        else:
+            # (made for this PyTorch: another's objects are laid out differently)
+            if torch.__version__.split("+")[0] == _binding.torch_version:
+                _binding.use(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                               ("qk_rope_fwd", "qk_rope_bwd", "qk_rope_bwd_workspace_size",
+                                "kv_append", "kv_gather", "kv_slots")))
+                _B = _binding
+        return getattr(_B, name)
+
+
+_B = _Unfound()
 _NO_ROWS = (0, 0, 0, 0, 0)
 _heads, _qk, _empty = capi.heads, capi.qk, torch.empty
 _NONE = _heads(*_NO_ROWS)
+
+
+def _tensors(**named):
+    """Tensors, or None for what is not given."""
+    for name, t in named.items():
+        if t is not None and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def _rows(name, t, want, dtype):
@@ -372,8 +415,6 @@ def _first(name, t):
 
 def _beside(name, t, shape):
     """The shape that a tensor of other heads of the same tokens has to have."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
     heads = t.shape[-2] if t.dim() > 1 else -1
     return ((shape[0], heads, shape[2]) if len(shape) == 3 else
             (shape[0], shape[1], heads, shape[3]))
@@ -421,6 +462,11 @@ def qk_rope_fwd(q, k, positions=None, table=None, wq=None, wk=None, eps: float =
     unless ``norm`` says so, rows are normed if one of them is given. Returns ``(q_out, k_out)``
     (allocated contiguous unless given; each may be its input itself).
     """
+    if q_out is None and k_out is None and stream is None:
+        out = _B.qk_rope_fwd(q, k, positions, table, wq, wk, eps, norm, interleaved)
+        if out is not None:
+            return out
+    _tensors(q=q, k=k, positions=positions, table=table, wq=wq, wk=wk, q_out=q_out, k_out=k_out)
     code, shape = _first("q", q)
     dtype, d, len_ = q.dtype, shape[-1], shape[-3]
     batch = 1 if len(shape) == 3 else shape[0]
@@ -470,6 +516,14 @@ def qk_rope_bwd(dq_out, dk_out, q, k, positions=None, table=None, wq=None, wk=No
     themselves among them. ``workspace``: a contiguous CUDA tensor of at least
     ``capi.qk_rope_bwd_workspace_size(d)`` bytes (allocated if not given).
     """
+    if (dq is None and dk is None and dwq is None and dwk is None and workspace is None
+            and stream is None):
+        out = _B.qk_rope_bwd(dq_out, dk_out, q, k, positions, table, wq, wk, eps, norm,
+                             interleaved, param_grads)
+        if out is not None:
+            return out
+    _tensors(dq_out=dq_out, dk_out=dk_out, q=q, k=k, positions=positions, table=table, wq=wq,
+             wk=wk, dq=dq, dk=dk, dwq=dwq, dwk=dwk, workspace=workspace)
     code, shape = _first("dq_out", dq_out)
     dtype, d, len_ = dq_out.dtype, shape[-1], shape[-3]
     batch = 1 if len(shape) == 3 else shape[0]
@@ -573,6 +627,13 @@ def kv_append(k, v, slots, k_cache, v_cache, positions=None, table=None, wk=None
     values divided by k_scale and v_scale, at most 448 in size. Returns ``q_out`` (None
     without q), which may be passed in, q itself among them.
     """
+    if q_out is None and stream is None:
+        out = _B.kv_append(k, v, slots, k_cache, v_cache, positions, table, wk, eps, q, wq, norm,
+                           interleaved, k_scale, v_scale)
+        if out is not None:
+            return out[0]
+    _tensors(k=k, v=v, slots=slots, k_cache=k_cache, v_cache=v_cache, positions=positions,
+             table=table, wk=wk, q=q, wq=wq, q_out=q_out)
     code, shape = _first("k", k)
     dtype, hk, d, len_ = k.dtype, shape[-2], shape[-1], shape[-3]
     batch = 1 if len(shape) == 3 else shape[0]
@@ -624,7 +685,12 @@ def kv_gather(k_cache, v_cache, slots, *, dtype=None, k_scale: float = 1.0, v_sc
     ``dtype`` (bfloat16 unless given); otherwise dtype is the cache's. k_out, v_out may be
     passed in (contiguous rows, any other strides).
     """
-    if not isinstance(k_cache, torch.Tensor):
+    if k_out is None and v_out is None and stream is None:
+        out = _B.kv_gather(k_cache, v_cache, slots, dtype, k_scale, v_scale)
+        if out is not None:
+            return out
+    _tensors(k_cache=k_cache, v_cache=v_cache, slots=slots, k_out=k_out, v_out=v_out)
+    if k_cache is None:
         raise TypeError("k_cache must be a torch.Tensor")
     if dtype is None:
         dtype = (k_out.dtype if k_out is not None else
@@ -667,7 +733,13 @@ def kv_slots(page_table, starts, offsets, n: int, page_size: int, *, slots=None,
     what ``kv_append`` and ``qk_rope_fwd`` take for every layer of a step; with starts of 0,
     what ``kv_gather`` takes for whole sequences.
     """
-    if not isinstance(page_table, torch.Tensor):
+    if slots is None and positions is None and stream is None:
+        out = _B.kv_slots(page_table, starts, offsets, n, page_size)
+        if out is not None:
+            return out
+    _tensors(page_table=page_table, starts=starts, offsets=offsets, slots=slots,
+             positions=positions)
+    if page_table is None:
         raise TypeError("page_table must be a torch.Tensor")
     shape = page_table.shape
     if len(shape) != 2:
