@@ -141,8 +141,8 @@ bool row_suits(const rn_qk& in, int v, int es) {
     return !in.norm || (!misaligned(in.wq, v * es) && !misaligned(in.wk, v * es));
 }
 
-// The parameters that calls on queries and keys share; per: heads of a unit.
-HeadsParams qk_params(const rn_qk& in, int per) {
+// The parameters that calls on queries and keys share; least: units an SM should have.
+HeadsParams qk_params(const rn_qk& in, const HeadShape& sh, int least) {
     HeadsParams p = {};
     p.len = fast_div((uint32_t)in.len);
     p.tokens = in.batch * in.len;
@@ -168,7 +168,7 @@ HeadsParams qk_params(const rn_qk& in, int per) {
         p.d[i] = (int)in.d;
         p.store[i] = 1.f;
     }
-    p.per = per;
+    p.per = heads_per_unit(sh.lpr, in.q.heads + in.k.heads, p.tokens, least);
     return p;
 }
 void set_y(HeadSeg& g, const rn_heads* h) {
@@ -292,7 +292,7 @@ int qk_rope_fwd(const rn_qk* in, const rn_heads* q_out, const rn_heads* k_out, v
                suits(*k_out, batch, len, w, es);
     });
     const HeadShape sh = head_shape(v, vec, d);
-    HeadsParams p = qk_params(*in, heads_per_unit(sh.lpr, in->q.heads + in->k.heads, batch * len));
+    HeadsParams p = qk_params(*in, sh, kFwdUnits);
     set_y(p.seg[0], q_out);
     set_y(p.seg[1], k_out);
     if (!set_units(p)) return RN_ERR_SIZE;
@@ -372,7 +372,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         at.q = *dq_out;
         at.k = *dk_out;
     }
-    HeadsParams p = qk_params(at, heads_per_unit(sh.lpr, in->q.heads + in->k.heads, batch * len));
+    HeadsParams p = qk_params(at, sh, plain ? kFwdUnits : kBwdUnits);
     set_y(p.seg[0], dq);
     set_y(p.seg[1], dk);
     p.back = true;
@@ -431,7 +431,7 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
                cache_suits(bk, e, cs) && cache_suits(bv, e, cs);
     });
     const HeadShape sh = head_shape(w, vec, d > cache->d_v ? d : cache->d_v);
-    HeadsParams p = qk_params(*in, heads_per_unit(sh.lpr, in->q.heads + in->k.heads, batch * len));
+    HeadsParams p = qk_params(*in, sh, kFwdUnits);
     set_y(p.seg[0], q_out);
     HeadSeg& k = p.seg[1];
     k.y = cache->k;

@@ -79,12 +79,17 @@ constexpr HeadShape head_shape(int v, int vec, int64_t d) {
 
 // Heads of a unit, one token's: what a warp holds at once (32 / lpr rows), kHeadsLoops times, so
 // that a token's factors serve many rows (16 times 182 us for 32768 tokens of 64 + 8 heads of 128 BF16,
-// four times 198); fewer where that leaves an SM fewer than four units.
+// four times 198); fewer where that leaves an SM fewer than `least` units: kFwdUnits in the forward
+// kernel (512 tokens of 32 + 8 heads of 128 BF16 with 4 5.8 us, 16 4.3, 48 4.9; 4097 of 12 + 3 of 96
+// FP16 8.7, 8.7, 10.8), kBwdUnits in the gradient's, whose warps take several (511 tokens of 12 + 12
+// heads of 64 FP32 with 4 4.4 us, 16 5.4).
 constexpr int kHeadsLoops = 16;
-constexpr int heads_per_unit(int lpr, int64_t heads, int64_t tokens) {
+constexpr int kFwdUnits = 16, kBwdUnits = 4;
+constexpr int heads_per_unit(int lpr, int64_t heads, int64_t tokens, int least) {
     const int at_once = 32 / lpr;
     int loops = kHeadsLoops;
-    while (loops > 1 && tokens * ((heads + at_once * loops - 1) / (at_once * loops)) < 152 * 4)
+    while (loops > 1 &&
+           tokens * ((heads + at_once * loops - 1) / (at_once * loops)) < 152 * least)
         loops /= 2;
     return loops * at_once;
 }
