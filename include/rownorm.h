@@ -4,7 +4,8 @@
  * Two operations over the rows of a row-major matrix x[rows][d] (FP32, or
  * BF16 / FP16 storage with FP32 arithmetic in the *_typed, *_strided and
  * *_batched entry points), with their backward passes (FP32), and further down
- * the token operators (embedding rows, log probabilities, their gradients):
+ * the token operators (embedding rows, log probabilities, their gradients) and
+ * the head operators (queries and keys, a paged cache):
  *
  *   LayerNorm:  mu_i      = (1/d) sum_j x_ij
  *               sigma_i^2 = (1/d) sum_j (x_ij - mu_i)^2
@@ -101,7 +102,8 @@ typedef enum rn_status {
     RN_ERR_SCRATCH = 9, /* the request needs more than a static scratch holds  */
     RN_ERR_HOSTMEM = 10, /* a forward call's parameter vectors, or embed_bwd's
                             workspace, in host memory                          */
-    RN_ERR_SCALE = 11   /* a scale that is not finite (log probabilities: > 0) */
+    RN_ERR_SCALE = 11   /* a scale that is not finite (log probabilities, caches: > 0;
+                           1 for caches of other than 8 bits)                 */
 } rn_status;
 
 /* Storage types of x, y and the parameter vectors (statistics are FP32). */

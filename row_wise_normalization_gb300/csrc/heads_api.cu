@@ -292,7 +292,7 @@ int qk_rope_fwd(const rn_qk* in, const rn_heads* q_out, const rn_heads* k_out, v
                suits(*k_out, batch, len, w, es);
     });
     const HeadShape sh = head_shape(v, vec, d);
-    HeadsParams p = qk_params(*in, sh, kFwdUnits);
+    HeadsParams p = qk_params(*in, sh, fwd_units(sh.v));
     set_y(p.seg[0], q_out);
     set_y(p.seg[1], k_out);
     if (!set_units(p)) return RN_ERR_SIZE;
@@ -372,7 +372,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
         at.q = *dq_out;
         at.k = *dk_out;
     }
-    HeadsParams p = qk_params(at, sh, plain ? kFwdUnits : kBwdUnits);
+    HeadsParams p = qk_params(at, sh, plain ? fwd_units(sh.v) : kBwdUnits);
     set_y(p.seg[0], dq);
     set_y(p.seg[1], dk);
     p.back = true;
@@ -431,7 +431,7 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
                cache_suits(bk, e, cs) && cache_suits(bv, e, cs);
     });
     const HeadShape sh = head_shape(w, vec, d > cache->d_v ? d : cache->d_v);
-    HeadsParams p = qk_params(*in, sh, kFwdUnits);
+    HeadsParams p = qk_params(*in, sh, fwd_units(sh.v));
     set_y(p.seg[0], q_out);
     HeadSeg& k = p.seg[1];
     k.y = cache->k;

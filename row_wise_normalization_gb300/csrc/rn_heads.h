@@ -79,12 +79,14 @@ constexpr HeadShape head_shape(int v, int vec, int64_t d) {
 
 // Heads of a unit, one token's: what a warp holds at once (32 / lpr rows), kHeadsLoops times, so
 // that a token's factors serve many rows (16 times 182 us for 32768 tokens of 64 + 8 heads of 128 BF16,
-// four times 198); fewer where that leaves an SM fewer than `least` units: kFwdUnits in the forward
-// kernel (512 tokens of 32 + 8 heads of 128 BF16 with 4 5.8 us, 16 4.3, 48 4.9; 4097 of 12 + 3 of 96
-// FP16 8.7, 8.7, 10.8), kBwdUnits in the gradient's, whose warps take several (511 tokens of 12 + 12
-// heads of 64 FP32 with 4 4.4 us, 16 5.4).
+// four times 198); fewer where that leaves an SM fewer than `least` units. In the forward kernel 16 (512
+// tokens of 32 + 8 heads of 128 BF16 with 4 5.8 us, 16 4.3, 48 4.9; 2048 of them with 12 9.7, 16 8.6),
+// 12 where accesses are narrow (332 tokens of 20 + 5 heads of 128 FP16, 106 values turned: 8.3, with 16
+// 11.1); in the gradient's, whose warps take several, 4 (511 tokens of 12 + 12 heads of 64 FP32 4.4,
+// with 16 5.4).
 constexpr int kHeadsLoops = 16;
-constexpr int kFwdUnits = 16, kBwdUnits = 4;
+constexpr int kBwdUnits = 4;
+constexpr int fwd_units(int v) { return v < 4 ? 12 : 16; }
 constexpr int heads_per_unit(int lpr, int64_t heads, int64_t tokens, int least) {
     const int at_once = 32 / lpr;
     int loops = kHeadsLoops;

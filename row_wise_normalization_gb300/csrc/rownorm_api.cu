@@ -1352,7 +1352,7 @@ const char* rn_status_str(int status) {
             return "the parameter vectors (gamma, beta, w) of a forward call and the workspace "
                    "of embed_bwd must be in device memory";
         case RN_ERR_SCALE:
-            return "scale must be finite (log probabilities: finite and > 0)";
+            return "scale must be finite (log probabilities, 8-bit caches: finite and > 0; other caches: 1)";
         case RN_ERR_SCRATCH:
             return "the request needs more than the static scratch holds (ln_bwd_noalloc: "
                    "d <= 4096)";
