@@ -294,7 +294,7 @@ int qk_rope_fwd(const rn_qk* in, const rn_heads* q_out, const rn_heads* k_out, v
                suits(in->k, batch, len, w, es) && suits(*q_out, batch, len, w, es) &&
                suits(*k_out, batch, len, w, es);
     });
-    const HeadShape sh = head_shape(v, vec, d);
+    const HeadShape sh = head_shape(v, vec, d, false);
     HeadsParams p = qk_params(*in, sh, fwd_units(sh.v));
     set_y(p.seg[0], q_out);
     set_y(p.seg[1], k_out);
@@ -368,7 +368,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
                suits(*dk_out, batch, len, w, es) && suits(*dq, batch, len, w, es) &&
                suits(*dk, batch, len, w, es);
     });
-    const HeadShape sh = head_shape(v, vec, d);
+    const HeadShape sh = head_shape(v, vec, d, in->norm != 0);
     const bool plain = !in->norm;      // a rotation alone: the forward kernel, turned back
     rn_qk at = *in;
     if (plain) {
@@ -433,7 +433,7 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
                suits(*v, batch, len, e, es) && suits(*q_out, batch, len, e, es) &&
                cache_suits(bk, e, cs) && cache_suits(bv, e, cs);
     });
-    const HeadShape sh = head_shape(w, vec, d > cache->d_v ? d : cache->d_v);
+    const HeadShape sh = head_shape(w, vec, d > cache->d_v ? d : cache->d_v, false);
     HeadsParams p = qk_params(*in, sh, fwd_units(sh.v));
     set_y(p.seg[0], q_out);
     HeadSeg& k = p.seg[1];

@@ -326,7 +326,7 @@ __device__ __forceinline__ float squares(const float (&x1)[CH][V], const float (
 // copies take no fewer than 4) or a lane holds many chunks of a row.
 template <typename T, int V, int CH>
 constexpr int heads_ring() {
-    return V * (int)sizeof(T) < 4 || CH > 2 ? 1 : CH == 2 ? 2 : 4;
+    return V * (int)sizeof(T) < 4 ? 1 : V * (int)sizeof(T) * CH <= 16 ? 4 : 2;
 }
 
 template <int B>
@@ -872,8 +872,16 @@ cudaError_t for_shape(HeadShape sh, F f) {
             }
         }
     }
-    if (sh.v == 2) return sh.ch == 1 ? f.template run<2, 32, 1>() : f.template run<2, 32, 4>();
-    return sh.ch == 2 ? f.template run<1, 32, 2>() : f.template run<1, 32, 8>();
+    if (sh.v == 2) {
+        if (sh.ch == 1) return f.template run<2, 32, 1>();
+        return sh.lpr == 8    ? f.template run<2, 8, 4>()
+               : sh.lpr == 16 ? f.template run<2, 16, 4>()
+                              : f.template run<2, 32, 4>();
+    }
+    if (sh.lpr == 16) return sh.ch == 4 ? f.template run<1, 16, 4>() : f.template run<1, 16, 8>();
+    return sh.ch == 2   ? f.template run<1, 32, 2>()
+           : sh.ch == 4 ? f.template run<1, 32, 4>()
+                        : f.template run<1, 32, 8>();
 }
 
 template <typename T, bool APPEND, bool E4M3>

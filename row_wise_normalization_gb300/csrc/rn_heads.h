@@ -65,16 +65,25 @@ struct HeadsParams {
 // + 8 heads of 80, 40 values of each turned, BF16 89 us, 140 by two elements); else 2 or 1 elements.
 // Lanes of a row: a power of two, or with 8-byte vectors 5, 6 or 10 too, of which more rows fit a warp
 // (that case 89 us, 105 by 16 lanes; with 16-byte vectors nothing gained: heads of 96 by 6 lanes 98 us,
-// by 8 98, their gradient 154 and 151).
-constexpr HeadShape head_shape(int v, int vec, int64_t d) {
+// by 8 98, their gradient 154 and 151). With narrow accesses fewer lanes spread a row's own cost over
+// fewer of its values, but split its sectors: what was faster, by width and direction (gradients by two
+// elements, 80 wide: 176 us by 8 lanes, 223 by 32; by one, 8192 tokens of 16 + 4 heads of 78 FP16: 53
+// by 16, 76 by 32; forward by one, 5836 tokens appended at 256 wide: 54 by 16, 62 by 32, but 9990
+// tokens of 16 + 16 heads of 78 51 by 32, 82 by 8).
+constexpr HeadShape head_shape(int v, int vec, int64_t d, bool bwd) {
     const int64_t pairs = (d / 2 + v - 1) / v;
     if (v >= 4) {
         for (int lpr : {4, 5, 6, 8, 10, 16})
             if (pairs <= lpr && (v != vec || (lpr & (lpr - 1)) == 0)) return {v, lpr, 1};
         return {v, 32, pairs > 32 ? 2 : 1};
     }
-    const int few = v == 2 ? 1 : 2, many = v == 2 ? 4 : 8;
-    return {v, 32, pairs > 32 * few ? many : few};
+    if (v == 2) {
+        if (pairs <= 32) return bwd ? HeadShape{2, 8, 4} : HeadShape{2, 32, 1};
+        return {2, pairs <= 64 ? 16 : 32, 4};
+    }
+    if (pairs <= 64) return bwd ? HeadShape{1, 16, 4} : HeadShape{1, 32, 2};
+    if (pairs <= 128) return bwd ? HeadShape{1, 32, 4} : HeadShape{1, 16, 8};
+    return {1, 32, 8};
 }
 
 // Heads of a unit, one token's: what a warp holds at once (32 / lpr rows), kHeadsLoops times, so

@@ -68,6 +68,8 @@ SHAPES = [
     (4, 3, 1, 512, 512), (3, 2, 1, 510, 510), (4, 2, 1, 510, 250), (7, 70, 9, 16, 8),
     (300, 8, 1, 128, 0), (40, 9, 5, 112, 56), (8, 6, 2, 192, 128), (5, 3, 2, 130, 66), (6, 2, 1, 508, 4),
     (5, 3, 2, 132, 128), (2, 65, 17, 64, 32), (7, 2, 2, 10, 6),
+    (11, 7, 4, 40, 40), (12, 13, 2, 48, 24), (10, 7, 3, 80, 40), (6, 5, 2, 72, 8), (7, 3, 2, 100, 100),
+    (5, 5, 1, 140, 140), (9, 9, 3, 78, 78), (4, 3, 2, 222, 222), (6, 9, 5, 24, 24), (3, 2, 2, 384, 256),
 ]
 
 
