@@ -178,16 +178,26 @@ void set_y(HeadSeg& g, const rn_heads* h) {
     g.yt = h->token_stride;
     g.yh = h->head_stride;
 }
-// The units of every segment; false where they are too many for one launch.
-bool set_units(HeadsParams& p) {
+// The units of every segment; false where they are too many for one launch. at_once: rows that a
+// warp holds; the forward kernel's take those of several tokens where a token has at most half as many
+// (12265 tokens of 8 queries, 2 keys and values of 64 BF16 appended: 12 us, 18 a token at a time),
+// as long as that leaves an SM `least` units (0: never).
+bool set_units(HeadsParams& p, int at_once, int least) {
     int64_t total = 0;
     for (int i = 0; i < 2; ++i) {           // (values go with their keys)
         HeadSeg& g = p.seg[i];
         const int64_t groups = (g.heads + p.per - 1) / p.per;
         g.per = fast_div((uint32_t)(groups > 0 ? groups : 1));
-        total += groups * p.tokens;
+        g.pack = 1;
+        if (least > 0 && groups == 1)
+            for (g.pack = at_once / g.heads; g.pack > 1 && p.tokens / g.pack < 152 * least;)
+                g.pack /= 2;
+        if (g.pack < 1) g.pack = 1;
+        g.few = fast_div((uint32_t)(g.heads > 0 ? g.heads : 1));
+        const int64_t units = groups * ((p.tokens + g.pack - 1) / g.pack);
+        total += units;
         if (total > kMaxCount) return false;
-        g.units = (uint32_t)(groups * p.tokens);
+        g.units = (uint32_t)units;
     }
     p.total = (uint32_t)total;
     return true;
@@ -298,7 +308,7 @@ int qk_rope_fwd(const rn_qk* in, const rn_heads* q_out, const rn_heads* k_out, v
     HeadsParams p = qk_params(*in, sh, fwd_units(sh.v));
     set_y(p.seg[0], q_out);
     set_y(p.seg[1], k_out);
-    if (!set_units(p)) return RN_ERR_SIZE;
+    if (!set_units(p, 32 / sh.lpr, fwd_units(sh.v))) return RN_ERR_SIZE;
     return done(heads_fwd_launch(in->dtype, -1, sh, p, (cudaStream_t)stream));
 }
 
@@ -379,7 +389,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
     set_y(p.seg[0], dq);
     set_y(p.seg[1], dk);
     p.back = true;
-    if (!set_units(p)) return RN_ERR_SIZE;
+    if (!set_units(p, 32 / sh.lpr, plain ? fwd_units(sh.v) : 0)) return RN_ERR_SIZE;
     if (plain) return done(heads_fwd_launch(in->dtype, -1, sh, p, s));
     const rn_heads* const g[2] = {dq_out, dk_out};
     for (int i = 0; i < 2; ++i) {
@@ -457,7 +467,7 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
     p.slots = slots;
     p.nslots = cache->pages * cache->page_size;
     p.page = fast_div((uint32_t)cache->page_size);
-    if (!set_units(p)) return RN_ERR_SIZE;
+    if (!set_units(p, 32 / sh.lpr, fwd_units(sh.v))) return RN_ERR_SIZE;
     return done(heads_fwd_launch(in->dtype, cache->dtype, sh, p, (cudaStream_t)stream));
 }
 

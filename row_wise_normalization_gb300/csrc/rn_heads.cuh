@@ -15,7 +15,7 @@
 // its vector of second ones: the rotation then needs no exchange, and the only
 // one left is the row's sum, log2(LPR) shuffles. A warp takes one token and up to
 // kHeadsLoops * 32 / LPR of its heads, for which cosines, sines and weights are
-// read once. Arithmetic is FP32 (packed in pairs), each value is rounded once, to its
+// read once (forward, and tokens of few heads: several tokens, a lane group's each). Arithmetic is FP32 (packed in pairs), each value is rounded once, to its
 // storage type.
 #pragma once
 
@@ -381,29 +381,39 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
     const bool key = APPEND && u0.seg == 1;
     const HeadSeg& W = p.seg[2];               // the values beside keys
     const int d = p.d[0], rp = p.rot / 2 / V;
-    const uint32_t b = fast_quot(u0.token, p.len), t = u0.token - b * p.len.d;
     const int end = S.heads < u0.head + p.per ? S.heads : u0.head + p.per;
+    // the lane group's token and head: where a token has few heads, a warp holds several tokens
+    uint32_t token = u0.token, off = 0;
+    int h = u0.head + sg;
+    if (S.pack > 1) {
+        off = fast_quot(sg, S.few);
+        h = sg - off * S.few.d;
+        token = u0.token * S.pack + off;
+    }
+    // (lanes behind the last row stand aside)
+    const bool side = sg < SG && off < (uint32_t)S.pack && token < (uint32_t)p.tokens;
+    if (!side) token = u0.token * S.pack;
+    const uint32_t b = fast_quot(token, p.len), t = token - b * p.len.d;
     int lo[CH], hi[CH];
     bool in[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int q = l + k * LPR;
-        in[k] = 2 * q * V < d && sg < SG;      // (lanes behind the last row stand aside)
+        in[k] = 2 * q * V < d && side;
         pair_at<V>(q, rp, d, p.interleaved, lo[k], hi[k]);
     }
-    int h = u0.head + sg;
     const T* X = (const T*)S.x + b * S.xb + t * S.xt + h * S.xh;
     const T* Z = key ? (const T*)W.x + b * W.xb + t * W.xt + h * W.xh : nullptr;
     // the lane group's next row (and value): into the ring, or registers
     Raw<B> n1[CH], n2[CH], z1[CH], z2[CH];
-    int ahead = u0.head, put = 0, get = 0;
+    int ahead = h, put = 0, get = 0;
     auto load = [&]() {
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const bool there = ahead + sg < end && in[k];
+            const bool there = ahead < end && in[k];
             if (APPEND && key) {
                 const int q = (l + k * LPR) * V, half = p.d[2] / 2;
-                const bool beside = ahead + sg < end && q < half && sg < SG;
+                const bool beside = ahead < end && q < half && side;
                 if constexpr (RING > 1) {
                     if (beside) {
                         copy_raw<B>(&ring[warp][put][SIDES * k + 2][lane], Z + q);
@@ -443,8 +453,8 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
     // the table's row.
     const bool norm = p.norm, eight = E4M3 && key;
     int64_t pos = 0, slot = 0;
-    if (rp > 0) pos = ld_id(p.positions, u0.token, p.itype);
-    if (key) slot = ld_id(p.slots, u0.token, p.itype);
+    if (rp > 0) pos = ld_id(p.positions, token, p.itype);
+    if (key) slot = ld_id(p.slots, token, p.itype);
 #pragma unroll
     for (int k = 0; k < (RING > 1 ? RING - 1 : 1); ++k) load();
     Raw<B> wa[CH], wb[CH];
@@ -483,18 +493,16 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
         }
     }
     int64_t at = b * S.yb + t * S.yt + h * S.yh, zat = 0;
+    bool kept = true;
     if (key) {
-        if (slot < 0 || slot >= p.nslots) {     // (the whole warp: one token)
-            if constexpr (RING > 1) copy_wait<0>();
-            return;
-        }
+        kept = slot >= 0 && slot < p.nslots;
         const uint32_t page = fast_quot((uint32_t)slot, p.page);
         const int64_t i = (uint32_t)slot - page * p.page.d;
         at = page * S.yb + i * S.yt + h * S.yh;
         zat = page * W.yb + i * W.yt + h * W.yh;
     }
     const float inv = 1.f / (float)d;
-    for (; h - sg < end; h += SG) {
+    for (int first = u0.head; first < end; first += SG, h += SG) {
         if constexpr (RING > 1) {
             load();
             copy_wait<RING - 1>();
@@ -513,13 +521,13 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
             unpack<T, V>(a[k], n1[k]);
             unpack<T, V>(e[k], n2[k]);
         }
-        if (key && h < end) {
+        if (key && h < end && kept) {
             // the value, as it is or in 8 bits
             char* const Y = (char*)W.y + zat * (E4M3 ? 1 : (int)sizeof(T));
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 const int q = (l + k * LPR) * V, half = p.d[2] / 2;
-                if (q >= half || sg >= SG) continue;
+                if (q >= half || !side) continue;
                 if constexpr (RING > 1) {
                     z1[k] = ld_ring(&ring[warp][get][SIDES * k + 2][lane]);
                     z2[k] = ld_ring(&ring[warp][get][SIDES * k + 3][lane]);
@@ -543,7 +551,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
             get = get + 1 == RING ? 0 : get + 1;
         float r = 1.f;
         if (norm) r = rsqrtf(fmaf(row_sum<LPR>(squares<V, CH>(a, e), lane), inv, p.eps));
-        if (h < end) {
+        if (h < end && kept) {
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 if (!in[k]) continue;

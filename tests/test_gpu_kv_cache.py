@@ -188,6 +188,55 @@ def test_append(n, hq, hk, d, dv, rot, page, norm, itype, layout, dtype, cache):
             assert torch.equal(got, want.to(out_t))
 
 
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("f32", "e4m3"), ("f16", "f16")])
+@pytest.mark.parametrize("hq,hk,d,rot,interleaved", [(2, 1, 64, 64, False), (1, 1, 128, 128, True), (3, 2, 64, 32, False),
+                                                     (4, 1, 32, 32, False), (2, 1, 80, 40, True), (8, 2, 16, 16, False),
+                                                     (5, 3, 64, 64, False), (2, 2, 256, 256, False)])
+def test_many_tokens_of_few_heads(hq, hk, d, rot, interleaved, dtype, cache):
+    """Long batches, whose warps take rows of several tokens: the same bits as in short ones, padding
+    and tokens without a slot among them."""
+    n = 20011
+    rng = np.random.default_rng([n, hq, d])
+    x = rounded(rng, (n, hq + 2 * hk, d), dtype)
+    q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+    w = rounded(rng, (d,), dtype)
+    table = table_of(rng, 60, rot)
+    pos = torch.from_numpy(rng.integers(-2, 62, n)).cuda()
+    ids = rng.permutation(24000)[:n]
+    ids[rng.random(n) < 0.05] = -1
+    slots = torch.from_numpy(ids).cuda()
+    t = E4M3 if cache == "e4m3" else DT[dtype]
+    kw = dict(interleaved=interleaved)
+    sc = dict(k_scale=0.25, v_scale=0.5) if cache == "e4m3" else {}
+
+    def caches():
+        return [torch.full((1500, 16, hk, d), 3.0, device="cuda").to(t) for _ in range(2)]
+
+    whole, parts = caches(), caches()
+    qa = rn.kv_append(k, v, slots, *whole, pos, table, w, q=q, wq=w, **kw, **sc)
+    qf, kf = rn.qk_rope_fwd(q, k, pos, table, w, w, **kw)
+    assert torch.equal(qa, qf)
+    for a in range(0, n, 501):
+        s = slice(a, a + 501)
+        rn.kv_append(k[s], v[s], slots[s], *parts, pos[s], table, w, **kw, **sc)
+        q1, k1 = rn.qk_rope_fwd(q[s], k[s], pos[s], table, w, w, **kw)
+        assert torch.equal(q1, qf[s]) and torch.equal(k1, kf[s])
+    for a, b in zip(whole, parts):
+        assert torch.equal(_bits(a), _bits(b))
+    # a batch of sequences, head by head
+    b4 = lambda z: z[:20000].reshape(8, 2500, z.shape[1], d).transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    q4, k4 = rn.qk_rope_fwd(b4(q), b4(k), pos[:20000], table, w, w, **kw)
+    assert torch.equal(q4.reshape(20000, hq, d), qf[:20000]) and torch.equal(k4.reshape(20000, hk, d), kf[:20000])
+    # the rotation alone, and back
+    r, _ = rn.qk_rope_fwd(q, None, pos, table, **kw)
+    back = rn.qk_rope_bwd(r, None, None, None, pos, table, **kw)[0]
+    there = (pos >= 0) & (pos < 60)
+    assert not bool(back[~there].any())
+    # two rotations of FP32 values with their roundings, cosines and sines of unit length to 2^-23
+    far = (back - q)[there].double().abs().max()
+    assert float(far) <= (4 * torch.finfo(DT[dtype]).eps + 2.0 ** -20) * float(q.double().abs().max())
+
+
 def test_append_saturates_and_keeps_nan():
     k = torch.tensor([1e6, -1e6, 448.0, 465.0, float("inf"), -float("inf"), float("nan"), 0.0],
                      device="cuda").view(1, 1, 8).repeat(1, 1, 2)
