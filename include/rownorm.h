@@ -486,9 +486,9 @@ int qk_rope_fwd(const rn_qk *in, const rn_heads *q_out, const rn_heads *k_out, v
  *   dwq, dwk  [d], of the rows' type, each may be NULL; they need norm and their weights
  *             (RN_ERR_NULL). Every token counts but those with positions outside the table.
  * With dwq or dwk, `workspace` (16-byte aligned, caller-owned, contents ignored) must hold
- * the bytes that qk_rope_bwd_workspace_size gives (RN_ERR_SIZE), and there are two launches; the sums are
- * FP32 in an order that sizes, strides and addresses' alignment alone fix (no atomics), so
- * results repeat bit for bit. Calls that may run at the same time need workspaces of their own.
+ * the bytes that qk_rope_bwd_workspace_size gives (RN_ERR_SIZE), and there are two launches; the
+ * sums are FP32 in an order that sizes, strides and addresses' alignment alone fix (no
+ * atomics), so results repeat bit for bit. Calls that may run at the same time need workspaces of their own.
  * batch * len == 0 gives dwq and dwk of zeros.
  */
 int qk_rope_bwd_workspace_size(int64_t d, size_t *bytes);

@@ -15,7 +15,8 @@
 // its vector of second ones: the rotation then needs no exchange, and the only
 // one left is the row's sum, log2(LPR) shuffles. A warp takes one token and up to
 // kHeadsLoops * 32 / LPR of its heads, for which cosines, sines and weights are
-// read once (forward, and tokens of few heads: several tokens, a lane group's each). Arithmetic is FP32 (packed in pairs), each value is rounded once, to its
+// read once (forward, where tokens have few heads: several tokens, a lane group's
+// each). Arithmetic is FP32 (packed in pairs), each value is rounded once, to its
 // storage type.
 #pragma once
 
@@ -361,8 +362,8 @@ __device__ __forceinline__ void copy_raw(Raw<B>* smem, const void* p) {
 
 // APPEND: keys (segment 1) go into the cache, at the token's slot, and with each the value of the same
 // head (segment 2, which has no units of its own: 32768 tokens of 8 heads of 128, BF16 into 8 bits,
-// without queries 45 us, 52 with units for values; three groups ahead there, 46 with four). A warp takes
-// p.per heads of its token, a row for each lane group at a time, with the next rows under way.
+// without queries went from 52 us to 45 by that, with three groups ahead, 46 with four; 43 now). A warp
+// takes p.per heads of its token, a row for each lane group at a time, with the next rows under way.
 template <typename T, int V, int LPR, int CH, bool APPEND, bool E4M3>
 __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
     heads_fwd_kernel(const HeadsParams p) {

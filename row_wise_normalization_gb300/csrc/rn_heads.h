@@ -10,8 +10,8 @@ namespace rn {
 constexpr int DT_E4M3 = 3;         // 8-bit floating point, caches only
 constexpr int64_t kMaxHeadDim = 512;
 // Warps of a CTA of the forward kernel: few, since a CTA's place is free again when its last warp
-// ends, and warps take different times (65536 keys' and values' rows a head into an 8-bit cache: two
-// warps a CTA 52 us, eight 56).
+// ends, and warps take different times (32768 tokens' 8 keys and values of 128, into an 8-bit cache:
+// two warps a CTA 52 us, eight 56, while keys and values had units of their own).
 constexpr int kHeadsWarps = 2;
 constexpr int kHeadsThreads = kHeadsWarps * 32;
 // Warps of a CTA of the gradient's kernel, of which an SM holds two: a lane that holds 16 values of a
