@@ -179,9 +179,9 @@ void set_y(HeadSeg& g, const rn_heads* h) {
     g.yh = h->head_stride;
 }
 // The units of every segment; false where they are too many for one launch. at_once: rows that a
-// warp holds; the forward kernel's take those of several tokens where a token has at most half as many
+// warp holds; it takes those of several tokens where a token has at most half as many
 // (12265 tokens of 8 queries, 2 keys and values of 64 BF16 appended: 12 us, 18 a token at a time),
-// as long as that leaves an SM `least` units (0: never).
+// as long as that leaves an SM `least` units.
 bool set_units(HeadsParams& p, int at_once, int least) {
     int64_t total = 0;
     for (int i = 0; i < 2; ++i) {           // (values go with their keys)
@@ -189,7 +189,7 @@ bool set_units(HeadsParams& p, int at_once, int least) {
         const int64_t groups = (g.heads + p.per - 1) / p.per;
         g.per = fast_div((uint32_t)(groups > 0 ? groups : 1));
         g.pack = 1;
-        if (least > 0 && groups == 1)
+        if (groups == 1)
             for (g.pack = at_once / g.heads; g.pack > 1 && p.tokens / g.pack < 152 * least;)
                 g.pack /= 2;
         if (g.pack < 1) g.pack = 1;
@@ -217,7 +217,8 @@ BwdCtas bwd_ctas(const HeadsParams& p, int at_once, int warps) {
     int64_t most[2], groups[2], work[2];
     for (int i = 0; i < 2; ++i) {
         most[i] = ((int64_t)p.seg[i].units + warps - 1) / warps;
-        groups[i] = (p.seg[i].heads + at_once - 1) / at_once * p.tokens;
+        groups[i] = p.seg[i].pack > 1 ? (int64_t)p.seg[i].units
+                                      : (p.seg[i].heads + at_once - 1) / at_once * p.tokens;
         work[i] = groups[i] + kBwdStart * (int64_t)p.seg[i].units;
     }
     int64_t ctas = (groups[0] + groups[1]) / (warps * kBwdGroups);
@@ -389,7 +390,7 @@ int qk_rope_bwd(const rn_qk* in, const rn_heads* dq_out, const rn_heads* dk_out,
     set_y(p.seg[0], dq);
     set_y(p.seg[1], dk);
     p.back = true;
-    if (!set_units(p, 32 / sh.lpr, plain ? fwd_units(sh.v) : 0)) return RN_ERR_SIZE;
+    if (!set_units(p, 32 / sh.lpr, fwd_units(sh.v))) return RN_ERR_SIZE;
     if (plain) return done(heads_fwd_launch(in->dtype, -1, sh, p, s));
     const rn_heads* const g[2] = {dq_out, dk_out};
     for (int i = 0; i < 2; ++i) {

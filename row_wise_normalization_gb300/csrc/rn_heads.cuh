@@ -15,8 +15,8 @@
 // its vector of second ones: the rotation then needs no exchange, and the only
 // one left is the row's sum, log2(LPR) shuffles. A warp takes one token and up to
 // kHeadsLoops * 32 / LPR of its heads, for which cosines, sines and weights are
-// read once (forward, where tokens have few heads: several tokens, a lane group's
-// each). Arithmetic is FP32 (packed in pairs), each value is rounded once, to its
+// read once (where tokens have few heads: several tokens, a lane group's each).
+// Arithmetic is FP32 (packed in pairs), each value is rounded once, to its
 // storage type.
 #pragma once
 
@@ -598,7 +598,10 @@ constexpr int heads_bwd_smem(int d) {
     return ring > sums ? ring : sums;
 }
 
-template <typename T, int V, int LPR, int CH, bool INTER>
+// PACK: a segment's units may be of several tokens, as the forward kernel's (15293 tokens of 2 + 2
+// heads of 32 FP16: 10 us, 34 a token at a time). A form of its own, since what it keeps for that
+// costs the others (32768 tokens of 32 + 8 heads of 80 BF16, 20 turned: 190 us with it, 176 without).
+template <typename T, int V, int LPR, int CH, bool INTER, bool PACK>
 __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
     heads_bwd_kernel(const HeadsParams p) {
     constexpr int SG = 32 / LPR, B = V * (int)sizeof(T), RING = heads_ring<T, V, CH>();
@@ -612,12 +615,28 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
     const float inv = 1.f / (float)d;
     const uint32_t stride = (seg ? gridDim.x - p.first_k : p.first_k) * WARPS;
     uint32_t unit = (blockIdx.x - (seg ? p.first_k : 0)) * WARPS + warp;
+    // the lane group's token of a unit and head of it, as in the forward kernel
+    uint32_t off = 0;
+    int mine = sg;
+    if (PACK && S.pack > 1) {
+        off = fast_quot(sg, S.few);
+        mine = sg - off * S.few.d;
+    }
+    const bool side = sg < SG && (!PACK || off < (uint32_t)S.pack);
+    auto token_of = [&](uint32_t unit) {
+        if (!PACK) return fast_quot(unit, S.per);
+        const uint32_t t = fast_quot(unit, S.per) * S.pack;
+        return side && t + off < (uint32_t)p.tokens ? t + off : t;
+    };
+    auto live = [&](uint32_t unit) {
+        return !PACK || (side && fast_quot(unit, S.per) * S.pack + off < (uint32_t)p.tokens);
+    };
     int lo[CH], hi[CH];
     bool in[CH];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         const int q = l + k * LPR;
-        in[k] = 2 * q * V < d && sg < SG;      // (lanes behind the last row stand aside)
+        in[k] = 2 * q * V < d && side;         // (lanes behind the last row stand aside)
         pair_at<V>(q, rp, d, INTER, lo[k], hi[k]);
     }
     Raw<B>* const ring = reinterpret_cast<Raw<B>*>(shared) + warp * (RING * 4 * CH * 32) + lane;
@@ -625,20 +644,22 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
     uint32_t next = unit;
     const T *X = nullptr, *G = nullptr;
     int left = 0, put = 0, get = 0;
+    bool held = true;                      // the lane group has a token of it
     Raw<B> x1[CH], x2[CH], g1[CH], g2[CH];
     auto enter = [&]() {
-        const uint32_t token = fast_quot(next, S.per);
-        const int head = (int)(next - token * S.per.d) * p.per;
+        const uint32_t token = token_of(next);
+        const int head = (int)(next - fast_quot(next, S.per) * S.per.d) * p.per;
         const uint32_t b = fast_quot(token, p.len), t = token - b * p.len.d;
         left = S.heads - head < p.per ? S.heads - head : p.per;
-        X = (const T*)S.x + b * S.xb + t * S.xt + (head + sg) * S.xh;
-        G = (const T*)S.dy + b * S.gb + t * S.gt + (head + sg) * S.gh;
+        held = live(next);
+        X = (const T*)S.x + b * S.xb + t * S.xt + (head + mine) * S.xh;
+        G = (const T*)S.dy + b * S.gb + t * S.gt + (head + mine) * S.gh;
     };
     auto load = [&]() {
         const bool more = next < S.units;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const bool there = more && sg < left && in[k];
+            const bool there = more && held && mine < left && in[k];
             if constexpr (RING > 1) {
                 if (there) {
                     Raw<B>* const at = ring + (put * CH + k) * 128;
@@ -690,27 +711,29 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
             wa[k] = wb[k] = pack<T, V>(ones);
         }
     }
-    uint32_t token = fast_quot(unit, S.per);
+    uint32_t token = token_of(unit);
     int64_t pos = rp > 0 && unit < S.units ? ld_id(p.positions, token, p.itype) : 0;
     while (unit < S.units) {
-        const int head = (int)(unit - token * S.per.d) * p.per;
+        const uint32_t group = PACK ? fast_quot(unit, S.per) : token;
+        const int head = (int)(unit - group * S.per.d) * p.per;
+        const bool holds = live(unit);
         const uint32_t b = fast_quot(token, p.len), t = token - b * p.len.d;
         const int rows = S.heads - head < p.per ? S.heads - head : p.per;
-        int64_t at = b * S.yb + t * S.yt + (head + sg) * S.yh;
+        int64_t at = b * S.yb + t * S.yt + (head + mine) * S.yh;
         const bool there = rp == 0 || (pos >= 0 && pos < p.table_rows);
         float c[CH][V], s[CH][V];
         ld_turn<V, CH, LPR>(c, s, p.table + (there ? pos : 0) * p.ldt, l, rp, INTER);
         unit += stride;
-        token = fast_quot(unit, S.per);
+        token = token_of(unit);
         if (rp > 0 && unit < S.units) pos = ld_id(p.positions, token, p.itype);
-        for (int h = sg; h - sg < rows; h += SG) {
+        for (int h = mine; h - mine < rows; h += SG) {
             if constexpr (RING > 1) {
                 load();
                 copy_wait<RING - 1>();
 #pragma unroll
                 for (int k = 0; k < CH; ++k) {
                     x1[k] = x2[k] = g1[k] = g2[k] = Raw<B>{};
-                    if (h < rows && in[k]) {       // (a lane reads what it copied itself)
+                    if (h < rows && holds && in[k]) {       // (a lane reads what it copied itself)
                         const Raw<B>* const at = ring + (get * CH + k) * 128;
                         x1[k] = ld_ring(at);
                         x2[k] = ld_ring(at + 32);
@@ -742,7 +765,7 @@ __global__ void __launch_bounds__(heads_bwd_warps(V, CH) * 32, kHeadsBwdPerSm)
             dot = row_sum<LPR>(dot, lane);
             const float r = rsqrtf(ss * inv + p.eps);
             const float m = -(dot * inv * r * r);
-            if (h < rows) {
+            if (h < rows && holds) {
 #pragma unroll
                 for (int k = 0; k < CH; ++k) {
                     if (!in[k]) continue;
@@ -908,9 +931,9 @@ struct BwdRun {
     const HeadsParams& p;
     int ctas;
     cudaStream_t s;
-    template <int V, int LPR, int CH, bool INTER>
+    template <int V, int LPR, int CH, bool INTER, bool PACK>
     cudaError_t launch() {
-        const auto kernel = heads_bwd_kernel<T, V, LPR, CH, INTER>;
+        const auto kernel = heads_bwd_kernel<T, V, LPR, CH, INTER, PACK>;
         const int smem = heads_bwd_smem<T, V, CH>(p.d[0]);
         constexpr int MOST = heads_bwd_smem<T, V, CH>((int)kMaxHeadDim);
         if constexpr (MOST > 48 * 1024) {
@@ -929,7 +952,12 @@ struct BwdRun {
     }
     template <int V, int LPR, int CH>
     cudaError_t run() {
-        return p.interleaved ? launch<V, LPR, CH, true>() : launch<V, LPR, CH, false>();
+        if constexpr (LPR <= 16)           // (a warp holds several rows)
+            if (p.seg[0].pack > 1 || p.seg[1].pack > 1)
+                return p.interleaved ? launch<V, LPR, CH, true, true>()
+                                     : launch<V, LPR, CH, false, true>();
+        return p.interleaved ? launch<V, LPR, CH, true, false>()
+                             : launch<V, LPR, CH, false, false>();
     }
 };
 

@@ -31,7 +31,7 @@ struct HeadSeg {
     int64_t yb, yt, yh;        // of y; into a cache: page, slot, head
     int heads;
     FastDiv per;               // warps' units that a token's rows take
-    int pack;                  // forward: tokens of a unit, whose heads (few) lane groups share
+    int pack;                  // tokens of a unit, whose heads (few) lane groups share
     FastDiv few;               // division by those
     uint32_t units;            // of all tokens
 };

@@ -223,6 +223,29 @@ def test_many_tokens_of_few_heads(hq, hk, d, rot, interleaved, dtype, cache):
         assert torch.equal(q1, qf[s]) and torch.equal(k1, kf[s])
     for a, b in zip(whole, parts):
         assert torch.equal(_bits(a), _bits(b))
+    # the gradient: the same bits again, and the weights' against its definition in 64 bits
+    g = rounded(rng, (n, hq + hk, d), dtype)
+    dq, dk, dwq, dwk = rn.qk_rope_bwd(g[:, :hq], g[:, hq:], q, k, pos, table, w, w, **kw)
+    for a in range(0, n, 501):
+        s = slice(a, a + 501)
+        part = rn.qk_rope_bwd(g[s, :hq], g[s, hq:], q[s], k[s], pos[s], table, w, w, **kw)
+        assert torch.equal(part[0], dq[s]) and torch.equal(part[1], dk[s])
+    live = ((pos >= 0) & (pos < 60)).double()[:, None, None]
+    row = table[pos.clamp(0, 59)].double()[:, None]
+    cs, sn = row[..., :rot // 2], row[..., rot // 2:]
+    first = slice(0, rot, 2) if interleaved else slice(0, rot // 2)
+    second = slice(1, rot, 2) if interleaved else slice(rot // 2, rot)
+    gd, xd = g.double() * live, x[:, :hq + hk].double()
+    turn, mag = gd.clone(), gd.abs()
+    turn[..., first] = gd[..., first] * cs + gd[..., second] * sn
+    turn[..., second] = gd[..., second] * cs - gd[..., first] * sn
+    mag[..., first] = (gd[..., first] * cs).abs() + (gd[..., second] * sn).abs()
+    mag[..., second] = (gd[..., second] * cs).abs() + (gd[..., first] * sn).abs()
+    r = (xd.square().mean(-1, keepdim=True) + EPS).rsqrt()
+    for sl, dw in ((slice(0, hq), dwq), (slice(hq, None), dwk)):
+        want = {"dw": f64((turn * xd * r)[:, sl].sum((0, 1))),
+                "dw_abs": f64((mag * xd.abs() * r)[:, sl].sum((0, 1)))}
+        head_checks.check_dw(f64(dw), want, n, hq + hk, dtype)
     # a batch of sequences, head by head
     b4 = lambda z: z[:20000].reshape(8, 2500, z.shape[1], d).transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
     q4, k4 = rn.qk_rope_fwd(b4(q), b4(k), pos[:20000], table, w, w, **kw)
