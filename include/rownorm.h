@@ -500,8 +500,8 @@ int qk_rope_bwd(const rn_qk *in, const rn_heads *dq_out, const rn_heads *dk_out,
  * k + g * k_page_stride + i * k_slot_stride + h * k_head_stride, d contiguous elements, and
  * its value likewise with d_v. Its slot is g * page_size + i. pages * page_size up to
  * 2^31 - 1. k and v may be disjoint blocks of one tensor. With dtype RN_DTYPE_E4M3 a value y
- * is held as y / scale, rounded to nearest even, at most 448 in size; scales are finite
- * and > 0 (RN_ERR_SCALE), and 1 for the other types. */
+ * is held as y / scale (the FP32 quotient), rounded to nearest even, at most 448 in size; scales
+ * are finite and > 0, with finite 1 / scale (RN_ERR_SCALE), and 1 for the other types. */
 typedef struct rn_cache {
     void *k, *v;
     int64_t k_page_stride, k_slot_stride, k_head_stride;

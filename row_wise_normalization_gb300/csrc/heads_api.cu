@@ -166,7 +166,6 @@ HeadsParams qk_params(const rn_qk& in, const HeadShape& sh, int least) {
         g.xh = x[i]->head_stride;
         g.heads = (int)x[i]->heads;
         p.d[i] = (int)in.d;
-        p.store[i] = 1.f;
     }
     p.per = heads_per_unit(sh.lpr, in.q.heads + in.k.heads, p.tokens, least);
     return p;
@@ -463,8 +462,8 @@ int kv_append(const rn_qk* in, const rn_heads* q_out, const rn_heads* v, const r
     g.yh = cache->v_head_stride;
     g.heads = (int)v->heads;
     p.d[2] = (int)cache->d_v;
-    p.store[1] = 1.f / cache->k_scale;
-    p.store[2] = 1.f / cache->v_scale;
+    p.scale[1] = e4m3_scale(cache->k_scale);
+    p.scale[2] = e4m3_scale(cache->v_scale);
     p.slots = slots;
     p.nslots = cache->pages * cache->page_size;
     p.page = fast_div((uint32_t)cache->page_size);

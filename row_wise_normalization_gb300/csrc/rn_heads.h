@@ -3,6 +3,8 @@
 // values), shared by the C-ABI unit and the kernel units.
 #pragma once
 
+#include <cmath>
+
 #include "rn_tokens.h"
 
 namespace rn {
@@ -36,6 +38,17 @@ struct HeadSeg {
     uint32_t units;            // of all tokens
 };
 
+// The scale of an 8-bit cache, m 2^x with 1/2 <= m < 1, for values that are multiplied by `power`
+// (exactly: what underflows is far below e4m3's smallest) and negated: see st_e4m3.
+struct E4m3Scale {
+    float m, inverse, most, power;      // m, -1 / m, -512 m, 2^-x
+};
+inline E4m3Scale e4m3_scale(float scale) {
+    int x = 0;
+    const float m = std::frexp(scale, &x);
+    return {m, -1.f / m, -512.f * m, std::ldexp(1.f, -x)};
+}
+
 // How a warp holds rows: lpr lanes each, every lane ch pairs of vectors of v elements.
 struct HeadShape {
     int v, lpr, ch;
@@ -56,7 +69,7 @@ struct HeadsParams {
     float* part;               // gradient: [CTAs][d] sums for the weights, or NULL
     int first_k;               // gradient: the first CTA of the keys
     float eps;
-    float store[3];            // factor of a row before it is stored
+    E4m3Scale scale[3];        // of what an 8-bit cache holds of keys (1) and values (2)
     int d[3];                  // width of each segment's rows
     int rot, itype;
     bool norm, interleaved, back;   // back: the transposed rotation
