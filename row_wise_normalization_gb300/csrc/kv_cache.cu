@@ -34,14 +34,7 @@ __global__ void __launch_bounds__(kSlotsThreads) kv_slots_kernel(const SlotsPara
     if (t >= p.n) return;
     auto at = [&](int i) { return held ? off[i] : ld_id(p.offsets, i, p.itype); };
     // the first end beyond t
-    int lo = 1, hi = p.seqs + 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (at(mid) > t)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
+    const int lo = first_beyond(at, p.seqs, t);
     int64_t pos = -1, slot = -1;
     if (lo <= p.seqs) {
         const int64_t first = at(lo - 1);

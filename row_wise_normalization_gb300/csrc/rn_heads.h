@@ -144,6 +144,26 @@ struct SlotsParams {
 };
 cudaError_t kv_slots_launch(const SlotsParams& p, cudaStream_t s);
 
+// The first of entries 1 .. seqs beyond t, seqs + 1 if none is, by bisection: at(i) are entries that
+// do not fall. (seqs is up to 2^30, so that lo + hi passes 32 bits.)
+template <typename At>
+#ifdef __CUDACC__
+__device__ __forceinline__
+#else
+inline
+#endif
+int first_beyond(At at, int seqs, int64_t t) {
+    int lo = 1, hi = seqs + 1;
+    while (lo < hi) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (at(mid) > t)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
 struct GatherSide {
     const void* cache;
     void* out;

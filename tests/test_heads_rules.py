@@ -1,5 +1,27 @@
-"""The head operators' rules that need no GPU."""
+"""The head operators' rules that need no GPU; those of the host code are compiled as plain C++."""
+import os
+import shutil
+import subprocess
 from fractions import Fraction
+
+import pytest
+
+from test_tokens_rules import CSRC, _cuda_include
+
+
+def run_rules(tmp_path, body):
+    """Compiles and runs a program of the rules' header, with overflows of signed numbers that end
+    it; returns what it prints."""
+    if shutil.which("g++") is None or not os.path.exists(
+            os.path.join(_cuda_include(), "cuda_runtime.h")):
+        pytest.skip("needs g++ and CUDA's headers")
+    src, exe = tmp_path / "rules.cpp", tmp_path / "rules"
+    src.write_text('#include <cstdio>\n#include <cstdint>\n#include "rn_heads.h"\n'
+                   "using namespace rn;\nint main() {\n" + body + "\nreturn 0; }\n")
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-ftrapv", "-I", CSRC, "-I",
+                           _cuda_include(), str(src), "-o", str(exe)])
+    return subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+
 
 E4M3_TIES = range(16, 33)        # five significant bits: every tie of e4m3, subnormal ones too
 
@@ -48,3 +70,28 @@ def test_a_corrected_product_is_the_quotient_beside_ties():
         rest = t * b - a                                   # (fused: one rounding)
         rest = _rounded(rest) if rest > 0 else -_rounded(-rest) if rest else rest
         assert _rounded(t - rest * inverse) == _rounded(Fraction(a, b)), (a, b)
+
+
+# ---- host code -------------------------------------------------------------
+def test_bisection_stays_within_the_offsets(tmp_path):
+    """Every entry that is looked at is one of 1 .. seqs, for as many sequences as are taken, and
+    the answer is the first end beyond the token."""
+    out = run_rules(tmp_path, r"""
+    long wrong = 0, looked = 0;
+    for (int seqs : {0, 1, 2, 3, 61, 4096, (1 << 29) + 1, (1 << 30) - 1, 1 << 30})
+        for (int64_t t : {(int64_t)-1, (int64_t)0, (int64_t)seqs / 2, (int64_t)seqs - 1, (int64_t)seqs,
+                          (int64_t)1 << 31}) {
+            // sequences of one token each: entry i is i
+            const int got = first_beyond(
+                [&](int i) {
+                    ++looked;
+                    if (i < 1 || i > seqs) ++wrong;
+                    return (int64_t)i;
+                },
+                seqs, t);
+            const int64_t want = t < 1 ? 1 : t >= seqs ? (int64_t)seqs + 1 : t + 1;
+            wrong += got != want;
+        }
+    printf("%ld %d", wrong, looked > 100);
+    """)
+    assert out.split() == ["0", "1"]
