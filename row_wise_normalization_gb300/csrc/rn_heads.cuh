@@ -891,8 +891,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 // ---- instances -----------------------------------------------------------------
-// Calls f.run<V, LPR, CH>() for a shape.
-template <typename T, typename F>
+// Calls f.run<V, LPR, CH>() for a shape, of those that head_shape gives for the direction.
+template <typename T, bool BWD, typename F>
 cudaError_t for_shape(HeadShape sh, F f) {
     constexpr int V = Elem<T>::kVec;
     if (sh.v == V) {
@@ -921,15 +921,21 @@ cudaError_t for_shape(HeadShape sh, F f) {
         }
     }
     if (sh.v == 2) {
-        if (sh.ch == 1) return f.template run<2, 32, 1>();
-        return sh.lpr == 8    ? f.template run<2, 8, 4>()
-               : sh.lpr == 16 ? f.template run<2, 16, 4>()
-                              : f.template run<2, 32, 4>();
+        if constexpr (BWD) {
+            if (sh.lpr == 8) return f.template run<2, 8, 4>();
+        } else {
+            if (sh.ch == 1) return f.template run<2, 32, 1>();
+        }
+        return sh.lpr == 16 ? f.template run<2, 16, 4>() : f.template run<2, 32, 4>();
     }
-    if (sh.lpr == 16) return sh.ch == 4 ? f.template run<1, 16, 4>() : f.template run<1, 16, 8>();
-    return sh.ch == 2   ? f.template run<1, 32, 2>()
-           : sh.ch == 4 ? f.template run<1, 32, 4>()
-                        : f.template run<1, 32, 8>();
+    if constexpr (BWD) {
+        if (sh.lpr == 16) return f.template run<1, 16, 4>();
+        if (sh.ch == 4) return f.template run<1, 32, 4>();
+    } else {
+        if (sh.lpr == 16) return f.template run<1, 16, 8>();
+        if (sh.ch == 2) return f.template run<1, 32, 2>();
+    }
+    return f.template run<1, 32, 8>();
 }
 
 template <typename T, bool APPEND, bool E4M3>
@@ -979,12 +985,12 @@ struct BwdRun {
 
 template <typename T, bool APPEND, bool E4M3>
 cudaError_t heads_fwd_t(HeadShape sh, const HeadsParams& p, cudaStream_t s) {
-    return for_shape<T>(sh, FwdRun<T, APPEND, E4M3>{p, s});
+    return for_shape<T, false>(sh, FwdRun<T, APPEND, E4M3>{p, s});
 }
 template <typename T>
 cudaError_t heads_bwd_t(HeadShape sh, const HeadsParams& p, int ctas, void* dwq, void* dwk,
                         cudaStream_t s) {
-    const cudaError_t err = for_shape<T>(sh, BwdRun<T>{p, ctas, s});
+    const cudaError_t err = for_shape<T, true>(sh, BwdRun<T>{p, ctas, s});
     if (err != cudaSuccess || !p.part) return err;
     return launch_pdl(heads_join_kernel<T>, 2 * ((p.d[0] + kJoinCols - 1) / kJoinCols),
                       kJoinThreads, 0, s, (const float*)p.part, p.d[0], p.first_k, ctas, (T*)dwq,

@@ -1,5 +1,6 @@
 """The head operators' rules that need no GPU; those of the host code are compiled as plain C++."""
 import os
+import re
 import shutil
 import subprocess
 from fractions import Fraction
@@ -95,3 +96,34 @@ def test_bisection_stays_within_the_offsets(tmp_path):
     printf("%ld %d", wrong, looked > 100);
     """)
     assert out.split() == ["0", "1"]
+
+
+# ---- what is compiled ------------------------------------------------------
+def test_kernels_that_are_compiled_are_those_that_calls_reach(tmp_path):
+    """Every shape that some width and access gives has its kernels in the library, and no other."""
+    lib = os.path.join(os.path.dirname(CSRC), "librownorm.so")
+    if shutil.which("nm") is None or not os.path.exists(lib):
+        pytest.skip("needs nm and the library")
+    out = run_rules(tmp_path, r"""
+    for (int vec : {4, 8})
+        for (int v : {vec, 4, 2, 1})
+            for (int64_t d = 2; d <= kMaxHeadDim; d += 2)
+                for (int bwd = 0; bwd < 2 && d % (2 * v) == 0; ++bwd) {
+                    const HeadShape s = head_shape(v, vec, d, bwd);
+                    printf("%d %d %d %d %d\n", vec, bwd, s.v, s.lpr, s.ch);
+                }
+    """)
+    want = set()
+    for line in set(out.split("\n")) - {""}:
+        vec, bwd, v, lpr, ch = map(int, line.split())
+        for t in ["f"] if vec == 4 else ["13__nv_bfloat16", "6__half"]:
+            if not bwd:          # (into a cache or not, of 8 bits or not)
+                want |= {("fwd", t, v, lpr, ch, *kind) for kind in ((0, 0), (1, 0), (1, 1))}
+            else:                # (neighbours or not, several tokens to a warp where it holds several rows)
+                want |= {("bwd", t, v, lpr, ch, inter, pack) for inter in (0, 1)
+                         for pack in ((0, 1) if lpr <= 16 else (0,))}
+    names = subprocess.run(["nm", lib], capture_output=True, text=True, check=True).stdout
+    got = {(m[0], m[1], *map(int, m[2:])) for m in re.findall(
+        r"heads_(fwd|bwd)_kernelI(f|13__nv_bfloat16|6__half)Li(\d+)ELi(\d+)ELi(\d+)ELb([01])ELb([01])E",
+        names)}
+    assert want - got == set() and got - want == set()
