@@ -20,6 +20,8 @@
 // storage type.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_fp8.h>
 
 #include "rn_heads.h"
@@ -180,34 +182,27 @@ __device__ __forceinline__ float row_sum(float v, int lane) {
 }
 
 // V values over a scale as e4m3: their FP32 quotients to nearest even, those beyond the largest to
-// that. A product with 1 / scale alone goes to the wrong side of ties (0.1708984375 / 7 is one), so
-// the product t is corrected by its remainder: t - (t m - n) / m, with what E4m3Scale holds. With
-// roundings of 2^-24 that is RN(x (1 + h)) of the quotient x, |h| <= 2^-46: a neighbour of x in FP32,
-// and x itself where it is an FP32 number, all ties of e4m3 among them. It is the nearer neighbour
-// unless x is within 2^-46 of the middle of two, of which only those on either side of a tie count;
-// all such x are quotients of few numbers, tried one by one in tests/test_heads_rules.py. (32768
-// tokens' 8 keys and values of 128 BF16: 47 us, 45 by the product alone, 49 with a second correction,
-// 70 by __fdiv_rn.) n is held to 512 scales: quotients stay finite, and NaN stays NaN. (Scales come
-// last: the rotation of values near FP32's largest stays finite.)
-__device__ __forceinline__ float held_to(float x, float most) {    // (with most's sign and x's)
-    float y;
-    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
-    return y;
-}
+// that. A product with 1 / scale rounded once goes to the wrong side of ties (0.1708984375 / 7 is one),
+// so the reciprocal is two numbers, hi <= 1 / scale and the rest: RN(a hi + RN(a lo)) is RN(x (1 + h))
+// of the quotient x, |h| < 9 2^-49 (each part is off by 2^-24 of itself at most, lo < 2^-23 hi). That is
+// x where x is an FP32 number, as all ties of e4m3 are; any other x is on the same side of a tie unless
+// it is that close to the middle between the tie and an FP32 number beside it, as quotients of few
+// numbers are: tests/test_heads_rules.py tries them all. Both parts are positive, so that infinities
+// stay infinite. (32768 tokens' 8 keys and values of 128 BF16: 45 us, 43 by the product alone, 47 by a
+// product corrected by its remainder, 70 by __fdiv_rn.)
+// (Scales come last: the rotation of values near FP32's largest stays finite.)
 template <int V>
-__device__ __forceinline__ void st_e4m3(uint8_t* p, const float* v, const E4m3Scale& e) {
+__device__ __forceinline__ void st_e4m3(uint8_t* p, const float* a, const E4m3Scale& e) {
     if constexpr (V == 1) {
-        const float n = held_to(v[0] * e.power, e.most), t = n * e.inverse;
-        *p = __nv_cvt_float_to_fp8(fmaf(fmaf(t, e.m, n), e.inverse, t), __NV_SATFINITE, __NV_E4M3);
+        *p = __nv_cvt_float_to_fp8(fmaf(a[0], e.hi, a[0] * e.lo), __NV_SATFINITE, __NV_E4M3);
     } else {
         uint32_t w[(V + 3) / 4] = {};
-        const F2 m = f2s(e.m), inverse = f2s(e.inverse), power = f2s(e.power);
+        const F2 hi = f2s(e.hi), lo = f2s(e.lo);
 #pragma unroll
         for (int k = 0; k < V; k += 2) {
+            const F2 t = f2(a[k], a[k + 1]);
             float2 q;
-            f2_get(mul2(f2(v[k], v[k + 1]), power), q.x, q.y);
-            const F2 n = f2(held_to(q.x, e.most), held_to(q.y, e.most)), t = mul2(n, inverse);
-            f2_get(fma2(fma2(t, m, n), inverse, t), q.x, q.y);
+            f2_get(fma2(t, hi, mul2(t, lo)), q.x, q.y);
             w[k / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3)
                         << (8 * (k % 4));
         }
@@ -216,6 +211,24 @@ __device__ __forceinline__ void st_e4m3(uint8_t* p, const float* v, const E4m3Sc
         for (int k = 0; k < (V + 3) / 4; ++k) r.w[k] = w[k];
         st_raw<V>(p, r);
     }
+}
+// The same of V values as they are stored, which take the scale's power first. (FP16 ones need none:
+// over scales that have one they are zero with or without it.)
+template <typename T, int V>
+__device__ __forceinline__ void st_e4m3_of(uint8_t* p, const Raw<V * (int)sizeof(T)>& r,
+                                           const E4m3Scale& e) {
+    float v[V];
+    unpack<T, V>(v, r);
+    if constexpr (!std::is_same<T, __half>::value) {
+        if constexpr (V == 1) {
+            v[0] *= e.power;
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; k += 2)
+                f2_get(mul2(f2(v[k], v[k + 1]), f2s(e.power)), v[k], v[k + 1]);
+        }
+    }
+    st_e4m3<V>(p, v, e);
 }
 
 // The unit of a warp: a token, a segment and its first head. Units of one segment lie together, so
@@ -550,11 +563,8 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
                     z2[k] = ld_ring(&ring[warp][get][SIDES * k + 3][lane]);
                 }
                 if constexpr (E4M3) {
-                    float v[V];
-                    unpack<T, V>(v, z1[k]);
-                    st_e4m3<V>((uint8_t*)Y + q, v, p.scale[2]);
-                    unpack<T, V>(v, z2[k]);
-                    st_e4m3<V>((uint8_t*)Y + q + half, v, p.scale[2]);
+                    st_e4m3_of<T, V>((uint8_t*)Y + q, z1[k], p.scale[2]);
+                    st_e4m3_of<T, V>((uint8_t*)Y + q + half, z2[k], p.scale[2]);
                 } else {
                     st_raw<B>((T*)Y + q, z1[k]);
                     st_raw<B>((T*)Y + q + half, z2[k]);
@@ -568,6 +578,7 @@ __global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
             get = get + 1 == RING ? 0 : get + 1;
         float r = 1.f;
         if (norm) r = rsqrtf(fmaf(row_sum<LPR>(squares<V, CH>(a, e), lane), inv, p.eps));
+        if (eight) r *= p.scale[1].power;
         if (h < end && kept) {
 #pragma unroll
             for (int k = 0; k < CH; ++k) {

@@ -38,15 +38,19 @@ struct HeadSeg {
     uint32_t units;            // of all tokens
 };
 
-// The scale of an 8-bit cache, m 2^x with 1/2 <= m < 1, for values that are multiplied by `power`
-// (exactly: what underflows is far below e4m3's smallest) and negated: see st_e4m3.
+// The scale of an 8-bit cache: 1 / (scale power) = hi + lo, both positive (see st_e4m3). power is 1, or
+// 2^-64 for scales above 2^96, so that lo keeps its bits: of values times that, only those lose any
+// that are far below e4m3's smallest.
 struct E4m3Scale {
-    float m, inverse, most, power;      // m, -1 / m, -512 m, 2^-x
+    float hi, lo, power;
 };
 inline E4m3Scale e4m3_scale(float scale) {
-    int x = 0;
-    const float m = std::frexp(scale, &x);
-    return {m, -1.f / m, -512.f * m, std::ldexp(1.f, -x)};
+    const float power = scale > 0x1p96f ? 0x1p-64f : 1.f;
+    const double s = (double)scale * power;
+    float hi = (float)(1. / s);
+    if (hi * s > 1.) hi = std::nextafter(hi, 0.f);      // (24 bits each: exact)
+    const float lo = (float)((1. - hi * s) / s);
+    return {hi, lo > 0.f ? lo : 0x1p-149f, power};
 }
 
 // How a warp holds rows: lpr lanes each, every lane ch pairs of vectors of v elements.

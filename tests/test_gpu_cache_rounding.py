@@ -6,44 +6,16 @@ import pytest
 import torch
 
 import row_wise_normalization_gb300 as rn
-from test_heads_rules import close_quotients
+from test_heads_rules import close_quotients, e4m3_codes
 from token_util import DT
 
 pytestmark = pytest.mark.gpu
 
 # powers of two; quotients that are often ties; scales as largest value / 448; reciprocals with the
-# largest rounding; the smallest scale that is taken, a subnormal one, the largest ones
+# largest rounding; the smallest scale that is taken, a subnormal one, large ones
 SCALES = [1.0, 2.0 ** -5, 3.0, 7.0, 1.7, 0.021, 1 / 448, 0.1, 1.9999999, 1.0000001,
-          float(np.float32(2.0 ** -128 * (1 + 2.0 ** -21))), 1e-38, 2.0 ** 127, 3.4028235e38]
-
-
-def _e4m3():
-    """The non-negative e4m3 values in the order of their codes."""
-    code = np.arange(127)
-    e, m = code >> 3, code & 7
-    return np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
-
-
-def codes(q):
-    """The e4m3 codes of FP32 numbers: nearest, ties to the even code, at most 448 in size; NaN 127."""
-    q = np.asarray(q, np.float32)
-    a, held = np.minimum(np.abs(q.astype(np.float64)), 448.0), _e4m3()
-    nan = np.isnan(a)
-    a = np.where(nan, 0.0, a)
-    hi = np.searchsorted(held, a).clip(1, 126)
-    lo = hi - 1
-    down, up = a - held[lo], held[hi] - a           # (exact: few bits of 64)
-    c = np.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
-    return np.where(nan, 127, c + np.where(np.signbit(q), 128, 0)).astype(np.uint8)
-
-
-def test_codes_of_exact_values_and_ties():
-    held = _e4m3().astype(np.float32)
-    assert np.array_equal(codes(held), np.arange(127)) and held[-1] == 448
-    assert np.array_equal(codes(-held), np.arange(127) + 128)
-    ties = (held[1:] + held[:-1]) / 2
-    assert np.array_equal(codes(ties) % 2, np.zeros(126))
-    assert codes([np.inf, -np.inf, np.nan, 464, 1e-4]).tolist() == [126, 254, 127, 126, 0]
+          float(np.float32(2.0 ** -128 * (1 + 2.0 ** -21))), 1e-38, 1.25 * 2.0 ** 65, 2.0 ** 96, 1.25 * 2.0 ** 96,
+          2.0 ** 127, 3.4028235e38]
 
 
 def _values(dtype, scale, count):
@@ -81,7 +53,7 @@ def test_what_is_held_is_the_quotient_rounded_once(scale, heads, d, dtype):
         got = cache.view(torch.uint8).view(-1, heads, d)[:n].cpu().numpy()
         with np.errstate(all="ignore"):
             q = rows.float().cpu().numpy() / np.float32(s)
-        want = codes(q)
+        want = e4m3_codes(q)
         bad = np.argwhere(np.where(want == 127, got & 127, got) != want)
         assert not bad.size, (len(bad), s, [(float(rows[tuple(i)]), int(got[tuple(i)]),
                                              int(want[tuple(i)])) for i in bad[:4]])
@@ -96,13 +68,13 @@ def test_quotients_beside_ties():
         x = np.array([a * 2.0 ** (e + 23 - a.bit_length()) for a in sorted(values)
                       for e in range(-13, 11)], np.float32)
         x = torch.from_numpy(np.resize(x, -(-x.size // 64) * 64)).view(-1, 1, 64).cuda()
-        for scale in (float(b), b * 2.0 ** -149, b * 2.0 ** 103):
+        for scale in (float(b), b * 2.0 ** -149, b * 2.0 ** 72, b * 2.0 ** 103):
             rows = x if scale == b else (x.double() * (scale / b)).float()
             kc, vc = (torch.zeros(len(rows), 1, 1, 64, dtype=torch.float8_e4m3fn, device="cuda")
                       for _ in range(2))
             rn.kv_append(rows, rows, torch.arange(len(rows), device="cuda"), kc, vc, k_scale=scale,
                          v_scale=scale)
-            want = codes(rows.cpu().numpy() / np.float32(scale))
+            want = e4m3_codes(rows.cpu().numpy() / np.float32(scale))
             for c in (kc, vc):
                 got = c.view(torch.uint8).view(-1, 1, 64).cpu().numpy()
                 assert np.array_equal(got, want), (b, scale)

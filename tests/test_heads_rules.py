@@ -5,6 +5,7 @@ import shutil
 import subprocess
 from fractions import Fraction
 
+import numpy as np
 import pytest
 
 from test_tokens_rules import CSRC, _cuda_include
@@ -24,7 +25,34 @@ def run_rules(tmp_path, body):
     return subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
 
 
-E4M3_TIES = range(16, 33)        # five significant bits: every tie of e4m3, subnormal ones too
+# ---- 8 bits ----------------------------------------------------------------
+def e4m3_values():
+    """The non-negative e4m3 values in the order of their codes."""
+    code = np.arange(127)
+    e, m = code >> 3, code & 7
+    return np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+
+
+def e4m3_codes(q):
+    """The e4m3 codes of FP32 numbers: nearest, ties to the even code, at most 448 in size; NaN 127."""
+    q = np.asarray(q, np.float32)
+    a, held = np.minimum(np.abs(q.astype(np.float64)), 448.0), e4m3_values()
+    nan = np.isnan(a)
+    a = np.where(nan, 0.0, a)
+    hi = np.searchsorted(held, a).clip(1, 126)
+    lo = hi - 1
+    down, up = a - held[lo], held[hi] - a           # (exact: few bits of 64)
+    c = np.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    return np.where(nan, 127, c + np.where(np.signbit(q), 128, 0)).astype(np.uint8)
+
+
+def test_codes_of_exact_values_and_ties():
+    held = e4m3_values().astype(np.float32)
+    assert np.array_equal(e4m3_codes(held), np.arange(127)) and held[-1] == 448
+    assert np.array_equal(e4m3_codes(-held), np.arange(127) + 128)
+    ties = (held[1:] + held[:-1]) / 2
+    assert np.array_equal(e4m3_codes(ties) % 2, np.zeros(126))
+    assert e4m3_codes([np.inf, -np.inf, np.nan, 464, 1e-4]).tolist() == [126, 254, 127, 126, 0]
 
 
 def _rounded(x):
@@ -40,15 +68,15 @@ def _rounded(x):
 
 def close_quotients():
     """All pairs of 24-bit numbers (a, b), b with all of them, whose quotient is within 9 2^-49 of the
-    middle between a tie of e4m3 and an FP32 number beside it.
+    middle between a number t of five bits, as every tie of e4m3 is, and an FP32 number beside it.
 
-    The middle is n = 2^20 t +- 1 of 25 bits, t of five, and a 2^l = n b + d with |d| <= 9, as n b <
-    2^49. As a < 2^24 and n b >= 2^47, l > 23, so that 2^20 divides +-b + d: b is within 9 of a
-    multiple of 2^20."""
+    The middle is n = 2^20 t +- 1 of 25 bits, and a 2^l = n b + d with |d| <= 9, as n b < 2^49. As
+    a < 2^24 and n b >= 2^47, l > 23, so that 2^20 divides +-b + d: b is within 9 of a multiple of
+    2^20."""
     for b in sorted({c * 2 ** 20 + e for c in range(8, 17) for e in range(-9, 10)}):
         if not 2 ** 23 <= b < 2 ** 24:
             continue
-        for t in E4M3_TIES:
+        for t in range(16, 33):
             for n in (2 ** 20 * t - 1, 2 ** 20 * t + 1):
                 if not 2 ** 24 <= n < 2 ** 25:
                     continue
@@ -59,18 +87,44 @@ def close_quotients():
                         yield a, b
 
 
-def test_a_corrected_product_is_the_quotient_beside_ties():
-    """t - (t b - a) / b with t = a / b by the reciprocal, each operation rounded once: its relative
-    error before the last rounding is at most 2^-46 = 8 2^-49, so that only these pairs, where that
-    could pass the middle of two FP32 numbers, need to be tried."""
-    pairs = set(close_quotients())
+def _reciprocals(tmp_path, scales):
+    """(hi, lo, power) of each scale, as the host code gives them."""
+    out = run_rules(tmp_path, "for (float s : {" + ", ".join(float(s).hex() + "f" for s in scales) +
+                    '}) {\n    const E4m3Scale e = e4m3_scale(s);\n'
+                    '    printf("%a %a %a\\n", e.hi, e.lo, e.power);\n}')
+    return [tuple(Fraction(float.fromhex(x)) for x in line.split()) for line in out.split("\n") if line]
+
+
+def test_reciprocals_of_scales(tmp_path):
+    """Both parts are positive, hi at most the reciprocal, and their sum is off by lo's rounding alone:
+    2^-47 of it. With as much for the product's that leaves h below 9 2^-49."""
+    rng = np.random.default_rng(5)
+    scales = rng.integers(0x00200008, 0x7f800000, 400).astype(np.uint32).view(np.float32)
+    scales = [*scales, 1.0, 3.0, 7.0, 2.0 ** -126, 2.0 ** 64, 2.0 ** 96, 2.0 ** 96 * 1.25, 2.0 ** 127,
+              float(np.float32(3.4028235e38)), *(
+                  b * 2.0 ** e for _, b in set(close_quotients()) for e in (0, 72, 104))]
+    for s, (hi, lo, power) in zip(scales, _reciprocals(tmp_path, scales)):
+        exact = 1 / (Fraction(float(s)) * power)
+        assert lo > 0 and hi <= exact and power in (1, Fraction(1, 2 ** 64)), float(s)
+        assert exact - hi < exact / 2 ** 22
+        assert abs(hi + lo - exact) <= (exact - hi) / 2 ** 24 + exact * Fraction(1, 2 ** 52), float(s)
+
+
+def test_the_product_by_a_reciprocal_of_two_parts_rounds_as_the_quotient(tmp_path):
+    """RN(a hi + RN(a lo)) is RN(x (1 + h)) of the quotient x = a / b, |h| < 9 2^-49. It can lie on another
+    side of a tie than the FP32 quotient only where x is that close to a middle beside the tie."""
+    pairs = sorted(set(close_quotients()))
     assert len(pairs) > 100
+    bs = sorted({b for _, b in pairs})
+    parts = dict(zip(bs, _reciprocals(tmp_path, bs)))
+    differ = 0
     for a, b in pairs:
-        inverse = _rounded(Fraction(1, b))
-        t = _rounded(a * inverse)
-        rest = t * b - a                                   # (fused: one rounding)
-        rest = _rounded(rest) if rest > 0 else -_rounded(-rest) if rest else rest
-        assert _rounded(t - rest * inverse) == _rounded(Fraction(a, b)), (a, b)
+        hi, lo, _ = parts[b]
+        got, want = _rounded(a * hi + _rounded(a * lo)), _rounded(Fraction(a, b))
+        differ += got != want
+        e = np.arange(-12, 36.0)                        # (quotients from 2^-36 on)
+        assert np.array_equal(e4m3_codes(float(got) * 2 ** e), e4m3_codes(float(want) * 2 ** e)), (a, b)
+    assert differ < 3                                   # (the search is for real)
 
 
 # ---- host code -------------------------------------------------------------
