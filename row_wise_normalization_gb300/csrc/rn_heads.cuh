@@ -389,12 +389,22 @@ __device__ __forceinline__ void copy_raw(Raw<B>* smem, const void* p) {
                      : "memory");
 }
 
+// CTAs an SM holds at least: twelve, which spills 4 to 16 bytes in the append's kernels of 16-byte
+// vectors of 16-bit rows and is the faster all the same (16384 tokens of 64 + 8 heads of 128 BF16 into
+// 8 bits 102 us, 103 by ten without a spill); ten where the append's lanes hold two chunks of four
+// values (8192 tokens of 16 + 4 heads of 512 FP32 126 us, 146 by twelve, which spill 36 to 60 bytes);
+// eight where lanes hold more chunks.
+template <int V, int CH, bool APPEND>
+constexpr int heads_ctas() {
+    return CH > 2 ? 8 : APPEND && CH == 2 && V == 4 ? 10 : 12;
+}
+
 // APPEND: keys (segment 1) go into the cache, at the token's slot, and with each the value of the same
 // head (segment 2, which has no units of its own: 32768 tokens of 8 heads of 128, BF16 into 8 bits,
 // without queries went from 52 us to 45 by that, with three groups ahead, 46 with four; 43 now). A warp
 // takes p.per heads of its token, a row for each lane group at a time, with the next rows under way.
 template <typename T, int V, int LPR, int CH, bool APPEND, bool E4M3>
-__global__ void __launch_bounds__(kHeadsThreads, CH > 2 ? 8 : 12)
+__global__ void __launch_bounds__(kHeadsThreads, heads_ctas<V, CH, APPEND>())
     heads_fwd_kernel(const HeadsParams p) {
     constexpr int SG = 32 / LPR, B = V * (int)sizeof(T);
     constexpr int DEEP = heads_ring<T, V, CH>(), RING = APPEND && DEEP > 3 ? 3 : DEEP;
