@@ -1,12 +1,12 @@
 // binding.cpp -- the common case of the head operators' calls, marshalled in C++.
 //
 // A decoding step waits for the host side of these calls: on GB300's host cores the checks, lookups
-// and allocations of one call in Python took 13 to 30 us, here 4 to 10, its kernel takes 2 to 4. Each function here takes
-// the arguments of the Python function of its name (tokens.py), and where they are plain (torch
-// tensors on the current device, of fitting shapes and types, outputs to be allocated, the current
-// stream) it allocates the outputs, calls the library and returns them as a tuple. In every other case it
-// returns None and has done nothing: the Python function then goes its own way, and
-// says what is wrong.
+// and allocations of one call in Python take 13 to 17 us (the gradient's 30), here 4 to 5 (10), its
+// kernel takes 2 to 4. Each function here takes the arguments of the Python function of its name
+// (tokens.py), and where they are plain (torch tensors on the current device, of fitting shapes and
+// types, outputs to be allocated, the current stream) it allocates the outputs, calls the library and
+// returns them as a tuple. In every other case (outputs or a stream given among them) it returns None
+// and has done nothing: the Python function then goes its own way, and says what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

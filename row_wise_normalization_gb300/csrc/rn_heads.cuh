@@ -352,8 +352,9 @@ __device__ __forceinline__ float squares(const float (&x1)[CH][V], const float (
 
 // Row groups that a warp copies ahead, in shared memory, where each lane reads what it copied
 // itself (32768 tokens of 64 + 8 heads of 128 BF16: 182 us; rows loaded into registers 226): four,
-// as deep as that gains anything; one, in registers, where accesses are of 2 bytes (asynchronous
-// copies take no fewer than 4) or a lane holds many chunks of a row.
+// as deep as that gains anything; two where a lane holds more than 16 bytes of either half of a row
+// (wide FP32 rows); one, in registers, where accesses are of 2 bytes (asynchronous copies take no fewer
+// than 4). The append, whose groups are twice as large, copies three ahead at most.
 template <typename T, int V, int CH>
 constexpr int heads_ring() {
     return V * (int)sizeof(T) < 4 ? 1 : V * (int)sizeof(T) * CH <= 16 ? 4 : 2;
@@ -401,7 +402,8 @@ constexpr int heads_ctas() {
 
 // APPEND: keys (segment 1) go into the cache, at the token's slot, and with each the value of the same
 // head (segment 2, which has no units of its own: 32768 tokens of 8 heads of 128, BF16 into 8 bits,
-// without queries went from 52 us to 45 by that, with three groups ahead, 46 with four; 43 now). A warp
+// without queries went from 52 us to 45 by that, with three groups ahead, 46 with four; 43 by later
+// steps, 45 with quotients by the scales in place of products by their reciprocals). A warp
 // takes p.per heads of its token, a row for each lane group at a time, with the next rows under way.
 template <typename T, int V, int LPR, int CH, bool APPEND, bool E4M3>
 __global__ void __launch_bounds__(kHeadsThreads, heads_ctas<V, CH, APPEND>())

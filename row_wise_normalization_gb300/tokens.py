@@ -624,8 +624,8 @@ def kv_append(k, v, slots, k_cache, v_cache, positions=None, table=None, wk=None
     plus the token's place in its page, each at most once; a token whose slot is outside the
     cache (-1: padding) is not stored. k_cache, v_cache: ``[pages, page_size, heads, d]`` with
     contiguous rows and any other strides, of k's type or float8_e4m3fn; an 8-bit cache holds
-    values divided by k_scale and v_scale, at most 448 in size. Returns ``q_out`` (None
-    without q), which may be passed in, q itself among them.
+    values divided by k_scale and v_scale (FP32 quotients, rounded to nearest even), at most 448 in
+    size. Returns ``q_out`` (None without q), which may be passed in, q itself among them.
     """
     if q_out is None and stream is None:
         out = _B.kv_append(k, v, slots, k_cache, v_cache, positions, table, wk, eps, q, wq, norm,

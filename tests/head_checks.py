@@ -14,7 +14,7 @@ u = 2^-24 is FP32's half step, uT the storage type's (2^-8 BF16, 2^-11 FP16, 2^-
 * dw: terms g x r 3 + 2 + 16 = 21 u, their sum one u for each addition of the longest chain:
   a lane's rows, 5 shuffles, 8 warps, then the CTAs' rows.
 * storage adds uT of the result, half the smallest subnormal step at least.
-* e4m3: the product with the scale's reciprocal 2 u more, then uT = 2^-4, half of 2^-9 at least.
+* e4m3: 2 u more (the quotient by the scale takes one of them), then uT = 2^-4, half of 2^-9 at least.
 """
 from __future__ import annotations
 
@@ -47,10 +47,11 @@ def check_rope_bwd(got, want, norm, dtype, what="dx"):
 
 
 def check_dw(got, want, tokens, heads, dtype, what="dw"):
-    """heads: of queries and keys together. CTAs of 8 warps, at least 304 of them where there is
-    work for as many, share the rows of both about evenly (within a factor of 2); a lane adds at
-    most one of a warp's rows at once, and a warp's unit is 16 of them at most. At most 2432 CTAs
-    are joined: 19 a thread, 2 shuffles, 32 warps."""
+    """heads: of queries and keys together. CTAs of 6 or 8 warps, at least 304 of them where there is
+    work for as many, share the rows of both about evenly: queries' and keys' CTAs are rounded from
+    their shares, at worst one where one and a half were due, and 1.5 rows / (304 * 6) is
+    2 rows / (304 * 8). A lane adds at most one of a warp's rows at once, and a warp's unit is 16 of
+    them at most. At most 2432 CTAs are joined: 19 a thread, 2 shuffles, 32 warps."""
     chain = 2 * -(-tokens * heads // (304 * 8)) + 16 + 5 + 8 + 19 + 2 + 32
     tol = (21 + chain) * U * want["dw_abs"]
     _near(got, want["dw"], _stored(tol, want["dw"], dtype), what)

@@ -14,8 +14,8 @@ pytestmark = pytest.mark.gpu
 # powers of two; quotients that are often ties; scales as largest value / 448; reciprocals with the
 # largest rounding; the smallest scale that is taken, a subnormal one, large ones
 SCALES = [1.0, 2.0 ** -5, 3.0, 7.0, 1.7, 0.021, 1 / 448, 0.1, 1.9999999, 1.0000001,
-          float(np.float32(2.0 ** -128 * (1 + 2.0 ** -21))), 1e-38, 1.25 * 2.0 ** 65, 2.0 ** 96, 1.25 * 2.0 ** 96,
-          2.0 ** 127, 3.4028235e38]
+          float(np.float32(2.0 ** -128 * (1 + 2.0 ** -21))), 1e-38, 1.25 * 2.0 ** 65, 2.0 ** 96,
+          1.25 * 2.0 ** 96, 2.0 ** 127, 3.4028235e38]
 
 
 def _values(dtype, scale, count):
